@@ -10,8 +10,10 @@ Names follow the C ABI: pack, unpack, write, read, upload, load_r4,
 load_r4_into, r4_to_bf16, gemv, gemv_bf16, gemv_slices, moe_gemv,
 moe_gemv_bf16, gemm, gemm_bf16, gemm_rebuild, gemm_plan, moe_gemm, moe_gemm_bf16,
 add_rmsnorm, silu_mul, silu_mul_rows, repeat, weighted_sum, exponent_stats,
-read_status; DecodeStep and MoeDecodeStep compose a batch-1 decode step from
-them and capture it in a CUDA graph.
+rotate, kv_append, kv_read, kv_attention, kv_reserve, kv_fork, kv_free,
+kv_copy_pages, kv_compact, read_status; Rotary and KvCache hold a rotation's
+frequencies and a paged 8-bit cache; DecodeStep and MoeDecodeStep compose a
+batch-1 decode step from them and capture it in a CUDA graph.
 """
 from __future__ import annotations
 
@@ -26,7 +28,7 @@ LIB_PATH = os.path.join(_PKG, "libdgt.so")
 DGT_OK = 0
 STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported shape", -3: "corrupt packed data",
           -4: "CUDA error", -5: "device wait timed out", -6: "out of host memory", -7: "I/O error",
-          -8: "unsupported device or configuration"}
+          -8: "unsupported device or configuration", -9: "no room left in the cache"}
 
 
 class DgtError(RuntimeError):
@@ -59,6 +61,23 @@ class GemmPlan(C.Structure):
     _fields_ = [("m_tile", C.c_int32), ("split_k", C.c_int32), ("test_flags", C.c_uint32), ("schedule", C.c_int32)]
 
 
+class HeadsStruct(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64), ("heads", C.c_uint32),
+                ("reserved", C.c_uint32)]
+
+
+class RotaryStruct(C.Structure):
+    _fields_ = [("rot_dim", C.c_uint32), ("axes", C.c_uint32), ("interleaved", C.c_uint32), ("reserved", C.c_uint32),
+                ("d_freq", C.c_void_p), ("d_axis", C.c_void_p)]
+
+
+class KvCacheStruct(C.Structure):
+    _fields_ = [("layers", C.c_uint32), ("pages", C.c_uint32), ("kv_heads", C.c_uint32), ("head_dim", C.c_uint32),
+                ("max_seqs", C.c_uint32), ("max_pages", C.c_uint32), ("k", C.c_void_p), ("v", C.c_void_p),
+                ("k_scale", C.c_void_p), ("v_scale", C.c_void_p), ("refs", C.c_void_p), ("table", C.c_void_p),
+                ("lens", C.c_void_p)]
+
+
 _lib = None
 
 
@@ -71,6 +90,7 @@ def lib():
                               "`python -c 'import __graft_entry__ as g; g.build()'`")
         L = C.CDLL(LIB_PATH)
         vp, u64, i32 = C.c_void_p, C.c_uint64, C.c_int
+        hp, kp = C.POINTER(HeadsStruct), C.POINTER(KvCacheStruct)
         sig = {
             "dgt_status_string": (C.c_char_p, [i32]),
             "dgt_version": (i32, []),
@@ -120,6 +140,19 @@ def lib():
             "dgt_silu_mul_rows": (i32, [vp, C.c_uint32, u64, vp, vp]),
             "dgt_repeat": (i32, [vp, u64, u64, vp, vp]),
             "dgt_weighted_sum": (i32, [vp, vp, C.c_uint32, u64, vp, vp]),
+            "dgt_rotary_freqs": (i32, [C.c_double, C.c_uint32, vp]),
+            "dgt_rotate": (i32, [C.POINTER(RotaryStruct), hp, hp, hp, hp, C.c_uint32, u64, vp, vp]),
+            "dgt_kv_append": (i32, [kp, C.c_uint32, hp, hp, u64, vp, vp, vp, C.c_uint32, vp, vp]),
+            "dgt_kv_read": (i32, [kp, C.c_int32, vp, vp, vp, C.c_uint32, u64, vp, vp, vp, vp]),
+            "dgt_kv_attention_workspace_bytes": (C.c_size_t, [kp, C.c_uint32, C.c_uint32, u64]),
+            "dgt_kv_attention": (i32, [kp, C.c_uint32, hp, u64, vp, vp, C.c_uint32, C.c_float, C.c_uint32,
+                                       C.c_uint32, vp, vp, vp, C.c_size_t, vp, vp]),
+            "dgt_kv_pages_workspace_bytes": (C.c_size_t, [kp]),
+            "dgt_kv_copy_pages": (i32, [kp, vp, vp, C.c_uint32, vp, vp]),
+            "dgt_kv_fork": (i32, [kp, vp, vp, C.c_uint32, vp, vp]),
+            "dgt_kv_reserve": (i32, [kp, vp, vp, C.c_uint32, vp, vp, C.c_size_t, vp, vp]),
+            "dgt_kv_free": (i32, [kp, vp, C.c_uint32, vp, vp]),
+            "dgt_kv_compact": (i32, [kp, vp, vp, C.c_size_t, vp, vp]),
             "dgt_exponent_stats": (i32, [vp, u64, C.c_uint32, vp, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
@@ -560,6 +593,224 @@ def gemm_rebuild(W: R4, X, scratch=None, plan=None, Y32=None, Y=None, ws=None, s
                                   _ptr(ws), 0 if ws is None else ws.numel(), _ptr(status), _stream(stream)),
            "dgt_gemm_rebuild")
     return Y32, Y
+
+
+# ---------------------------------------------------------------------------
+# rotary positions
+# ---------------------------------------------------------------------------
+def _heads(x, name):
+    """The dgt_heads view of a bf16 tensor [tokens, heads, dim] on the device."""
+    import torch
+    if x.dim() != 3 or x.dtype != torch.bfloat16 or not x.is_cuda or (x.numel() and x.stride(2) != 1):
+        raise ValueError(f"{name}: a CUDA bfloat16 tensor [tokens, heads, dim] with a contiguous last dimension")
+    # a stride that no element uses may be anything
+    ts, hs = (x.stride(i) if x.shape[i] > 1 else 0 for i in (0, 1))
+    return HeadsStruct(x.data_ptr(), ts, hs, x.shape[1], 0)
+
+
+def _i32(x, name, n=None):
+    import torch
+    if x.dtype != torch.int32 or not x.is_cuda or not x.is_contiguous() or (n is not None and x.numel() != n):
+        raise ValueError(f"{name}: a contiguous CUDA int32 tensor" + ("" if n is None else f" of {n} elements"))
+    return x.data_ptr()
+
+
+class Rotary:
+    """What a rotation turns and by how much (dgt_rotary), its tables on the
+    device.  The first rot_dim dimensions of a head are turned; pair i is
+    dimensions (i, i + rot_dim/2), or (2i, 2i + 1) when interleaved, with
+    frequency base^(-2i/rot_dim) radians per position, or inv_freq[i].
+    sections: how many pairs each axis (time, height, width, ...) turns, in
+    order (None: one axis); axis: the axis of each pair, instead."""
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, sections=None, interleaved: bool = False, inv_freq=None,
+                 axis=None, device="cuda"):
+        import math
+        import torch
+        half = rot_dim // 2
+        freq = np.zeros(max(half, 1), np.uint64)
+        if inv_freq is None:
+            _check(lib().dgt_rotary_freqs(float(base), rot_dim, freq.ctypes.data), "dgt_rotary_freqs")
+        else:
+            if rot_dim % 2 or len(inv_freq) != half:
+                raise ValueError("inv_freq: rot_dim / 2 frequencies")
+            freq[:] = [round(math.ldexp(float(f) / (2 * math.pi), 64)) % 2 ** 64 for f in inv_freq]
+        if axis is None:
+            sections = [half] if sections is None else [int(n) for n in sections]
+            if sum(sections) != half or min(sections) < 0:
+                raise ValueError("sections: they add up to rot_dim / 2 pairs")
+            axis = [i for i, n in enumerate(sections) for _ in range(n)]
+            self.axes = len(sections)
+        else:
+            if len(axis) != half or min(axis) < 0:
+                raise ValueError("axis: one for each of the rot_dim / 2 pairs")
+            self.axes = max(axis) + 1
+        self.rot_dim, self.interleaved = rot_dim, bool(interleaved)
+        self.freq = torch.from_numpy(freq.view(np.int64).copy()).to(device)
+        self.axis = torch.tensor(axis, dtype=torch.uint8, device=device)
+        self.s = RotaryStruct(rot_dim, self.axes, int(self.interleaved), 0, self.freq.data_ptr(),
+                              self.axis.data_ptr())
+
+
+def rotate(rotary: Rotary, q, pos, k=None, q_out=None, k_out=None, stream=None):
+    """dgt_rotate: q (and k) bf16 [tokens, heads, dim] turned to their
+    positions, pos int32 [tokens] or [axes, tokens].  The outputs may be the
+    inputs.  Returns (q_out, k_out) (k_out None without k)."""
+    import torch
+    tokens, _, dim = q.shape
+    p = _i32(pos, "pos", rotary.axes * tokens)
+    if k is not None and (k.shape[0] != tokens or k.shape[2] != dim):
+        raise ValueError("k: the same tokens and head size as q")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
+        raise ValueError("outputs: the shapes of the inputs")
+    if k is None:
+        k_out = None
+    hs = [None if x is None else C.byref(_heads(x, n)) for x, n in ((q, "q"), (k, "k"), (q_out, "q_out"),
+                                                                    (k_out, "k_out"))]
+    _check(lib().dgt_rotate(C.byref(rotary.s), *hs, dim, tokens, p, _stream(stream)), "dgt_rotate")
+    return q_out, k_out
+
+
+# ---------------------------------------------------------------------------
+# paged 8-bit cache of keys and values
+# ---------------------------------------------------------------------------
+KV_PAGE = 64
+
+
+class KvCache:
+    """A paged cache of keys and values as e4m3 codes with a power-of-two scale
+    for each page and kv head (dgt_kv_cache; the block layout is in dgt.h).  A
+    page holds 64 tokens in every layer.  Device tensors: k, v uint8 [layers,
+    pages, kv_heads, 64 * head_dim], k_scale, v_scale float32 [layers, pages,
+    kv_heads]; refs int32 [pages], table int32 [max_seqs, max_pages] and lens
+    int32 [max_seqs] for the sequences, slots 0..max_seqs-1."""
+
+    def __init__(self, layers: int, pages: int, kv_heads: int, head_dim: int, max_seqs: int, max_pages: int,
+                 device="cuda"):
+        import torch
+        z = lambda dt, *s: torch.zeros(s, dtype=dt, device=device)
+        block = KV_PAGE * head_dim
+        self.layers, self.pages, self.kv_heads, self.head_dim = layers, pages, kv_heads, head_dim
+        self.max_seqs, self.max_pages = max_seqs, max_pages
+        self.k, self.v = (z(torch.uint8, layers, pages, kv_heads, block) for _ in range(2))
+        self.k_scale, self.v_scale = (z(torch.float32, layers, pages, kv_heads) for _ in range(2))
+        self.refs = z(torch.int32, pages)
+        self.table = torch.full((max_seqs, max_pages), -1, dtype=torch.int32, device=device)
+        self.lens = z(torch.int32, max_seqs)
+        self.s = KvCacheStruct(layers, pages, kv_heads, head_dim, max_seqs, max_pages,
+                               *(t.data_ptr() for t in (self.k, self.v, self.k_scale, self.v_scale, self.refs,
+                                                        self.table, self.lens)))
+        self.ws = torch.empty(max(int(lib().dgt_kv_pages_workspace_bytes(C.byref(self.s))), 256), dtype=torch.uint8,
+                              device=device)   # of the page operations
+
+
+def kv_append(cache: KvCache, layer: int, k, v, seqs, start, cu=None, status=None, stream=None):
+    """dgt_kv_append: new keys and values, bf16 [tokens, kv_heads, head_dim],
+    quantised into the pages of the sequences `seqs` int32 [batch] from
+    positions `start` int32 [batch] on.  cu int32 [batch + 1]: the rows of
+    each (None: one row each)."""
+    tokens, batch = k.shape[0], seqs.numel()
+    if k.shape != v.shape or tuple(k.shape[1:]) != (cache.kv_heads, cache.head_dim):
+        raise ValueError("k, v: [tokens, kv_heads, head_dim]")
+    _check(lib().dgt_kv_append(C.byref(cache.s), layer, C.byref(_heads(k, "k")), C.byref(_heads(v, "v")), tokens,
+                               _i32(seqs, "seqs"), _i32(start, "start", batch),
+                               None if cu is None else _i32(cu, "cu", batch + 1), batch, _ptr(status),
+                               _stream(stream)), "dgt_kv_append")
+
+
+def kv_read(cache: KvCache, layer, seqs, first, cu, tokens: int, status=None, stream=None):
+    """dgt_kv_read: the values of the sequences' positions first[b] .. as bf16
+    (k, v), each [tokens, kv_heads, head_dim]; layer None: [layers, tokens,
+    ...].  cu int32 [batch + 1] (None: one position each), tokens: their sum."""
+    import torch
+    batch = seqs.numel()
+    lead = (cache.layers,) if layer is None else ()
+    out = [torch.empty((*lead, tokens, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16, device=cache.k.device)
+           for _ in range(2)]
+    _check(lib().dgt_kv_read(C.byref(cache.s), -1 if layer is None else layer, _i32(seqs, "seqs"),
+                             _i32(first, "first", batch), None if cu is None else _i32(cu, "cu", batch + 1), batch,
+                             tokens, _ptr(out[0]), _ptr(out[1]), _ptr(status), _stream(stream)), "dgt_kv_read")
+    return out
+
+
+def kv_attention_workspace(cache: KvCache, q_heads: int, batch: int, tokens: int):
+    """A workspace for kv_attention calls of these sizes (zeroed, as its first use wants it)."""
+    import torch
+    nb = int(lib().dgt_kv_attention_workspace_bytes(C.byref(cache.s), q_heads, batch, tokens))
+    return torch.zeros(max(nb, 256), dtype=torch.uint8, device=cache.k.device)
+
+
+def kv_attention(cache: KvCache, layer: int, q, seqs, cu=None, scale=None, window: int = 0, sinks: int = 0, out=None,
+                 lse=None, ws=None, status=None, stream=None):
+    """dgt_kv_attention: the new rows q, bf16 [tokens, q_heads, head_dim], the
+    last ones of the sequences `seqs` int32 [batch], over the cache.  cu int32
+    [batch + 1]: the rows of each (None: one row each).  scale: of the scores
+    (None: head_dim^-0.5).  window > 0: a row sees its last `window` positions
+    and the first `sinks`.  lse: float32 [tokens, q_heads] or None.  Returns
+    out, bf16 [tokens, q_heads, head_dim]."""
+    import torch
+    tokens, heads, dim = q.shape
+    batch = seqs.numel()
+    if dim != cache.head_dim:
+        raise ValueError("q: [tokens, q_heads, head_dim] with the cache's head_dim")
+    if window < 0 or sinks < 0:
+        raise ValueError("window and sinks: not negative")
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=q.device)
+    if tuple(out.shape) != (tokens, heads, dim) or out.dtype != torch.bfloat16 or not out.is_contiguous():
+        raise ValueError("out: a contiguous bfloat16 tensor of q's shape")
+    if lse is not None and (lse.numel() != tokens * heads or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse: a contiguous float32 tensor [tokens, q_heads]")
+    if ws is None:
+        ws = kv_attention_workspace(cache, heads, batch, tokens)
+    _check(lib().dgt_kv_attention(C.byref(cache.s), layer, C.byref(_heads(q, "q")), tokens, _i32(seqs, "seqs"),
+                                  None if cu is None else _i32(cu, "cu", batch + 1), batch,
+                                  dim ** -0.5 if scale is None else scale, window, sinks, _ptr(out), _ptr(lse),
+                                  _ptr(ws), ws.numel(), _ptr(status), _stream(stream)), "dgt_kv_attention")
+    return out
+
+
+def kv_reserve(cache: KvCache, seqs, count, start=None, status=None, stream=None):
+    """dgt_kv_reserve: room for count[i] more tokens of sequence seqs[i] (int32
+    on the device), copying a shared partly filled page first.  Returns start
+    int32: the lengths before (-1 everywhere when there is too little room)."""
+    import torch
+    n = seqs.numel()
+    if start is None:
+        start = torch.empty(n, dtype=torch.int32, device=seqs.device)
+    _check(lib().dgt_kv_reserve(C.byref(cache.s), _i32(seqs, "seqs"), _i32(count, "count", n), n,
+                                _i32(start, "start", n), _ptr(cache.ws), cache.ws.numel(), _ptr(status),
+                                _stream(stream)), "dgt_kv_reserve")
+    return start
+
+
+def kv_fork(cache: KvCache, src, dst, status=None, stream=None):
+    """dgt_kv_fork: sequences dst[i] become copies of src[i] that share its pages."""
+    _check(lib().dgt_kv_fork(C.byref(cache.s), _i32(src, "src"), _i32(dst, "dst", src.numel()), src.numel(),
+                             _ptr(status), _stream(stream)), "dgt_kv_fork")
+
+
+def kv_free(cache: KvCache, seqs, status=None, stream=None):
+    """dgt_kv_free: the sequences give up their pages."""
+    _check(lib().dgt_kv_free(C.byref(cache.s), _i32(seqs, "seqs"), seqs.numel(), _ptr(status), _stream(stream)),
+           "dgt_kv_free")
+
+
+def kv_copy_pages(cache: KvCache, src, dst, status=None, stream=None):
+    """dgt_kv_copy_pages: pages src[i] -> dst[i] (int32 on the device) in every layer."""
+    _check(lib().dgt_kv_copy_pages(C.byref(cache.s), _i32(src, "src"), _i32(dst, "dst", src.numel()), src.numel(),
+                                   _ptr(status), _stream(stream)), "dgt_kv_copy_pages")
+
+
+def kv_compact(cache: KvCache, live=None, status=None, stream=None):
+    """dgt_kv_compact: the used pages move to the lowest numbers; live (int32
+    [1] on the device) gets their count."""
+    _check(lib().dgt_kv_compact(C.byref(cache.s), None if live is None else _i32(live, "live", 1), _ptr(cache.ws),
+                                cache.ws.numel(), _ptr(status), _stream(stream)), "dgt_kv_compact")
 
 
 # ---------------------------------------------------------------------------

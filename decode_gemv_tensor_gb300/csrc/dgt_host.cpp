@@ -333,6 +333,7 @@ const char *dgt_status_string(int status) {
         case DGT_ERR_OOM: return "out of host memory";
         case DGT_ERR_IO: return "I/O error";
         case DGT_ERR_UNSUPPORTED: return "unsupported device or configuration";
+        case DGT_ERR_FULL: return "no room left in the cache";
         default: return "unknown status";
     }
 }

@@ -1,0 +1,679 @@
+// dgt_kv.cu -- the paged 8-bit cache: quantising append, reading back, and the
+// page operations (copy, fork, reserve with copy on write, free, compact).
+//
+// An append is a pass over the new rows: the block's largest magnitude gives
+// the power-of-two scale, the codes follow by one multiplication and one
+// rounding (exact scaling, so the result depends on no order).  Page copies
+// move whole pages, bytes untouched.  Page bookkeeping is integer work on a
+// few words per sequence, done by one CTA in the order of the list.
+#include "dgt_kv.cuh"
+
+#include "dgt_device.cuh"
+
+namespace dgt {
+
+// Smallest e with amax <= 448 * 2^e, clamped to KV_EMIN (448 = 1.75 * 2^8).
+__device__ __forceinline__ int scale_exp(float amax) {
+    const uint32_t u = __float_as_uint(amax);
+    const int x = (int)(u >> 23) - 127;             // subnormals: -127, below the clamp
+    const int e = x - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return e < KV_EMIN ? KV_EMIN : e;
+}
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
+    return (uint16_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// The code byte pair to two floats.
+__device__ __forceinline__ float2 e4m3x2_f32(uint16_t c) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3);
+    return __half22float2(__half2(h));
+}
+
+__device__ __forceinline__ float finite_or_zero(float x, bool &bad) {
+    if ((__float_as_uint(x) & 0x7F800000u) == 0x7F800000u) {
+        bad = true;
+        return 0.0f;
+    }
+    return x;
+}
+
+struct AppendArgs {
+    dgt_kv_cache c;
+    uint32_t layer, batch;
+    uint64_t tokens;
+    dgt_heads x[2];
+    const int32_t *seqs, *start, *cu;
+    int32_t *status;
+};
+
+constexpr uint32_t AP_THREADS = 128;
+
+// One CTA: (block item, head, keys or values).
+template <uint32_t D>
+__global__ void __launch_bounds__(AP_THREADS) k_kv_append(AppendArgs a) {
+    __shared__ float red[AP_THREADS / 32];
+    __shared__ int redbad[AP_THREADS / 32];
+    __shared__ __align__(16) uint8_t tile[KV_P * (D + 4)];
+    pdl_trigger();
+    pdl_wait();
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t head = blockIdx.y, side = blockIdx.z;
+    uint32_t b = blockIdx.x, blk = 0, row0 = blockIdx.x, n = 1;
+    if (a.cu) {
+        b = item_entry(a.cu, a.batch, blockIdx.x, KV_P, 2);
+        blk = blockIdx.x - item_base(a.cu, b, KV_P, 2);
+        row0 = (uint32_t)a.cu[b];
+        n = (uint32_t)(a.cu[b + 1] - a.cu[b]);
+    }
+    if (n == 0) return;
+    const int32_t seq = a.seqs[b], start = a.start[b];
+    if ((uint64_t)row0 + n > a.tokens || seq < 0 || (uint32_t)seq >= a.c.max_seqs || start < 0 ||
+        (uint64_t)start + n > (uint64_t)a.c.max_pages * KV_P) {
+        if (tid == 0) set_status(a.status, DGT_ERR_ARG);
+        return;
+    }
+    const uint32_t pi = (uint32_t)start / KV_P + blk;
+    if ((uint64_t)pi * KV_P >= (uint64_t)start + n) return;   // an empty number
+    const int32_t page = a.c.table[(uint64_t)seq * a.c.max_pages + pi];
+    if (page < 0 || (uint32_t)page >= a.c.pages) {
+        if (tid == 0) set_status(a.status, DGT_ERR_ARG);
+        return;
+    }
+    const uint32_t t0 = pi * KV_P;
+    const uint32_t lo = blk == 0 ? (uint32_t)start - t0 : 0;
+    const uint32_t hi = min(KV_P, (uint32_t)start + n - t0);
+    const dgt_heads &x = a.x[side];
+    const uint16_t *src = x.data + (int64_t)head * x.head_stride +
+                          (int64_t)(row0 + (t0 + lo - (uint32_t)start)) * x.token_stride;
+    const uint64_t bi = kv_block(a.c, a.layer, (uint32_t)page, head);
+    uint8_t *dst = (side ? a.c.v : a.c.k) + bi * (KV_P * D);
+    float *scale_p = (side ? a.c.v_scale : a.c.k_scale) + bi;
+
+    // the new rows' largest magnitude
+    constexpr uint32_t CH = D / 16;   // 16-element chunks of a row
+    const uint32_t chunks = (hi - lo) * CH;
+    float amax = 0.0f;
+    bool bad = false;
+    for (uint32_t i = tid; i < chunks; i += AP_THREADS) {
+        const uint16_t *p = src + (int64_t)(i / CH) * x.token_stride + (i % CH) * 16;
+        const uint4 u0 = *reinterpret_cast<const uint4 *>(p), u1 = *reinterpret_cast<const uint4 *>(p + 8);
+        const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            amax = fmaxf(amax, fabsf(finite_or_zero(bf16lo(w[j]), bad)));
+            amax = fmaxf(amax, fabsf(finite_or_zero(bf16hi(w[j]), bad)));
+        }
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(DGT_FULL, amax, d));
+    bad = __any_sync(DGT_FULL, bad);
+    if (lane == 0) {
+        red[warp] = amax;
+        redbad[warp] = bad;
+    }
+    const float s_old = lo ? *scale_p : 0.0f;   // read by all before thread 0 writes it
+    __syncthreads();
+#pragma unroll
+    for (uint32_t i = 0; i < AP_THREADS / 32; i++) {
+        amax = fmaxf(amax, red[i]);
+        bad = bad || redbad[i];
+    }
+    int e = scale_exp(amax);
+    bool grow = false;
+    float down = 1.0f;
+    if (lo) {
+        if (s_old != s_old) {
+            bad = true;
+        } else {
+            const int eo = (int)(__float_as_uint(s_old) >> 23) - 127;
+            if (eo >= e) {
+                e = eo;
+            } else {
+                grow = true;
+                down = s_old / exp2_int(e);   // a power of two below 1
+            }
+        }
+    }
+    const float inv = exp2_int(-e);
+    if (tid == 0) *scale_p = bad ? __uint_as_float(0x7FC00000u) : exp2_int(e);
+
+    // tokens that were there, to the new scale: two codes of a word at a time
+    if (grow) {
+        const uint32_t words = side ? D * KV_P / 4 : KV_P * D / 4;
+        for (uint32_t i = tid; i < words; i += AP_THREADS) {
+            // the four bytes of a value word are four tokens of a dimension,
+            // those of a key word four dimensions of a token
+            uint32_t keep = 0xFFFFFFFFu;   // bytes that stay as they are
+            if (side) {
+                const uint32_t t = (i * 4) % KV_P;
+                if (t >= lo) continue;
+                keep = lo - t >= 4 ? 0u : 0xFFFFFFFFu << (8 * (lo - t));
+            } else {
+                const uint32_t t = D == 64 ? (i * 4) / 64 : ((i * 4) % (KV_P * 128)) / 128;
+                if (t >= lo) continue;
+                keep = 0u;
+            }
+            uint32_t *wp = reinterpret_cast<uint32_t *>(dst) + i;
+            const uint32_t w = *wp;
+            const float2 f0 = e4m3x2_f32((uint16_t)w), f1 = e4m3x2_f32((uint16_t)(w >> 16));
+            const uint32_t r = (uint32_t)e4m3x2(f0.x * down, f0.y * down) |
+                               (uint32_t)e4m3x2(f1.x * down, f1.y * down) << 16;
+            *wp = (w & keep) | (r & ~keep);
+        }
+        __syncthreads();   // a value word may hold old and new tokens
+    }
+
+    // the new rows
+    for (uint32_t i = tid; i < chunks; i += AP_THREADS) {
+        const uint32_t r = i / CH, c = i % CH;
+        const uint16_t *p = src + (int64_t)r * x.token_stride + c * 16;
+        const uint4 u0 = *reinterpret_cast<const uint4 *>(p), u1 = *reinterpret_cast<const uint4 *>(p + 8);
+        const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+        uint32_t o[4];
+        bool ignore = false;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float f0 = finite_or_zero(bf16lo(w[2 * j]), ignore) * inv;
+            const float f1 = finite_or_zero(bf16hi(w[2 * j]), ignore) * inv;
+            const float f2 = finite_or_zero(bf16lo(w[2 * j + 1]), ignore) * inv;
+            const float f3 = finite_or_zero(bf16hi(w[2 * j + 1]), ignore) * inv;
+            o[j] = (uint32_t)e4m3x2(f0, f1) | (uint32_t)e4m3x2(f2, f3) << 16;
+        }
+        if (side == 0) {
+            *reinterpret_cast<uint4 *>(dst + kv_k_off(D, lo + r, c * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+        } else {
+            uint32_t *tp = reinterpret_cast<uint32_t *>(tile + (lo + r) * (D + 4) + c * 16);
+#pragma unroll
+            for (int j = 0; j < 4; j++) tp[j] = o[j];
+        }
+    }
+    if (side == 0) return;
+    __syncthreads();
+    // values: transposed out of shared memory, a word of four tokens at a time
+    const uint32_t w0 = lo / 4, w1 = (hi + 3) / 4;
+    for (uint32_t i = tid; i < D * (w1 - w0); i += AP_THREADS) {
+        const uint32_t d = i / (w1 - w0), t = (w0 + i % (w1 - w0)) * 4;
+        uint32_t w = 0;
+#pragma unroll
+        for (uint32_t j = 0; j < 4; j++) w |= (uint32_t)tile[(t + j) * (D + 4) + d] << (8 * j);
+        uint8_t *q = dst + kv_v_off(t, d);
+        if (t >= lo && t + 4 <= hi) {
+            *reinterpret_cast<uint32_t *>(q) = w;
+        } else {
+            for (uint32_t j = 0; j < 4; j++)
+                if (t + j >= lo && t + j < hi) q[j] = (uint8_t)(w >> (8 * j));
+        }
+    }
+}
+
+struct ReadArgs {
+    dgt_kv_cache c;
+    uint32_t layer0, layers, batch;
+    uint64_t tokens;
+    const int32_t *seqs, *first, *cu;
+    uint16_t *out[2];
+    int32_t *status;
+};
+
+constexpr uint32_t RD_THREADS = 128;
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    return (uint32_t)f32_to_bf16_rne(lo) | (uint32_t)f32_to_bf16_rne(hi) << 16;
+}
+
+// One CTA: (block item, head, layer and keys or values).
+template <uint32_t D>
+__global__ void __launch_bounds__(RD_THREADS) k_kv_read(ReadArgs a) {
+    __shared__ __align__(16) uint8_t tile[D * (KV_P + 4)];
+    pdl_trigger();
+    pdl_wait();
+    const uint32_t tid = threadIdx.x;
+    const uint32_t head = blockIdx.y, side = blockIdx.z & 1, layer = a.layer0 + blockIdx.z / 2;
+    if (!a.out[side]) return;
+    uint32_t b = blockIdx.x, blk = 0, row0 = blockIdx.x, n = 1;
+    if (a.cu) {
+        b = item_entry(a.cu, a.batch, blockIdx.x, KV_P, 2);
+        blk = blockIdx.x - item_base(a.cu, b, KV_P, 2);
+        row0 = (uint32_t)a.cu[b];
+        n = (uint32_t)(a.cu[b + 1] - a.cu[b]);
+    }
+    if (n == 0) return;
+    const int32_t seq = a.seqs[b], first = a.first[b];
+    if ((uint64_t)row0 + n > a.tokens || seq < 0 || (uint32_t)seq >= a.c.max_seqs || first < 0 ||
+        (uint64_t)first + n > (uint64_t)a.c.max_pages * KV_P) {
+        if (tid == 0) set_status(a.status, DGT_ERR_ARG);
+        return;
+    }
+    const uint32_t pi = (uint32_t)first / KV_P + blk;
+    if ((uint64_t)pi * KV_P >= (uint64_t)first + n) return;
+    const int32_t page = a.c.table[(uint64_t)seq * a.c.max_pages + pi];
+    if (page < 0 || (uint32_t)page >= a.c.pages) {
+        if (tid == 0) set_status(a.status, DGT_ERR_ARG);
+        return;
+    }
+    const uint32_t t0 = pi * KV_P;
+    const uint32_t lo = blk == 0 ? (uint32_t)first - t0 : 0;
+    const uint32_t hi = min(KV_P, (uint32_t)first + n - t0);
+    const uint64_t bi = kv_block(a.c, layer, (uint32_t)page, head);
+    const uint8_t *src = (side ? a.c.v : a.c.k) + bi * (KV_P * D);
+    const float s = (side ? a.c.v_scale : a.c.k_scale)[bi];
+    uint16_t *out = a.out[side] + (((uint64_t)(layer - a.layer0) * a.tokens + row0 + (t0 + lo - (uint32_t)first)) *
+                                       a.c.kv_heads + head) * D;
+    if (side) {
+        for (uint32_t i = tid; i < D * KV_P / 16; i += RD_THREADS) {
+            const uint4 u = reinterpret_cast<const uint4 *>(src)[i];
+            uint32_t *tp = reinterpret_cast<uint32_t *>(tile + (i / 4) * (KV_P + 4) + (i % 4) * 16);
+            tp[0] = u.x, tp[1] = u.y, tp[2] = u.z, tp[3] = u.w;
+        }
+        __syncthreads();
+    }
+    constexpr uint32_t CH = D / 8;
+    for (uint32_t i = tid; i < (hi - lo) * CH; i += RD_THREADS) {
+        const uint32_t r = i / CH, c = (i % CH) * 8;
+        uint32_t w[2];
+        if (side) {
+            w[0] = w[1] = 0;
+#pragma unroll
+            for (uint32_t j = 0; j < 8; j++)
+                w[j / 4] |= (uint32_t)tile[(c + j) * (KV_P + 4) + lo + r] << (8 * (j & 3));
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2 *>(src + kv_k_off(D, lo + r, c));
+            w[0] = u.x, w[1] = u.y;
+        }
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float2 f = e4m3x2_f32((uint16_t)(w[j / 2] >> (16 * (j & 1))));
+            o[j] = bf16_pair(f.x * s, f.y * s);
+        }
+        *reinterpret_cast<uint4 *>(out + (uint64_t)r * a.c.kv_heads * D + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// ---- pages ------------------------------------------------------------------
+// Copy list on the device: n pairs, or *count of them; a pair with a negative
+// source or destination is skipped, one out of range reported.
+struct CopyArgs {
+    dgt_kv_cache c;
+    const int32_t *src, *dst, *count;
+    uint32_t n;
+    int32_t *status;
+};
+
+constexpr uint32_t CP_THREADS = 256;
+
+// Item: (pair, layer, keys or values), one page of one layer and side, the
+// scales with it.  CTAs walk the items.
+__global__ void __launch_bounds__(CP_THREADS) k_kv_copy(CopyArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    const uint32_t n = a.count ? min(a.n, (uint32_t)max(*a.count, 0)) : a.n;
+    const uint64_t items = (uint64_t)n * a.c.layers * 2;
+    const uint32_t quads = a.c.kv_heads * (KV_P * a.c.head_dim / 16);
+    for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const uint32_t side = (uint32_t)(it & 1), layer = (uint32_t)(it / 2 % a.c.layers);
+        const uint64_t i = it / 2 / a.c.layers;
+        const int32_t s = a.src[i], d = a.dst[i];
+        if (s < 0 && d < 0) continue;
+        if (s < 0 || d < 0 || (uint32_t)s >= a.c.pages || (uint32_t)d >= a.c.pages) {
+            if (threadIdx.x == 0) set_status(a.status, DGT_ERR_ARG);
+            continue;
+        }
+        if (s == d) continue;
+        const uint64_t bs = kv_block(a.c, layer, (uint32_t)s, 0), bd = kv_block(a.c, layer, (uint32_t)d, 0);
+        uint8_t *base = side ? a.c.v : a.c.k;
+        float *sc = side ? a.c.v_scale : a.c.k_scale;
+        const uint4 *from = reinterpret_cast<const uint4 *>(base + bs * (KV_P * a.c.head_dim));
+        uint4 *to = reinterpret_cast<uint4 *>(base + bd * (KV_P * a.c.head_dim));
+        for (uint32_t q = threadIdx.x; q < quads; q += CP_THREADS) to[q] = from[q];
+        for (uint32_t h = threadIdx.x; h < a.c.kv_heads; h += CP_THREADS) sc[bd + h] = sc[bs + h];
+    }
+}
+
+// One CTA per pair: the target's table row becomes the source's, every page
+// of it one reference more.
+__global__ void __launch_bounds__(256) k_kv_fork(dgt_kv_cache c, const int32_t *from, const int32_t *to,
+                                                int32_t *status) {
+    pdl_trigger();
+    pdl_wait();
+    const int32_t f = from[blockIdx.x], t = to[blockIdx.x];
+    if (f < 0 || t < 0 || (uint32_t)f >= c.max_seqs || (uint32_t)t >= c.max_seqs || f == t) {
+        if (threadIdx.x == 0) set_status(status, DGT_ERR_ARG);
+        return;
+    }
+    int32_t *dst = c.table + (uint64_t)t * c.max_pages;
+    const int32_t *src = c.table + (uint64_t)f * c.max_pages;
+    if (dst[0] >= 0 || c.lens[t] != 0) {
+        if (threadIdx.x == 0) set_status(status, DGT_ERR_ARG);
+        return;
+    }
+    __syncthreads();   // every thread has looked before any writes
+    for (uint32_t i = threadIdx.x; i < c.max_pages; i += blockDim.x) {
+        const int32_t p = src[i];
+        if (p >= 0 && (uint32_t)p < c.pages) {
+            dst[i] = p;
+            atomicAdd(&c.refs[p], 1);
+        }
+    }
+    if (threadIdx.x == 0) c.lens[t] = c.lens[f];
+}
+
+// One CTA per sequence.
+__global__ void __launch_bounds__(256) k_kv_free(dgt_kv_cache c, const int32_t *seqs, int32_t *status) {
+    pdl_trigger();
+    pdl_wait();
+    const int32_t s = seqs[blockIdx.x];
+    if (s < 0 || (uint32_t)s >= c.max_seqs) {
+        if (threadIdx.x == 0) set_status(status, DGT_ERR_ARG);
+        return;
+    }
+    int32_t *row = c.table + (uint64_t)s * c.max_pages;
+    for (uint32_t i = threadIdx.x; i < c.max_pages; i += blockDim.x) {
+        // an exchange: a sequence that the list holds twice gives each page up once
+        if (row[i] < 0) continue;
+        const int32_t p = atomicExch(&row[i], -1);
+        if (p >= 0 && (uint32_t)p < c.pages) atomicSub(&c.refs[p], 1);
+    }
+    if (threadIdx.x == 0) c.lens[s] = 0;
+}
+
+constexpr uint32_t PG_THREADS = 1024;
+constexpr uint32_t PG_MAX = 1024;   // sequences of one reserve call
+
+// Exclusive prefix sum over the CTA (PG_THREADS threads); *total its sum.
+__device__ __forceinline__ uint32_t cta_excl_scan(uint32_t v, uint32_t *total, uint32_t *part) {
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t wsum;
+    const uint32_t x = warp_excl_scan(v, &wsum);
+    if (lane == 0) part[warp] = wsum;
+    __syncthreads();
+    uint32_t all;
+    const uint32_t before = warp_excl_scan(part[lane], &all);
+    const uint32_t base = __shfl_sync(DGT_FULL, before, warp);
+    __syncthreads();
+    *total = all;
+    return base + x;
+}
+
+struct ReserveArgs {
+    dgt_kv_cache c;
+    const int32_t *seqs, *count;
+    uint32_t n;
+    int32_t *start, *src, *dst, *free;   // workspace: copy pairs [n], free pages found
+    int32_t *status;
+};
+
+// Copy on write in list order: of the listed sequences that share a partly
+// filled last page, the k-th (from 0) finds refs - k references left, and
+// copies it when that is more than its own.
+__global__ void __launch_bounds__(PG_THREADS) k_kv_reserve(ReserveArgs a) {
+    __shared__ int32_t seq_s[PG_MAX], last_s[PG_MAX];
+    __shared__ uint32_t part[32];
+    pdl_trigger();
+    pdl_wait();
+    const uint32_t t = threadIdx.x;
+    const dgt_kv_cache &c = a.c;
+    int32_t seq = -1, len = 0, cnt = 0, last = -1;
+    uint32_t have = 0, add = 0, bad = 0, full = 0;
+    if (t < a.n) {
+        seq = a.seqs[t];
+        cnt = a.count[t];
+        if (seq < 0 || (uint32_t)seq >= c.max_seqs || cnt < 0) {
+            bad = 1;
+            seq = -1;
+        } else {
+            len = c.lens[seq];
+            if (len < 0 || (uint64_t)len > (uint64_t)c.max_pages * KV_P) {
+                bad = 1;
+            } else {
+                have = ((uint32_t)len + KV_P - 1) / KV_P;
+                const uint64_t want = ((uint64_t)len + (uint32_t)cnt + KV_P - 1) / KV_P;
+                if (want > c.max_pages) full = 1;
+                else add = (uint32_t)want - have;
+                if (have) {
+                    const int32_t p = c.table[(uint64_t)seq * c.max_pages + have - 1];
+                    if (p < 0 || (uint32_t)p >= c.pages) bad = 1;
+                    else if (((uint32_t)len & (KV_P - 1)) && cnt > 0) last = p;
+                }
+            }
+        }
+    }
+    if (t < PG_MAX) {
+        seq_s[t] = seq;
+        last_s[t] = last;
+    }
+    __syncthreads();
+    uint32_t rank = 0;
+    if (t < a.n)
+        for (uint32_t j = 0; j < t; j++) {
+            if (seq >= 0 && seq_s[j] == seq) bad = 1;
+            rank += last >= 0 && last_s[j] == last;
+        }
+    const uint32_t copy = last >= 0 && c.refs[last] - (int32_t)rank > 1 ? 1u : 0u;
+    const uint32_t anybad = __syncthreads_or(bad);
+    const uint32_t anyfull = __syncthreads_or(full);
+    uint32_t total;
+    const uint32_t base = cta_excl_scan(bad || full ? 0 : add + copy, &total, part);
+    // the lowest free pages, in order
+    uint32_t found = 0;
+    if (!anybad && !anyfull && total <= c.pages) {
+        for (uint64_t p0 = 0; p0 < c.pages && found < total; p0 += PG_THREADS * 4) {
+            uint32_t m = 0;
+            const uint64_t p = p0 + 4 * t;
+#pragma unroll
+            for (uint32_t j = 0; j < 4; j++)
+                if (p + j < c.pages && c.refs[p + j] == 0) m |= 1u << j;
+            uint32_t here;
+            uint32_t at = found + cta_excl_scan(__popc(m), &here, part);
+#pragma unroll
+            for (uint32_t j = 0; j < 4; j++)
+                if ((m >> j) & 1u) {
+                    if (at < total) a.free[at] = (int32_t)(p + j);
+                    at++;
+                }
+            found += here;
+        }
+    }
+    __syncthreads();
+    const bool ok = !anybad && !anyfull && found >= total;
+    if (t < a.n) {
+        a.src[t] = a.dst[t] = -1;
+        if (!ok) {
+            a.start[t] = -1;
+        } else {
+            a.start[t] = len;
+            c.lens[seq] = len + cnt;
+            int32_t *row = c.table + (uint64_t)seq * c.max_pages;
+            uint32_t at = base;
+            if (copy) {
+                const int32_t p = a.free[at++];
+                a.src[t] = last;
+                a.dst[t] = p;
+                row[have - 1] = p;
+                atomicSub(&c.refs[last], 1);
+                c.refs[p] = 1;
+            }
+            for (uint32_t i = 0; i < add; i++) {
+                const int32_t p = a.free[at + i];
+                row[have + i] = p;
+                c.refs[p] = 1;
+            }
+        }
+    }
+    if (!ok && t == 0) set_status(a.status, anybad ? DGT_ERR_ARG : DGT_ERR_FULL);
+}
+
+struct CompactArgs {
+    dgt_kv_cache c;
+    int32_t *src, *dst, *count, *map;   // workspace: moves, how many, page -> new page
+    int32_t *live;
+};
+
+// Counts the used pages, pairs the k-th used page past that count with the
+// k-th free page below it, and moves refs.
+__global__ void __launch_bounds__(PG_THREADS) k_kv_compact_plan(CompactArgs a) {
+    __shared__ uint32_t part[32];
+    pdl_trigger();
+    pdl_wait();
+    const dgt_kv_cache &c = a.c;
+    const uint32_t t = threadIdx.x;
+    uint32_t mine = 0, live;
+    for (uint64_t p = t; p < c.pages; p += PG_THREADS) mine += c.refs[p] > 0;
+    cta_excl_scan(mine, &live, part);
+    uint32_t holes = 0, movers = 0;
+    for (uint64_t p0 = 0; p0 < c.pages; p0 += PG_THREADS) {
+        const uint64_t p = p0 + t;
+        const bool used = p < c.pages && c.refs[p] > 0;
+        const uint32_t hole = p < live && !used, mover = p >= live && used;
+        uint32_t nh, nm;
+        const uint32_t ih = holes + cta_excl_scan(hole, &nh, part);
+        const uint32_t im = movers + cta_excl_scan(mover, &nm, part);
+        if (hole) a.dst[ih] = (int32_t)p;
+        if (mover) a.src[im] = (int32_t)p;
+        holes += nh;
+        movers += nm;
+    }
+    __syncthreads();
+    for (uint64_t p = t; p < c.pages; p += PG_THREADS) a.map[p] = (int32_t)p;
+    __syncthreads();
+    for (uint32_t i = t; i < movers; i += PG_THREADS) {
+        const int32_t s = a.src[i], d = a.dst[i];
+        a.map[s] = d;
+        c.refs[d] = c.refs[s];
+        c.refs[s] = 0;
+    }
+    if (t == 0) {
+        *a.count = (int32_t)movers;
+        if (a.live) *a.live = (int32_t)live;
+    }
+}
+
+__global__ void __launch_bounds__(256) k_kv_compact_tables(dgt_kv_cache c, const int32_t *map) {
+    pdl_trigger();
+    pdl_wait();
+    const uint64_t n = (uint64_t)c.max_seqs * c.max_pages;
+    for (uint64_t i = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (uint64_t)gridDim.x * blockDim.x) {
+        const int32_t p = c.table[i];
+        if (p >= 0 && (uint32_t)p < c.pages) c.table[i] = map[p];
+    }
+}
+
+static int launched(cudaError_t e) { return e == cudaSuccess ? DGT_OK : DGT_ERR_CUDA; }
+
+static int copy_launch(const CopyArgs &a, cudaStream_t st) {
+    DeviceInfo di;
+    if (device_info(&di) != DGT_OK) return DGT_ERR_CUDA;
+    const uint64_t items = (uint64_t)a.n * a.c.layers * 2, most = (uint64_t)di.sms * 8;
+    return launched(launch_pdl(k_kv_copy, dim3((unsigned)(items < most ? items : most)), dim3(CP_THREADS), 0, st, a));
+}
+
+}  // namespace dgt
+
+using namespace dgt;
+
+extern "C" int dgt_kv_append(const dgt_kv_cache *cache, uint32_t layer, const dgt_heads *k, const dgt_heads *v,
+                             uint64_t tokens, const int32_t *d_seqs, const int32_t *d_start, const int32_t *d_cu,
+                             uint32_t batch, int32_t *d_status, void *stream) {
+    int rc = kv_check(cache);
+    if (rc != DGT_OK) return rc;
+    if (layer >= cache->layers) return DGT_ERR_ARG;
+    if ((rc = batch_check(tokens, batch, d_cu)) != DGT_OK) return rc;
+    if (tokens == 0 || batch == 0) return DGT_OK;
+    if (!d_seqs || !d_start) return DGT_ERR_ARG;
+    if ((rc = heads_check(k, cache->kv_heads)) != DGT_OK || (rc = heads_check(v, cache->kv_heads)) != DGT_OK) return rc;
+    AppendArgs a{*cache, layer, batch, tokens, {*k, *v}, d_seqs, d_start, d_cu, d_status};
+    const unsigned items = d_cu ? (unsigned)(tokens / KV_P + 2ull * batch) : batch;
+    const dim3 grid(items, cache->kv_heads, 2);
+    auto fn = cache->head_dim == 64 ? k_kv_append<64> : cache->head_dim == 128 ? k_kv_append<128> : k_kv_append<256>;
+    return launched(launch_pdl(fn, grid, dim3(AP_THREADS), 0, (cudaStream_t)stream, a));
+}
+
+extern "C" int dgt_kv_read(const dgt_kv_cache *cache, int32_t layer, const int32_t *d_seqs, const int32_t *d_first,
+                           const int32_t *d_cu, uint32_t batch, uint64_t tokens, uint16_t *d_k, uint16_t *d_v,
+                           int32_t *d_status, void *stream) {
+    int rc = kv_check(cache);
+    if (rc != DGT_OK) return rc;
+    if (layer < -1 || (layer >= 0 && (uint32_t)layer >= cache->layers)) return DGT_ERR_ARG;
+    if ((rc = batch_check(tokens, batch, d_cu)) != DGT_OK) return rc;
+    if (tokens == 0 || batch == 0 || (!d_k && !d_v)) return DGT_OK;
+    if (!d_seqs || !d_first || !aligned16(d_k) || !aligned16(d_v)) return DGT_ERR_ARG;
+    const uint32_t layers = layer < 0 ? cache->layers : 1;
+    if (layers > 32767) return DGT_ERR_SHAPE;
+    ReadArgs a{*cache, layer < 0 ? 0u : (uint32_t)layer, layers, batch, tokens, d_seqs, d_first, d_cu, {d_k, d_v},
+               d_status};
+    const unsigned items = d_cu ? (unsigned)(tokens / KV_P + 2ull * batch) : batch;
+    const dim3 grid(items, cache->kv_heads, 2 * layers);
+    auto fn = cache->head_dim == 64 ? k_kv_read<64> : cache->head_dim == 128 ? k_kv_read<128> : k_kv_read<256>;
+    return launched(launch_pdl(fn, grid, dim3(RD_THREADS), 0, (cudaStream_t)stream, a));
+}
+
+extern "C" int dgt_kv_copy_pages(const dgt_kv_cache *cache, const int32_t *d_src, const int32_t *d_dst, uint32_t n,
+                                 int32_t *d_status, void *stream) {
+    const int rc = kv_check(cache);
+    if (rc != DGT_OK) return rc;
+    if (n == 0) return DGT_OK;
+    if (!d_src || !d_dst) return DGT_ERR_ARG;
+    return copy_launch(CopyArgs{*cache, d_src, d_dst, nullptr, n, d_status}, (cudaStream_t)stream);
+}
+
+extern "C" int dgt_kv_fork(const dgt_kv_cache *cache, const int32_t *d_from, const int32_t *d_to, uint32_t n,
+                           int32_t *d_status, void *stream) {
+    const int rc = kv_check(cache);
+    if (rc != DGT_OK) return rc;
+    if (n == 0) return DGT_OK;
+    if (!d_from || !d_to) return DGT_ERR_ARG;
+    return launched(launch_pdl(k_kv_fork, dim3(n), dim3(256), 0, (cudaStream_t)stream, *cache, d_from, d_to, d_status));
+}
+
+extern "C" int dgt_kv_free(const dgt_kv_cache *cache, const int32_t *d_seqs, uint32_t n, int32_t *d_status,
+                           void *stream) {
+    const int rc = kv_check(cache);
+    if (rc != DGT_OK) return rc;
+    if (n == 0) return DGT_OK;
+    if (!d_seqs) return DGT_ERR_ARG;
+    return launched(launch_pdl(k_kv_free, dim3(n), dim3(256), 0, (cudaStream_t)stream, *cache, d_seqs, d_status));
+}
+
+// Workspace: a reserve's copy pairs and free list, or a compaction's moves, map
+// and count.
+extern "C" size_t dgt_kv_pages_workspace_bytes(const dgt_kv_cache *cache) {
+    if (!cache) return 0;
+    const size_t reserve = 2 * (size_t)PG_MAX + cache->pages, compact = 3 * (size_t)cache->pages + 1;
+    return 4 * (reserve > compact ? reserve : compact);
+}
+
+extern "C" int dgt_kv_reserve(const dgt_kv_cache *cache, const int32_t *d_seqs, const int32_t *d_count, uint32_t n,
+                              int32_t *d_start, void *d_ws, size_t ws_bytes, int32_t *d_status, void *stream) {
+    int rc = kv_check(cache);
+    if (rc != DGT_OK) return rc;
+    if (n > PG_MAX) return DGT_ERR_SHAPE;
+    if (n == 0) return DGT_OK;
+    if (!d_seqs || !d_count || !d_start || !d_ws || ws_bytes < dgt_kv_pages_workspace_bytes(cache)) return DGT_ERR_ARG;
+    int32_t *w = (int32_t *)d_ws;
+    const ReserveArgs a{*cache, d_seqs, d_count, n, d_start, w, w + PG_MAX, w + 2 * PG_MAX, d_status};
+    rc = launched(launch_pdl(k_kv_reserve, dim3(1), dim3(PG_THREADS), 0, (cudaStream_t)stream, a));
+    if (rc != DGT_OK) return rc;
+    return copy_launch(CopyArgs{*cache, a.src, a.dst, nullptr, n, d_status}, (cudaStream_t)stream);
+}
+
+extern "C" int dgt_kv_compact(const dgt_kv_cache *cache, int32_t *d_live, void *d_ws, size_t ws_bytes,
+                              int32_t *d_status, void *stream) {
+    int rc = kv_check(cache);
+    if (rc != DGT_OK) return rc;
+    if (!d_ws || ws_bytes < dgt_kv_pages_workspace_bytes(cache)) return DGT_ERR_ARG;
+    int32_t *w = (int32_t *)d_ws;
+    const size_t P = cache->pages;
+    const CompactArgs a{*cache, w, w + P, w + 3 * P, w + 2 * P, d_live};
+    DeviceInfo di;
+    if (device_info(&di) != DGT_OK) return DGT_ERR_CUDA;
+    rc = launched(launch_pdl(k_kv_compact_plan, dim3(1), dim3(PG_THREADS), 0, (cudaStream_t)stream, a));
+    if (rc != DGT_OK) return rc;
+    rc = copy_launch(CopyArgs{*cache, a.src, a.dst, a.count, (uint32_t)(P / 2 + 1), d_status}, (cudaStream_t)stream);
+    if (rc != DGT_OK) return rc;
+    const uint64_t entries = (uint64_t)cache->max_seqs * cache->max_pages, most = (uint64_t)di.sms * 8;
+    const uint64_t g = (entries + 255) / 256;
+    return launched(launch_pdl(k_kv_compact_tables, dim3((unsigned)(g < most ? g : most)), dim3(256), 0,
+                               (cudaStream_t)stream, *cache, (const int32_t *)a.map));
+}

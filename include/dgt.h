@@ -50,6 +50,7 @@ extern "C" {
 #define DGT_ERR_OOM (-6)         /* host allocation failed                      */
 #define DGT_ERR_IO (-7)          /* file open / read / write failed             */
 #define DGT_ERR_UNSUPPORTED (-8) /* no kernel for this device or configuration  */
+#define DGT_ERR_FULL (-9)        /* the page pool or a page table has no room    */
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *dgt_status_string(int status);
@@ -521,6 +522,192 @@ int dgt_silu_mul(const float *d_g, const float *d_u, uint64_t n, uint16_t *d_out
 int dgt_silu_mul_rows(const float *d_gu, uint32_t rows, uint64_t n, uint16_t *d_out, void *stream);
 int dgt_repeat(const uint16_t *d_v, uint64_t n_in, uint64_t n_out, uint16_t *d_out, void *stream);
 int dgt_weighted_sum(const float *d_y, const float *d_p, uint32_t slots, uint64_t n, float *d_out, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Rotary positions                                                         */
+/* ------------------------------------------------------------------------ */
+/*
+ * A tensor [tokens, heads, head_dim] of bf16 bits whose last dimension is
+ * contiguous; strides in elements.  A slice of a stacked projection's rows is
+ * one, a contiguous tensor is one with strides (heads * head_dim, head_dim).
+ */
+typedef struct dgt_heads {
+    uint16_t *data;
+    int64_t token_stride, head_stride;
+    uint32_t heads;
+    uint32_t reserved;
+} dgt_heads;
+
+/*
+ * What a rotation turns and by how much.  The first rot_dim (even) dimensions
+ * of a head form rot_dim / 2 pairs: pair i is dimensions (i, i + rot_dim/2),
+ * or (2i, 2i + 1) when interleaved.  d_axis[i] is the axis (time, height,
+ * width, ...) whose position turns pair i; d_freq[i] is its frequency in
+ * revolutions per position as a 0.64 fixed-point fraction.  Position times
+ * frequency modulo 2^64 is then the fraction of a revolution, exact however
+ * far the position: a frequency's own rounding, 2^-65 revolutions, times the
+ * position is all the error that grows with it.
+ */
+typedef struct dgt_rotary {
+    uint32_t rot_dim, axes;
+    uint32_t interleaved, reserved;
+    const uint64_t *d_freq;   /* device, rot_dim / 2 */
+    const uint8_t *d_axis;    /* device, rot_dim / 2, each < axes (others turn by axis 0) */
+} dgt_rotary;
+
+/* Host: out[i] = round(2^64 * base^(-2i / rot_dim) / (2 pi)), i < rot_dim/2.
+   Errors: DGT_ERR_ARG (null, base <= 1 or not finite), DGT_ERR_SHAPE. */
+int dgt_rotary_freqs(double base, uint32_t rot_dim, uint64_t *out);
+
+/*
+ * (a, b) -> (a cos t - b sin t, b cos t + a sin t) for every pair of every
+ * head of q and k (k: NULL or data NULL for none), t = the pair's position on
+ * its axis times its frequency; dimensions from rot_dim on are copied.  Each
+ * product and sum in fp32, rounded once to bf16.  d_pos: device int32
+ * [axes, tokens], any sign.  The outputs may be the inputs themselves
+ * (in place), and otherwise do not overlap them.  head_dim: a multiple of 16,
+ * at most 1024; rot_dim / 2 a multiple of 8, rot_dim <= head_dim; strides
+ * multiples of 8 and 16-byte aligned data (else DGT_ERR_ARG); heads <= 1024,
+ * axes 1..8.  Asynchronous.  Errors: DGT_ERR_ARG, DGT_ERR_SHAPE,
+ * DGT_ERR_CUDA.
+ */
+int dgt_rotate(const dgt_rotary *rot, const dgt_heads *q, const dgt_heads *k, const dgt_heads *q_out,
+               const dgt_heads *k_out, uint32_t head_dim, uint64_t tokens, const int32_t *d_pos, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Paged 8-bit cache of keys and values                                     */
+/* ------------------------------------------------------------------------ */
+/*
+ * Pages of DGT_KV_PAGE tokens.  One page number stands for that page in every
+ * layer.  Per layer, page and kv head a key block and a value block of
+ * DGT_KV_PAGE * head_dim e4m3 codes each, and one float scale each: a value
+ * is code * scale.  Scales are powers of two, the smallest 2^e, e >= -100,
+ * with amax <= 448 * 2^e, so that rounding codes to a larger scale is exact
+ * but for the smallest ones.  A block that was given a value that is not
+ * finite has the scale NaN: every token of it reads as NaN until the page is
+ * begun anew.  Codes are always finite.
+ *
+ * Block layout (what the attention kernels read without conversion).  Keys:
+ * token t's row of head_dim bytes in panels of 128 dimensions (64 when
+ * head_dim is 64), each panel 64 rows; in a row of a panel the 16-byte chunk
+ * c stands at chunk c ^ (t % 8) (head_dim 64: c ^ (t / 2 % 4)).  Values:
+ * transposed, dimension d's 64 token bytes at d * 64.
+ *
+ * Sequences are slots 0..max_seqs-1: table row s lists the pages of sequence
+ * s in order (-1: none), lens[s] its tokens, refs[p] how many table rows hold
+ * page p (0: free).  A new cache has every byte of k and v zero, refs and
+ * lens zero and table -1; the scales need no initial value.
+ * Everything is device memory, caller-owned; k and v 16-byte aligned.
+ * head_dim 64, 128 or 256; kv_heads 1..256; layers >= 1; pages 1..2^22;
+ * max_seqs 1..2^20; max_pages 1..2^20 (else DGT_ERR_SHAPE).
+ */
+#define DGT_KV_PAGE 64
+typedef struct dgt_kv_cache {
+    uint32_t layers, pages, kv_heads, head_dim, max_seqs, max_pages;
+    uint8_t *k, *v;            /* [layers, pages, kv_heads, 64 * head_dim] */
+    float *k_scale, *v_scale;  /* [layers, pages, kv_heads]                */
+    int32_t *refs;             /* [pages]                                  */
+    int32_t *table;            /* [max_seqs, max_pages]                    */
+    int32_t *lens;             /* [max_seqs]                               */
+} dgt_kv_cache;
+
+/*
+ * Calls below take sequences by slot: d_seqs is device int32 [batch].  Rows of
+ * several sequences stand one after the other, those of entry b from d_cu[b]
+ * to d_cu[b + 1] (device int32 [batch + 1], d_cu[0] = 0, not decreasing,
+ * d_cu[batch] = tokens); d_cu NULL: one row each.  What the device finds
+ * wrong is reported in d_status (int32 or NULL, never cleared by the call)
+ * and skipped: a slot, page number or position outside its range is
+ * DGT_ERR_ARG.  tokens <= 2^24, batch <= 65536.  All asynchronous.
+ *
+ * dgt_kv_append: writes token rows k and v (heads = kv_heads) of entry b at
+ * positions d_start[b], d_start[b] + 1, ... of its sequence in `layer`.  Pages
+ * must be there (dgt_kv_reserve) and be the sequence's own.  A block whose
+ * first token is written is begun anew; one that already holds tokens keeps
+ * its scale unless the new tokens need a larger one, and then its codes are
+ * rounded (nearest, ties to even) to that.  lens is not read or written.
+ * Strides multiples of 8, data 16-byte aligned (else DGT_ERR_ARG).
+ */
+int dgt_kv_append(const dgt_kv_cache *cache, uint32_t layer, const dgt_heads *k, const dgt_heads *v, uint64_t tokens,
+                  const int32_t *d_seqs, const int32_t *d_start, const int32_t *d_cu, uint32_t batch,
+                  int32_t *d_status, void *stream);
+
+/*
+ * dgt_kv_read: the values of positions d_first[b] .. of entry b's sequence as
+ * bf16 (exact): d_k, d_v device bf16 [tokens, kv_heads, head_dim], either may
+ * be NULL.  layer -1: every layer, d_k and d_v [layers, tokens, ...].
+ */
+int dgt_kv_read(const dgt_kv_cache *cache, int32_t layer, const int32_t *d_seqs, const int32_t *d_first,
+                const int32_t *d_cu, uint32_t batch, uint64_t tokens, uint16_t *d_k, uint16_t *d_v, int32_t *d_status,
+                void *stream);
+
+/*
+ * dgt_kv_attention: the new rows of entry b (n of them) are the last n of the
+ * lens[b] tokens that its sequence holds, their own keys and values among
+ * them: row i stands at position p = lens - n + i and sees the positions
+ * j <= p, with window > 0 only those with j > p - window or j < sinks
+ * (window 0: no window).  Query head h reads kv head h / (q_heads / kv_heads).
+ *   t_j = scale * (q . k_j),  out = sum_j exp(t_j) v_j / sum_j exp(t_j),
+ *   lse = log sum_j exp(t_j)  (natural)
+ * over the positions that it sees; a row that sees none has out 0, lse -inf.
+ * A position that a row does not see adds nothing to it, whatever it holds;
+ * a row of q that is not finite gives NaN.  q: bf16, heads = q_heads (a
+ * multiple of kv_heads, at most 64 times it), strides multiples of 8, data
+ * 16-byte aligned.  d_out: device bf16 [tokens, q_heads, head_dim],
+ * contiguous, 16-byte aligned; d_lse: device float [tokens, q_heads] or NULL.
+ * q is scaled to its row's exponent and kept in fp16 (exact to 2^-31 of the
+ * row's largest element), the weights exp(t_j - max) are rounded to fp16
+ * (2^-11 relative), every sum is fp32.
+ * d_ws: device, dgt_kv_attention_workspace_bytes(...) bytes, 256-byte aligned,
+ * zeroed before its first use (every call leaves it so); calls that may
+ * overlap need one each.  DGT_ERR_TIMEOUT in the status: a bounded wait ran
+ * out, the outputs are then unspecified.
+ */
+size_t dgt_kv_attention_workspace_bytes(const dgt_kv_cache *cache, uint32_t q_heads, uint32_t batch,
+                                        uint64_t tokens);
+int dgt_kv_attention(const dgt_kv_cache *cache, uint32_t layer, const dgt_heads *q, uint64_t tokens,
+                     const int32_t *d_seqs, const int32_t *d_cu, uint32_t batch, float scale, uint32_t window,
+                     uint32_t sinks, uint16_t *d_out, float *d_lse, void *d_ws, size_t ws_bytes, int32_t *d_status,
+                     void *stream);
+
+/*
+ * Pages.  All in stream order, so a captured graph can hold them.
+ *
+ * dgt_kv_copy_pages: pages d_src[i] -> d_dst[i] (device int32 [n]) in every
+ * layer, codes and scales, for page numbers in range; no page is a source and
+ * a destination, and no destination occurs twice.  Tables and refs stay.
+ *
+ * dgt_kv_fork: sequence d_to[i] becomes a copy of sequence d_from[i] that
+ * shares its pages.  A target that holds pages is left alone, with
+ * DGT_ERR_ARG in the status.  No target occurs twice or is a source.
+ *
+ * dgt_kv_reserve: makes room for d_count[i] more tokens of sequence d_seqs[i]
+ * (n <= 1024, each sequence once) and moves lens on; d_start[i] gets the
+ * length before.  In the order of the list: a partly filled last page that
+ * another sequence shares is copied to a free page (copy on write), then free
+ * pages are added; always the lowest free page number first.  When the pool
+ * or a table row has too little room, nothing changes, every d_start[i] is -1
+ * and the status is DGT_ERR_FULL.  The same, with DGT_ERR_ARG, for a slot out
+ * of range, one that occurs twice, a negative count or a table that does not
+ * hold lens.  d_ws: dgt_kv_pages_workspace_bytes() bytes, 256-byte aligned.
+ *
+ * dgt_kv_free: the sequences give up their pages; length 0.
+ *
+ * dgt_kv_compact: the pages in use move to the lowest numbers (the k-th used
+ * page from the count of used pages on moves to the k-th free page below it),
+ * contents, refs and tables alike.  d_live: device int32 or NULL, gets the
+ * count of used pages.
+ */
+size_t dgt_kv_pages_workspace_bytes(const dgt_kv_cache *cache);
+int dgt_kv_copy_pages(const dgt_kv_cache *cache, const int32_t *d_src, const int32_t *d_dst, uint32_t n,
+                      int32_t *d_status, void *stream);
+int dgt_kv_fork(const dgt_kv_cache *cache, const int32_t *d_from, const int32_t *d_to, uint32_t n, int32_t *d_status,
+                void *stream);
+int dgt_kv_reserve(const dgt_kv_cache *cache, const int32_t *d_seqs, const int32_t *d_count, uint32_t n,
+                   int32_t *d_start, void *d_ws, size_t ws_bytes, int32_t *d_status, void *stream);
+int dgt_kv_free(const dgt_kv_cache *cache, const int32_t *d_seqs, uint32_t n, int32_t *d_status, void *stream);
+int dgt_kv_compact(const dgt_kv_cache *cache, int32_t *d_live, void *d_ws, size_t ws_bytes, int32_t *d_status,
+                   void *stream);
 
 /* ------------------------------------------------------------------------ */
 /* Exponent statistics                                                      */
