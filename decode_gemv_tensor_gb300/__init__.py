@@ -147,6 +147,8 @@ def lib():
             "dgt_kv_attention_workspace_bytes": (C.c_size_t, [kp, C.c_uint32, C.c_uint32, u64]),
             "dgt_kv_attention": (i32, [kp, C.c_uint32, hp, u64, vp, vp, C.c_uint32, C.c_float, C.c_uint32,
                                        C.c_uint32, vp, vp, vp, C.c_size_t, vp, vp]),
+            "dgt_kv_attention_ex": (i32, [kp, C.c_uint32, hp, u64, vp, vp, C.c_uint32, C.c_float, C.c_uint32,
+                                          C.c_uint32, vp, vp, vp, C.c_size_t, vp, C.c_uint, vp]),
             "dgt_kv_pages_workspace_bytes": (C.c_size_t, [kp]),
             "dgt_kv_copy_pages": (i32, [kp, vp, vp, C.c_uint32, vp, vp]),
             "dgt_kv_fork": (i32, [kp, vp, vp, C.c_uint32, vp, vp]),
@@ -745,13 +747,14 @@ def kv_attention_workspace(cache: KvCache, q_heads: int, batch: int, tokens: int
 
 
 def kv_attention(cache: KvCache, layer: int, q, seqs, cu=None, scale=None, window: int = 0, sinks: int = 0, out=None,
-                 lse=None, ws=None, status=None, stream=None):
-    """dgt_kv_attention: the new rows q, bf16 [tokens, q_heads, head_dim], the
+                 lse=None, ws=None, status=None, stream=None, test_wait_polls=None):
+    """dgt_kv_attention_ex: the new rows q, bf16 [tokens, q_heads, head_dim], the
     last ones of the sequences `seqs` int32 [batch], over the cache.  cu int32
     [batch + 1]: the rows of each (None: one row each).  scale: of the scores
     (None: head_dim^-0.5).  window > 0: a row sees its last `window` positions
-    and the first `sinks`.  lse: float32 [tokens, q_heads] or None.  Returns
-    out, bf16 [tokens, q_heads, head_dim]."""
+    and the first `sinks`.  lse: float32 [tokens, q_heads] or None.
+    test_wait_polls: the failure-path test hook (see test_wait_flags).
+    Returns out, bf16 [tokens, q_heads, head_dim]."""
     import torch
     tokens, heads, dim = q.shape
     batch = seqs.numel()
@@ -767,10 +770,11 @@ def kv_attention(cache: KvCache, layer: int, q, seqs, cu=None, scale=None, windo
         raise ValueError("lse: a contiguous float32 tensor [tokens, q_heads]")
     if ws is None:
         ws = kv_attention_workspace(cache, heads, batch, tokens)
-    _check(lib().dgt_kv_attention(C.byref(cache.s), layer, C.byref(_heads(q, "q")), tokens, _i32(seqs, "seqs"),
-                                  None if cu is None else _i32(cu, "cu", batch + 1), batch,
-                                  dim ** -0.5 if scale is None else scale, window, sinks, _ptr(out), _ptr(lse),
-                                  _ptr(ws), ws.numel(), _ptr(status), _stream(stream)), "dgt_kv_attention")
+    _check(lib().dgt_kv_attention_ex(C.byref(cache.s), layer, C.byref(_heads(q, "q")), tokens, _i32(seqs, "seqs"),
+                                     None if cu is None else _i32(cu, "cu", batch + 1), batch,
+                                     dim ** -0.5 if scale is None else scale, window, sinks, _ptr(out), _ptr(lse),
+                                     _ptr(ws), ws.numel(), _ptr(status), test_wait_flags(test_wait_polls),
+                                     _stream(stream)), "dgt_kv_attention")
     return out
 
 

@@ -3,7 +3,21 @@
 // For a query row q at position p and the positions j that it sees,
 //   t_j = scale * q . k_j,   out = sum_j e^(t_j - m) v_j / sum_j e^(t_j - m),
 // in one pass over the cache with the running maximum m: when a page raises
-// it, the sums so far are multiplied by e^(old - new).
+// it, the sums so far are multiplied by e^(old - new).  Exponentials are in
+// base 2, with log2(e) inside the scale.
+//
+// The values' scales differ from page to page, so two maxima run: m of the
+// scores (the denominator l counts exp2(t - m)) and mu of score + log2(value
+// scale) (the numerator sums codes times exp2(t + log2 vs - mu)).  Then no
+// page's weight is lost to another page's scale, and the quotient is
+// exp2(mu - m) * numerator / l.
+//
+// Work is cut evenly over the CTAs whatever the lengths: a segment is one tile
+// of query rows and one kv head, its units are the pages that the tile sees,
+// and CTA c of C takes units [c U / C, (c + 1) U / C) of all U.  A segment that
+// ends up in several CTAs leaves partial sums in the workspace; the CTA that
+// arrives last adds them in page order, so results do not depend on timing.
+// Lengths are read on the device: a captured graph follows them.
 #include "dgt_kv.cuh"
 
 #include "dgt_device.cuh"
@@ -12,167 +26,756 @@ namespace dgt {
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
+constexpr float W_LOG2 = 12.0f;        // weights of the numerator reach 2^12 (fp16 holds them to 2^-24)
+constexpr uint32_t AT_WARPS = 8;
+constexpr uint32_t AT_CHUNK = 128;     // row tiles described in shared memory at a time
+constexpr uint32_t AT_MAX_CTAS = 160;
 
 struct AttnArgs {
     dgt_kv_cache c;
-    uint32_t layer, batch, q_heads, window, sinks;
+    uint32_t layer, batch, q_heads, window, sinks, group, slots, per_entry;
     uint64_t tokens;
     dgt_heads q;
     const int32_t *seqs, *cu;
     float scale_log2;   // scale * log2(e)
     uint16_t *out;
     float *lse;
+    int32_t *count;     // workspace: arrivals at the segment that CTA c begins and others end, zero between calls
+    float *part;        // workspace: two partial results per CTA
     int32_t *status;
+    uint32_t min_units, spin;
 };
 
-__device__ __forceinline__ float e4m3_f32(uint8_t c) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3)));
+// A tile of query rows: rows [row0, row0 + rows) of its entry's flattened
+// (token, head of the group) rows, at positions pos0 + row / group.
+struct Slot {
+    uint32_t base, np;          // first unit (of the chunk's), pages per head (0: none is seen)
+    uint32_t sp, wp;            // pages seen before the window's, the window's first page
+    int32_t seq, pos0;          // table row; position of the entry's first row
+    uint32_t tok0, row0, rows;  // entry's first token row, tile's first flattened row, row count
+    __device__ __forceinline__ uint32_t per_head() const { return np ? np : 1; }
+    __device__ __forceinline__ uint32_t page_index(uint32_t i) const { return i < sp ? i : wp + i - sp; }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// Two e4m3 codes (the low or high half of w) as two fp16.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
 }
 
-// One warp per (row, query head).  Lane l scores tokens l and l + 32 of a
-// page, then owns dimensions l, l + 32, ... of the output.
-template <uint32_t D>
-__global__ void __launch_bounds__(128) k_kv_attention_rows(AttnArgs a) {
-    __shared__ float qs[4][D];
-    __shared__ float ps[4][KV_P];
+// The row tile of number `slot`, RT rows each; units 0 for an empty number.
+__device__ __forceinline__ Slot slot_info(const AttnArgs &a, uint32_t slot, uint32_t RT, uint32_t *units) {
+    Slot s{};
+    uint32_t b, rt, n = 1;
+    *units = 0;
+    if (a.cu) {
+        b = item_entry(a.cu, a.batch, slot, RT, 1, a.group);
+        rt = slot - item_base(a.cu, b, RT, 1, a.group);
+        s.tok0 = (uint32_t)a.cu[b];
+        n = (uint32_t)(a.cu[b + 1] - a.cu[b]);
+        if ((uint64_t)s.tok0 + n > a.tokens) {
+            set_status(a.status, DGT_ERR_ARG);
+            return s;
+        }
+    } else {
+        b = slot / a.per_entry;
+        rt = slot % a.per_entry;
+        s.tok0 = b;
+    }
+    const uint64_t all = (uint64_t)n * a.group, first = (uint64_t)rt * RT;
+    if (first >= all) return s;
+    s.row0 = (uint32_t)first;
+    s.rows = (uint32_t)min((uint64_t)RT, all - first);
+    *units = a.c.kv_heads;
+    s.seq = a.seqs[b];
+    int32_t len = 0;
+    if (s.seq < 0 || (uint32_t)s.seq >= a.c.max_seqs) {
+        set_status(a.status, DGT_ERR_ARG);
+        return s;
+    }
+    len = a.c.lens[s.seq];
+    if (len < 0 || (uint64_t)len > (uint64_t)a.c.max_pages * KV_P) {
+        set_status(a.status, DGT_ERR_ARG);
+        len = 0;
+    }
+    s.pos0 = len > 0 ? len - (int32_t)n : -0x40000000;
+    const int32_t pf = s.pos0 + (int32_t)(s.row0 / a.group);
+    const int32_t pl = s.pos0 + (int32_t)((s.row0 + s.rows - 1) / a.group);
+    if (pl < 0) return s;
+    const uint32_t lo = a.window && pf >= 0 && (uint32_t)pf >= a.window ? (uint32_t)pf - a.window + 1 : 0;
+    s.wp = lo / KV_P;
+    s.sp = min((min(a.sinks, lo) + KV_P - 1) / KV_P, s.wp);
+    s.np = s.sp + (uint32_t)pl / KV_P - s.wp + 1;
+    *units = a.c.kv_heads * s.np;
+    return s;
+}
+
+// The queries: rows of up to eight per n-tile (NT of them) are the N side of
+// the matrix instructions, a page's 64 tokens their M side for S = K Q^T, and
+// 16 dimensions at a time for O += V^T P^T; the accumulators of S, packed and
+// transposed eight by eight, are the operand P^T.  Which token stands in which
+// row of S is free, and so chosen that a lane's value word (four tokens of a
+// dimension) is what the second product wants, and which dimension in which
+// step likewise, so that keys and values are read 16 bytes at a time without
+// bank conflicts (see kv_k_off).
+//
+// Every warp works alone on its share of a CTA's pages with its own ring of
+// bulk copies (one item: 64 tokens by up to 128 dimensions of one side), and
+// looks ahead into the CTA's next segment; warps meet only at a segment's end.
+template <uint32_t D, uint32_t NT>
+struct AttnCfg {
+    static constexpr uint32_t PD = D < 128 ? D : 128, PAN = D / PD;
+    static constexpr uint32_t IB = KV_P * PD, IPP = 2 * PAN;
+    static constexpr uint32_t NS = (D == 64 ? 6 : 3) - (NT == 4 ? (D == 64 ? 2 : 1) : 0);
+    static constexpr uint32_t RT = 8 * NT;
+    static constexpr uint32_t KSTEPS = D / 16;           // k-steps of the first product
+    static constexpr bool QREG = NT * D <= 256;          // query fragments in registers
+    static constexpr uint32_t RS = 64 + 4;               // row of the merge scratch, padded
+    static constexpr uint32_t ring = 0, scratch = AT_WARPS * NS * IB, q = scratch + AT_WARPS * 8 * RS * 4,
+                              bytes = q + KSTEPS * NT * 256;
+    static constexpr uint32_t PART = RT * (D + 4);       // floats of a partial result
+};
+
+template <uint32_t D, uint32_t NT>
+__global__ void __launch_bounds__(AT_WARPS * 32, 1) k_kv_attention(AttnArgs a) {
+    using Cfg = AttnCfg<D, NT>;
+    constexpr uint32_t RT = Cfg::RT, NS = Cfg::NS, IB = Cfg::IB, PD = Cfg::PD, PAN = Cfg::PAN, IPP = Cfg::IPP;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bar[AT_WARPS][NS];
+    __shared__ Slot slots[AT_CHUNK];
+    __shared__ float stat[AT_WARPS][RT][3];
+    __shared__ float rowstat[RT][3];
+    __shared__ float rowfac[RT];
+    __shared__ uint64_t usum[AT_WARPS];
+    __shared__ uint32_t wsum[AT_WARPS];
+    __shared__ int last_flag;
+    const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    if (tid < AT_WARPS * NS) mbar_init(smem_u32(&bar[tid / NS][tid % NS]), 1);
+    fence_mbarrier_init();
+    __syncthreads();
     pdl_trigger();
     pdl_wait();
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint64_t item = (uint64_t)blockIdx.x * 4 + warp;
-    if (item >= a.tokens * a.q_heads) return;
-    const uint64_t row = item / a.q_heads;
-    const uint32_t h = (uint32_t)(item % a.q_heads), hk = h / (a.q_heads / a.c.kv_heads);
-    uint32_t b = (uint32_t)row, i = 0, n = 1;
-    if (a.cu) {
-        uint32_t lo = 0, hi = a.batch;   // the last entry that starts at or before the row
-        while (hi - lo > 1) {
-            const uint32_t mid = (lo + hi) >> 1;
-            if ((uint64_t)a.cu[mid] <= row) lo = mid;
-            else hi = mid;
-        }
-        b = lo;
-        i = (uint32_t)row - (uint32_t)a.cu[b];
-        n = (uint32_t)(a.cu[b + 1] - a.cu[b]);
+
+    // ---- the CTA's units
+    uint64_t mine = 0;
+    uint32_t units;
+    Slot si{};
+    for (uint32_t s = tid; s < a.slots; s += AT_WARPS * 32) {
+        si = slot_info(a, s, RT, &units);
+        mine += units;
     }
-    const int32_t seq = a.seqs[b];
-    int64_t pos = -1;
-    if (seq < 0 || (uint32_t)seq >= a.c.max_seqs) {
-        if (lane == 0) set_status(a.status, DGT_ERR_ARG);
-    } else {
-        int64_t len = a.c.lens[seq];
-        if (len < 0 || len > (int64_t)a.c.max_pages * KV_P) {
-            if (lane == 0) set_status(a.status, DGT_ERR_ARG);
-            len = 0;
-        }
-        if (len > 0) pos = len - n + i;
-    }
-    const uint16_t *q = a.q.data + (int64_t)row * a.q.token_stride + (int64_t)h * a.q.head_stride;
-    for (uint32_t d = lane; d < D; d += 32) qs[warp][d] = __uint_as_float((uint32_t)q[d] << 16);
-    __syncwarp();
-    float m = -INFINITY, l = 0.0f, acc[D / 32];
+    const uint32_t units0 = a.slots <= AT_CHUNK ? (uint32_t)mine : 0;   // one slot per thread: kept for the scan below
+    uint64_t sum = mine;
 #pragma unroll
-    for (uint32_t j = 0; j < D / 32; j++) acc[j] = 0.0f;
-    const int64_t lo = a.window && pos >= (int64_t)a.window ? pos - a.window + 1 : 0;   // the window's first position
-    const int64_t sinks = min((int64_t)a.sinks, lo);
-    for (int64_t t0 = 0; t0 <= pos; t0 += KV_P) {
-        if (t0 >= sinks && t0 + KV_P <= lo) {
-            t0 = lo / KV_P * KV_P;
-            if (t0 > pos) break;
-        }
-        const int32_t page = a.c.table[(uint64_t)seq * a.c.max_pages + t0 / KV_P];
-        if (page < 0 || (uint32_t)page >= a.c.pages) {
-            if (lane == 0) set_status(a.status, DGT_ERR_ARG);
-            continue;
-        }
-        const uint64_t bi = kv_block(a.c, a.layer, (uint32_t)page, hk);
-        const uint8_t *kb = a.c.k + bi * (KV_P * D), *vb = a.c.v + bi * (KV_P * D);
-        const float ks = a.c.k_scale[bi], vs = a.c.v_scale[bi];
-        float t[2], mx = m;
+    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(DGT_FULL, sum, d);
+    if (lane == 0) usum[warp] = sum;
+    __syncthreads();
+    uint64_t U = 0;
 #pragma unroll
-        for (int e = 0; e < 2; e++) {
-            const uint32_t tok = lane + 32 * e;
-            float s = 0.0f;
-            for (uint32_t d = 0; d < D; d += 16) {
-                const uint4 u = *reinterpret_cast<const uint4 *>(kb + kv_k_off(D, tok, d));
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (uint32_t w = 0; w < AT_WARPS; w++) U += usum[w];
+    const uint64_t most = (U + a.min_units - 1) / a.min_units;
+    const uint64_t C = most < gridDim.x ? most : gridDim.x;
+    if (blockIdx.x >= C) return;
+    const uint64_t ua = blockIdx.x * U / C, ub = (blockIdx.x + 1) * U / C;
+
+    const uint32_t ring = smem_u32(smem) + warp * NS * IB;
+    float *scratch = reinterpret_cast<float *>(smem + Cfg::scratch);
+    const uint32_t qs = smem_u32(smem + Cfg::q);
+    uint32_t issued = 0, taken = 0;   // items of this warp's ring
+    bool dead = false;                // a wait ran out: no more work from this warp
+
+    uint64_t base0 = 0;
+    for (uint32_t s0 = 0; s0 < a.slots && base0 < ub; s0 += AT_CHUNK) {
+        // ---- describe the next row tiles
+        __syncthreads();
+        units = 0;
+        if (a.slots <= AT_CHUNK) units = units0;
+        else if (tid < AT_CHUNK && s0 + tid < a.slots) si = slot_info(a, s0 + tid, RT, &units);
+        uint32_t wtot;
+        uint32_t before = warp_excl_scan(units, &wtot);
+        if (lane == 0) wsum[warp] = wtot;
+        __syncthreads();
+        uint32_t tot = 0;
 #pragma unroll
-                for (int j = 0; j < 16; j++)
-                    s = fmaf(qs[warp][d + j], e4m3_f32((uint8_t)(w[j / 4] >> (8 * (j & 3)))), s);
+        for (uint32_t w = 0; w < AT_CHUNK / 32; w++) {
+            if (w < warp) before += wsum[w];
+            tot += wsum[w];
+        }
+        if (tid < AT_CHUNK) {
+            si.base = before;
+            slots[tid] = si;
+        }
+        __syncthreads();
+        const uint64_t first = base0 > ua ? base0 : ua, end = base0 + tot < ub ? base0 + tot : ub;
+        const uint32_t u0 = (uint32_t)(first - base0), u1 = end > first ? (uint32_t)(end - base0) : u0;
+        const uint64_t chunk_base = base0;
+        base0 += tot;
+        if (u0 == u1) continue;
+
+        // a run of pages [pa, pe) of head h's segment of a slot, beginning at unit u
+        struct Run {
+            uint32_t u, slot, h, pa, pe, wa, wb;
+        };
+        const uint32_t nslots = min(AT_CHUNK, a.slots - s0);
+        auto make_run = [&](uint32_t u, uint32_t slot) {
+            Run r;
+            while (slot + 1 < nslots && slots[slot + 1].base <= u) slot++;
+            const Slot &s = slots[slot];
+            const uint32_t n = s.per_head();
+            r.u = u, r.slot = slot, r.h = (u - s.base) / n, r.pa = (u - s.base) % n;
+            r.pe = min(n, r.pa + (u1 - u));
+            const uint32_t cnt = s.np ? r.pe - r.pa : 0;
+            r.wa = r.pa + warp * cnt / AT_WARPS, r.wb = r.pa + (warp + 1) * cnt / AT_WARPS;
+            return r;
+        };
+
+        // ---- issue side: page numbers and scales of up to 32 pages in the lanes
+        Run ir = make_run(u0, 0);
+        uint32_t ix = ir.wa, ik = 0, ibs = ir.wa, ibe = ir.wa;
+        bool more = true, fresh = false;   // fresh: a batch that the consuming side has not taken over
+        int bpid = -1;
+        float bks = 0.0f, bvs = 0.0f;
+        auto load_batch = [&]() {
+            const Slot &s = slots[ir.slot];
+            ibs = ix;
+            ibe = min(ix + 32, ir.wb);
+            bpid = -1;
+            if (ix + lane < ibe) {
+                const int32_t p = a.c.table[(uint64_t)s.seq * a.c.max_pages + s.page_index(ix + lane)];
+                if (p < 0 || (uint32_t)p >= a.c.pages) {
+                    set_status(a.status, DGT_ERR_ARG);
+                } else {
+                    bpid = p;
+                    const uint64_t bi = kv_block(a.c, a.layer, (uint32_t)p, ir.h);
+                    bks = a.c.k_scale[bi];
+                    bvs = a.c.v_scale[bi];
+                }
             }
-            const int64_t j = t0 + tok;
-            const bool see = j <= pos && (j >= lo || j < sinks);
-            t[e] = see ? s * (ks * a.scale_log2) : -INFINITY;
-            mx = fmaxf(mx, t[e]);
-        }
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(DGT_FULL, mx, d));
-        const float base = mx == -INFINITY ? 0.0f : mx;
-        const float alpha = exp2f(m - base);
-        m = mx;
-        __syncwarp();
-        float sum = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-            const float p = exp2f(t[e] - base);
-            ps[warp][lane + 32 * e] = p;
-            sum += p;
-        }
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(DGT_FULL, sum, d);
-        l = l * alpha + sum;
-        __syncwarp();
-#pragma unroll
-        for (uint32_t j = 0; j < D / 32; j++) {
-            const uint32_t d = lane + 32 * j;
-            float s = 0.0f;
-            for (uint32_t tok = 0; tok < KV_P; tok += 16) {
-                const uint4 u = *reinterpret_cast<const uint4 *>(vb + kv_v_off(tok, d));
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int k = 0; k < 16; k++)
-                    s = fmaf(ps[warp][tok + k], e4m3_f32((uint8_t)(w[k / 4] >> (8 * (k & 3)))), s);
+            fresh = true;
+        };
+        auto issue = [&]() {
+            while (more && issued - taken < NS) {
+                if (ix == ibe) {
+                    if (fresh) break;
+                    while (ix == ir.wb) {
+                        const uint32_t next = ir.u + (ir.pe - ir.pa);
+                        if (next >= u1) {
+                            more = false;
+                            break;
+                        }
+                        ir = make_run(next, ir.slot);
+                        ix = ir.wa;
+                    }
+                    if (!more) break;
+                    load_batch();
+                }
+                const int p = __shfl_sync(DGT_FULL, bpid, ix - ibs);
+                if (lane == 0) {
+                    // a page that is not there is passed over when its turn comes; page 0 stands in
+                    const uint64_t bi = kv_block(a.c, a.layer, p < 0 ? 0u : (uint32_t)p, ir.h);
+                    const uint8_t *src = (ik < PAN ? a.c.k : a.c.v) + bi * (KV_P * D) + (ik % PAN) * IB;
+                    const uint32_t st = issued % NS, fb = smem_u32(&bar[warp][st]);
+                    fence_proxy_async_smem();
+                    mbar_arrive_expect_tx(fb, IB);
+                    bulk_g2s(ring + st * IB, src, IB, fb);
+                }
+                issued++;
+                if (++ik == IPP) {
+                    ik = 0;
+                    ix++;
+                }
             }
-            acc[j] = acc[j] * alpha + (sum == 0.0f ? 0.0f : s * vs);   // a page that the row sees nothing of adds nothing
-        }
-    }
-    uint16_t *out = a.out + (row * a.q_heads + h) * D;
-    const bool none = m == -INFINITY && l == 0.0f;
+        };
+        // the next item's stage once it has arrived; false when the wait ran out
+        auto arrive = [&](uint32_t &addr) {
+            const uint32_t st = taken % NS;
+            addr = ring + st * IB;
+            // a lane that saw the phase end speaks for all
+            if (__any_sync(DGT_FULL, mbar_wait_n(smem_u32(&bar[warp][st]), (taken / NS) & 1u, a.spin))) return true;
+            if (lane == 0) set_status(a.status, DGT_ERR_TIMEOUT);
+            return false;
+        };
+        auto release = [&]() {
+            __syncwarp();
+            taken++;
+            issue();
+        };
+        if (dead) more = false;
+        issue();
+
+        // ---- consume the CTA's runs of this chunk
+        for (uint32_t u = u0, hint = 0; u < u1;) {
+            const Run r = make_run(u, hint);
+            hint = r.slot;
+            u += r.pe - r.pa;
+            const Slot s = slots[r.slot];
+
+            // queries: a row per warp at a time, scaled to its exponent, in fragment order
+            __syncthreads();
+            for (uint32_t row = warp; row < RT; row += AT_WARPS) {
+                float x[D / 32], amax = 0.0f;
+                const uint32_t flat = s.row0 + row;
+                const bool live = row < s.rows;
+                const uint16_t *qp = a.q.data + (int64_t)(s.tok0 + flat / a.group) * a.q.token_stride +
+                                     (int64_t)(r.h * a.group + flat % a.group) * a.q.head_stride;
+                uint32_t bits[D / 64];
 #pragma unroll
-    for (uint32_t j = 0; j < D / 32; j++) out[lane + 32 * j] = f32_to_bf16_rne(none ? 0.0f : acc[j] / l);
-    if (a.lse && lane == 0) a.lse[row * a.q_heads + h] = none ? -INFINITY : (m + log2f(l)) * LN2;
+                for (uint32_t j = 0; j < D / 64; j++)
+                    bits[j] = live ? reinterpret_cast<const uint32_t *>(qp)[lane + 32 * j] : 0u;
+#pragma unroll
+                for (uint32_t j = 0; j < D / 64; j++) {
+                    x[2 * j] = bf16lo(bits[j]);
+                    x[2 * j + 1] = bf16hi(bits[j]);
+                    // by bits, so that a NaN counts as the largest
+                    amax = __uint_as_float(max(__float_as_uint(amax), max(__float_as_uint(x[2 * j]) & 0x7FFFFFFFu,
+                                                                         __float_as_uint(x[2 * j + 1]) & 0x7FFFFFFFu)));
+                }
+                const uint32_t top = __reduce_max_sync(DGT_FULL, __float_as_uint(amax)) >> 23;
+                // the largest element to [2^14, 2^15): exact in fp16 down to 2^-31 of it
+                const int up = 14 + 127 - (int)top, up0 = min(up, 100);
+                const float f0 = top == 255 ? 0.0f : __uint_as_float((uint32_t)(up0 + 127) << 23);
+                const float f1 = __uint_as_float((uint32_t)(up - up0 + 127) << 23);
+                if (lane == 0)
+                    rowfac[row] = top == 255 ? __uint_as_float(0x7FC00000u) : ldexpf(a.scale_log2, -up);
+#pragma unroll
+                for (uint32_t j = 0; j < D / 64; j++) {
+                    const uint32_t d = 2 * (lane + 32 * j);   // the pair's first dimension
+                    uint32_t step, cc;
+                    if (D == 64) {
+                        cc = d >> 4;
+                        step = (d & 15) >> 2;
+                    } else {
+                        cc = (d & 127) >> 5;
+                        step = (d >> 7) * 8 + ((d & 31) >> 2);
+                    }
+                    const uint32_t fr = ((step * NT + row / 8) * 32 + (row & 7) * 4 + cc) * 8 + ((d >> 1) & 1) * 4;
+                    // not finite: the row's factor says so, the operand stays clean
+                    const float lo = top == 255 ? 0.0f : x[2 * j] * f0 * f1, hi = top == 255 ? 0.0f : x[2 * j + 1] * f0 * f1;
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + fr), "r"(f16_pair(lo, hi)) : "memory");
+                }
+            }
+            __syncthreads();
+
+            uint2 qf[Cfg::QREG ? Cfg::KSTEPS * NT : 1];
+            auto load_q = [&](uint32_t i) {
+                uint2 v;
+                asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(qs + (i * 32 + lane) * 8));
+                return v;
+            };
+            if (Cfg::QREG) {
+#pragma unroll
+                for (uint32_t i = 0; i < (Cfg::QREG ? Cfg::KSTEPS * NT : 1); i++) qf[i] = load_q(i);
+            }
+            // per column (query row 8 nt + 2 c + e): factor, position, window start, maxima, sum
+            float fac[NT][2], m[NT][2], mu[NT][2], l[NT][2];
+            float o[D / 16][NT][4];
+            int32_t pos[NT][2];
+#pragma unroll
+            for (uint32_t nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (uint32_t e = 0; e < 2; e++) {
+                    const uint32_t row = 8 * nt + 2 * c + e;
+                    fac[nt][e] = rowfac[row];
+                    pos[nt][e] = row < s.rows ? s.pos0 + (int32_t)((s.row0 + row) / a.group) : -1;
+                    m[nt][e] = mu[nt][e] = -INFINITY;
+                    l[nt][e] = 0.0f;
+                }
+#pragma unroll
+            for (uint32_t i = 0; i < D / 16; i++)
+#pragma unroll
+                for (uint32_t nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) o[i][nt][j] = 0.0f;
+            const int32_t pf = s.pos0 + (int32_t)(s.row0 / a.group);
+            const int32_t pl = s.pos0 + (int32_t)((s.row0 + s.rows - 1) / a.group);
+
+            int cpid = -1;
+            float cks = 0.0f, cvs = 0.0f;
+            uint32_t cbs = r.wa, cbe = r.wa;
+            for (uint32_t x = r.wa; x < r.wb && !dead; x++) {
+                if (x == cbe) {
+                    cpid = bpid, cks = bks, cvs = bvs, cbs = ibs, cbe = ibe;
+                    fresh = false;
+                    issue();
+                }
+                const int pid = __shfl_sync(DGT_FULL, cpid, x - cbs);
+                const float ks = __shfl_sync(DGT_FULL, cks, x - cbs), vs = __shfl_sync(DGT_FULL, cvs, x - cbs);
+                uint32_t addr;
+                float sc[4][NT][4];
+#pragma unroll
+                for (int t = 0; t < 4; t++)
+#pragma unroll
+                    for (uint32_t nt = 0; nt < NT; nt++)
+#pragma unroll
+                        for (int j = 0; j < 4; j++) sc[t][nt][j] = 0.0f;
+
+                // S: m-tile t holds tokens 16 (i / 2) + 4 t + i % 2 (rows i < 8) and those + 2 (rows 8 + i)
+#pragma unroll
+                for (uint32_t pan = 0; pan < PAN; pan++) {
+                    if (!dead && !arrive(addr)) dead = true;
+                    if (!dead && pid >= 0) {
+#pragma unroll
+                        for (uint32_t t = 0; t < 4; t++) {
+                            const uint32_t ta = 16 * (g >> 1) + 4 * t + (g & 1), tb = ta + 2;
+#pragma unroll
+                            for (uint32_t i = 0; i < PD / 64; i++) {
+                                const uint32_t ch = PD == 64 ? c : 2 * c + i;
+                                const uint4 ua4 = lds16(addr + ta * PD + ((ch ^ (PD == 64 ? (ta >> 1) & 3 : ta & 7)) << 4));
+                                const uint4 ub4 = lds16(addr + tb * PD + ((ch ^ (PD == 64 ? (tb >> 1) & 3 : tb & 7)) << 4));
+                                const uint32_t wa[4] = {ua4.x, ua4.y, ua4.z, ua4.w}, wb[4] = {ub4.x, ub4.y, ub4.z, ub4.w};
+#pragma unroll
+                                for (uint32_t w = 0; w < 4; w++) {
+                                    const uint32_t a0 = e4m3_lo(wa[w]), a2 = e4m3_hi(wa[w]);
+                                    const uint32_t a1 = e4m3_lo(wb[w]), a3 = e4m3_hi(wb[w]);
+#pragma unroll
+                                    for (uint32_t nt = 0; nt < NT; nt++) {
+                                        const uint32_t qi = (pan * 8 + i * 4 + w) * NT + nt;
+                                        const uint2 b = Cfg::QREG ? qf[Cfg::QREG ? qi : 0] : load_q(qi);
+                                        mma16816(sc[t][nt], a0, a1, a2, a3, b.x, b.y);
+                                    }
+                                }
+                            }
+                        }
+                    }
+                    if (!dead) release();
+                }
+                if (dead) break;
+                if (pid < 0) {
+#pragma unroll
+                    for (uint32_t pan = 0; pan < PAN; pan++) {
+                        if (!dead && !arrive(addr)) dead = true;
+                        if (!dead) release();
+                    }
+                    continue;
+                }
+
+                // weights; a page that every row sees whole needs no comparisons
+                const int32_t t0 = (int32_t)(s.page_index(x) * KV_P);
+                const bool whole = t0 + (int32_t)KV_P - 1 <= pf &&
+                                   (!a.window || t0 > pl - (int32_t)a.window || (uint32_t)t0 + KV_P <= a.sinks);
+                // log2 of the values' scale, a power of two (0, never written: 2^-127 does as well)
+                const float ev = (float)((int)(__float_as_uint(vs) >> 23) - 127);
+                uint32_t pw[4][NT][2];
+#pragma unroll
+                for (uint32_t nt = 0; nt < NT; nt++) {
+                    float tm[2] = {-INFINITY, -INFINITY}, al[2], ao[2], bs[2], cw[2];
+#pragma unroll
+                    for (uint32_t t = 0; t < 4; t++)
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            float v = sc[t][nt][j] * (fac[nt][j & 1] * ks);
+                            if (!whole) {
+                                const int32_t tok = t0 + (int32_t)(16 * (g >> 1) + 4 * t + (g & 1) + 2 * (j >> 1));
+                                const int32_t p = pos[nt][j & 1];
+                                const bool see = tok <= p && (!a.window || (int64_t)tok > (int64_t)p - a.window ||
+                                                              (uint32_t)tok < a.sinks);
+                                if (!see) v = -INFINITY;
+                            }
+                            sc[t][nt][j] = v;
+                            tm[j & 1] = fmaxf(tm[j & 1], v);
+                        }
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        tm[e] = fmaxf(tm[e], __shfl_xor_sync(DGT_FULL, tm[e], 4));
+                        tm[e] = fmaxf(tm[e], __shfl_xor_sync(DGT_FULL, tm[e], 8));
+                        tm[e] = fmaxf(tm[e], __shfl_xor_sync(DGT_FULL, tm[e], 16));
+                        const float mn = fmaxf(m[nt][e], tm[e]), un = fmaxf(mu[nt][e], tm[e] + ev);
+                        bs[e] = finite_base(mn);
+                        const float ubs = finite_base(un);
+                        al[e] = ex2(m[nt][e] - bs[e]);
+                        ao[e] = ex2(mu[nt][e] - ubs);
+                        cw[e] = vs != vs ? vs : ex2(fminf(bs[e] + ev - ubs + W_LOG2, 126.0f));
+                        m[nt][e] = mn;
+                        mu[nt][e] = un;
+                    }
+                    float ps[2] = {0.0f, 0.0f};
+#pragma unroll
+                    for (uint32_t t = 0; t < 4; t++) {
+                        float w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const float p = ex2(sc[t][nt][j] - bs[j & 1]);
+                            ps[j & 1] += p;
+                            w[j] = p * cw[j & 1];
+                            // a token that the row does not see has no weight, whatever its value's scale is
+                            if (!whole && sc[t][nt][j] == -INFINITY) w[j] = 0.0f;
+                        }
+                        pw[t][nt][0] = transpose8x8(f16_pair(w[0], w[1]));
+                        pw[t][nt][1] = transpose8x8(f16_pair(w[2], w[3]));
+                    }
+                    l[nt][0] = l[nt][0] * al[0] + ps[0];
+                    l[nt][1] = l[nt][1] * al[1] + ps[1];
+                    if (__any_sync(DGT_FULL, ao[0] != 1.0f || ao[1] != 1.0f)) {
+#pragma unroll
+                        for (uint32_t i = 0; i < D / 16; i++) {
+                            o[i][nt][0] *= ao[0];
+                            o[i][nt][1] *= ao[1];
+                            o[i][nt][2] *= ao[0];
+                            o[i][nt][3] *= ao[1];
+                        }
+                    }
+                }
+
+                // O: 16 dimensions at a time, k-step t the tokens of m-tile t
+#pragma unroll
+                for (uint32_t pan = 0; pan < PAN; pan++) {
+                    if (!dead && !arrive(addr)) dead = true;
+                    if (!dead) {
+#pragma unroll
+                        for (uint32_t i = 0; i < PD / 16; i++) {
+                            const uint4 ua4 = lds16(addr + (16 * i + g) * KV_P + 16 * c);
+                            const uint4 ub4 = lds16(addr + (16 * i + g + 8) * KV_P + 16 * c);
+                            const uint32_t wa[4] = {ua4.x, ua4.y, ua4.z, ua4.w}, wb[4] = {ub4.x, ub4.y, ub4.z, ub4.w};
+#pragma unroll
+                            for (uint32_t t = 0; t < 4; t++) {
+                                const uint32_t a0 = e4m3_lo(wa[t]), a2 = e4m3_hi(wa[t]);
+                                const uint32_t a1 = e4m3_lo(wb[t]), a3 = e4m3_hi(wb[t]);
+#pragma unroll
+                                for (uint32_t nt = 0; nt < NT; nt++)
+                                    mma16816(o[pan * (PD / 16) + i][nt], a0, a1, a2, a3, pw[t][nt][0], pw[t][nt][1]);
+                            }
+                        }
+                        release();
+                    }
+                }
+            }
+            if (dead) {
+                // let every copy in flight land before the CTA can end
+                more = false;
+                for (uint32_t i = taken; i < issued; i++) mbar_wait(smem_u32(&bar[warp][i % NS]), (i / NS) & 1u);
+                issued = taken;
+            }
+
+            // ---- the warps' sums to one
+#pragma unroll
+            for (uint32_t nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    float v = l[nt][e];
+                    v += __shfl_xor_sync(DGT_FULL, v, 4);
+                    v += __shfl_xor_sync(DGT_FULL, v, 8);
+                    v += __shfl_xor_sync(DGT_FULL, v, 16);
+                    if (g == 0) {
+                        float *st = stat[warp][8 * nt + 2 * c + e];
+                        st[0] = m[nt][e], st[1] = mu[nt][e], st[2] = v;
+                    }
+                }
+            __syncthreads();
+            if (tid < RT) {
+                float M = -INFINITY, MU = -INFINITY, L = 0.0f;
+                for (uint32_t w = 0; w < AT_WARPS; w++) {
+                    M = fmaxf(M, stat[w][tid][0]);
+                    MU = fmaxf(MU, stat[w][tid][1]);
+                }
+                for (uint32_t w = 0; w < AT_WARPS; w++)
+                    L += stat[w][tid][2] * ex2(stat[w][tid][0] - finite_base(M));
+                rowstat[tid][0] = M, rowstat[tid][1] = MU, rowstat[tid][2] = L;
+            }
+            const uint32_t n = s.per_head();
+            const bool complete = r.pa == 0 && r.pe == n;
+            float *part = a.part + (2 * (uint64_t)blockIdx.x + (r.pa == 0 ? 1 : 0)) * Cfg::PART;
+            auto write_out = [&](uint32_t row, uint32_t d, float v, float M, float MU, float L) {
+                const uint32_t flat = s.row0 + row;
+                const uint64_t at = (uint64_t)(s.tok0 + flat / a.group) * a.q_heads + r.h * a.group + flat % a.group;
+                const bool none = M == -INFINITY && L == 0.0f;
+                a.out[at * D + d] = f32_to_bf16_rne(none ? 0.0f : v * ex2(finite_base(MU) - finite_base(M) - W_LOG2) / L);
+                if (a.lse && d == 0) a.lse[at] = none ? -INFINITY : (M + __log2f(L)) * LN2;
+            };
+#pragma unroll
+            for (uint32_t nt = 0; nt < NT; nt++) {
+                float f[2];
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    float MU = -INFINITY;
+                    for (uint32_t w = 0; w < AT_WARPS; w++) MU = fmaxf(MU, stat[w][8 * nt + 2 * c + e][1]);
+                    f[e] = ex2(mu[nt][e] - finite_base(MU));
+                }
+#pragma unroll
+                for (uint32_t d0 = 0; d0 < D; d0 += 64) {
+                    __syncthreads();
+#pragma unroll
+                    for (uint32_t i = 0; i < 4; i++)
+#pragma unroll
+                        for (int j = 0; j < 4; j++)
+                            scratch[(warp * 8 + 2 * c + (j & 1)) * Cfg::RS + 16 * i + g + 8 * (j >> 1)] =
+                                o[d0 / 16 + i][nt][j] * f[j & 1];
+                    __syncthreads();
+                    for (uint32_t i = tid; i < 8 * 64; i += AT_WARPS * 32) {
+                        const uint32_t row = 8 * nt + i / 64, d = d0 + i % 64;
+                        if (row >= s.rows) continue;
+                        float v = 0.0f;
+#pragma unroll
+                        for (uint32_t w = 0; w < AT_WARPS; w++) v += scratch[(w * 8 + i / 64) * Cfg::RS + i % 64];
+                        const float *st = rowstat[row];
+                        if (complete) {
+                            write_out(row, d, v, st[0], st[1], st[2]);
+                        } else {
+                            float *pr = part + row * (D + 4);
+                            pr[4 + d] = v;
+                            if (d < 3) pr[d] = st[d];
+                        }
+                    }
+                }
+            }
+            if (complete) continue;
+
+            // ---- partial: the last CTA of the segment to arrive adds its parts in page order
+            __threadfence();
+            __syncthreads();
+            const uint64_t sa = chunk_base + s.base + (uint64_t)r.h * n, sb = sa + n;   // the segment's units
+            const uint64_t c0 = ((sa + 1) * C - 1) / U, c1 = (sb * C - 1) / U;
+            if (tid == 0) {
+                const int32_t was = atomicAdd(&a.count[c0], 1);
+                last_flag = was == (int32_t)(c1 - c0);
+                if (last_flag) a.count[c0] = 0;
+            }
+            __syncthreads();
+            if (!last_flag) continue;
+            __threadfence();
+            for (uint32_t i = tid; i < s.rows * D; i += AT_WARPS * 32) {
+                const uint32_t row = i / D, d = i % D;
+                auto at = [&](uint64_t cta) { return a.part + (2 * cta + (cta == c0 ? 1 : 0)) * Cfg::PART + row * (D + 4); };
+                float M = -INFINITY, MU = -INFINITY, L = 0.0f, v = 0.0f;
+                for (uint64_t k = c0; k <= c1; k++) {
+                    const float4 st = __ldcg(reinterpret_cast<const float4 *>(at(k)));
+                    M = fmaxf(M, st.x);
+                    MU = fmaxf(MU, st.y);
+                }
+                for (uint64_t k = c0; k <= c1; k++) {
+                    const float4 st = __ldcg(reinterpret_cast<const float4 *>(at(k)));
+                    L += st.z * ex2(st.x - finite_base(M));
+                    v += __ldcg(at(k) + 4 + d) * ex2(st.y - finite_base(MU));
+                }
+                write_out(row, d, v, M, MU, L);
+            }
+        }
+        more = false;   // everything of this chunk has been taken
+    }
+}
+
+template <uint32_t D, uint32_t NT>
+static int attn_launch(const AttnArgs &a, cudaStream_t st) {
+    DeviceInfo di;
+    if (device_info(&di) != DGT_OK) return DGT_ERR_CUDA;
+    constexpr uint32_t smem = AttnCfg<D, NT>::bytes;
+    auto fn = k_kv_attention<D, NT>;
+    static std::atomic<uint64_t> ready;   // devices that allow the shared memory
+    const uint64_t bit = di.device < 64 ? 1ull << di.device : 0;
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        if (cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+            cudaSuccess)
+            return DGT_ERR_CUDA;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    const unsigned grid = (unsigned)di.sms < AT_MAX_CTAS ? (unsigned)di.sms : AT_MAX_CTAS;
+    return launch_pdl(fn, dim3(grid), dim3(AT_WARPS * 32), smem, st, a) == cudaSuccess ? DGT_OK : DGT_ERR_CUDA;
+}
+
+// Rows of a tile, in n-tiles of eight: as many as an entry's rows (the mean of
+// a batch) fill, up to what the registers hold beside D accumulators a row.
+static uint32_t n_tiles(uint32_t head_dim, uint32_t group, uint32_t batch, uint64_t tokens) {
+    const uint64_t rows = group * ((tokens + batch - 1) / batch);
+    if (rows <= 8) return 1;
+    if (rows <= 16 || head_dim == 256) return 2;
+    return 4;
+}
+static uint64_t slot_count(uint32_t RT, uint32_t group, uint32_t batch, uint64_t tokens, bool ragged) {
+    if (!ragged) return (uint64_t)batch * ((group + RT - 1) / RT);
+    return tokens * group / RT + batch;
 }
 
 }  // namespace dgt
 
 using namespace dgt;
 
+// Arrival counters, then two partial results per CTA.
+constexpr size_t AT_COUNT_BYTES = (AT_MAX_CTAS * 4 + 255) / 256 * 256;
 extern "C" size_t dgt_kv_attention_workspace_bytes(const dgt_kv_cache *cache, uint32_t q_heads, uint32_t batch,
                                                    uint64_t tokens) {
-    (void)cache, (void)q_heads, (void)batch, (void)tokens;
-    return 0;
+    if (!cache || cache->kv_heads == 0 || batch == 0 || q_heads < cache->kv_heads) return 0;
+    const uint32_t RT = 8 * n_tiles(cache->head_dim, q_heads / cache->kv_heads, batch, tokens);
+    return AT_COUNT_BYTES + (size_t)AT_MAX_CTAS * 2 * RT * (cache->head_dim + 4) * 4;
+}
+
+extern "C" int dgt_kv_attention_ex(const dgt_kv_cache *cache, uint32_t layer, const dgt_heads *q, uint64_t tokens,
+                                   const int32_t *d_seqs, const int32_t *d_cu, uint32_t batch, float scale,
+                                   uint32_t window, uint32_t sinks, uint16_t *d_out, float *d_lse, void *d_ws,
+                                   size_t ws_bytes, int32_t *d_status, unsigned flags, void *stream) {
+    int rc = kv_check(cache);
+    if (rc != DGT_OK) return rc;
+    if (!q || layer >= cache->layers) return DGT_ERR_ARG;
+    if (flags & ~(DGT_TEST_SHORT_WAITS | DGT_TEST_WAIT_POLLS(0xFFFF))) return DGT_ERR_ARG;
+    if ((rc = batch_check(tokens, batch, d_cu)) != DGT_OK) return rc;
+    if (tokens == 0 || batch == 0) return DGT_OK;
+    if (!d_seqs || !d_out || !aligned16(d_out)) return DGT_ERR_ARG;
+    if (q->heads == 0 || q->heads % cache->kv_heads || q->heads / cache->kv_heads > 64) return DGT_ERR_SHAPE;
+    if ((rc = heads_check(q, q->heads)) != DGT_OK) return rc;
+    if (!d_ws || ((uintptr_t)d_ws & 255) ||
+        ws_bytes < dgt_kv_attention_workspace_bytes(cache, q->heads, batch, tokens))
+        return DGT_ERR_ARG;
+    AttnArgs a{};
+    a.c = *cache;
+    a.layer = layer, a.batch = batch, a.q_heads = q->heads, a.tokens = tokens;
+    // a window past every position is none
+    a.window = window < 0x40000000u ? window : 0u;
+    a.sinks = a.window ? (sinks < 0x40000000u ? sinks : 0x40000000u) : 0u;
+    a.group = q->heads / cache->kv_heads;
+    a.q = *q, a.seqs = d_seqs, a.cu = d_cu, a.scale_log2 = scale * LOG2E, a.out = d_out, a.lse = d_lse;
+    a.status = d_status;
+    const uint32_t nt = n_tiles(cache->head_dim, a.group, batch, tokens), RT = 8 * nt;
+    const uint64_t slots = slot_count(RT, a.group, batch, tokens, d_cu != nullptr);
+    a.slots = (uint32_t)slots;
+    a.per_entry = (a.group + RT - 1) / RT;
+    a.count = (int32_t *)d_ws;
+    a.part = (float *)((uint8_t *)d_ws + AT_COUNT_BYTES);
+    a.min_units = 1;
+    a.spin = wait_limit_from_flags(flags);
+    cudaStream_t st = (cudaStream_t)stream;
+    switch (cache->head_dim) {
+        case 64: return nt == 1 ? attn_launch<64, 1>(a, st) : nt == 2 ? attn_launch<64, 2>(a, st) : attn_launch<64, 4>(a, st);
+        case 128: return nt == 1 ? attn_launch<128, 1>(a, st) : nt == 2 ? attn_launch<128, 2>(a, st) : attn_launch<128, 4>(a, st);
+        default: return nt == 1 ? attn_launch<256, 1>(a, st) : attn_launch<256, 2>(a, st);
+    }
 }
 
 extern "C" int dgt_kv_attention(const dgt_kv_cache *cache, uint32_t layer, const dgt_heads *q, uint64_t tokens,
                                 const int32_t *d_seqs, const int32_t *d_cu, uint32_t batch, float scale,
                                 uint32_t window, uint32_t sinks, uint16_t *d_out, float *d_lse, void *d_ws,
                                 size_t ws_bytes, int32_t *d_status, void *stream) {
-    int rc = kv_check(cache);
-    if (rc != DGT_OK) return rc;
-    if (!q || layer >= cache->layers) return DGT_ERR_ARG;
-    if ((rc = batch_check(tokens, batch, d_cu)) != DGT_OK) return rc;
-    if (tokens == 0 || batch == 0) return DGT_OK;
-    if (!d_seqs || !d_out || !aligned16(d_out)) return DGT_ERR_ARG;
-    if (q->heads == 0 || q->heads % cache->kv_heads || q->heads / cache->kv_heads > 64) return DGT_ERR_SHAPE;
-    if ((rc = heads_check(q, q->heads)) != DGT_OK) return rc;
-    if (ws_bytes < dgt_kv_attention_workspace_bytes(cache, q->heads, batch, tokens)) return DGT_ERR_ARG;
-    (void)d_ws;
-    AttnArgs a{*cache, layer, batch, q->heads, window, window ? sinks : 0u, tokens, *q, d_seqs, d_cu, scale * LOG2E,
-               d_out, d_lse, d_status};
-    auto fn = cache->head_dim == 64    ? k_kv_attention_rows<64>
-              : cache->head_dim == 128 ? k_kv_attention_rows<128>
-                                       : k_kv_attention_rows<256>;
-    const uint64_t items = tokens * q->heads;
-    return launch_pdl(fn, dim3((unsigned)((items + 3) / 4)), dim3(128), 0, (cudaStream_t)stream, a) == cudaSuccess
-               ? DGT_OK
-               : DGT_ERR_CUDA;
+    return dgt_kv_attention_ex(cache, layer, q, tokens, d_seqs, d_cu, batch, scale, window, sinks, d_out, d_lse, d_ws,
+                               ws_bytes, d_status, 0, stream);
 }

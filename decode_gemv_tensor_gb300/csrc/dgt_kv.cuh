@@ -40,7 +40,7 @@ static inline int kv_check(const dgt_kv_cache *c) {
     if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return DGT_ERR_SHAPE;
     if (c->kv_heads == 0 || c->kv_heads > 256 || c->layers == 0 || c->layers > (1u << 16)) return DGT_ERR_SHAPE;
     if (c->pages == 0 || c->pages > (1u << 22)) return DGT_ERR_SHAPE;
-    if (c->max_seqs == 0 || c->max_seqs > (1u << 20) || c->max_pages == 0 || c->max_pages > (1u << 20))
+    if (c->max_seqs == 0 || c->max_seqs > (1u << 20) || c->max_pages == 0 || c->max_pages > (1u << 16))
         return DGT_ERR_SHAPE;
     return DGT_OK;
 }
@@ -58,22 +58,24 @@ static inline int batch_check(uint64_t tokens, uint32_t batch, const int32_t *cu
     return DGT_OK;
 }
 
-// Items of up to `step` rows cut from the entries of a batch, numbered without
-// a prefix sum: entry b's items are numbered from floor(cu[b] / step) + per * b
-// on.  Consecutive entries are then at least floor(n_b / step) + per numbers
-// apart, so `per` = 1 has room for the ceil(n_b / step) pieces of an entry and
-// per = 2 for the blocks that it touches wherever it starts; numbers past an
-// entry's pieces are empty.  The count of numbers is known on the host:
-// floor(tokens / step) + per * batch.
-__device__ __forceinline__ uint32_t item_base(const int32_t *cu, uint32_t b, uint32_t step, uint32_t per) {
-    return (uint32_t)cu[b] / step + per * b;
+// Items of up to `step` rows cut from the entries of a batch (each of their
+// tokens `mult` rows), numbered without a prefix sum: entry b's items are
+// numbered from floor(cu[b] * mult / step) + per * b on.  Consecutive entries
+// are then at least floor(rows_b / step) + per numbers apart, so `per` = 1 has
+// room for the ceil(rows_b / step) pieces of an entry and per = 2 for the
+// blocks that it touches wherever it starts; numbers past an entry's pieces
+// are empty.  The count of numbers is known on the host:
+// floor(tokens * mult / step) + per * batch.
+__device__ __forceinline__ uint32_t item_base(const int32_t *cu, uint32_t b, uint32_t step, uint32_t per,
+                                              uint32_t mult = 1) {
+    return (uint32_t)((uint64_t)(uint32_t)cu[b] * mult / step) + per * b;
 }
 __device__ __forceinline__ uint32_t item_entry(const int32_t *cu, uint32_t batch, uint32_t item, uint32_t step,
-                                               uint32_t per) {
+                                               uint32_t per, uint32_t mult = 1) {
     uint32_t lo = 0, hi = batch;   // the last b with item_base(b) <= item
     while (hi - lo > 1) {
         const uint32_t mid = (lo + hi) >> 1;
-        if (item_base(cu, mid, step, per) <= item) lo = mid;
+        if (item_base(cu, mid, step, per, mult) <= item) lo = mid;
         else hi = mid;
     }
     return lo;

@@ -599,7 +599,7 @@ int dgt_rotate(const dgt_rotary *rot, const dgt_heads *q, const dgt_heads *k, co
  * lens zero and table -1; the scales need no initial value.
  * Everything is device memory, caller-owned; k and v 16-byte aligned.
  * head_dim 64, 128 or 256; kv_heads 1..256; layers >= 1; pages 1..2^22;
- * max_seqs 1..2^20; max_pages 1..2^20 (else DGT_ERR_SHAPE).
+ * max_seqs 1..2^20; max_pages 1..2^16 (else DGT_ERR_SHAPE).
  */
 #define DGT_KV_PAGE 64
 typedef struct dgt_kv_cache {
@@ -659,9 +659,11 @@ int dgt_kv_read(const dgt_kv_cache *cache, int32_t layer, const int32_t *d_seqs,
  * row's largest element), the weights exp(t_j - max) are rounded to fp16
  * (2^-11 relative), every sum is fp32.
  * d_ws: device, dgt_kv_attention_workspace_bytes(...) bytes, 256-byte aligned,
- * zeroed before its first use (every call leaves it so); calls that may
- * overlap need one each.  DGT_ERR_TIMEOUT in the status: a bounded wait ran
- * out, the outputs are then unspecified.
+ * zeroed before its first use: it begins with arrival counters that every
+ * call, of whatever sizes, leaves at zero; the rest need not be kept.  Calls
+ * that may overlap need one each.  The results do not depend on timing.  DGT_ERR_TIMEOUT in the status: a bounded wait ran
+ * out, the outputs are then unspecified.  flags: 0, or the failure-path test
+ * hook DGT_TEST_SHORT_WAITS | DGT_TEST_WAIT_POLLS(n); others DGT_ERR_ARG.
  */
 size_t dgt_kv_attention_workspace_bytes(const dgt_kv_cache *cache, uint32_t q_heads, uint32_t batch,
                                         uint64_t tokens);
@@ -669,6 +671,10 @@ int dgt_kv_attention(const dgt_kv_cache *cache, uint32_t layer, const dgt_heads 
                      const int32_t *d_seqs, const int32_t *d_cu, uint32_t batch, float scale, uint32_t window,
                      uint32_t sinks, uint16_t *d_out, float *d_lse, void *d_ws, size_t ws_bytes, int32_t *d_status,
                      void *stream);
+int dgt_kv_attention_ex(const dgt_kv_cache *cache, uint32_t layer, const dgt_heads *q, uint64_t tokens,
+                        const int32_t *d_seqs, const int32_t *d_cu, uint32_t batch, float scale, uint32_t window,
+                        uint32_t sinks, uint16_t *d_out, float *d_lse, void *d_ws, size_t ws_bytes, int32_t *d_status,
+                        unsigned flags, void *stream);
 
 /*
  * Pages.  All in stream order, so a captured graph can hold them.

@@ -255,7 +255,11 @@ def test_strides_streams_graphs_and_repeats(dgt):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want), lens
-    assert not ws.any()
+    # the same workspace for calls of other sizes
+    p = rand(g, 2, 2, 128)
+    s.c.lens.copy_(i32([333, 64]))
+    want = dgt.kv_attention(s.c, 0, p, i32([1, 0]))
+    assert torch.equal(dgt.kv_attention(s.c, 0, p, i32([1, 0]), ws=ws), want)
 
 
 def test_what_the_device_finds_wrong(dgt):
@@ -306,3 +310,20 @@ def test_offsets_past_32_bits(dgt):
     c.table[0] = i32([69999, 69997, 5])
     assert torch.equal(dgt.kv_attention(c, 1, q, i32([0])).view(torch.int16).cpu(),
                        torch.from_numpy(y).bfloat16().view(torch.int16))
+
+
+@pytest.mark.parametrize("polls", [0, 1])
+@pytest.mark.parametrize("dim,rows", [(64, 1), (128, 1), (256, 1), (128, 9)])
+def test_a_wait_that_runs_out_is_reported(dgt, dim, rows, polls):
+    # the test hook: waits give up after `polls` polls, the status says so, and the next call is as ever
+    g = np.random.default_rng(dim)
+    s = Setup(dgt, g, [3000, 70], 2, dim)
+    counts = [rows, 1]
+    q, cu = rand(g, rows + 1, 6, dim), i32([0, rows, rows + 1])
+    ws = dgt.kv_attention_workspace(s.c, 6, 2, rows + 1)
+    want = dgt.kv_attention(s.c, 0, q, i32([0, 1]), cu=cu, ws=ws)
+    st = i32([0])
+    dgt.kv_attention(s.c, 0, q, i32([0, 1]), cu=cu, ws=ws, status=st, test_wait_polls=polls)
+    code = dgt.read_status(st)
+    assert code == -5 if polls == 0 else code in (0, -5)
+    assert torch.equal(dgt.kv_attention(s.c, 0, q, i32([0, 1]), cu=cu, ws=ws), want)

@@ -147,3 +147,10 @@ def test_block_layout_is_a_permutation():
                 seen.add(d // panel * 64 * panel + t * panel + ((c ^ x) * 16) + d % 16)
         assert seen == set(range(64 * dim))
         assert {d * 64 + t for d in range(dim) for t in range(64)} == set(range(64 * dim))
+
+
+def test_attention_flags(lib):
+    c = C.byref(cache())
+    for flags in (1, 4, 1 << 15):
+        assert lib.dgt_kv_attention_ex(c, 0, heads(8), 1, P, None, 1, 1.0, 0, 0, P, None, P, 1 << 30, None, flags,
+                                       None) == ARG
