@@ -180,6 +180,23 @@ def _stream(stream=None):
     return C.c_void_p(s.cuda_stream)
 
 
+_raw_stream = None
+
+
+def _stream_on(x, stream):
+    """The stream handle for work on tensor x.  torch's raw-handle query where
+    it has one: 0.1 us instead of the 3 us of a Stream object, for calls whose
+    kernels take as long as that."""
+    global _raw_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw_stream(x.device.index)
+
+
 # ---------------------------------------------------------------------------
 # host: pack / unpack / container
 # ---------------------------------------------------------------------------
@@ -603,11 +620,13 @@ def gemm_rebuild(W: R4, X, scratch=None, plan=None, Y32=None, Y=None, ws=None, s
 def _heads(x, name):
     """The dgt_heads view of a bf16 tensor [tokens, heads, dim] on the device."""
     import torch
-    if x.dim() != 3 or x.dtype != torch.bfloat16 or not x.is_cuda or (x.numel() and x.stride(2) != 1):
-        raise ValueError(f"{name}: a CUDA bfloat16 tensor [tokens, heads, dim] with a contiguous last dimension")
+    if x.dim() != 3 or x.dtype != torch.bfloat16 or not x.is_cuda:
+        raise ValueError(f"{name}: a CUDA bfloat16 tensor [tokens, heads, dim]")
+    (n, h, _), (ts, hs, es) = x.shape, x.stride()
+    if es != 1 and x.numel():
+        raise ValueError(f"{name}: a contiguous last dimension")
     # a stride that no element uses may be anything
-    ts, hs = (x.stride(i) if x.shape[i] > 1 else 0 for i in (0, 1))
-    return HeadsStruct(x.data_ptr(), ts, hs, x.shape[1], 0)
+    return HeadsStruct(x.data_ptr(), ts if n > 1 else 0, hs if h > 1 else 0, h, 0)
 
 
 def _i32(x, name, n=None):
@@ -658,22 +677,30 @@ def rotate(rotary: Rotary, q, pos, k=None, q_out=None, k_out=None, stream=None):
     """dgt_rotate: q (and k) bf16 [tokens, heads, dim] turned to their
     positions, pos int32 [tokens] or [axes, tokens].  The outputs may be the
     inputs.  Returns (q_out, k_out) (k_out None without k)."""
-    import torch
-    tokens, _, dim = q.shape
+    tokens, nq, dim = q.shape
     p = _i32(pos, "pos", rotary.axes * tokens)
-    if k is not None and (k.shape[0] != tokens or k.shape[2] != dim):
-        raise ValueError("k: the same tokens and head size as q")
+    hq, hk, ok = _heads(q, "q"), None, None
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
-        raise ValueError("outputs: the shapes of the inputs")
+        q_out = q.new_empty((tokens, nq, dim))
+        oq = HeadsStruct(q_out.data_ptr(), nq * dim, dim, nq, 0)
+    else:
+        oq = _heads(q_out, "q_out")
     if k is None:
         k_out = None
-    hs = [None if x is None else C.byref(_heads(x, n)) for x, n in ((q, "q"), (k, "k"), (q_out, "q_out"),
-                                                                    (k_out, "k_out"))]
-    _check(lib().dgt_rotate(C.byref(rotary.s), *hs, dim, tokens, p, _stream(stream)), "dgt_rotate")
+    else:
+        hk, nk = _heads(k, "k"), k.shape[1]
+        if k.shape[0] != tokens or k.shape[2] != dim:
+            raise ValueError("k: the same tokens and head size as q")
+        if k_out is None:
+            k_out = k.new_empty((tokens, nk, dim))
+            ok = HeadsStruct(k_out.data_ptr(), nk * dim, dim, nk, 0)
+        else:
+            ok = _heads(k_out, "k_out")
+            if k_out.shape != k.shape:
+                raise ValueError("k_out: the shape of k")
+    if q_out.shape != q.shape:
+        raise ValueError("q_out: the shape of q")
+    _check(lib().dgt_rotate(rotary.s, hq, hk, oq, ok, dim, tokens, p, _stream_on(q, stream)), "dgt_rotate")
     return q_out, k_out
 
 
@@ -718,10 +745,10 @@ def kv_append(cache: KvCache, layer: int, k, v, seqs, start, cu=None, status=Non
     tokens, batch = k.shape[0], seqs.numel()
     if k.shape != v.shape or tuple(k.shape[1:]) != (cache.kv_heads, cache.head_dim):
         raise ValueError("k, v: [tokens, kv_heads, head_dim]")
-    _check(lib().dgt_kv_append(C.byref(cache.s), layer, C.byref(_heads(k, "k")), C.byref(_heads(v, "v")), tokens,
+    _check(lib().dgt_kv_append(cache.s, layer, _heads(k, "k"), _heads(v, "v"), tokens,
                                _i32(seqs, "seqs"), _i32(start, "start", batch),
                                None if cu is None else _i32(cu, "cu", batch + 1), batch, _ptr(status),
-                               _stream(stream)), "dgt_kv_append")
+                               _stream_on(cache.k, stream)), "dgt_kv_append")
 
 
 def kv_read(cache: KvCache, layer, seqs, first, cu, tokens: int, status=None, stream=None):
@@ -730,19 +757,20 @@ def kv_read(cache: KvCache, layer, seqs, first, cu, tokens: int, status=None, st
     ...].  cu int32 [batch + 1] (None: one position each), tokens: their sum."""
     import torch
     batch = seqs.numel()
-    lead = (cache.layers,) if layer is None else ()
-    out = [torch.empty((*lead, tokens, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16, device=cache.k.device)
-           for _ in range(2)]
-    _check(lib().dgt_kv_read(C.byref(cache.s), -1 if layer is None else layer, _i32(seqs, "seqs"),
+    shape = (tokens, cache.kv_heads, cache.head_dim)
+    if layer is None:
+        shape = (cache.layers, *shape)
+    out = [cache.k.new_empty(shape, dtype=torch.bfloat16) for _ in range(2)]
+    _check(lib().dgt_kv_read(cache.s, -1 if layer is None else layer, _i32(seqs, "seqs"),
                              _i32(first, "first", batch), None if cu is None else _i32(cu, "cu", batch + 1), batch,
-                             tokens, _ptr(out[0]), _ptr(out[1]), _ptr(status), _stream(stream)), "dgt_kv_read")
+                             tokens, _ptr(out[0]), _ptr(out[1]), _ptr(status), _stream_on(cache.k, stream)), "dgt_kv_read")
     return out
 
 
 def kv_attention_workspace(cache: KvCache, q_heads: int, batch: int, tokens: int):
     """A workspace for kv_attention calls of these sizes (zeroed, as its first use wants it)."""
     import torch
-    nb = int(lib().dgt_kv_attention_workspace_bytes(C.byref(cache.s), q_heads, batch, tokens))
+    nb = int(lib().dgt_kv_attention_workspace_bytes(cache.s, q_heads, batch, tokens))
     return torch.zeros(max(nb, 256), dtype=torch.uint8, device=cache.k.device)
 
 
@@ -763,18 +791,18 @@ def kv_attention(cache: KvCache, layer: int, q, seqs, cu=None, scale=None, windo
     if window < 0 or sinks < 0:
         raise ValueError("window and sinks: not negative")
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=q.device)
-    if tuple(out.shape) != (tokens, heads, dim) or out.dtype != torch.bfloat16 or not out.is_contiguous():
+        out = q.new_empty((tokens, heads, dim))
+    elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
         raise ValueError("out: a contiguous bfloat16 tensor of q's shape")
     if lse is not None and (lse.numel() != tokens * heads or lse.dtype != torch.float32 or not lse.is_contiguous()):
         raise ValueError("lse: a contiguous float32 tensor [tokens, q_heads]")
     if ws is None:
         ws = kv_attention_workspace(cache, heads, batch, tokens)
-    _check(lib().dgt_kv_attention_ex(C.byref(cache.s), layer, C.byref(_heads(q, "q")), tokens, _i32(seqs, "seqs"),
+    _check(lib().dgt_kv_attention_ex(cache.s, layer, _heads(q, "q"), tokens, _i32(seqs, "seqs"),
                                      None if cu is None else _i32(cu, "cu", batch + 1), batch,
                                      dim ** -0.5 if scale is None else scale, window, sinks, _ptr(out), _ptr(lse),
                                      _ptr(ws), ws.numel(), _ptr(status), test_wait_flags(test_wait_polls),
-                                     _stream(stream)), "dgt_kv_attention")
+                                     _stream_on(cache.k, stream)), "dgt_kv_attention")
     return out
 
 
@@ -785,36 +813,36 @@ def kv_reserve(cache: KvCache, seqs, count, start=None, status=None, stream=None
     import torch
     n = seqs.numel()
     if start is None:
-        start = torch.empty(n, dtype=torch.int32, device=seqs.device)
-    _check(lib().dgt_kv_reserve(C.byref(cache.s), _i32(seqs, "seqs"), _i32(count, "count", n), n,
+        start = seqs.new_empty(n)
+    _check(lib().dgt_kv_reserve(cache.s, _i32(seqs, "seqs"), _i32(count, "count", n), n,
                                 _i32(start, "start", n), _ptr(cache.ws), cache.ws.numel(), _ptr(status),
-                                _stream(stream)), "dgt_kv_reserve")
+                                _stream_on(cache.k, stream)), "dgt_kv_reserve")
     return start
 
 
 def kv_fork(cache: KvCache, src, dst, status=None, stream=None):
     """dgt_kv_fork: sequences dst[i] become copies of src[i] that share its pages."""
-    _check(lib().dgt_kv_fork(C.byref(cache.s), _i32(src, "src"), _i32(dst, "dst", src.numel()), src.numel(),
-                             _ptr(status), _stream(stream)), "dgt_kv_fork")
+    _check(lib().dgt_kv_fork(cache.s, _i32(src, "src"), _i32(dst, "dst", src.numel()), src.numel(),
+                             _ptr(status), _stream_on(cache.k, stream)), "dgt_kv_fork")
 
 
 def kv_free(cache: KvCache, seqs, status=None, stream=None):
     """dgt_kv_free: the sequences give up their pages."""
-    _check(lib().dgt_kv_free(C.byref(cache.s), _i32(seqs, "seqs"), seqs.numel(), _ptr(status), _stream(stream)),
+    _check(lib().dgt_kv_free(cache.s, _i32(seqs, "seqs"), seqs.numel(), _ptr(status), _stream_on(cache.k, stream)),
            "dgt_kv_free")
 
 
 def kv_copy_pages(cache: KvCache, src, dst, status=None, stream=None):
     """dgt_kv_copy_pages: pages src[i] -> dst[i] (int32 on the device) in every layer."""
-    _check(lib().dgt_kv_copy_pages(C.byref(cache.s), _i32(src, "src"), _i32(dst, "dst", src.numel()), src.numel(),
-                                   _ptr(status), _stream(stream)), "dgt_kv_copy_pages")
+    _check(lib().dgt_kv_copy_pages(cache.s, _i32(src, "src"), _i32(dst, "dst", src.numel()), src.numel(),
+                                   _ptr(status), _stream_on(cache.k, stream)), "dgt_kv_copy_pages")
 
 
 def kv_compact(cache: KvCache, live=None, status=None, stream=None):
     """dgt_kv_compact: the used pages move to the lowest numbers; live (int32
     [1] on the device) gets their count."""
-    _check(lib().dgt_kv_compact(C.byref(cache.s), None if live is None else _i32(live, "live", 1), _ptr(cache.ws),
-                                cache.ws.numel(), _ptr(status), _stream(stream)), "dgt_kv_compact")
+    _check(lib().dgt_kv_compact(cache.s, None if live is None else _i32(live, "live", 1), _ptr(cache.ws),
+                                cache.ws.numel(), _ptr(status), _stream_on(cache.k, stream)), "dgt_kv_compact")
 
 
 # ---------------------------------------------------------------------------

@@ -11,75 +11,13 @@
 // scale) (the numerator sums codes times exp2(t + log2 vs - mu)).  Then no
 // page's weight is lost to another page's scale, and the quotient is
 // exp2(mu - m) * numerator / l.
-//
-// Work is cut evenly over the CTAs whatever the lengths: a segment is one tile
-// of query rows and one kv head, its units are the pages that the tile sees,
-// and CTA c of C takes units [c U / C, (c + 1) U / C) of all U.  A segment that
-// ends up in several CTAs leaves partial sums in the workspace; the CTA that
-// arrives last adds them in page order, so results do not depend on timing.
-// Lengths are read on the device: a captured graph follows them.
-#include "dgt_kv.cuh"
-
-#include "dgt_device.cuh"
+#include "dgt_attn.cuh"
 
 namespace dgt {
 
-constexpr float LOG2E = 1.4426950408889634f;
-constexpr float LN2 = 0.6931471805599453f;
 constexpr float W_LOG2 = 12.0f;        // weights of the numerator reach 2^12 (fp16 holds them to 2^-24)
 constexpr uint32_t AT_WARPS = 8;
-constexpr uint32_t AT_CHUNK = 128;     // row tiles described in shared memory at a time
-constexpr uint32_t AT_MAX_CTAS = 160;
 
-struct AttnArgs {
-    dgt_kv_cache c;
-    uint32_t layer, batch, q_heads, window, sinks, group, slots, per_entry;
-    uint64_t tokens;
-    dgt_heads q;
-    const int32_t *seqs, *cu;
-    float scale_log2;   // scale * log2(e)
-    uint16_t *out;
-    float *lse;
-    int32_t *count;     // workspace: arrivals at the segment that CTA c begins and others end, zero between calls
-    float *part;        // workspace: two partial results per CTA
-    int32_t *status;
-    uint32_t min_units, spin;
-};
-
-// A tile of query rows: rows [row0, row0 + rows) of its entry's flattened
-// (token, head of the group) rows, at positions pos0 + row / group.
-struct Slot {
-    uint32_t base, np;          // first unit (of the chunk's), pages per head (0: none is seen)
-    uint32_t sp, wp;            // pages seen before the window's, the window's first page
-    int32_t seq, pos0;          // table row; position of the entry's first row
-    uint32_t tok0, row0, rows;  // entry's first token row, tile's first flattened row, row count
-    __device__ __forceinline__ uint32_t per_head() const { return np ? np : 1; }
-    __device__ __forceinline__ uint32_t page_index(uint32_t i) const { return i < sp ? i : wp + i - sp; }
-};
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.0f : m; }
-
-// Two e4m3 codes (the low or high half of w) as two fp16.
-__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
-    return r;
-}
-__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
-    return r;
-}
-__device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -95,53 +33,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
-}
-
-// The row tile of number `slot`, RT rows each; units 0 for an empty number.
-__device__ __forceinline__ Slot slot_info(const AttnArgs &a, uint32_t slot, uint32_t RT, uint32_t *units) {
-    Slot s{};
-    uint32_t b, rt, n = 1;
-    *units = 0;
-    if (a.cu) {
-        b = item_entry(a.cu, a.batch, slot, RT, 1, a.group);
-        rt = slot - item_base(a.cu, b, RT, 1, a.group);
-        s.tok0 = (uint32_t)a.cu[b];
-        n = (uint32_t)(a.cu[b + 1] - a.cu[b]);
-        if ((uint64_t)s.tok0 + n > a.tokens) {
-            set_status(a.status, DGT_ERR_ARG);
-            return s;
-        }
-    } else {
-        b = slot / a.per_entry;
-        rt = slot % a.per_entry;
-        s.tok0 = b;
-    }
-    const uint64_t all = (uint64_t)n * a.group, first = (uint64_t)rt * RT;
-    if (first >= all) return s;
-    s.row0 = (uint32_t)first;
-    s.rows = (uint32_t)min((uint64_t)RT, all - first);
-    *units = a.c.kv_heads;
-    s.seq = a.seqs[b];
-    int32_t len = 0;
-    if (s.seq < 0 || (uint32_t)s.seq >= a.c.max_seqs) {
-        set_status(a.status, DGT_ERR_ARG);
-        return s;
-    }
-    len = a.c.lens[s.seq];
-    if (len < 0 || (uint64_t)len > (uint64_t)a.c.max_pages * KV_P) {
-        set_status(a.status, DGT_ERR_ARG);
-        len = 0;
-    }
-    s.pos0 = len > 0 ? len - (int32_t)n : -0x40000000;
-    const int32_t pf = s.pos0 + (int32_t)(s.row0 / a.group);
-    const int32_t pl = s.pos0 + (int32_t)((s.row0 + s.rows - 1) / a.group);
-    if (pl < 0) return s;
-    const uint32_t lo = a.window && pf >= 0 && (uint32_t)pf >= a.window ? (uint32_t)pf - a.window + 1 : 0;
-    s.wp = lo / KV_P;
-    s.sp = min((min(a.sinks, lo) + KV_P - 1) / KV_P, s.wp);
-    s.np = s.sp + (uint32_t)pl / KV_P - s.wp + 1;
-    *units = a.c.kv_heads * s.np;
-    return s;
 }
 
 // The queries: rows of up to eight per n-tile (NT of them) are the N side of
@@ -191,22 +82,9 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) k_kv_attention(AttnArgs a) {
     pdl_wait();
 
     // ---- the CTA's units
-    uint64_t mine = 0;
-    uint32_t units;
     Slot si{};
-    for (uint32_t s = tid; s < a.slots; s += AT_WARPS * 32) {
-        si = slot_info(a, s, RT, &units);
-        mine += units;
-    }
-    const uint32_t units0 = a.slots <= AT_CHUNK ? (uint32_t)mine : 0;   // one slot per thread: kept for the scan below
-    uint64_t sum = mine;
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(DGT_FULL, sum, d);
-    if (lane == 0) usum[warp] = sum;
-    __syncthreads();
-    uint64_t U = 0;
-#pragma unroll
-    for (uint32_t w = 0; w < AT_WARPS; w++) U += usum[w];
+    uint32_t units0;
+    const uint64_t U = all_units<AT_WARPS>(a, RT, usum, si, units0);
     const uint64_t most = (U + a.min_units - 1) / a.min_units;
     const uint64_t C = most < gridDim.x ? most : gridDim.x;
     if (blockIdx.x >= C) return;
@@ -221,50 +99,27 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) k_kv_attention(AttnArgs a) {
     uint64_t base0 = 0;
     for (uint32_t s0 = 0; s0 < a.slots && base0 < ub; s0 += AT_CHUNK) {
         // ---- describe the next row tiles
-        __syncthreads();
-        units = 0;
-        if (a.slots <= AT_CHUNK) units = units0;
-        else if (tid < AT_CHUNK && s0 + tid < a.slots) si = slot_info(a, s0 + tid, RT, &units);
-        uint32_t wtot;
-        uint32_t before = warp_excl_scan(units, &wtot);
-        if (lane == 0) wsum[warp] = wtot;
-        __syncthreads();
-        uint32_t tot = 0;
-#pragma unroll
-        for (uint32_t w = 0; w < AT_CHUNK / 32; w++) {
-            if (w < warp) before += wsum[w];
-            tot += wsum[w];
-        }
-        if (tid < AT_CHUNK) {
-            si.base = before;
-            slots[tid] = si;
-        }
-        __syncthreads();
+        const uint32_t tot = describe<AT_WARPS>(a, RT, s0, si, units0, slots, wsum);
         const uint64_t first = base0 > ua ? base0 : ua, end = base0 + tot < ub ? base0 + tot : ub;
         const uint32_t u0 = (uint32_t)(first - base0), u1 = end > first ? (uint32_t)(end - base0) : u0;
         const uint64_t chunk_base = base0;
         base0 += tot;
         if (u0 == u1) continue;
 
-        // a run of pages [pa, pe) of head h's segment of a slot, beginning at unit u
-        struct Run {
-            uint32_t u, slot, h, pa, pe, wa, wb;
-        };
         const uint32_t nslots = min(AT_CHUNK, a.slots - s0);
+        struct Share : Run {
+            uint32_t wa, wb;   // this warp's pages
+        };
         auto make_run = [&](uint32_t u, uint32_t slot) {
-            Run r;
-            while (slot + 1 < nslots && slots[slot + 1].base <= u) slot++;
-            const Slot &s = slots[slot];
-            const uint32_t n = s.per_head();
-            r.u = u, r.slot = slot, r.h = (u - s.base) / n, r.pa = (u - s.base) % n;
-            r.pe = min(n, r.pa + (u1 - u));
-            const uint32_t cnt = s.np ? r.pe - r.pa : 0;
+            Share r;
+            static_cast<Run &>(r) = run_at(slots, nslots, u, u1, slot);
+            const uint32_t cnt = slots[r.slot].np ? r.pe - r.pa : 0;
             r.wa = r.pa + warp * cnt / AT_WARPS, r.wb = r.pa + (warp + 1) * cnt / AT_WARPS;
             return r;
         };
 
         // ---- issue side: page numbers and scales of up to 32 pages in the lanes
-        Run ir = make_run(u0, 0);
+        Share ir = make_run(u0, 0);
         uint32_t ix = ir.wa, ik = 0, ibs = ir.wa, ibe = ir.wa;
         bool more = true, fresh = false;   // fresh: a batch that the consuming side has not taken over
         int bpid = -1;
@@ -339,7 +194,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) k_kv_attention(AttnArgs a) {
 
         // ---- consume the CTA's runs of this chunk
         for (uint32_t u = u0, hint = 0; u < u1;) {
-            const Run r = make_run(u, hint);
+            const Share r = make_run(u, hint);
             hint = r.slot;
             u += r.pe - r.pa;
             const Slot s = slots[r.slot];
@@ -608,13 +463,6 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) k_kv_attention(AttnArgs a) {
             const uint32_t n = s.per_head();
             const bool complete = r.pa == 0 && r.pe == n;
             float *part = a.part + (2 * (uint64_t)blockIdx.x + (r.pa == 0 ? 1 : 0)) * Cfg::PART;
-            auto write_out = [&](uint32_t row, uint32_t d, float v, float M, float MU, float L) {
-                const uint32_t flat = s.row0 + row;
-                const uint64_t at = (uint64_t)(s.tok0 + flat / a.group) * a.q_heads + r.h * a.group + flat % a.group;
-                const bool none = M == -INFINITY && L == 0.0f;
-                a.out[at * D + d] = f32_to_bf16_rne(none ? 0.0f : v * ex2(finite_base(MU) - finite_base(M) - W_LOG2) / L);
-                if (a.lse && d == 0) a.lse[at] = none ? -INFINITY : (M + __log2f(L)) * LN2;
-            };
 #pragma unroll
             for (uint32_t nt = 0; nt < NT; nt++) {
                 float f[2];
@@ -642,7 +490,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) k_kv_attention(AttnArgs a) {
                         for (uint32_t w = 0; w < AT_WARPS; w++) v += scratch[(w * 8 + i / 64) * Cfg::RS + i % 64];
                         const float *st = rowstat[row];
                         if (complete) {
-                            write_out(row, d, v, st[0], st[1], st[2]);
+                            write_out<D>(a, s, r.h, row, d, v, st[0], st[1], st[2], W_LOG2);
                         } else {
                             float *pr = part + row * (D + 4);
                             pr[4 + d] = v;
@@ -666,22 +514,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) k_kv_attention(AttnArgs a) {
             __syncthreads();
             if (!last_flag) continue;
             __threadfence();
-            for (uint32_t i = tid; i < s.rows * D; i += AT_WARPS * 32) {
-                const uint32_t row = i / D, d = i % D;
-                auto at = [&](uint64_t cta) { return a.part + (2 * cta + (cta == c0 ? 1 : 0)) * Cfg::PART + row * (D + 4); };
-                float M = -INFINITY, MU = -INFINITY, L = 0.0f, v = 0.0f;
-                for (uint64_t k = c0; k <= c1; k++) {
-                    const float4 st = __ldcg(reinterpret_cast<const float4 *>(at(k)));
-                    M = fmaxf(M, st.x);
-                    MU = fmaxf(MU, st.y);
-                }
-                for (uint64_t k = c0; k <= c1; k++) {
-                    const float4 st = __ldcg(reinterpret_cast<const float4 *>(at(k)));
-                    L += st.z * ex2(st.x - finite_base(M));
-                    v += __ldcg(at(k) + 4 + d) * ex2(st.y - finite_base(MU));
-                }
-                write_out(row, d, v, M, MU, L);
-            }
+            join_parts<D, Cfg::PART>(a, s, r.h, c0, c1, tid, AT_WARPS * 32, W_LOG2);
         }
         more = false;   // everything of this chunk has been taken
     }
@@ -705,13 +538,18 @@ static int attn_launch(const AttnArgs &a, cudaStream_t st) {
     return launch_pdl(fn, dim3(grid), dim3(AT_WARPS * 32), smem, st, a) == cudaSuccess ? DGT_OK : DGT_ERR_CUDA;
 }
 
-// Rows of a tile, in n-tiles of eight: as many as an entry's rows (the mean of
-// a batch) fill, up to what the registers hold beside D accumulators a row.
-static uint32_t n_tiles(uint32_t head_dim, uint32_t group, uint32_t batch, uint64_t tokens) {
+// Rows of a tile, by an entry's rows (the mean of a batch): in n-tiles of
+// eight, as many as they fill, up to what the registers hold beside D
+// accumulators a row; from PROMPT_ROWS on the tensor-core tiles.
+constexpr uint64_t PROMPT_ROWS = 64;
+struct Plan {
+    uint32_t nt, RT;   // nt 0: tensor-core tiles
+};
+static Plan attn_plan(uint32_t head_dim, uint32_t group, uint32_t batch, uint64_t tokens) {
     const uint64_t rows = group * ((tokens + batch - 1) / batch);
-    if (rows <= 8) return 1;
-    if (rows <= 16 || head_dim == 256) return 2;
-    return 4;
+    if (rows >= PROMPT_ROWS) return {0, prompt_rows(head_dim)};
+    const uint32_t nt = rows <= 8 ? 1 : rows <= 16 || head_dim == 256 ? 2 : 4;
+    return {nt, 8 * nt};
 }
 static uint64_t slot_count(uint32_t RT, uint32_t group, uint32_t batch, uint64_t tokens, bool ragged) {
     if (!ragged) return (uint64_t)batch * ((group + RT - 1) / RT);
@@ -727,7 +565,7 @@ constexpr size_t AT_COUNT_BYTES = (AT_MAX_CTAS * 4 + 255) / 256 * 256;
 extern "C" size_t dgt_kv_attention_workspace_bytes(const dgt_kv_cache *cache, uint32_t q_heads, uint32_t batch,
                                                    uint64_t tokens) {
     if (!cache || cache->kv_heads == 0 || batch == 0 || q_heads < cache->kv_heads) return 0;
-    const uint32_t RT = 8 * n_tiles(cache->head_dim, q_heads / cache->kv_heads, batch, tokens);
+    const uint32_t RT = attn_plan(cache->head_dim, q_heads / cache->kv_heads, batch, tokens).RT;
     return AT_COUNT_BYTES + (size_t)AT_MAX_CTAS * 2 * RT * (cache->head_dim + 4) * 4;
 }
 
@@ -756,7 +594,8 @@ extern "C" int dgt_kv_attention_ex(const dgt_kv_cache *cache, uint32_t layer, co
     a.group = q->heads / cache->kv_heads;
     a.q = *q, a.seqs = d_seqs, a.cu = d_cu, a.scale_log2 = scale * LOG2E, a.out = d_out, a.lse = d_lse;
     a.status = d_status;
-    const uint32_t nt = n_tiles(cache->head_dim, a.group, batch, tokens), RT = 8 * nt;
+    const Plan plan = attn_plan(cache->head_dim, a.group, batch, tokens);
+    const uint32_t nt = plan.nt, RT = plan.RT;
     const uint64_t slots = slot_count(RT, a.group, batch, tokens, d_cu != nullptr);
     a.slots = (uint32_t)slots;
     a.per_entry = (a.group + RT - 1) / RT;
@@ -765,6 +604,7 @@ extern "C" int dgt_kv_attention_ex(const dgt_kv_cache *cache, uint32_t layer, co
     a.min_units = 1;
     a.spin = wait_limit_from_flags(flags);
     cudaStream_t st = (cudaStream_t)stream;
+    if (nt == 0) return prompt_launch(a, st);
     switch (cache->head_dim) {
         case 64: return nt == 1 ? attn_launch<64, 1>(a, st) : nt == 2 ? attn_launch<64, 2>(a, st) : attn_launch<64, 4>(a, st);
         case 128: return nt == 1 ? attn_launch<128, 1>(a, st) : nt == 2 ? attn_launch<128, 2>(a, st) : attn_launch<128, 4>(a, st);
