@@ -677,11 +677,12 @@ def rotate(rotary: Rotary, q, pos, k=None, q_out=None, k_out=None, stream=None):
     """dgt_rotate: q (and k) bf16 [tokens, heads, dim] turned to their
     positions, pos int32 [tokens] or [axes, tokens].  The outputs may be the
     inputs.  Returns (q_out, k_out) (k_out None without k)."""
+    import torch
     tokens, nq, dim = q.shape
     p = _i32(pos, "pos", rotary.axes * tokens)
     hq, hk, ok = _heads(q, "q"), None, None
     if q_out is None:
-        q_out = q.new_empty((tokens, nq, dim))
+        q_out = torch.empty((tokens, nq, dim), dtype=torch.bfloat16, device=q.device)
         oq = HeadsStruct(q_out.data_ptr(), nq * dim, dim, nq, 0)
     else:
         oq = _heads(q_out, "q_out")
@@ -692,7 +693,7 @@ def rotate(rotary: Rotary, q, pos, k=None, q_out=None, k_out=None, stream=None):
         if k.shape[0] != tokens or k.shape[2] != dim:
             raise ValueError("k: the same tokens and head size as q")
         if k_out is None:
-            k_out = k.new_empty((tokens, nk, dim))
+            k_out = torch.empty((tokens, nk, dim), dtype=torch.bfloat16, device=q.device)
             ok = HeadsStruct(k_out.data_ptr(), nk * dim, dim, nk, 0)
         else:
             ok = _heads(k_out, "k_out")
@@ -760,7 +761,8 @@ def kv_read(cache: KvCache, layer, seqs, first, cu, tokens: int, status=None, st
     shape = (tokens, cache.kv_heads, cache.head_dim)
     if layer is None:
         shape = (cache.layers, *shape)
-    out = [cache.k.new_empty(shape, dtype=torch.bfloat16) for _ in range(2)]
+    dev = cache.k.device
+    out = [torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in range(2)]
     _check(lib().dgt_kv_read(cache.s, -1 if layer is None else layer, _i32(seqs, "seqs"),
                              _i32(first, "first", batch), None if cu is None else _i32(cu, "cu", batch + 1), batch,
                              tokens, _ptr(out[0]), _ptr(out[1]), _ptr(status), _stream_on(cache.k, stream)), "dgt_kv_read")
@@ -791,7 +793,7 @@ def kv_attention(cache: KvCache, layer: int, q, seqs, cu=None, scale=None, windo
     if window < 0 or sinks < 0:
         raise ValueError("window and sinks: not negative")
     if out is None:
-        out = q.new_empty((tokens, heads, dim))
+        out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=q.device)
     elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
         raise ValueError("out: a contiguous bfloat16 tensor of q's shape")
     if lse is not None and (lse.numel() != tokens * heads or lse.dtype != torch.float32 or not lse.is_contiguous()):
@@ -813,7 +815,7 @@ def kv_reserve(cache: KvCache, seqs, count, start=None, status=None, stream=None
     import torch
     n = seqs.numel()
     if start is None:
-        start = seqs.new_empty(n)
+        start = torch.empty(n, dtype=torch.int32, device=seqs.device)
     _check(lib().dgt_kv_reserve(cache.s, _i32(seqs, "seqs"), _i32(count, "count", n), n,
                                 _i32(start, "start", n), _ptr(cache.ws), cache.ws.numel(), _ptr(status),
                                 _stream_on(cache.k, stream)), "dgt_kv_reserve")

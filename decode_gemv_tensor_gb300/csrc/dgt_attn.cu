@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) k_kv_attention(AttnArgs a) {
     __shared__ float stat[AT_WARPS][RT][3];
     __shared__ float rowstat[RT][3];
     __shared__ float rowfac[RT];
+    __shared__ float2 joined[RT];
     __shared__ uint64_t usum[AT_WARPS];
     __shared__ uint32_t wsum[AT_WARPS];
     __shared__ int last_flag;
@@ -514,7 +515,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) k_kv_attention(AttnArgs a) {
             __syncthreads();
             if (!last_flag) continue;
             __threadfence();
-            join_parts<D, Cfg::PART>(a, s, r.h, c0, c1, tid, AT_WARPS * 32, W_LOG2);
+            join_parts<D, Cfg::PART>(a, s, r.h, c0, c1, tid, AT_WARPS * 32, W_LOG2, joined, [] { __syncthreads(); });
         }
         more = false;   // everything of this chunk has been taken
     }

@@ -197,27 +197,74 @@ __device__ __forceinline__ void write_out(const AttnArgs &a, const Slot &s, uint
     if (a.lse && d == 0) a.lse[at] = none ? -INFINITY : (M + __log2f(L)) * LN2;
 }
 
-// The parts of a segment's units [sa, sb), left by the CTAs that hold them
-// (two parts of PART floats a CTA: a row's M, MU, L, then its numerators),
-// added in page order by `threads` threads, this one number t.
-template <uint32_t D, uint32_t PART>
+// The parts of a segment, left by the CTAs c0..c1 that hold its units (two
+// parts of PART floats a CTA: a row's M, MU, L, then its numerators), added in
+// page order by `threads` threads, this one number t, which all call it; sync
+// is their barrier and `rowof` a shared array of a tile's rows.  First a thread
+// per row finds the row's maxima and denominator, then four elements at a time
+// are weighted and added, several loads in flight.
+template <uint32_t D, uint32_t PART, typename Sync>
 __device__ __forceinline__ void join_parts(const AttnArgs &a, const Slot &s, uint32_t h, uint64_t c0, uint64_t c1,
-                                           uint32_t t, uint32_t threads, float wlog2) {
-    for (uint32_t i = t; i < s.rows * D; i += threads) {
-        const uint32_t row = i / D, d = i % D;
-        auto at = [&](uint64_t cta) { return a.part + (2 * cta + (cta == c0 ? 1 : 0)) * PART + row * (D + 4); };
-        float M = -INFINITY, MU = -INFINITY, L = 0.0f, v = 0.0f;
-        for (uint64_t k = c0; k <= c1; k++) {
-            const float4 st = __ldcg(reinterpret_cast<const float4 *>(at(k)));
-            M = fmaxf(M, st.x);
+                                           uint32_t t, uint32_t threads, float wlog2, float2 *rowof, Sync sync) {
+    const uint32_t parts = (uint32_t)(c1 - c0 + 1);
+    // part 0 is the one that begins the segment, at the end of its CTA's work
+    auto at = [&](uint32_t k, uint32_t row) { return a.part + (2 * (c0 + k) + (k == 0 ? 1 : 0)) * PART + row * (D + 4); };
+    for (uint32_t row = t; row < s.rows; row += threads) {
+        float M = -INFINITY, MU = -INFINITY, L = 0.0f;
+#pragma unroll 4
+        for (uint32_t k = 0; k < parts; k++) {
+            const float4 st = __ldcg(reinterpret_cast<const float4 *>(at(k, row)));
+            const float m = fmaxf(M, st.x);
+            L = L * ex2(M - finite_base(m)) + st.z * ex2(st.x - finite_base(m));
+            M = m;
             MU = fmaxf(MU, st.y);
         }
-        for (uint64_t k = c0; k <= c1; k++) {
-            const float4 st = __ldcg(reinterpret_cast<const float4 *>(at(k)));
-            L += st.z * ex2(st.x - finite_base(M));
-            v += __ldcg(at(k) + 4 + d) * ex2(st.y - finite_base(MU));
+        const bool none = M == -INFINITY && L == 0.0f;
+        rowof[row] = make_float2(finite_base(MU), none ? 0.0f : ex2(finite_base(MU) - finite_base(M) - wlog2) / L);
+        if (a.lse) {
+            const uint32_t flat = s.row0 + row;
+            a.lse[(uint64_t)(s.tok0 + flat / a.group) * a.q_heads + h * a.group + flat % a.group] =
+                none ? -INFINITY : (M + __log2f(L)) * LN2;
         }
-        write_out<D>(a, s, h, row, d, v, M, MU, L, wlog2);
+    }
+    sync();
+    constexpr uint32_t Q = D / 4, B = 4;   // B elements of four in flight
+    const uint32_t all = s.rows * Q;
+    for (uint32_t i0 = t; i0 < all; i0 += B * threads) {
+        float v[B][4] = {};
+        float2 ro[B];
+#pragma unroll
+        for (uint32_t b = 0; b < B; b++) ro[b] = rowof[min(i0 + b * threads, all - 1) / Q];
+#pragma unroll 2
+        for (uint32_t k = 0; k < parts; k++) {
+            float mu[B];
+            float4 x[B];
+#pragma unroll
+            for (uint32_t b = 0; b < B; b++) {
+                const uint32_t i = min(i0 + b * threads, all - 1);
+                const float *p = at(k, i / Q);
+                mu[b] = __ldcg(p + 1);
+                x[b] = __ldcg(reinterpret_cast<const float4 *>(p + 4 + (i % Q) * 4));
+            }
+#pragma unroll
+            for (uint32_t b = 0; b < B; b++) {
+                const float f = ex2(mu[b] - ro[b].x);
+                v[b][0] += x[b].x * f, v[b][1] += x[b].y * f, v[b][2] += x[b].z * f, v[b][3] += x[b].w * f;
+            }
+        }
+#pragma unroll
+        for (uint32_t b = 0; b < B; b++) {
+            const uint32_t i = i0 + b * threads;
+            if (i >= all) break;
+            const uint32_t flat = s.row0 + i / Q;
+            const uint64_t o = (uint64_t)(s.tok0 + flat / a.group) * a.q_heads + h * a.group + flat % a.group;
+            uint32_t w[2];
+#pragma unroll
+            for (int e = 0; e < 2; e++)
+                w[e] = (uint32_t)f32_to_bf16_rne(v[b][2 * e] * ro[b].y) |
+                       (uint32_t)f32_to_bf16_rne(v[b][2 * e + 1] * ro[b].y) << 16;
+            *reinterpret_cast<uint2 *>(a.out + o * D + (i % Q) * 4) = make_uint2(w[0], w[1]);
+        }
     }
 }
 

@@ -11,10 +11,12 @@
 // memory where the scores were, and four warps turn value pages into fp16
 // operand tiles once for all the rows of a CTA.
 //
-// Per CTA two tiles of 128 rows (head_dim 256: one) share every page: while
-// one tile's 128 threads (a row each) take exponentials, the tensor cores work
-// on the other.  The numerator's reference maximum moves only when a row has
-// grown by 2^8 past it, so the accumulators are rarely rescaled.
+// Per CTA two tiles of 128 rows (head_dim 256: one) share every page.  Each has
+// two score buffers in tensor memory, so that the scores of the page after
+// next are made while its 128 threads (a row each) take exponentials, and the
+// threads never wait for a product.  The numerator's reference maximum moves
+// only when a row has grown by 2^8 past it, so the accumulators are rarely
+// rescaled.
 #include "dgt_attn.cuh"
 
 #include "dgt_tc.cuh"
@@ -23,29 +25,52 @@ namespace dgt {
 
 constexpr float PR_W_LOG2 = 4.0f;    // weights at the reference; 2^8 above it they reach 2^12
 constexpr float PR_GROW = 8.0f;
-constexpr uint32_t PR_WARPS = 14;    // 0-7 rows, 8-11 values to fp16, 12 matrix instructions, 13 copies
-constexpr uint32_t PR_META = 8;
+constexpr uint32_t PR_WARPS = 15;    // 0-7 rows, 8-11 values to fp16, 12-13 matrix instructions, 14 copies
+constexpr uint32_t PR_CONV = 128;    // threads that convert values
+constexpr uint32_t PR_META = 16;
 
 template <uint32_t D>
 struct PromptCfg {
-    static constexpr uint32_t NSTR = D <= 128 ? 2 : 1;   // row tiles of 128
-    static constexpr uint32_t TP = D <= 128 ? 2 : 1;     // pages of a key tile
-    static constexpr uint32_t TN = KV_P * TP, RT = 128 * NSTR;
-    static constexpr uint32_t RB = D < 128 ? 64 : 128, PAN = D / RB;   // operand row bytes, panels
-    static constexpr uint32_t PB = KV_P * D;                           // bytes of a page's block
-    static constexpr uint32_t KS = 3, VS = 2, WS = 2;                  // stages: keys, values, fp16 values
-    static constexpr uint32_t QP = 128 * D;                            // one part of a row tile
-    static constexpr uint32_t q = 0, k = q + NSTR * 2 * QP, v = k + KS * TP * PB, w = v + VS * TP * PB,
-                              bytes = w + WS * TP * PB * 2 + 1024;
-    static constexpr uint32_t SCOL = 256, SSTEP = TN;                  // score columns: a buffer of TN per tile
+    static constexpr uint32_t NSTR = D <= 128 ? 2 : 1, RT = 128 * NSTR;   // row tiles of 128
+    static constexpr uint32_t RB = D < 128 ? 64 : 128, PAN = D / RB;       // operand row bytes, panels
+    static constexpr uint32_t PB = KV_P * D;                               // bytes of a page's block
+    static constexpr uint32_t KS = D <= 128 ? 6 : 3, VS = D <= 128 ? 4 : 2, WS = VS;   // stages: keys, values, fp16 values
+    static constexpr uint32_t QP = 128 * D;                                // one part of a row tile
+    static constexpr uint32_t q = 0, k = q + NSTR * 2 * QP, v = k + KS * PB, w = v + VS * PB,
+                              bytes = w + WS * PB * 2 + 1024;
+    static constexpr uint32_t SCOL = 256;   // score columns: two buffers of 64 per row tile
     static constexpr uint32_t PART = RT * (D + 4);
 };
 
-// What a key tile is: its pages' scales (a page that is not there: used 0).
-struct TileMeta {
-    float ks[2], vs[2];
-    uint32_t used[2];
+// A place in a ring of barriers: stage and phase.
+struct Ring {
+    uint32_t st, ph;
+    __device__ __forceinline__ void next(uint32_t n) {
+        if (++st == n) st = 0, ph ^= 1;
+    }
 };
+
+// A page's scales (used 0: it is not there).
+struct PageMeta {
+    float ks, vs;
+    uint32_t used;
+};
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ void fma2(float a0, float a1, float b, float c, float &d0, float &d1) {
+    asm("{\n\t.reg .b64 x, y, z, r;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %5};\n\t"
+        "fma.rn.f32x2 r, x, y, z;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1) {
+    asm("{\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(d0), "+f"(d1)
+        : "f"(a0), "f"(a1));
+}
 
 __device__ __forceinline__ void bar_rows() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -76,31 +101,36 @@ __device__ __forceinline__ void split16(const uint32_t (&bits)[8], float f0, flo
 template <uint32_t D>
 __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
     using Cfg = PromptCfg<D>;
-    constexpr uint32_t NSTR = Cfg::NSTR, TP = Cfg::TP, TN = Cfg::TN, RT = Cfg::RT, RB = Cfg::RB, PAN = Cfg::PAN,
-                       PB = Cfg::PB, QP = Cfg::QP, KS = Cfg::KS, VS = Cfg::VS, WS = Cfg::WS;
+    constexpr uint32_t NSTR = Cfg::NSTR, RT = Cfg::RT, RB = Cfg::RB, PAN = Cfg::PAN, PB = Cfg::PB, QP = Cfg::QP,
+                       KS = Cfg::KS, VS = Cfg::VS, WS = Cfg::WS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t kfull[KS], kfree[KS], vfull[VS], vfree[VS], wfull[WS], wfree[WS];
-    __shared__ __align__(8) uint64_t sfull[2], pfull[2], ofull[2], qfull[2], mfull[PR_META], drained;
-    __shared__ TileMeta meta[PR_META];
+    __shared__ __align__(8) uint64_t sfull[4], pfull[4], ofull[2], ofin[2], qfull[2], mfull[PR_META], drained;
+    __shared__ PageMeta meta[PR_META];
+    __shared__ float2 joined[RT];
     __shared__ Slot slots[AT_CHUNK];
     __shared__ uint64_t usum[PR_WARPS];
     __shared__ uint32_t wsum[PR_WARPS];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag, last_flag;
-    const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the warp's number out of a shuffle: the compiler then knows that it is the warp's
+    const uint32_t tid = threadIdx.x, warp = __shfl_sync(DGT_FULL, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
     if (tid == 0) {
-        for (uint32_t i = 0; i < KS; i++) mbar_init(smem_u32(&kfull[i]), 1), mbar_init(smem_u32(&kfree[i]), 1);
-        for (uint32_t i = 0; i < VS; i++) mbar_init(smem_u32(&vfull[i]), 1), mbar_init(smem_u32(&vfree[i]), 4);
-        for (uint32_t i = 0; i < WS; i++) mbar_init(smem_u32(&wfull[i]), 4), mbar_init(smem_u32(&wfree[i]), 1);
-        for (uint32_t i = 0; i < 2; i++) {
+        for (uint32_t i = 0; i < KS; i++) mbar_init(smem_u32(&kfull[i]), 1), mbar_init(smem_u32(&kfree[i]), NSTR);
+        for (uint32_t i = 0; i < VS; i++) mbar_init(smem_u32(&vfull[i]), 1), mbar_init(smem_u32(&vfree[i]), PR_CONV / 32);
+        for (uint32_t i = 0; i < WS; i++) mbar_init(smem_u32(&wfull[i]), PR_CONV / 32), mbar_init(smem_u32(&wfree[i]), NSTR);
+        for (uint32_t i = 0; i < 4; i++) {
             mbar_init(smem_u32(&sfull[i]), 1);
             mbar_init(smem_u32(&pfull[i]), 4);
+        }
+        for (uint32_t i = 0; i < 2; i++) {
             mbar_init(smem_u32(&ofull[i]), 1);
+            mbar_init(smem_u32(&ofin[i]), 1);
             mbar_init(smem_u32(&qfull[i]), 4);
         }
         for (uint32_t i = 0; i < PR_META; i++) mbar_init(smem_u32(&mfull[i]), 1);
-        mbar_init(smem_u32(&drained), 1);
+        mbar_init(smem_u32(&drained), NSTR);
         abort_flag = 0;
         fence_mbarrier_init();
     }
@@ -124,9 +154,10 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
     const uint64_t ua = C ? blockIdx.x * U / C : 0, ub = blockIdx.x < C ? (blockIdx.x + 1) * U / C : 0;
 
     bool dead = false;   // a wait ran out, here or elsewhere in the CTA: no more work from this warp
-    // a whole warp's wait
-    auto wait = [&](uint64_t &bar, uint32_t parity) {
-        if (!dead && !__any_sync(DGT_FULL, wait_or_abort(smem_u32(&bar), parity, abortp, a.spin))) {
+    // a whole warp's wait: mostly the phase has ended already
+    auto wait_at = [&](uint32_t bar, uint32_t parity) {
+        if (__all_sync(DGT_FULL, !dead && a.spin && mbar_try_wait(bar, parity))) return true;
+        if (!dead && !__any_sync(DGT_FULL, wait_or_abort(bar, parity, abortp, a.spin))) {
             dead = true;
             if (lane == 0) set_status(a.status, DGT_ERR_TIMEOUT);
             *abortp = 1;
@@ -134,8 +165,10 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
         __syncwarp();   // the lane that saw the phase end has seen it for all
         return !dead;
     };
-    uint32_t it = 0;               // key tiles so far, the same in every role
-    uint32_t qc[2] = {0, 0};       // per row tile: segments, key tiles so far
+    auto wait = [&](uint64_t &bar, uint32_t parity) { return wait_at(smem_u32(&bar), parity); };
+    Ring kr{0, 0}, wr{0, 0};       // the matrix instructions' next stages of keys and fp16 values
+    uint32_t it = 0;               // pages so far, the same in every role
+    uint32_t qc[2] = {0, 0};       // per row tile: segments, pages so far
     uint32_t sc[2] = {0, 0};
     uint32_t kissued = 0, vissued = 0;   // the copying warp's items
 
@@ -153,16 +186,16 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
             u += r.pe - r.pa;
             const Slot &s = slots[r.slot];
             const uint32_t n = s.per_head();
-            const uint32_t T = s.np ? (r.pe - r.pa + TP - 1) / TP : 0;
+            const uint32_t T = s.np ? r.pe - r.pa : 0;
             const uint32_t ns = NSTR == 2 && s.rows > 128 ? 2 : 1;   // row tiles that hold rows
 
-            if (warp == 13) {
+            if (warp == 14) {
                 // ---- copies
                 int pid = -1;
                 float ks = 0.0f, vs = 0.0f;
                 for (uint32_t j = 0; j < T && !dead; j++) {
-                    const uint32_t x = r.pa + j * TP, c = it + j;
-                    if ((j * TP) % 32 == 0) {
+                    const uint32_t x = r.pa + j, c = it + j;
+                    if (j % 32 == 0) {
                         pid = -1;
                         if (x + lane < r.pe) {
                             const int32_t p = a.c.table[(uint64_t)s.seq * a.c.max_pages + s.page_index(x + lane)];
@@ -177,129 +210,114 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                         }
                     }
                     if (c >= KS && !wait(kfree[c % KS], (c / KS - 1) & 1u)) break;
-                    uint64_t bi[TP];
-                    uint32_t have = 0;
-#pragma unroll
-                    for (uint32_t p = 0; p < TP; p++) {
-                        const uint32_t from = (j * TP + p) % 32;
-                        const int id = __shfl_sync(DGT_FULL, pid, from);
-                        const float kk = __shfl_sync(DGT_FULL, ks, from), vv = __shfl_sync(DGT_FULL, vs, from);
-                        bi[p] = kv_block(a.c, a.layer, id < 0 ? 0u : (uint32_t)id, r.h);
-                        if (id >= 0) have |= 1u << p;
-                        if (lane == 0) {
-                            TileMeta &m = meta[c % PR_META];
-                            m.ks[p] = id < 0 ? 1.0f : kk, m.vs[p] = id < 0 ? 1.0f : vv, m.used[p] = id >= 0;
-                        }
-                    }
+                    const int id = __shfl_sync(DGT_FULL, pid, j % 32);
+                    const float kk = __shfl_sync(DGT_FULL, ks, j % 32), vv = __shfl_sync(DGT_FULL, vs, j % 32);
+                    const uint64_t bi = kv_block(a.c, a.layer, id < 0 ? 0u : (uint32_t)id, r.h);
+                    const uint32_t kb = smem_u32(&kfull[c % KS]), vb = smem_u32(&vfull[c % VS]);
                     if (lane == 0) {
-                        const uint32_t bytes = __popc(have) * PB;
+                        PageMeta &m = meta[c % PR_META];
+                        m.ks = id < 0 ? 1.0f : kk, m.vs = id < 0 ? 1.0f : vv, m.used = id >= 0;
                         mbar_arrive(smem_u32(&mfull[c % PR_META]));
-                        const uint32_t kb = smem_u32(&kfull[c % KS]);
-                        mbar_arrive_expect_tx(kb, bytes);
-#pragma unroll
-                        for (uint32_t p = 0; p < TP; p++)
-                            if ((have >> p) & 1u)
-                                bulk_g2s(base + Cfg::k + ((c % KS) * TP + p) * PB, a.c.k + bi[p] * PB, PB, kb);
+                        if (id >= 0) {
+                            mbar_arrive_expect_tx(kb, PB);
+                            bulk_g2s(base + Cfg::k + (c % KS) * PB, a.c.k + bi * PB, PB, kb);
+                        } else {
+                            mbar_arrive(kb);
+                        }
                     }
                     kissued = c + 1;
                     if (c >= VS && !wait(vfree[c % VS], (c / VS - 1) & 1u)) break;
                     if (lane == 0) {
-                        const uint32_t bytes = __popc(have) * PB, vb = smem_u32(&vfull[c % VS]);
-                        mbar_arrive_expect_tx(vb, bytes);
-#pragma unroll
-                        for (uint32_t p = 0; p < TP; p++)
-                            if ((have >> p) & 1u)
-                                bulk_g2s(base + Cfg::v + ((c % VS) * TP + p) * PB, a.c.v + bi[p] * PB, PB, vb);
+                        if (id >= 0) {
+                            mbar_arrive_expect_tx(vb, PB);
+                            bulk_g2s(base + Cfg::v + (c % VS) * PB, a.c.v + bi * PB, PB, vb);
+                        } else {
+                            mbar_arrive(vb);
+                        }
                     }
                     vissued = c + 1;
                     __syncwarp();
                 }
-            } else if (warp == 12) {
-                // ---- matrix instructions, one lane
-                constexpr uint32_t idesc_s = (1u << 4) | ((TN >> 3) << 17) | ((128u >> 4) << 24);
+            } else if (warp >= 12) {
+                // ---- matrix instructions, a warp for each row tile.  The whole warp walks the pages, one
+                // lane issues: page and buffer numbers out of shuffles keep the descriptors in uniform
+                // registers (computed by the issuing lane alone they cost 70 cycles an instruction, twice
+                // what it runs).
+                constexpr uint32_t idesc_s = (1u << 4) | ((KV_P >> 3) << 17) | ((128u >> 4) << 24);
                 constexpr uint32_t idesc_o = (1u << 4) | ((D >> 3) << 17) | ((128u >> 4) << 24);
+                const uint32_t t = warp - 12;
+                const bool leader = elect_one();
+                const uint32_t tmu = __shfl_sync(DGT_FULL, tm, 0);
                 auto desc = [&](uint32_t addr) { return RB == 128 ? sw128_desc(addr) : sw64_desc(addr); };
-                auto scores = [&](uint32_t t, uint32_t c, uint32_t col) {
-                    if (lane == 0) {
-                        const uint32_t kt = base + Cfg::k + (c % KS) * TP * PB;
-#pragma unroll
-                        for (uint32_t part = 0; part < 2; part++)
-#pragma unroll
-                            for (uint32_t pan = 0; pan < PAN; pan++) {
-                                const uint64_t ad = desc(base + Cfg::q + (2 * t + part) * QP + pan * 128 * RB);
-                                const uint64_t bd = desc(kt + pan * KV_P * RB);
-#pragma unroll
-                                for (uint32_t i = 0; i < RB / 32; i++)
-                                    mma_e4m3(tm + col, ad + 2 * i, bd + 2 * i, idesc_s, part + pan + i > 0 ? 1u : 0u);
-                            }
-                    }
+                auto commit = [&](uint32_t bar) {
+                    if (leader) mma_commit(bar);
                 };
-                auto values = [&](uint32_t t, uint32_t c, uint32_t col, bool accumulate) {
-                    if (lane == 0) {
+                const uint32_t kb0 = smem_u32(kfull), kf0 = smem_u32(kfree), wb0 = smem_u32(wfull), wf0 = smem_u32(wfree);
+                const uint32_t sf0 = smem_u32(sfull) + 16 * t, pf0 = smem_u32(pfull) + 16 * t;
+                const uint32_t scol = tmu + Cfg::SCOL + 2 * t * KV_P;
+                const uint64_t qd = desc(base + Cfg::q + 2 * t * QP), kd = desc(base + Cfg::k);
+                const uint64_t wd = sw128_desc(base + Cfg::w);
+                // scores with the keys' stage st into buffer n
+                auto scores = [&](uint32_t st, uint32_t n) {
 #pragma unroll
-                        for (uint32_t p = 0; p < TP; p++) {
-                            const uint64_t bd = sw128_desc(base + Cfg::w + ((c % WS) * TP + p) * PB * 2);
+                    for (uint32_t part = 0; part < 2; part++)
 #pragma unroll
-                            for (uint32_t i = 0; i < 4; i++)
-                                mma_f16_ta(tm + t * D, tm + col + p * 32 + i * 8, bd + 2 * i, idesc_o,
-                                           accumulate || p + i > 0 ? 1u : 0u);
-                        }
-                    }
+                        for (uint32_t pan = 0; pan < PAN; pan++)
+#pragma unroll
+                            for (uint32_t i = 0; i < RB / 32; i++)
+                                if (leader)
+                                    mma_e4m3(scol + n * KV_P, qd + (part * QP + pan * 128 * RB) / 16 + 2 * i,
+                                             kd + (st * PB + pan * KV_P * RB) / 16 + 2 * i, idesc_s,
+                                             part + pan + i > 0 ? 1u : 0u);
+                    commit(sf0 + 8 * n);
+                    commit(kf0 + 8 * st);
                 };
-                auto commit = [&](uint64_t &bar) {
-                    if (lane == 0) mma_commit(smem_u32(&bar));
-                    __syncwarp();
-                };
-                if (NSTR == 2) {
-                    if (T && wait(kfull[it % KS], (it / KS) & 1u)) {
-                        for (uint32_t t = 0; t < ns; t++) {
-                            if (!wait(qfull[t], qc[t] & 1u)) break;
-                            tc_fence_after();
-                            scores(t, it, Cfg::SCOL + t * Cfg::SSTEP);
-                            commit(sfull[t]);
-                        }
-                        commit(kfree[it % KS]);
+                if (t < ns) {
+                    // The pipe runs a warp's instructions in order: a buffer's next scores are issued behind
+                    // the products that read its weights.
+                    for (uint32_t j = 0; j < 2 && j < T; j++) {
+                        const uint32_t x = __shfl_sync(DGT_FULL, kr.st | ((sc[t] + j) & 1) << 8, 0);
+                        if (!wait_at(kb0 + 8 * kr.st, kr.ph) || (j == 0 && !wait(qfull[t], qc[t] & 1u))) break;
+                        tc_fence_after();
+                        scores(x & 255, x >> 8);
+                        kr.next(KS);
                     }
                     for (uint32_t j = 0; j < T && !dead; j++) {
-                        const uint32_t c = it + j;
-                        for (uint32_t t = 0; t < ns && !dead; t++) {
-                            if (!wait(pfull[t], (sc[t] + j) & 1u) || (t == 0 && !wait(wfull[c % WS], (c / WS) & 1u))) break;
-                            tc_fence_after();
-                            values(t, c, Cfg::SCOL + t * Cfg::SSTEP, j > 0);
-                            commit(ofull[t]);
-                            if (j + 1 < T) {
-                                if (t == 0 && !wait(kfull[(c + 1) % KS], ((c + 1) / KS) & 1u)) break;
-                                scores(t, c + 1, Cfg::SCOL + t * Cfg::SSTEP);
-                                commit(sfull[t]);
-                            }
-                        }
-                        if (dead) break;
-                        commit(wfree[c % WS]);
-                        if (j + 1 < T) commit(kfree[(c + 1) % KS]);
-                    }
-                } else {
-                    // one row tile, two score buffers: the next tile's scores before this one's values
-                    if (T && wait(kfull[it % KS], (it / KS) & 1u) && wait(qfull[0], qc[0] & 1u)) {
+                        const uint32_t n = sc[t] + j;
+                        const uint32_t x = __shfl_sync(DGT_FULL, kr.st | wr.st << 8 | (n & 1) << 16 | (j ? 1u << 24 : 0u), 0);
+                        const uint32_t ks = x & 255, ws = x >> 8 & 255, nb = x >> 16 & 1, more = x >> 24;
+                        if ((j + 2 < T && !wait_at(kb0 + 8 * ks, kr.ph)) || !wait_at(wb0 + 8 * ws, wr.ph) ||
+                            !wait_at(pf0 + 8 * nb, (n >> 1) & 1u))
+                            break;
                         tc_fence_after();
-                        scores(0, it, Cfg::SCOL + (it & 1) * Cfg::SSTEP);
-                        commit(sfull[it & 1]);
-                        commit(kfree[it % KS]);
-                    }
-                    for (uint32_t j = 0; j < T && !dead; j++) {
-                        const uint32_t c = it + j, b = c & 1;
-                        if (j + 1 < T) {
-                            if (!wait(kfull[(c + 1) % KS], ((c + 1) / KS) & 1u)) break;
-                            scores(0, c + 1, Cfg::SCOL + (1 - b) * Cfg::SSTEP);
-                            commit(sfull[1 - b]);
-                            commit(kfree[(c + 1) % KS]);
+#pragma unroll
+                        for (uint32_t i = 0; i < 4; i++)
+                            if (leader)
+                                mma_f16_ta(tmu + t * D, scol + nb * KV_P + i * 8, wd + ws * (PB * 2 / 16) + 2 * i, idesc_o,
+                                           i > 0 ? 1u : more);
+                        commit(smem_u32(&ofull[t]));
+                        commit(wf0 + 8 * ws);
+                        wr.next(WS);
+                        if (j + 2 < T) {
+                            scores(ks, nb);
+                            kr.next(KS);
+                        } else if (j + 1 == T) {
+                            commit(smem_u32(&ofin[t]));
                         }
-                        if (!wait(pfull[b], (c >> 1) & 1u) || !wait(wfull[c % WS], (c / WS) & 1u)) break;
-                        tc_fence_after();
-                        values(0, c, Cfg::SCOL + b * Cfg::SSTEP, j > 0);
-                        commit(ofull[0]);
-                        commit(wfree[c % WS]);
+                    }
+                } else if (t < NSTR) {
+                    // no rows: give the pages back as they come
+                    for (uint32_t j = 0; j < T; j++) {
+                        if (!wait_at(kb0 + 8 * kr.st, kr.ph) || !wait_at(wb0 + 8 * wr.st, wr.ph)) break;
+                        if (leader) {
+                            mbar_arrive(kf0 + 8 * kr.st);
+                            mbar_arrive(wf0 + 8 * wr.st);
+                        }
+                        kr.next(KS);
+                        wr.next(WS);
                     }
                 }
+                __syncwarp();
             } else if (warp >= 8) {
                 // ---- value pages to fp16 operand tiles: rows of 64 tokens, 128-byte swizzle
                 const uint32_t ct = tid - 256;
@@ -307,20 +325,23 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                     const uint32_t c = it + j;
                     if (!wait(vfull[c % VS], (c / VS) & 1u)) break;
                     if (c >= WS && !wait(wfree[c % WS], (c / WS - 1) & 1u)) break;
-                    const TileMeta &m = meta[c % PR_META];
+                    const uint32_t src = base + Cfg::v + (c % VS) * PB, dst = base + Cfg::w + (c % WS) * PB * 2;
+                    const bool used = meta[c % PR_META].used != 0;
+                    // 16 bytes a thread: row at / 4, its tokens 16 (at % 4) ..
+                    constexpr uint32_t B = 4;
+#pragma unroll 1
+                    for (uint32_t i0 = ct; i0 < D * 4; i0 += B * PR_CONV) {
+                        uint4 x[B];
 #pragma unroll
-                    for (uint32_t p = 0; p < TP; p++) {
-                        const uint32_t src = base + Cfg::v + ((c % VS) * TP + p) * PB;
-                        const uint32_t dst = base + Cfg::w + ((c % WS) * TP + p) * PB * 2;
-                        const bool used = m.used[p] != 0;
-#pragma unroll 4
-                        for (uint32_t i = ct; i < D * 4; i += 128) {
-                            const uint32_t row = i >> 2, q = i & 3;
-                            uint4 x = make_uint4(0, 0, 0, 0);
-                            if (used) x = lds128(src + row * KV_P + q * 16);
-                            const uint32_t o = dst + row * 128;
-                            sts128(o + (((2 * q) ^ (row & 7)) << 4), e4m3_lo(x.x), e4m3_hi(x.x), e4m3_lo(x.y), e4m3_hi(x.y));
-                            sts128(o + (((2 * q + 1) ^ (row & 7)) << 4), e4m3_lo(x.z), e4m3_hi(x.z), e4m3_lo(x.w), e4m3_hi(x.w));
+                        for (uint32_t i = 0; i < B; i++) {
+                            x[i] = make_uint4(0, 0, 0, 0);
+                            if (used) x[i] = lds128(src + (i0 + i * PR_CONV) * 16);
+                        }
+#pragma unroll
+                        for (uint32_t i = 0; i < B; i++) {
+                            const uint32_t at = i0 + i * PR_CONV, row = at >> 2, q = at & 3, o = dst + row * 128;
+                            sts128(o + (((2 * q) ^ (row & 7)) << 4), e4m3_lo(x[i].x), e4m3_hi(x[i].x), e4m3_lo(x[i].y), e4m3_hi(x[i].y));
+                            sts128(o + (((2 * q + 1) ^ (row & 7)) << 4), e4m3_lo(x[i].z), e4m3_hi(x[i].z), e4m3_lo(x[i].w), e4m3_hi(x[i].w));
                         }
                     }
                     fence_proxy_async_smem();
@@ -343,13 +364,18 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                     const uint16_t *qp = a.q.data + (int64_t)(s.tok0 + flat / a.group) * a.q.token_stride +
                                          (int64_t)(r.h * a.group + flat % a.group) * a.q.head_stride;
                     uint32_t top = 0;
-                    if (live)
-#pragma unroll 4
-                        for (uint32_t i = 0; i < D / 8; i++) {
-                            const uint4 x = reinterpret_cast<const uint4 *>(qp)[i];
-                            top = max(top, max(max(x.x & 0x7FFFu, x.x >> 16 & 0x7FFFu), max(x.y & 0x7FFFu, x.y >> 16 & 0x7FFFu)));
-                            top = max(top, max(max(x.z & 0x7FFFu, x.z >> 16 & 0x7FFFu), max(x.w & 0x7FFFu, x.w >> 16 & 0x7FFFu)));
+                    uint4 x[16];   // 128 dimensions in flight
+#pragma unroll
+                    for (uint32_t d0 = 0; d0 < D; d0 += 128) {
+#pragma unroll
+                        for (uint32_t i = 0; i < (D < 128 ? D / 8 : 16); i++)
+                            x[i] = live ? reinterpret_cast<const uint4 *>(qp + d0)[i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (uint32_t i = 0; i < (D < 128 ? D / 8 : 16); i++) {
+                            top = max(top, max(max(x[i].x & 0x7FFFu, x[i].x >> 16 & 0x7FFFu), max(x[i].y & 0x7FFFu, x[i].y >> 16 & 0x7FFFu)));
+                            top = max(top, max(max(x[i].z & 0x7FFFu, x[i].z >> 16 & 0x7FFFu), max(x[i].w & 0x7FFFu, x[i].w >> 16 & 0x7FFFu)));
                         }
+                    }
                     top >>= 7;
                     // the largest element to [2^7, 2^8)
                     const bool bad = top == 255;
@@ -359,20 +385,26 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                     if (a.scale_log2 < 0.0f) f0 = -f0;
                     fac = bad ? __uint_as_float(0x7FC00000u) : ldexpf(fabsf(a.scale_log2), -up);
                     const uint32_t q0 = base + Cfg::q + 2 * t * QP, rr = row & 127;
-#pragma unroll 2
-                    for (uint32_t i = 0; i < D / 16; i++) {
-                        uint32_t bits[8] = {};
-                        if (live && !bad) {
-                            const uint4 x = reinterpret_cast<const uint4 *>(qp)[2 * i], y = reinterpret_cast<const uint4 *>(qp)[2 * i + 1];
-                            bits[0] = x.x, bits[1] = x.y, bits[2] = x.z, bits[3] = x.w;
-                            bits[4] = y.x, bits[5] = y.y, bits[6] = y.z, bits[7] = y.w;
+#pragma unroll
+                    for (uint32_t d0 = 0; d0 < D; d0 += 128) {
+                        if (D > 128) {
+#pragma unroll
+                            for (uint32_t i = 0; i < 16; i++)
+                                x[i] = live ? reinterpret_cast<const uint4 *>(qp + d0)[i] : make_uint4(0, 0, 0, 0);
                         }
-                        uint4 hi, lo;
-                        split16(bits, f0, f1, hi, lo);
-                        const uint32_t pan = i / (RB / 16), ch = i % (RB / 16);
-                        const uint32_t at = pan * 128 * RB + rr * RB + ((ch ^ (RB == 128 ? rr & 7 : (rr >> 1) & 3)) << 4);
-                        sts128(q0 + at, hi.x, hi.y, hi.z, hi.w);
-                        sts128(q0 + QP + at, lo.x, lo.y, lo.z, lo.w);
+#pragma unroll
+                        for (uint32_t i = 0; i < (D < 128 ? D : 128) / 16; i++) {
+                            uint32_t bits[8] = {x[2 * i].x, x[2 * i].y, x[2 * i].z, x[2 * i].w,
+                                                x[2 * i + 1].x, x[2 * i + 1].y, x[2 * i + 1].z, x[2 * i + 1].w};
+                            if (bad)
+#pragma unroll
+                                for (int e = 0; e < 8; e++) bits[e] = 0;
+                            uint4 hi, lo;
+                            split16(bits, f0, f1, hi, lo);
+                            const uint32_t at = d0 / 128 * 128 * RB + rr * RB + ((i ^ (RB == 128 ? rr & 7 : (rr >> 1) & 3)) << 4);
+                            sts128(q0 + at, hi.x, hi.y, hi.z, hi.w);
+                            sts128(q0 + QP + at, lo.x, lo.y, lo.z, lo.w);
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -381,58 +413,46 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                 const int32_t pf = s.pos0 + (int32_t)(s.row0 / a.group);
                 const int32_t pl = s.pos0 + (int32_t)((s.row0 + s.rows - 1) / a.group);
                 for (uint32_t j = 0; mine && j < T && !dead; j++) {
-                    const uint32_t c = it + j, sb = NSTR == 2 ? t : c & 1;
-                    const uint32_t sp = NSTR == 2 ? (sc[t] + j) & 1u : (c >> 1) & 1u;
-                    if (!wait(mfull[c % PR_META], (c / PR_META) & 1u) || !wait(sfull[sb], sp)) break;
+                    const uint32_t c = it + j, sn = sc[t] + j, sb = 2 * t + (sn & 1);
+                    if (!wait(mfull[c % PR_META], (c / PR_META) & 1u) || !wait(sfull[sb], (sn >> 1) & 1u)) break;
                     tc_fence_after();
-                    const uint32_t st = tm + tl + Cfg::SCOL + sb * Cfg::SSTEP;
-                    float f[TP], ev[TP], vsc[TP], tmx[TP];
-                    uint32_t see[TP][2];
-                    bool whole[TP];
-                    uint32_t sv[2][32];
-                    float mn = m, un = mu;
-#pragma unroll
-                    for (uint32_t p = 0; p < TP; p++) {
-                        const TileMeta &mt = meta[c % PR_META];
-                        const bool used = mt.used[p] != 0;
-                        f[p] = fac * mt.ks[p];
-                        vsc[p] = mt.vs[p];
-                        ev[p] = (float)((int)(__float_as_uint(vsc[p]) >> 23) - 127);
-                        // which of the page's 64 tokens the row sees
-                        const int32_t t0 = (int32_t)(s.page_index(r.pa + j * TP + p) * KV_P);
-                        whole[p] = used && t0 + (int32_t)KV_P - 1 <= pf &&
-                                   (!a.window || t0 > pl - (int32_t)a.window || (uint32_t)t0 + KV_P <= a.sinks);
-                        see[p][0] = see[p][1] = 0xFFFFFFFFu;
-                        if (!whole[p]) {
-                            const int32_t hi = used ? min(max(pos - t0 + 1, 0), 64) : 0;   // tokens [0, hi) are not ahead of the row
-                            const int32_t lo = a.window ? min(max(pos - (int32_t)a.window + 1 - t0, 0), 64) : 0;
-                            const int32_t sk = a.window ? min(max((int32_t)a.sinks - t0, 0), 64) : 0;
-                            const uint64_t one = 1ull;
-                            const uint64_t below_hi = hi >= 64 ? ~0ull : (one << hi) - 1;
-                            const uint64_t below_lo = lo >= 64 ? ~0ull : (one << lo) - 1;
-                            const uint64_t below_sk = sk >= 64 ? ~0ull : (one << sk) - 1;
-                            const uint64_t v = below_hi & (~below_lo | below_sk);
-                            see[p][0] = (uint32_t)v, see[p][1] = (uint32_t)(v >> 32);
-                        }
-                        tmem_ld32(st + p * KV_P, sv[0]);
-                        tmem_ld32(st + p * KV_P + 32, sv[1]);
-                        tmem_wait_ld();
-                        float mx = -INFINITY;
-                        if (whole[p]) {
-#pragma unroll
-                            for (int i = 0; i < 32; i++)
-                                mx = fmaxf(mx, fmaxf(__uint_as_float(sv[0][i]), __uint_as_float(sv[1][i])));
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; i++) {
-                                if ((see[p][0] >> i) & 1u) mx = fmaxf(mx, __uint_as_float(sv[0][i]));
-                                if ((see[p][1] >> i) & 1u) mx = fmaxf(mx, __uint_as_float(sv[1][i]));
-                            }
-                        }
-                        tmx[p] = mx == -INFINITY ? mx : mx * f[p];
-                        mn = fmaxf(mn, tmx[p]);
-                        un = fmaxf(un, tmx[p] + ev[p]);
+                    const uint32_t st = tm + tl + Cfg::SCOL + sb * KV_P;
+                    uint32_t sv[64];
+                    tmem_ld64(st, sv);
+                    // the page's factors, and which of its 64 tokens the row sees
+                    const PageMeta &mt = meta[c % PR_META];
+                    const float vs = mt.vs, ev = (float)((int)(__float_as_uint(vs) >> 23) - 127);
+                    float f = fac * mt.ks;
+                    if (f == 0.0f) f = 1e-30f;   // scores of zero, also for what is set to -inf below
+                    const bool used = mt.used != 0;
+                    const int32_t t0 = (int32_t)(s.page_index(r.pa + j) * KV_P);
+                    const bool whole = used && t0 + (int32_t)KV_P - 1 <= pf &&
+                                       (!a.window || t0 > pl - (int32_t)a.window || (uint32_t)t0 + KV_P <= a.sinks);
+                    uint64_t see = ~0ull;
+                    if (!whole) {
+                        const int32_t hi = used ? min(max(pos - t0 + 1, 0), 64) : 0;   // tokens [0, hi) are not ahead of the row
+                        const int32_t lo = a.window ? min(max(pos - (int32_t)a.window + 1 - t0, 0), 64) : 0;
+                        const int32_t sk = a.window ? min(max((int32_t)a.sinks - t0, 0), 64) : 0;
+                        const uint64_t below_hi = hi >= 64 ? ~0ull : (1ull << hi) - 1;
+                        const uint64_t below_lo = lo >= 64 ? ~0ull : (1ull << lo) - 1;
+                        const uint64_t below_sk = sk >= 64 ? ~0ull : (1ull << sk) - 1;
+                        see = below_hi & (~below_lo | below_sk);
                     }
+                    tmem_wait_ld();
+                    if (!whole) {
+#pragma unroll
+                        for (int i = 0; i < 64; i++)
+                            if (!((see >> i) & 1u)) sv[i] = 0xFF800000u;
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < 64; i += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(sv[i + k])), __uint_as_float(sv[i + 4 + k]));
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    const float tx = top == -INFINITY ? top : top * f;
+                    const float mn = fmaxf(m, tx), un = fmaxf(mu, tx + ev);
                     const float bm = finite_base(mn);
                     l *= ex2(m - bm);
                     m = mn;
@@ -440,11 +460,46 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                     const float ao = grow ? ex2(mu - un) : 1.0f;
                     if (grow) mu = un;
                     const float bu = finite_base(mu);
-                    if (j > 0 && __any_sync(DGT_FULL, grow)) {
-                        // this row tile's accumulators: the products of the tile before are done
-                        if (NSTR == 1 && !wait(ofull[0], (sc[0] + j - 1) & 1u)) break;
-                        tc_fence_after();
+                    // weights: the value's scale inside the exponent, and their sum freed of it
+                    const float lc = bm + ev - bu + PR_W_LOG2;
+                    const bool fast = __all_sync(DGT_FULL, fabsf(lc) < 40.0f && vs == vs && f == f);
+                    const float bb = fast ? lc - bm : -bm;
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
+                    for (int i = 0; i < 32; i++) {
+                        float u, v;
+                        fma2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]), f, bb, u, v);
+                        sv[2 * i] = __float_as_uint(ex2(u));
+                        sv[2 * i + 1] = __float_as_uint(ex2(v));
+                    }
+                    if (fast) {
+#pragma unroll
+                        for (int i = 0; i < 32; i++)
+                            add2(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], __uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
+                    } else {
+                        // scales that are not finite or far apart: weights and their sum one by one, and none
+                        // for a token that the row does not see, whatever its scales are
+                        const float cw = vs != vs ? vs : ex2(fminf(lc, 126.0f));
+#pragma unroll
+                        for (int i = 0; i < 64; i++) {
+                            const bool v = (see >> i) & 1u;
+                            if (v) sum[i & 3] += __uint_as_float(sv[i]);
+                            sv[i] = v ? __float_as_uint(__uint_as_float(sv[i]) * cw) : 0u;
+                        }
+                    }
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int i = 0; i < 32; i++) pk[i] = f16_pair(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
+                    tmem_st32(st, pk);
+                    const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    l += fast ? all * ex2(-lc) : all;
+                    if (j > 0 && __any_sync(DGT_FULL, grow)) {
+                        // The accumulators may move once the products of the page before are done.  Those of
+                        // the page before that are: this page's scores came behind them, so the phase is the
+                        // next of the barrier or the one just past.
+                        if (!wait(ofull[t], (sn - 1) & 1u)) break;
+                        tc_fence_after();
+#pragma unroll 1
                         for (uint32_t d0 = 0; d0 < D; d0 += 32) {
                             uint32_t o[32];
                             tmem_ld32(tm + tl + t * D + d0, o);
@@ -454,54 +509,6 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                             tmem_st32(tm + tl + t * D + d0, o);
                         }
                     }
-#pragma unroll
-                    for (uint32_t p = 0; p < TP; p++) {
-                        if (TP > 1) {
-                            tmem_ld32(st + p * KV_P, sv[0]);
-                            tmem_ld32(st + p * KV_P + 32, sv[1]);
-                            tmem_wait_ld();
-                        }
-                        const float lc = bm + ev[p] - bu + PR_W_LOG2;
-                        uint32_t pk[32];
-                        float sum = 0.0f;
-                        if (__all_sync(DGT_FULL, fabsf(lc) < 40.0f && vsc[p] == vsc[p])) {
-                            // weights with the value's scale inside the exponent, their sum without it
-                            const float b = lc - bm;
-#pragma unroll
-                            for (int h = 0; h < 2; h++)
-#pragma unroll
-                                for (int i = 0; i < 16; i++) {
-                                    float x = ex2(fmaf(__uint_as_float(sv[h][2 * i]), f[p], b));
-                                    float y = ex2(fmaf(__uint_as_float(sv[h][2 * i + 1]), f[p], b));
-                                    if (!whole[p]) {
-                                        x = (see[p][h] >> (2 * i)) & 1u ? x : 0.0f;
-                                        y = (see[p][h] >> (2 * i + 1)) & 1u ? y : 0.0f;
-                                    }
-                                    sum += x;
-                                    sum += y;
-                                    pk[16 * h + i] = f16_pair(x, y);
-                                }
-                            l += sum * ex2(-lc);
-                        } else {
-                            const float cw = vsc[p] != vsc[p] ? vsc[p] : ex2(fminf(lc, 126.0f));
-#pragma unroll
-                            for (int h = 0; h < 2; h++)
-#pragma unroll
-                                for (int i = 0; i < 16; i++) {
-                                    float w[2];
-#pragma unroll
-                                    for (int e = 0; e < 2; e++) {
-                                        const bool v = (see[p][h] >> (2 * i + e)) & 1u;
-                                        const float x = ex2(fmaf(__uint_as_float(sv[h][2 * i + e]), f[p], -bm));
-                                        sum += v ? x : 0.0f;
-                                        w[e] = v ? x * cw : 0.0f;
-                                    }
-                                    pk[16 * h + i] = f16_pair(w[0], w[1]);
-                                }
-                            l += sum;
-                        }
-                        tmem_st32(st + p * 32, pk);
-                    }
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -510,7 +517,7 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
 
                 // ---- the segment's end: this row's quotient, or its part
                 const bool complete = r.pa == 0 && r.pe == n;
-                if (mine && T) wait(ofull[t], (sc[t] + T - 1) & 1u);
+                if (mine && T) wait(ofin[t], qc[t] & 1u);
                 tc_fence_after();
                 float *part = a.part + (2 * (uint64_t)blockIdx.x + (r.pa == 0 ? 1 : 0)) * Cfg::PART + row * (D + 4);
                 const bool none = m == -INFINITY && l == 0.0f;
@@ -561,7 +568,7 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                     bar_rows();
                     if (last_flag) {
                         __threadfence();
-                        join_parts<D, Cfg::PART>(a, s, r.h, c0, c1, tid, 256, PR_W_LOG2);
+                        join_parts<D, Cfg::PART>(a, s, r.h, c0, c1, tid, 256, PR_W_LOG2, joined, bar_rows);
                     }
                 }
             }
@@ -571,14 +578,15 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
     }
 
     // copies land and matrix instructions end before shared and tensor memory are given back
-    if (warp == 13) {
+    if (warp == 14) {
         for (uint32_t i = kissued > KS ? kissued - KS : 0; i < kissued; i++)
             mbar_wait(smem_u32(&kfull[i % KS]), (i / KS) & 1u);
         for (uint32_t i = vissued > VS ? vissued - VS : 0; i < vissued; i++)
             mbar_wait(smem_u32(&vfull[i % VS]), (i / VS) & 1u);
     }
-    if (warp == 12 && lane == 0) {
-        mma_commit(smem_u32(&drained));
+    if (warp >= 12 && warp < 12 + NSTR) {
+        // committed by the lane that issued the instructions
+        if (elect_one()) mma_commit(smem_u32(&drained));
         mbar_wait(smem_u32(&drained), 0);
     }
     tc_fence_before();
