@@ -50,6 +50,12 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Two fp32 to bf16, nearest with ties to even.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 __device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.0f : m; }
 
 // Two e4m3 codes (the low or high half of w) as two fp16.
@@ -260,9 +266,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, const Slot &s, uin
             const uint64_t o = (uint64_t)(s.tok0 + flat / a.group) * a.q_heads + h * a.group + flat % a.group;
             uint32_t w[2];
 #pragma unroll
-            for (int e = 0; e < 2; e++)
-                w[e] = (uint32_t)f32_to_bf16_rne(v[b][2 * e] * ro[b].y) |
-                       (uint32_t)f32_to_bf16_rne(v[b][2 * e + 1] * ro[b].y) << 16;
+            for (int e = 0; e < 2; e++) w[e] = bf16x2(v[b][2 * e] * ro[b].y, v[b][2 * e + 1] * ro[b].y);
             *reinterpret_cast<uint2 *>(a.out + o * D + (i % Q) * 4) = make_uint2(w[0], w[1]);
         }
     }

@@ -74,28 +74,12 @@ __device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1) {
 
 __device__ __forceinline__ void bar_rows() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// Sixteen scaled query elements to their two e4m3 parts.
-__device__ __forceinline__ void split16(const uint32_t (&bits)[8], float f0, float f1, uint4 &hi, uint4 &lo) {
-    uint32_t h[4], l[4];
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        float x[4];
-        x[0] = bf16lo(bits[2 * j]) * f0 * f1, x[1] = bf16hi(bits[2 * j]) * f0 * f1;
-        x[2] = bf16lo(bits[2 * j + 1]) * f0 * f1, x[3] = bf16hi(bits[2 * j + 1]) * f0 * f1;
-        h[j] = l[j] = 0;
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-            const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * e], x[2 * e + 1]), __NV_SATFINITE,
-                                                                     __NV_E4M3);
-            const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
-            const __nv_fp8x2_storage_t r = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * e] - y.x, x[2 * e + 1] - y.y),
-                                                                     __NV_SATFINITE, __NV_E4M3);
-            h[j] |= (uint32_t)c << (16 * e);
-            l[j] |= (uint32_t)r << (16 * e);
-        }
-    }
-    hi = make_uint4(h[0], h[1], h[2], h[3]);
-    lo = make_uint4(l[0], l[1], l[2], l[3]);
+// Two query elements, scaled, to their two e4m3 parts (the low 16 bits).
+__device__ __forceinline__ void split2(uint32_t bits, float f0, float f1, uint32_t &hi, uint32_t &lo) {
+    const float x = bf16lo(bits) * f0 * f1, y = bf16hi(bits) * f0 * f1;
+    hi = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+    const float2 z = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));
+    lo = __nv_cvt_float2_to_fp8x2(make_float2(x - z.x, y - z.y), __NV_SATFINITE, __NV_E4M3);
 }
 
 template <uint32_t D>
@@ -361,50 +345,43 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                 const int32_t pos = live ? s.pos0 + (int32_t)(flat / a.group) : -1;
                 float m = -INFINITY, mu = -INFINITY, l = 0.0f, fac = 0.0f;
                 if (mine && T) {
-                    const uint16_t *qp = a.q.data + (int64_t)(s.tok0 + flat / a.group) * a.q.token_stride +
-                                         (int64_t)(r.h * a.group + flat % a.group) * a.q.head_stride;
+                    const uint4 *qp = reinterpret_cast<const uint4 *>(
+                        a.q.data + (int64_t)(s.tok0 + flat / a.group) * a.q.token_stride +
+                        (int64_t)(r.h * a.group + flat % a.group) * a.q.head_stride);
                     uint32_t top = 0;
-                    uint4 x[16];   // 128 dimensions in flight
+#pragma unroll 1
+                    for (uint32_t i0 = 0; i0 < D / 8; i0 += 8) {
+                        uint4 x[8];
 #pragma unroll
-                    for (uint32_t d0 = 0; d0 < D; d0 += 128) {
+                        for (uint32_t i = 0; i < 8; i++) x[i] = live ? qp[i0 + i] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                        for (uint32_t i = 0; i < (D < 128 ? D / 8 : 16); i++)
-                            x[i] = live ? reinterpret_cast<const uint4 *>(qp + d0)[i] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                        for (uint32_t i = 0; i < (D < 128 ? D / 8 : 16); i++) {
+                        for (uint32_t i = 0; i < 8; i++) {
                             top = max(top, max(max(x[i].x & 0x7FFFu, x[i].x >> 16 & 0x7FFFu), max(x[i].y & 0x7FFFu, x[i].y >> 16 & 0x7FFFu)));
                             top = max(top, max(max(x[i].z & 0x7FFFu, x[i].z >> 16 & 0x7FFFu), max(x[i].w & 0x7FFFu, x[i].w >> 16 & 0x7FFFu)));
                         }
                     }
                     top >>= 7;
-                    // the largest element to [2^7, 2^8)
+                    // the largest element to [2^7, 2^8); one that is not finite: the row's factor says so
                     const bool bad = top == 255;
                     const int up = 7 + 127 - (int)top, up0 = min(up, 100);
-                    float f0 = bad ? 0.0f : __uint_as_float((uint32_t)(up0 + 127) << 23);
+                    float f0 = __uint_as_float((uint32_t)(up0 + 127) << 23);
                     const float f1 = __uint_as_float((uint32_t)(up - up0 + 127) << 23);
                     if (a.scale_log2 < 0.0f) f0 = -f0;
                     fac = bad ? __uint_as_float(0x7FC00000u) : ldexpf(fabsf(a.scale_log2), -up);
-                    const uint32_t q0 = base + Cfg::q + 2 * t * QP, rr = row & 127;
+                    const uint32_t rr = row & 127, q0 = base + Cfg::q + 2 * t * QP + rr * RB;
+                    const uint32_t sw = RB == 128 ? rr & 7 : (rr >> 1) & 3;
+                    // 16 elements at a time, again from the cache: kept rolled, the code runs once a segment
+#pragma unroll 1
+                    for (uint32_t i = 0; i < D / 16; i++) {
+                        uint4 x[2] = {};
+                        if (live && !bad) x[0] = qp[2 * i], x[1] = qp[2 * i + 1];
+                        const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+                        uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (uint32_t d0 = 0; d0 < D; d0 += 128) {
-                        if (D > 128) {
-#pragma unroll
-                            for (uint32_t i = 0; i < 16; i++)
-                                x[i] = live ? reinterpret_cast<const uint4 *>(qp + d0)[i] : make_uint4(0, 0, 0, 0);
-                        }
-#pragma unroll
-                        for (uint32_t i = 0; i < (D < 128 ? D : 128) / 16; i++) {
-                            uint32_t bits[8] = {x[2 * i].x, x[2 * i].y, x[2 * i].z, x[2 * i].w,
-                                                x[2 * i + 1].x, x[2 * i + 1].y, x[2 * i + 1].z, x[2 * i + 1].w};
-                            if (bad)
-#pragma unroll
-                                for (int e = 0; e < 8; e++) bits[e] = 0;
-                            uint4 hi, lo;
-                            split16(bits, f0, f1, hi, lo);
-                            const uint32_t at = d0 / 128 * 128 * RB + rr * RB + ((i ^ (RB == 128 ? rr & 7 : (rr >> 1) & 3)) << 4);
-                            sts128(q0 + at, hi.x, hi.y, hi.z, hi.w);
-                            sts128(q0 + QP + at, lo.x, lo.y, lo.z, lo.w);
-                        }
+                        for (int e = 0; e < 8; e++) split2(w[e], f0, f1, hi[e], lo[e]);
+                        const uint32_t at = q0 + i / (RB / 16) * 128 * RB + (((i % (RB / 16)) ^ sw) << 4);
+                        sts128(at, hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
+                        sts128(at + QP, lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -537,11 +514,8 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                             for (int i = 0; i < 32; i += 8) {
                                 uint32_t w[4];
 #pragma unroll
-                                for (int e = 0; e < 4; e++) {
-                                    const float x = none ? 0.0f : __uint_as_float(o[i + 2 * e]) * quot;
-                                    const float y = none ? 0.0f : __uint_as_float(o[i + 2 * e + 1]) * quot;
-                                    w[e] = (uint32_t)f32_to_bf16_rne(x) | (uint32_t)f32_to_bf16_rne(y) << 16;
-                                }
+                                for (int e = 0; e < 4; e++)
+                                    w[e] = bf16x2(__uint_as_float(o[i + 2 * e]) * quot, __uint_as_float(o[i + 2 * e + 1]) * quot);
                                 *reinterpret_cast<uint4 *>(a.out + at * D + d0 + i) = make_uint4(w[0], w[1], w[2], w[3]);
                             }
                         } else {
