@@ -16,7 +16,7 @@
 namespace dgt {
 
 constexpr float W_LOG2 = 12.0f;        // weights of the numerator reach 2^12 (fp16 holds them to 2^-24)
-constexpr uint32_t AT_WARPS = 8;
+constexpr uint32_t AT_WARPS = 4;
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t r;
@@ -51,7 +51,7 @@ template <uint32_t D, uint32_t NT>
 struct AttnCfg {
     static constexpr uint32_t PD = D < 128 ? D : 128, PAN = D / PD;
     static constexpr uint32_t IB = KV_P * PD, IPP = 2 * PAN;
-    static constexpr uint32_t NS = (D == 64 ? 6 : 3) - (NT == 4 ? (D == 64 ? 2 : 1) : 0);
+    static constexpr uint32_t NS = D == 64 ? (NT <= 2 ? 6 : 5) : (NT <= (D == 128 ? 2 : 1) ? 3 : 2);
     static constexpr uint32_t RT = 8 * NT;
     static constexpr uint32_t KSTEPS = D / 16;           // k-steps of the first product
     static constexpr bool QREG = NT * D <= 256;          // query fragments in registers
@@ -62,7 +62,7 @@ struct AttnCfg {
 };
 
 template <uint32_t D, uint32_t NT>
-__global__ void __launch_bounds__(AT_WARPS * 32, 1) k_kv_attention(AttnArgs a) {
+__global__ void __launch_bounds__(AT_WARPS * 32, 2) k_kv_attention(AttnArgs a) {
     using Cfg = AttnCfg<D, NT>;
     constexpr uint32_t RT = Cfg::RT, NS = Cfg::NS, IB = Cfg::IB, PD = Cfg::PD, PAN = Cfg::PAN, IPP = Cfg::IPP;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -71,7 +71,6 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) k_kv_attention(AttnArgs a) {
     __shared__ float stat[AT_WARPS][RT][3];
     __shared__ float rowstat[RT][3];
     __shared__ float rowfac[RT];
-    __shared__ float2 joined[RT];
     __shared__ uint64_t usum[AT_WARPS];
     __shared__ uint32_t wsum[AT_WARPS];
     __shared__ int last_flag;
@@ -83,9 +82,8 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) k_kv_attention(AttnArgs a) {
     pdl_wait();
 
     // ---- the CTA's units
-    Slot si{};
-    uint32_t units0;
-    const uint64_t U = all_units<AT_WARPS>(a, RT, usum, si, units0);
+    uint32_t tot = describe<AT_WARPS>(a, RT, 0, slots, wsum);
+    const uint64_t U = a.slots <= AT_CHUNK ? tot : all_units<AT_WARPS>(a, RT, usum);
     const uint64_t most = (U + a.min_units - 1) / a.min_units;
     const uint64_t C = most < gridDim.x ? most : gridDim.x;
     if (blockIdx.x >= C) return;
@@ -100,7 +98,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) k_kv_attention(AttnArgs a) {
     uint64_t base0 = 0;
     for (uint32_t s0 = 0; s0 < a.slots && base0 < ub; s0 += AT_CHUNK) {
         // ---- describe the next row tiles
-        const uint32_t tot = describe<AT_WARPS>(a, RT, s0, si, units0, slots, wsum);
+        if (s0) tot = describe<AT_WARPS>(a, RT, s0, slots, wsum);
         const uint64_t first = base0 > ua ? base0 : ua, end = base0 + tot < ub ? base0 + tot : ub;
         const uint32_t u0 = (uint32_t)(first - base0), u1 = end > first ? (uint32_t)(end - base0) : u0;
         const uint64_t chunk_base = base0;
@@ -119,8 +117,22 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) k_kv_attention(AttnArgs a) {
             return r;
         };
 
+        // a row's elements 2 lane + 64 j and the next
+        auto load_row = [&](const Slot &s, uint32_t h, uint32_t row, uint32_t (&bits)[D / 64]) {
+            const uint32_t flat = s.row0 + row;
+            const bool live = row < s.rows;
+            const uint16_t *qp = a.q.data + (int64_t)(s.tok0 + flat / a.group) * a.q.token_stride +
+                                 (int64_t)(h * a.group + flat % a.group) * a.q.head_stride;
+#pragma unroll
+            for (uint32_t j = 0; j < D / 64; j++)
+                bits[j] = live ? reinterpret_cast<const uint32_t *>(qp)[lane + 32 * j] : 0u;
+        };
         // ---- issue side: page numbers and scales of up to 32 pages in the lanes
         Share ir = make_run(u0, 0);
+        // the first run's queries travel while its pages are looked up
+        uint32_t ahead[D / 64];
+        load_row(slots[ir.slot], ir.h, warp, ahead);
+        bool at_hand = true;
         uint32_t ix = ir.wa, ik = 0, ibs = ir.wa, ibe = ir.wa;
         bool more = true, fresh = false;   // fresh: a batch that the consuming side has not taken over
         int bpid = -1;
@@ -200,18 +212,22 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) k_kv_attention(AttnArgs a) {
             u += r.pe - r.pa;
             const Slot s = slots[r.slot];
 
+            if (s.np == 0) {
+                write_none<D>(a, s, r.h, tid, AT_WARPS * 32);
+                at_hand = false;
+                continue;
+            }
             // queries: a row per warp at a time, scaled to its exponent, in fragment order
             __syncthreads();
             for (uint32_t row = warp; row < RT; row += AT_WARPS) {
                 float x[D / 32], amax = 0.0f;
-                const uint32_t flat = s.row0 + row;
-                const bool live = row < s.rows;
-                const uint16_t *qp = a.q.data + (int64_t)(s.tok0 + flat / a.group) * a.q.token_stride +
-                                     (int64_t)(r.h * a.group + flat % a.group) * a.q.head_stride;
                 uint32_t bits[D / 64];
+                if (at_hand && row == warp) {
 #pragma unroll
-                for (uint32_t j = 0; j < D / 64; j++)
-                    bits[j] = live ? reinterpret_cast<const uint32_t *>(qp)[lane + 32 * j] : 0u;
+                    for (uint32_t j = 0; j < D / 64; j++) bits[j] = ahead[j];
+                } else {
+                    load_row(s, r.h, row, bits);
+                }
 #pragma unroll
                 for (uint32_t j = 0; j < D / 64; j++) {
                     x[2 * j] = bf16lo(bits[j]);
@@ -246,6 +262,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) k_kv_attention(AttnArgs a) {
             }
             __syncthreads();
 
+            at_hand = false;
             uint2 qf[Cfg::QREG ? Cfg::KSTEPS * NT : 1];
             auto load_q = [&](uint32_t i) {
                 uint2 v;
@@ -451,15 +468,22 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) k_kv_attention(AttnArgs a) {
                     }
                 }
             __syncthreads();
-            if (tid < RT) {
-                float M = -INFINITY, MU = -INFINITY, L = 0.0f;
-                for (uint32_t w = 0; w < AT_WARPS; w++) {
-                    M = fmaxf(M, stat[w][tid][0]);
-                    MU = fmaxf(MU, stat[w][tid][1]);
+            if (warp < NT) {
+                // a row per four lanes, a warp's sums in each
+                const float *st = stat[c][8 * warp + g];
+                float M = st[0], MU = st[1];
+#pragma unroll
+                for (int d = 1; d < 4; d <<= 1) {
+                    M = fmaxf(M, __shfl_xor_sync(DGT_FULL, M, d));
+                    MU = fmaxf(MU, __shfl_xor_sync(DGT_FULL, MU, d));
                 }
-                for (uint32_t w = 0; w < AT_WARPS; w++)
-                    L += stat[w][tid][2] * ex2(stat[w][tid][0] - finite_base(M));
-                rowstat[tid][0] = M, rowstat[tid][1] = MU, rowstat[tid][2] = L;
+                float L = st[2] * ex2(st[0] - finite_base(M));
+#pragma unroll
+                for (int d = 1; d < 4; d <<= 1) L += __shfl_xor_sync(DGT_FULL, L, d);
+                if (c == 0) {
+                    float *o2 = rowstat[8 * warp + g];
+                    o2[0] = M, o2[1] = MU, o2[2] = L;
+                }
             }
             const uint32_t n = s.per_head();
             const bool complete = r.pa == 0 && r.pe == n;
@@ -503,19 +527,19 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1) k_kv_attention(AttnArgs a) {
             if (complete) continue;
 
             // ---- partial: the last CTA of the segment to arrive adds its parts in page order
-            __threadfence();
-            __syncthreads();
             const uint64_t sa = chunk_base + s.base + (uint64_t)r.h * n, sb = sa + n;   // the segment's units
             const uint64_t c0 = ((sa + 1) * C - 1) / U, c1 = (sb * C - 1) / U;
+            __syncthreads();
             if (tid == 0) {
+                __threadfence();   // what the CTA wrote, the barrier before it, is seen with the arrival
                 const int32_t was = atomicAdd(&a.count[c0], 1);
                 last_flag = was == (int32_t)(c1 - c0);
                 if (last_flag) a.count[c0] = 0;
+                __threadfence();
             }
             __syncthreads();
             if (!last_flag) continue;
-            __threadfence();
-            join_parts<D, Cfg::PART>(a, s, r.h, c0, c1, tid, AT_WARPS * 32, W_LOG2, joined, [] { __syncthreads(); });
+            join_parts<D, Cfg::PART, RT>(a, s, r.h, c0, c1, tid, AT_WARPS * 32, W_LOG2, scratch, [] { __syncthreads(); });
         }
         more = false;   // everything of this chunk has been taken
     }
@@ -535,7 +559,7 @@ static int attn_launch(const AttnArgs &a, cudaStream_t st) {
             return DGT_ERR_CUDA;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    const unsigned grid = (unsigned)di.sms < AT_MAX_CTAS ? (unsigned)di.sms : AT_MAX_CTAS;
+    const unsigned grid = 2u * di.sms < AT_MAX_CTAS ? 2u * di.sms : AT_MAX_CTAS;
     return launch_pdl(fn, dim3(grid), dim3(AT_WARPS * 32), smem, st, a) == cudaSuccess ? DGT_OK : DGT_ERR_CUDA;
 }
 
@@ -549,7 +573,7 @@ struct Plan {
 static Plan attn_plan(uint32_t head_dim, uint32_t group, uint32_t batch, uint64_t tokens) {
     const uint64_t rows = group * ((tokens + batch - 1) / batch);
     if (rows >= PROMPT_ROWS) return {0, prompt_rows(head_dim)};
-    const uint32_t nt = rows <= 8 ? 1 : rows <= 16 || head_dim == 256 ? 2 : 4;
+    const uint32_t nt = rows <= 8 ? 1 : rows <= 16 || head_dim == 256 ? 2 : rows <= 24 ? 3 : 4;
     return {nt, 8 * nt};
 }
 static uint64_t slot_count(uint32_t RT, uint32_t group, uint32_t batch, uint64_t tokens, bool ragged) {
@@ -607,8 +631,16 @@ extern "C" int dgt_kv_attention_ex(const dgt_kv_cache *cache, uint32_t layer, co
     cudaStream_t st = (cudaStream_t)stream;
     if (nt == 0) return prompt_launch(a, st);
     switch (cache->head_dim) {
-        case 64: return nt == 1 ? attn_launch<64, 1>(a, st) : nt == 2 ? attn_launch<64, 2>(a, st) : attn_launch<64, 4>(a, st);
-        case 128: return nt == 1 ? attn_launch<128, 1>(a, st) : nt == 2 ? attn_launch<128, 2>(a, st) : attn_launch<128, 4>(a, st);
+        case 64:
+            return nt == 1   ? attn_launch<64, 1>(a, st)
+                   : nt == 2 ? attn_launch<64, 2>(a, st)
+                   : nt == 3 ? attn_launch<64, 3>(a, st)
+                             : attn_launch<64, 4>(a, st);
+        case 128:
+            return nt == 1   ? attn_launch<128, 1>(a, st)
+                   : nt == 2 ? attn_launch<128, 2>(a, st)
+                   : nt == 3 ? attn_launch<128, 3>(a, st)
+                             : attn_launch<128, 4>(a, st);
         default: return nt == 1 ? attn_launch<256, 1>(a, st) : attn_launch<256, 2>(a, st);
     }
 }

@@ -16,8 +16,8 @@ namespace dgt {
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
-constexpr uint32_t AT_CHUNK = 128;     // row tiles described in shared memory at a time
-constexpr uint32_t AT_MAX_CTAS = 160;
+constexpr uint32_t AT_CHUNK = 64;      // row tiles described in shared memory at a time
+constexpr uint32_t AT_MAX_CTAS = 320;
 
 struct AttnArgs {
     dgt_kv_cache c;
@@ -125,18 +125,15 @@ __device__ __forceinline__ Slot slot_info(const AttnArgs &a, uint32_t slot, uint
 uint32_t prompt_rows(uint32_t head_dim);
 int prompt_launch(const AttnArgs &a, cudaStream_t st);
 
-// All units of a call, summed by a CTA of WARPS warps.  With at most AT_CHUNK
-// row tiles a thread meets one tile, which it keeps for describe().
+// All units of a call, summed by a CTA of WARPS warps.
 template <uint32_t WARPS>
-__device__ __forceinline__ uint64_t all_units(const AttnArgs &a, uint32_t RT, uint64_t *usum, Slot &si,
-                                              uint32_t &units0) {
+__device__ __forceinline__ uint64_t all_units(const AttnArgs &a, uint32_t RT, uint64_t *usum) {
     uint64_t sum = 0;
-    uint32_t units = 0;
+    uint32_t units;
     for (uint32_t s = threadIdx.x; s < a.slots; s += WARPS * 32) {
-        si = slot_info(a, s, RT, &units);
+        slot_info(a, s, RT, &units);
         sum += units;
     }
-    units0 = a.slots <= AT_CHUNK ? units : 0;
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(DGT_FULL, sum, d);
     if (lane_id() == 0) usum[threadIdx.x >> 5] = sum;
@@ -149,18 +146,17 @@ __device__ __forceinline__ uint64_t all_units(const AttnArgs &a, uint32_t RT, ui
 
 // The row tiles s0 .. s0 + AT_CHUNK - 1 into shared memory; returns their units.
 template <uint32_t WARPS>
-__device__ __forceinline__ uint32_t describe(const AttnArgs &a, uint32_t RT, uint32_t s0, Slot &si, uint32_t units0,
-                                             Slot *slots, uint32_t *wsum) {
+__device__ __forceinline__ uint32_t describe(const AttnArgs &a, uint32_t RT, uint32_t s0, Slot *slots, uint32_t *wsum) {
     const uint32_t tid = threadIdx.x, warp = tid >> 5;
     __syncthreads();   // the tiles described before are done with
-    uint32_t units = units0;
-    if (a.slots > AT_CHUNK) {
-        units = 0;
-        if (tid < AT_CHUNK && s0 + tid < a.slots) si = slot_info(a, s0 + tid, RT, &units);
+    Slot s{};
+    uint32_t units = 0, before = 0;
+    if (warp < AT_CHUNK / 32) {
+        if (s0 + tid < a.slots) s = slot_info(a, s0 + tid, RT, &units);
+        uint32_t wtot;
+        before = warp_excl_scan(units, &wtot);
+        if (lane_id() == 0) wsum[warp] = wtot;
     }
-    uint32_t wtot;
-    uint32_t before = warp_excl_scan(units, &wtot);
-    if (lane_id() == 0) wsum[warp] = wtot;
     __syncthreads();
     uint32_t tot = 0;
 #pragma unroll
@@ -168,9 +164,9 @@ __device__ __forceinline__ uint32_t describe(const AttnArgs &a, uint32_t RT, uin
         if (w < warp) before += wsum[w];
         tot += wsum[w];
     }
-    if (tid < AT_CHUNK) {
-        si.base = before;
-        slots[tid] = si;
+    if (warp < AT_CHUNK / 32) {
+        s.base = before;
+        slots[tid] = s;
     }
     __syncthreads();
     return tot;
@@ -203,58 +199,91 @@ __device__ __forceinline__ void write_out(const AttnArgs &a, const Slot &s, uint
     if (a.lse && d == 0) a.lse[at] = none ? -INFINITY : (M + __log2f(L)) * LN2;
 }
 
+// Rows that see nothing: out 0, lse -inf.
+template <uint32_t D>
+__device__ __forceinline__ void write_none(const AttnArgs &a, const Slot &s, uint32_t h, uint32_t t, uint32_t threads) {
+    for (uint32_t i = t; i < s.rows * (D / 8); i += threads) {
+        const uint32_t flat = s.row0 + i / (D / 8);
+        const uint64_t at = (uint64_t)(s.tok0 + flat / a.group) * a.q_heads + h * a.group + flat % a.group;
+        reinterpret_cast<uint4 *>(a.out + at * D)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
+        if (a.lse && i % (D / 8) == 0) a.lse[at] = -INFINITY;
+    }
+}
+
 // The parts of a segment, left by the CTAs c0..c1 that hold its units (two
 // parts of PART floats a CTA: a row's M, MU, L, then its numerators), added in
 // page order by `threads` threads, this one number t, which all call it; sync
-// is their barrier and `rowof` a shared array of a tile's rows.  First a thread
-// per row finds the row's maxima and denominator, then four elements at a time
+// is their barrier, sh shared memory of join_floats(RT) floats.  The parts'
+// statistics come in blocks, a load per thread; then four elements at a time
 // are weighted and added, several loads in flight.
-template <uint32_t D, uint32_t PART, typename Sync>
+constexpr uint32_t JOIN_PARTS = 32;   // parts of a block, when rows are few
+__host__ __device__ constexpr uint32_t join_block(uint32_t RT) { return RT >= 128 ? 2 : JOIN_PARTS * 8 / RT; }
+__host__ __device__ constexpr uint32_t join_floats(uint32_t RT) { return join_block(RT) * RT * 3 + 4 * RT; }
+template <uint32_t D, uint32_t PART, uint32_t RT, typename Sync>
 __device__ __forceinline__ void join_parts(const AttnArgs &a, const Slot &s, uint32_t h, uint64_t c0, uint64_t c1,
-                                           uint32_t t, uint32_t threads, float wlog2, float2 *rowof, Sync sync) {
+                                           uint32_t t, uint32_t threads, float wlog2, float *sh, Sync sync) {
+    constexpr uint32_t KB = join_block(RT);
+    float *rows = sh + KB * RT * 3;   // per row M, MU, L, then the quotient's factor
     const uint32_t parts = (uint32_t)(c1 - c0 + 1);
     // part 0 is the one that begins the segment, at the end of its CTA's work
     auto at = [&](uint32_t k, uint32_t row) { return a.part + (2 * (c0 + k) + (k == 0 ? 1 : 0)) * PART + row * (D + 4); };
-    for (uint32_t row = t; row < s.rows; row += threads) {
-        float M = -INFINITY, MU = -INFINITY, L = 0.0f;
-#pragma unroll 4
-        for (uint32_t k = 0; k < parts; k++) {
-            const float4 st = __ldcg(reinterpret_cast<const float4 *>(at(k, row)));
-            const float m = fmaxf(M, st.x);
-            L = L * ex2(M - finite_base(m)) + st.z * ex2(st.x - finite_base(m));
-            M = m;
-            MU = fmaxf(MU, st.y);
+    auto load_block = [&](uint32_t k0) {
+        for (uint32_t i = t; i < KB * RT; i += threads) {
+            const uint32_t k = k0 + i / RT, row = i % RT;
+            if (k < parts && row < s.rows) {
+                const float4 st = __ldcg(reinterpret_cast<const float4 *>(at(k, row)));
+                sh[3 * i] = st.x, sh[3 * i + 1] = st.y, sh[3 * i + 2] = st.z;
+            }
         }
-        const bool none = M == -INFINITY && L == 0.0f;
-        rowof[row] = make_float2(finite_base(MU), none ? 0.0f : ex2(finite_base(MU) - finite_base(M) - wlog2) / L);
-        if (a.lse) {
-            const uint32_t flat = s.row0 + row;
-            a.lse[(uint64_t)(s.tok0 + flat / a.group) * a.q_heads + h * a.group + flat % a.group] =
-                none ? -INFINITY : (M + __log2f(L)) * LN2;
+        sync();
+    };
+    for (uint32_t k0 = 0; k0 < parts; k0 += KB) {
+        if (k0) sync();
+        load_block(k0);
+        for (uint32_t row = t; row < s.rows; row += threads) {
+            float *r = rows + 4 * row;
+            float M = k0 ? r[0] : -INFINITY, MU = k0 ? r[1] : -INFINITY, L = k0 ? r[2] : 0.0f;
+            const uint32_t n = min(KB, parts - k0);
+            float m = M;
+            for (uint32_t k = 0; k < n; k++) {
+                m = fmaxf(m, sh[3 * (k * RT + row)]);
+                MU = fmaxf(MU, sh[3 * (k * RT + row) + 1]);
+            }
+            const float b = finite_base(m);
+            L *= ex2(M - b);
+            for (uint32_t k = 0; k < n; k++) L += sh[3 * (k * RT + row) + 2] * ex2(sh[3 * (k * RT + row)] - b);
+            r[0] = m, r[1] = MU, r[2] = L;
+            if (k0 + KB >= parts) {
+                const bool none = m == -INFINITY && L == 0.0f;
+                r[3] = none ? 0.0f : ex2(finite_base(MU) - b - wlog2) / L;
+                if (a.lse) {
+                    const uint32_t flat = s.row0 + row;
+                    a.lse[(uint64_t)(s.tok0 + flat / a.group) * a.q_heads + h * a.group + flat % a.group] =
+                        none ? -INFINITY : (m + __log2f(L)) * LN2;
+                }
+            }
         }
     }
     sync();
-    constexpr uint32_t Q = D / 4, B = 4;   // B elements of four in flight
+    const bool one = parts <= KB;   // the statistics of every part are still here
+    constexpr uint32_t Q = D / 4, B = RT >= 128 ? 4 : 1, UN = RT >= 128 ? 2 : 8;   // B elements of four in flight, UN parts
     const uint32_t all = s.rows * Q;
     for (uint32_t i0 = t; i0 < all; i0 += B * threads) {
         float v[B][4] = {};
-        float2 ro[B];
-#pragma unroll
-        for (uint32_t b = 0; b < B; b++) ro[b] = rowof[min(i0 + b * threads, all - 1) / Q];
-#pragma unroll 2
+#pragma unroll UN
         for (uint32_t k = 0; k < parts; k++) {
             float mu[B];
             float4 x[B];
 #pragma unroll
             for (uint32_t b = 0; b < B; b++) {
-                const uint32_t i = min(i0 + b * threads, all - 1);
-                const float *p = at(k, i / Q);
-                mu[b] = __ldcg(p + 1);
+                const uint32_t i = min(i0 + b * threads, all - 1), row = i / Q;
+                const float *p = at(k, row);
+                mu[b] = one ? sh[3 * (k * RT + row) + 1] : __ldcg(p + 1);
                 x[b] = __ldcg(reinterpret_cast<const float4 *>(p + 4 + (i % Q) * 4));
             }
 #pragma unroll
             for (uint32_t b = 0; b < B; b++) {
-                const float f = ex2(mu[b] - ro[b].x);
+                const float f = ex2(mu[b] - finite_base(rows[4 * (min(i0 + b * threads, all - 1) / Q) + 1]));
                 v[b][0] += x[b].x * f, v[b][1] += x[b].y * f, v[b][2] += x[b].z * f, v[b][3] += x[b].w * f;
             }
         }
@@ -262,14 +291,14 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, const Slot &s, uin
         for (uint32_t b = 0; b < B; b++) {
             const uint32_t i = i0 + b * threads;
             if (i >= all) break;
+            const float quot = rows[4 * (i / Q) + 3];
             const uint32_t flat = s.row0 + i / Q;
             const uint64_t o = (uint64_t)(s.tok0 + flat / a.group) * a.q_heads + h * a.group + flat % a.group;
-            uint32_t w[2];
-#pragma unroll
-            for (int e = 0; e < 2; e++) w[e] = bf16x2(v[b][2 * e] * ro[b].y, v[b][2 * e + 1] * ro[b].y);
-            *reinterpret_cast<uint2 *>(a.out + o * D + (i % Q) * 4) = make_uint2(w[0], w[1]);
+            *reinterpret_cast<uint2 *>(a.out + o * D + (i % Q) * 4) =
+                make_uint2(bf16x2(v[b][0] * quot, v[b][1] * quot), bf16x2(v[b][2] * quot, v[b][3] * quot));
         }
     }
+    sync();   // sh and the parts are done with
 }
 
 }  // namespace dgt

@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
     __shared__ __align__(8) uint64_t kfull[KS], kfree[KS], vfull[VS], vfree[VS], wfull[WS], wfree[WS];
     __shared__ __align__(8) uint64_t sfull[4], pfull[4], ofull[2], ofin[2], qfull[2], mfull[PR_META], drained;
     __shared__ PageMeta meta[PR_META];
-    __shared__ float2 joined[RT];
+    __shared__ float joined[join_floats(RT)];
     __shared__ Slot slots[AT_CHUNK];
     __shared__ uint64_t usum[PR_WARPS];
     __shared__ uint32_t wsum[PR_WARPS];
@@ -130,9 +130,8 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
     const uint32_t tm = tmem_slot;
     volatile int *abortp = &abort_flag;
 
-    Slot si{};
-    uint32_t units0;
-    const uint64_t U = all_units<PR_WARPS>(a, RT, usum, si, units0);
+    uint32_t tot = describe<PR_WARPS>(a, RT, 0, slots, wsum);
+    const uint64_t U = a.slots <= AT_CHUNK ? tot : all_units<PR_WARPS>(a, RT, usum);
     const uint64_t most = (U + a.min_units - 1) / a.min_units;
     const uint64_t C = most < gridDim.x ? most : gridDim.x;
     const uint64_t ua = C ? blockIdx.x * U / C : 0, ub = blockIdx.x < C ? (blockIdx.x + 1) * U / C : 0;
@@ -158,7 +157,7 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
 
     uint64_t base0 = 0;
     for (uint32_t s0 = 0; s0 < a.slots && base0 < ub; s0 += AT_CHUNK) {
-        const uint32_t tot = describe<PR_WARPS>(a, RT, s0, si, units0, slots, wsum);
+        if (s0) tot = describe<PR_WARPS>(a, RT, s0, slots, wsum);
         const uint64_t first = base0 > ua ? base0 : ua, end = base0 + tot < ub ? base0 + tot : ub;
         const uint32_t u0 = (uint32_t)(first - base0), u1 = end > first ? (uint32_t)(end - base0) : u0;
         const uint64_t chunk_base = base0;
@@ -532,18 +531,17 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                     // the last CTA of the segment to arrive adds its parts in page order
                     const uint64_t sa = chunk_base + s.base + (uint64_t)r.h * n, sb = sa + n;
                     const uint64_t c0 = ((sa + 1) * C - 1) / U, c1 = (sb * C - 1) / U;
-                    __threadfence();
                     bar_rows();
                     if (tid == 0) {
+                        __threadfence();   // what the rows' threads wrote, the barrier before it, is seen with the arrival
                         const int32_t was = atomicAdd(&a.count[c0], 1);
                         last_flag = was == (int32_t)(c1 - c0);
                         if (last_flag) a.count[c0] = 0;
+                        __threadfence();
                     }
                     bar_rows();
-                    if (last_flag) {
-                        __threadfence();
-                        join_parts<D, Cfg::PART>(a, s, r.h, c0, c1, tid, 256, PR_W_LOG2, joined, bar_rows);
-                    }
+                    if (last_flag)
+                        join_parts<D, Cfg::PART, RT>(a, s, r.h, c0, c1, tid, 256, PR_W_LOG2, joined, bar_rows);
                 }
             }
             it += T;
