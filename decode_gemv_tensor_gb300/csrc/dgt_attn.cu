@@ -51,11 +51,11 @@ template <uint32_t D, uint32_t NT>
 struct AttnCfg {
     static constexpr uint32_t PD = D < 128 ? D : 128, PAN = D / PD;
     static constexpr uint32_t IB = KV_P * PD, IPP = 2 * PAN;
-    static constexpr uint32_t NS = D == 64 ? (NT <= 2 ? 6 : 5) : (NT <= (D == 128 ? 2 : 1) ? 3 : 2);
+    static constexpr uint32_t NS = D == 64 ? 4 : 2;      // deeper rings were no faster (16 KB a warp in flight is enough)
     static constexpr uint32_t RT = 8 * NT;
     static constexpr uint32_t KSTEPS = D / 16;           // k-steps of the first product
     static constexpr bool QREG = NT * D <= 256;          // query fragments in registers
-    static constexpr uint32_t RS = 64 + 4;               // row of the merge scratch, padded
+    static constexpr uint32_t RS = D + 4;                // row of the merge scratch, padded
     static constexpr uint32_t ring = 0, scratch = AT_WARPS * NS * IB, q = scratch + AT_WARPS * 8 * RS * 4,
                               bytes = q + KSTEPS * NT * 256;
     static constexpr uint32_t PART = RT * (D + 4);       // floats of a partial result
@@ -68,11 +68,11 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) k_kv_attention(AttnArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bar[AT_WARPS][NS];
     __shared__ Slot slots[AT_CHUNK];
+    __shared__ uint32_t fits[16];
     __shared__ float stat[AT_WARPS][RT][3];
     __shared__ float rowstat[RT][3];
     __shared__ float rowfac[RT];
     __shared__ uint64_t usum[AT_WARPS];
-    __shared__ uint32_t wsum[AT_WARPS];
     __shared__ int last_flag;
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     if (tid < AT_WARPS * NS) mbar_init(smem_u32(&bar[tid / NS][tid % NS]), 1);
@@ -82,12 +82,11 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) k_kv_attention(AttnArgs a) {
     pdl_wait();
 
     // ---- the CTA's units
-    uint32_t tot = describe<AT_WARPS>(a, RT, 0, slots, wsum);
-    const uint64_t U = a.slots <= AT_CHUNK ? tot : all_units<AT_WARPS>(a, RT, usum);
-    const uint64_t most = (U + a.min_units - 1) / a.min_units;
-    const uint64_t C = most < gridDim.x ? most : gridDim.x;
-    if (blockIdx.x >= C) return;
-    const uint64_t ua = blockIdx.x * U / C, ub = (blockIdx.x + 1) * U / C;
+    Units here = describe<AT_WARPS>(a, RT, 0, slots, usum);
+    const Units all = a.slots <= AT_CHUNK ? here : all_units<AT_WARPS>(a, RT, usum);
+    const Cuts cut = cut_plan(a, all, slots, gridDim.x, fits);
+    if (blockIdx.x >= cut.C) return;
+    const uint64_t ub = cut.parts ? cut.U : cut.raw(blockIdx.x + 1);
 
     const uint32_t ring = smem_u32(smem) + warp * NS * IB;
     float *scratch = reinterpret_cast<float *>(smem + Cfg::scratch);
@@ -98,20 +97,21 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) k_kv_attention(AttnArgs a) {
     uint64_t base0 = 0;
     for (uint32_t s0 = 0; s0 < a.slots && base0 < ub; s0 += AT_CHUNK) {
         // ---- describe the next row tiles
-        if (s0) tot = describe<AT_WARPS>(a, RT, s0, slots, wsum);
-        const uint64_t first = base0 > ua ? base0 : ua, end = base0 + tot < ub ? base0 + tot : ub;
-        const uint32_t u0 = (uint32_t)(first - base0), u1 = end > first ? (uint32_t)(end - base0) : u0;
+        if (s0) here = describe<AT_WARPS>(a, RT, s0, slots, usum);
+        const uint32_t tot = (uint32_t)here.units();
+        const uint32_t nslots = min(AT_CHUNK, a.slots - s0);
         const uint64_t chunk_base = base0;
         base0 += tot;
-        if (u0 == u1) continue;
+        uint32_t u0, u1;
+        cut.share(slots, nslots, chunk_base, tot, u0, u1);
+        if (u0 >= u1) continue;
 
-        const uint32_t nslots = min(AT_CHUNK, a.slots - s0);
         struct Share : Run {
             uint32_t wa, wb;   // this warp's pages
         };
-        auto make_run = [&](uint32_t u, uint32_t slot) {
+        auto make_run = [&](uint32_t u) {
             Share r;
-            static_cast<Run &>(r) = run_at(slots, nslots, u, u1, slot);
+            static_cast<Run &>(r) = run_at(slots, nslots, u, u1);
             const uint32_t cnt = slots[r.slot].np ? r.pe - r.pa : 0;
             r.wa = r.pa + warp * cnt / AT_WARPS, r.wb = r.pa + (warp + 1) * cnt / AT_WARPS;
             return r;
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) k_kv_attention(AttnArgs a) {
                 bits[j] = live ? reinterpret_cast<const uint32_t *>(qp)[lane + 32 * j] : 0u;
         };
         // ---- issue side: page numbers and scales of up to 32 pages in the lanes
-        Share ir = make_run(u0, 0);
+        Share ir = make_run(u0);
         // the first run's queries travel while its pages are looked up
         uint32_t ahead[D / 64];
         load_row(slots[ir.slot], ir.h, warp, ahead);
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) k_kv_attention(AttnArgs a) {
                             more = false;
                             break;
                         }
-                        ir = make_run(next, ir.slot);
+                        ir = make_run(next);
                         ix = ir.wa;
                     }
                     if (!more) break;
@@ -206,9 +206,8 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) k_kv_attention(AttnArgs a) {
         issue();
 
         // ---- consume the CTA's runs of this chunk
-        for (uint32_t u = u0, hint = 0; u < u1;) {
-            const Share r = make_run(u, hint);
-            hint = r.slot;
+        for (uint32_t u = u0; u < u1;) {
+            const Share r = make_run(u);
             u += r.pe - r.pa;
             const Slot s = slots[r.slot];
 
@@ -219,15 +218,21 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) k_kv_attention(AttnArgs a) {
             }
             // queries: a row per warp at a time, scaled to its exponent, in fragment order
             __syncthreads();
-            for (uint32_t row = warp; row < RT; row += AT_WARPS) {
-                float x[D / 32], amax = 0.0f;
-                uint32_t bits[D / 64];
-                if (at_hand && row == warp) {
+            uint32_t rows[RT / AT_WARPS][D / 64];   // all loads first
 #pragma unroll
-                    for (uint32_t j = 0; j < D / 64; j++) bits[j] = ahead[j];
+            for (uint32_t i = 0; i < RT / AT_WARPS; i++) {
+                if (i == 0 && at_hand) {
+#pragma unroll
+                    for (uint32_t j = 0; j < D / 64; j++) rows[0][j] = ahead[j];
                 } else {
-                    load_row(s, r.h, row, bits);
+                    load_row(s, r.h, warp + i * AT_WARPS, rows[i]);
                 }
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < RT / AT_WARPS; i++) {
+                const uint32_t row = warp + i * AT_WARPS;
+                const uint32_t(&bits)[D / 64] = rows[i];
+                float x[D / 32], amax = 0.0f;
 #pragma unroll
                 for (uint32_t j = 0; j < D / 64; j++) {
                     x[2 * j] = bf16lo(bits[j]);
@@ -497,30 +502,36 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) k_kv_attention(AttnArgs a) {
                     for (uint32_t w = 0; w < AT_WARPS; w++) MU = fmaxf(MU, stat[w][8 * nt + 2 * c + e][1]);
                     f[e] = ex2(mu[nt][e] - finite_base(MU));
                 }
+                __syncthreads();
 #pragma unroll
-                for (uint32_t d0 = 0; d0 < D; d0 += 64) {
-                    __syncthreads();
+                for (uint32_t i = 0; i < D / 16; i++)
 #pragma unroll
-                    for (uint32_t i = 0; i < 4; i++)
+                    for (int j = 0; j < 4; j++)
+                        scratch[(warp * 8 + 2 * c + (j & 1)) * Cfg::RS + 16 * i + g + 8 * (j >> 1)] = o[i][nt][j] * f[j & 1];
+                __syncthreads();
+                // four elements a thread
+                const uint32_t live = s.rows > 8 * nt ? min(8u, s.rows - 8 * nt) : 0u;
+#pragma unroll 2
+                for (uint32_t i = tid; i < live * (D / 4); i += AT_WARPS * 32) {
+                    const uint32_t rr = i / (D / 4), row = 8 * nt + rr, d = (i % (D / 4)) * 4;
+                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-                        for (int j = 0; j < 4; j++)
-                            scratch[(warp * 8 + 2 * c + (j & 1)) * Cfg::RS + 16 * i + g + 8 * (j >> 1)] =
-                                o[d0 / 16 + i][nt][j] * f[j & 1];
-                    __syncthreads();
-                    for (uint32_t i = tid; i < 8 * 64; i += AT_WARPS * 32) {
-                        const uint32_t row = 8 * nt + i / 64, d = d0 + i % 64;
-                        if (row >= s.rows) continue;
-                        float v = 0.0f;
-#pragma unroll
-                        for (uint32_t w = 0; w < AT_WARPS; w++) v += scratch[(w * 8 + i / 64) * Cfg::RS + i % 64];
-                        const float *st = rowstat[row];
-                        if (complete) {
-                            write_out<D>(a, s, r.h, row, d, v, st[0], st[1], st[2], W_LOG2);
-                        } else {
-                            float *pr = part + row * (D + 4);
-                            pr[4 + d] = v;
-                            if (d < 3) pr[d] = st[d];
-                        }
+                    for (uint32_t w = 0; w < AT_WARPS; w++) {
+                        const float4 x = *reinterpret_cast<const float4 *>(&scratch[(w * 8 + rr) * Cfg::RS + d]);
+                        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+                    }
+                    const float *st = rowstat[row];
+                    if (complete) {
+                        const bool none = st[0] == -INFINITY && st[2] == 0.0f;
+                        const float q = none ? 0.0f : ex2(finite_base(st[1]) - finite_base(st[0]) - W_LOG2) / st[2];
+                        const uint32_t flat = s.row0 + row;
+                        const uint64_t at = (uint64_t)(s.tok0 + flat / a.group) * a.q_heads + r.h * a.group + flat % a.group;
+                        *reinterpret_cast<uint2 *>(a.out + at * D + d) = make_uint2(bf16x2(v.x * q, v.y * q), bf16x2(v.z * q, v.w * q));
+                        if (a.lse && d == 0) a.lse[at] = none ? -INFINITY : (st[0] + __log2f(st[2])) * LN2;
+                    } else {
+                        float *pr = part + row * (D + 4);
+                        *reinterpret_cast<float4 *>(pr + 4 + d) = v;
+                        if (d == 0) *reinterpret_cast<float4 *>(pr) = make_float4(st[0], st[1], st[2], 0.0f);
                     }
                 }
             }
@@ -528,15 +539,10 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) k_kv_attention(AttnArgs a) {
 
             // ---- partial: the last CTA of the segment to arrive adds its parts in page order
             const uint64_t sa = chunk_base + s.base + (uint64_t)r.h * n, sb = sa + n;   // the segment's units
-            const uint64_t c0 = ((sa + 1) * C - 1) / U, c1 = (sb * C - 1) / U;
+            uint32_t c0, c1;
+            cut.holders(sa, sb, c0, c1);
             __syncthreads();
-            if (tid == 0) {
-                __threadfence();   // what the CTA wrote, the barrier before it, is seen with the arrival
-                const int32_t was = atomicAdd(&a.count[c0], 1);
-                last_flag = was == (int32_t)(c1 - c0);
-                if (last_flag) a.count[c0] = 0;
-                __threadfence();
-            }
+            if (tid == 0) last_flag = arrive_last(&a.count[c0], c1 - c0 + 1);
             __syncthreads();
             if (!last_flag) continue;
             join_parts<D, Cfg::PART, RT>(a, s, r.h, c0, c1, tid, AT_WARPS * 32, W_LOG2, scratch, [] { __syncthreads(); });
@@ -590,8 +596,8 @@ constexpr size_t AT_COUNT_BYTES = (AT_MAX_CTAS * 4 + 255) / 256 * 256;
 extern "C" size_t dgt_kv_attention_workspace_bytes(const dgt_kv_cache *cache, uint32_t q_heads, uint32_t batch,
                                                    uint64_t tokens) {
     if (!cache || cache->kv_heads == 0 || batch == 0 || q_heads < cache->kv_heads) return 0;
-    const uint32_t RT = attn_plan(cache->head_dim, q_heads / cache->kv_heads, batch, tokens).RT;
-    return AT_COUNT_BYTES + (size_t)AT_MAX_CTAS * 2 * RT * (cache->head_dim + 4) * 4;
+    const Plan p = attn_plan(cache->head_dim, q_heads / cache->kv_heads, batch, tokens);
+    return AT_COUNT_BYTES + (size_t)(p.nt ? AT_MAX_CTAS : PR_MAX_CTAS) * 2 * p.RT * (cache->head_dim + 4) * 4;
 }
 
 extern "C" int dgt_kv_attention_ex(const dgt_kv_cache *cache, uint32_t layer, const dgt_heads *q, uint64_t tokens,
@@ -626,7 +632,8 @@ extern "C" int dgt_kv_attention_ex(const dgt_kv_cache *cache, uint32_t layer, co
     a.per_entry = (a.group + RT - 1) / RT;
     a.count = (int32_t *)d_ws;
     a.part = (float *)((uint8_t *)d_ws + AT_COUNT_BYTES);
-    a.min_units = 1;
+    a.min_units = nt ? 4 : 8;   // a page a warp
+    a.slack = nt ? 12 : 16;
     a.spin = wait_limit_from_flags(flags);
     cudaStream_t st = (cudaStream_t)stream;
     if (nt == 0) return prompt_launch(a, st);

@@ -1,12 +1,14 @@
 // dgt_attn.cuh -- what the attention kernels share: arguments, row tiles, and
 // how the work is cut.
 //
-// Work is cut evenly over the CTAs whatever the lengths: a segment is one tile
-// of query rows and one kv head, its units are the pages that the tile sees,
-// and CTA c of C takes units [c U / C, (c + 1) U / C) of all U.  A segment that
-// ends up in several CTAs leaves partial sums in the workspace; the CTA that
-// arrives last adds them in page order, so results do not depend on timing.
-// Lengths are read on the device: a captured graph follows them.
+// Work is cut evenly over the CTAs whatever the lengths.  A segment is one tile
+// of query rows and one kv head, its units are the pages that the tile sees.
+// Where that comes out even enough, every segment is cut into equal parts, a
+// CTA for each; otherwise CTA c of C takes units [c U / C, (c + 1) U / C) of
+// all U, a cut close to a segment's border moved there.  A segment that ends up
+// in several CTAs leaves partial sums in the workspace; the CTA that arrives
+// last adds them in page order, so results do not depend on timing.  Lengths
+// are read on the device: a captured graph follows them.
 #pragma once
 #include "dgt_kv.cuh"
 
@@ -17,7 +19,7 @@ namespace dgt {
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr uint32_t AT_CHUNK = 64;      // row tiles described in shared memory at a time
-constexpr uint32_t AT_MAX_CTAS = 320;
+constexpr uint32_t AT_MAX_CTAS = 320, PR_MAX_CTAS = 160;
 
 struct AttnArgs {
     dgt_kv_cache c;
@@ -31,7 +33,7 @@ struct AttnArgs {
     int32_t *count;     // workspace: arrivals at the segment that CTA c begins and others end, zero between calls
     float *part;        // workspace: two partial results per CTA
     int32_t *status;
-    uint32_t min_units, spin;
+    uint32_t min_units, slack, spin;   // pages of a part at least; pages that parts may be above an even share
 };
 
 // A tile of query rows: rows [row0, row0 + rows) of its entry's flattened
@@ -125,28 +127,35 @@ __device__ __forceinline__ Slot slot_info(const AttnArgs &a, uint32_t slot, uint
 uint32_t prompt_rows(uint32_t head_dim);
 int prompt_launch(const AttnArgs &a, cudaStream_t st);
 
-// All units of a call, summed by a CTA of WARPS warps.
+// Units and row tiles that hold rows, counted together.
+struct Units {
+    uint64_t packed;   // units below, tiles from bit 40 on
+    __device__ __forceinline__ uint64_t units() const { return packed & ((1ull << 40) - 1); }
+    __device__ __forceinline__ uint32_t tiles() const { return (uint32_t)(packed >> 40); }
+};
+
+// All of a call's, summed by a CTA of WARPS warps.
 template <uint32_t WARPS>
-__device__ __forceinline__ uint64_t all_units(const AttnArgs &a, uint32_t RT, uint64_t *usum) {
+__device__ __forceinline__ Units all_units(const AttnArgs &a, uint32_t RT, uint64_t *usum) {
     uint64_t sum = 0;
     uint32_t units;
     for (uint32_t s = threadIdx.x; s < a.slots; s += WARPS * 32) {
         slot_info(a, s, RT, &units);
-        sum += units;
+        if (units) sum += units + (1ull << 40);
     }
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(DGT_FULL, sum, d);
     if (lane_id() == 0) usum[threadIdx.x >> 5] = sum;
     __syncthreads();
-    uint64_t U = 0;
+    Units u{0};
 #pragma unroll
-    for (uint32_t w = 0; w < WARPS; w++) U += usum[w];
-    return U;
+    for (uint32_t w = 0; w < WARPS; w++) u.packed += usum[w];
+    return u;
 }
 
 // The row tiles s0 .. s0 + AT_CHUNK - 1 into shared memory; returns their units.
 template <uint32_t WARPS>
-__device__ __forceinline__ uint32_t describe(const AttnArgs &a, uint32_t RT, uint32_t s0, Slot *slots, uint32_t *wsum) {
+__device__ __forceinline__ Units describe(const AttnArgs &a, uint32_t RT, uint32_t s0, Slot *slots, uint64_t *usum) {
     const uint32_t tid = threadIdx.x, warp = tid >> 5;
     __syncthreads();   // the tiles described before are done with
     Slot s{};
@@ -155,48 +164,147 @@ __device__ __forceinline__ uint32_t describe(const AttnArgs &a, uint32_t RT, uin
         if (s0 + tid < a.slots) s = slot_info(a, s0 + tid, RT, &units);
         uint32_t wtot;
         before = warp_excl_scan(units, &wtot);
-        if (lane_id() == 0) wsum[warp] = wtot;
+        const uint32_t tiles = __popc(__ballot_sync(DGT_FULL, units != 0));
+        if (lane_id() == 0) usum[warp] = wtot + ((uint64_t)tiles << 40);
     }
     __syncthreads();
-    uint32_t tot = 0;
+    Units u{0};
 #pragma unroll
     for (uint32_t w = 0; w < AT_CHUNK / 32; w++) {
-        if (w < warp) before += wsum[w];
-        tot += wsum[w];
+        if (w < warp) before += (uint32_t)usum[w];
+        u.packed += usum[w];
     }
     if (warp < AT_CHUNK / 32) {
         s.base = before;
         slots[tid] = s;
     }
     __syncthreads();
-    return tot;
+    return u;
 }
 
 // A run of pages [pa, pe) of head h's segment of a described tile, beginning
-// at unit u and ending by unit u1; `slot`: a tile at or before it.
+// at unit u and ending by unit u1.
 struct Run {
     uint32_t u, slot, h, pa, pe;
 };
-__device__ __forceinline__ Run run_at(const Slot *slots, uint32_t nslots, uint32_t u, uint32_t u1, uint32_t slot) {
+__device__ __forceinline__ Run run_at(const Slot *slots, uint32_t nslots, uint32_t u, uint32_t u1) {
+    uint32_t lo = 0, hi = nslots;   // the last tile that begins at or before u
+    while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) >> 1;
+        if (slots[mid].base <= u) lo = mid;
+        else hi = mid;
+    }
     Run r;
-    while (slot + 1 < nslots && slots[slot + 1].base <= u) slot++;
-    const Slot &s = slots[slot];
+    const Slot &s = slots[lo];
     const uint32_t n = s.per_head();
-    r.u = u, r.slot = slot, r.h = (u - s.base) / n, r.pa = (u - s.base) % n;
+    r.u = u, r.slot = lo, r.h = (u - s.base) / n, r.pa = (u - s.base) % n;
     r.pe = min(n, r.pa + (u1 - u));
     return r;
 }
 
-// One element of a finished row: v its numerator, M, MU, L its maxima and
-// denominator, weights of up to 2^wlog2.
-template <uint32_t D>
-__device__ __forceinline__ void write_out(const AttnArgs &a, const Slot &s, uint32_t h, uint32_t row, uint32_t d,
-                                          float v, float M, float MU, float L, float wlog2) {
-    const uint32_t flat = s.row0 + row;
-    const uint64_t at = (uint64_t)(s.tok0 + flat / a.group) * a.q_heads + h * a.group + flat % a.group;
-    const bool none = M == -INFINITY && L == 0.0f;
-    a.out[at * D + d] = f32_to_bf16_rne(none ? 0.0f : v * ex2(finite_base(MU) - finite_base(M) - wlog2) / L);
-    if (a.lse && d == 0) a.lse[at] = none ? -INFINITY : (M + __log2f(L)) * LN2;
+// Where the CTAs' shares begin.
+struct Cuts {
+    uint64_t U;
+    uint32_t C, tol;          // CTA c at unit c U / C, or at a segment's border within tol of that
+    bool parts;               // or: one part of one segment, units [u0, u1) of the only chunk,
+    uint32_t u0, u1, c0, c1;  // the segment's other parts with the CTAs c0..c1
+    __device__ __forceinline__ uint64_t raw(uint32_t c) const {
+        return U < (1u << 22) ? (uint32_t)U * c / C : U * c / C;   // C < 2^10
+    }
+    // unit u of a described chunk, moved to a segment's border
+    __device__ __forceinline__ uint32_t snap(const Slot *slots, uint32_t nslots, uint32_t u) const {
+        if (tol == 0) return u;
+        const Run r = run_at(slots, nslots, u, u + 1);
+        const uint32_t n = slots[r.slot].per_head(), below = r.pa, above = n - r.pa;
+        return below <= tol || above <= tol ? (below <= above ? u - below : u + above) : u;
+    }
+    // this CTA's units of the chunk [base, base + tot)
+    __device__ __forceinline__ void share(const Slot *slots, uint32_t nslots, uint64_t base, uint32_t tot, uint32_t &a,
+                                          uint32_t &b) const {
+        if (parts) {
+            a = u0, b = u1;
+            return;
+        }
+        const uint64_t ua = raw(blockIdx.x), ub = raw(blockIdx.x + 1);
+        a = ua <= base ? 0 : ua >= base + tot ? tot : snap(slots, nslots, (uint32_t)(ua - base));
+        b = ub >= base + tot ? tot : ub <= base ? 0 : snap(slots, nslots, (uint32_t)(ub - base));
+    }
+    // the CTAs first..last that hold units of the segment [sa, sb)
+    __device__ __forceinline__ void holders(uint64_t sa, uint64_t sb, uint32_t &first, uint32_t &last) const {
+        if (parts) {
+            first = c0, last = c1;
+            return;
+        }
+        // cuts c with sa + tol < raw(c) < sb - tol stay inside
+        first = (uint32_t)(((sa + tol + 1) * C + U - 1) / U) - 1;
+        last = sb <= tol ? 0u : (uint32_t)(((sb - tol) * C + U - 1) / U) - 1;
+    }
+};
+
+// How a call is cut over `grid` CTAs.  Parts: of at most T pages, T the least
+// for which all parts have a CTA, and min_units; taken while T is no more than
+// `slack` pages above an even share, because a second segment in a CTA costs a
+// segment's end (statistics, stores, the counter, the join: about what twelve
+// pages of 128 dimensions cost).  Otherwise even shares, whose cuts move by an
+// eighth of a share at most.  All warps call it; `fits` is shared memory.
+__device__ __forceinline__ Cuts cut_plan(const AttnArgs &a, Units all, const Slot *slots, uint32_t grid, uint32_t *fits) {
+    const uint64_t U = all.units(), S = (uint64_t)all.tiles() * a.c.kv_heads;
+    const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, heads = a.c.kv_heads;
+    Cuts k;
+    k.U = U;
+    k.C = (uint32_t)min((uint64_t)grid, U);   // shares of one unit at least: cuts inside a segment are distinct
+    k.tol = k.C ? (U < (1u << 30) ? min((uint32_t)U / k.C / 8, 16u) : 16u) : 0u;
+    k.parts = a.slots <= AT_CHUNK && S <= grid && U && U < (1u << 30);
+    if (!k.parts) return k;
+    // two tiles a lane
+    uint32_t n[2], p[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const uint32_t s = 2 * lane + i;
+        // a number without rows has no units: as far as the next begins
+        const uint32_t next = s + 1 < a.slots ? slots[s + 1].base : (uint32_t)U;
+        n[i] = s < a.slots && next > slots[s].base ? slots[s].per_head() : 0;
+    }
+    const uint32_t T0 = max(((uint32_t)U + grid - 1) / grid, a.min_units), step = max(a.slack / 15, 1u);
+    if (warp < 4) {
+#pragma unroll
+        for (uint32_t i = 0; i < 4; i++) {
+            const uint32_t T = T0 + (4 * i + warp) * step;
+            const uint32_t sum = ((n[0] + T - 1) / T + (n[1] + T - 1) / T) * heads;
+            const uint32_t cnt = __reduce_add_sync(DGT_FULL, sum);
+            if (lane == 0) fits[4 * i + warp] = cnt <= grid;
+        }
+    }
+    __syncthreads();
+    const uint32_t ok = __ballot_sync(DGT_FULL, lane < 16 && fits[lane & 15]);
+    if (!ok) {
+        k.parts = false;
+        return k;
+    }
+    const uint32_t T = T0 + (__ffs(ok) - 1) * step;
+#pragma unroll
+    for (int i = 0; i < 2; i++) p[i] = (n[i] + T - 1) / T;
+    uint32_t cnt;
+    const uint32_t ex = warp_excl_scan((p[0] + p[1]) * heads, &cnt);
+    k.C = cnt;
+    // the tile of this CTA's part
+    const uint32_t cta = blockIdx.x, mid = ex + p[0] * heads;
+    const uint32_t who = __ballot_sync(DGT_FULL, cta >= ex && cta < mid + p[1] * heads);
+    if (!who) {
+        k.u0 = k.u1 = 0;
+        return k;
+    }
+    const int src = __ffs(who) - 1;
+    const bool second = cta >= mid;
+    const uint32_t first = __shfl_sync(DGT_FULL, second ? mid : ex, src);
+    const uint32_t parts = __shfl_sync(DGT_FULL, second ? p[1] : p[0], src), pages = __shfl_sync(DGT_FULL, second ? n[1] : n[0], src);
+    const uint32_t slot = 2 * src + __shfl_sync(DGT_FULL, (uint32_t)second, src);
+    const uint32_t h = (cta - first) / parts, j = (cta - first) % parts, at = slots[slot].base + h * pages;
+    k.u0 = at + j * pages / parts;
+    k.u1 = at + (j + 1) * pages / parts;
+    k.c0 = first + h * parts;
+    k.c1 = k.c0 + parts - 1;
+    return k;
 }
 
 // Rows that see nothing: out 0, lse -inf.
@@ -213,92 +321,124 @@ __device__ __forceinline__ void write_none(const AttnArgs &a, const Slot &s, uin
 // The parts of a segment, left by the CTAs c0..c1 that hold its units (two
 // parts of PART floats a CTA: a row's M, MU, L, then its numerators), added in
 // page order by `threads` threads, this one number t, which all call it; sync
-// is their barrier, sh shared memory of join_floats(RT) floats.  The parts'
-// statistics come in blocks, a load per thread; then four elements at a time
-// are weighted and added, several loads in flight.
-constexpr uint32_t JOIN_PARTS = 32;   // parts of a block, when rows are few
-__host__ __device__ constexpr uint32_t join_block(uint32_t RT) { return RT >= 128 ? 2 : JOIN_PARTS * 8 / RT; }
-__host__ __device__ constexpr uint32_t join_floats(uint32_t RT) { return join_block(RT) * RT * 3 + 4 * RT; }
+// is their barrier, sh shared memory of join_floats(RT) floats.  First a warp
+// per row, a part per lane, finds the row's maxima and denominator; then four
+// elements at a time are weighted and added, the parts' loads in flight
+// together.
+constexpr uint32_t JOIN_PARTS = 32;
+__host__ __device__ constexpr uint32_t join_floats(uint32_t RT) { return RT >= 128 ? 2 * RT : (JOIN_PARTS + 2) * RT; }
 template <uint32_t D, uint32_t PART, uint32_t RT, typename Sync>
-__device__ __forceinline__ void join_parts(const AttnArgs &a, const Slot &s, uint32_t h, uint64_t c0, uint64_t c1,
+__device__ __forceinline__ void join_parts(const AttnArgs &a, const Slot &s, uint32_t h, uint32_t c0, uint32_t c1,
                                            uint32_t t, uint32_t threads, float wlog2, float *sh, Sync sync) {
-    constexpr uint32_t KB = join_block(RT);
-    float *rows = sh + KB * RT * 3;   // per row M, MU, L, then the quotient's factor
-    const uint32_t parts = (uint32_t)(c1 - c0 + 1);
+    constexpr bool MANY = RT >= 128;   // many rows, few parts: a thread per row, weights found again
+    float2 *rows = reinterpret_cast<float2 *>(sh);   // per row MU, the quotient's factor
+    float *weight = sh + 2 * RT;                     // per part and row
+    const uint32_t parts = c1 - c0 + 1;
     // part 0 is the one that begins the segment, at the end of its CTA's work
-    auto at = [&](uint32_t k, uint32_t row) { return a.part + (2 * (c0 + k) + (k == 0 ? 1 : 0)) * PART + row * (D + 4); };
-    auto load_block = [&](uint32_t k0) {
-        for (uint32_t i = t; i < KB * RT; i += threads) {
-            const uint32_t k = k0 + i / RT, row = i % RT;
-            if (k < parts && row < s.rows) {
-                const float4 st = __ldcg(reinterpret_cast<const float4 *>(at(k, row)));
-                sh[3 * i] = st.x, sh[3 * i + 1] = st.y, sh[3 * i + 2] = st.z;
-            }
-        }
-        sync();
+    auto at = [&](uint32_t k, uint32_t row) {
+        return a.part + (2 * (uint64_t)(c0 + k) + (k == 0 ? 1 : 0)) * PART + row * (D + 4);
     };
-    for (uint32_t k0 = 0; k0 < parts; k0 += KB) {
-        if (k0) sync();
-        load_block(k0);
+    auto finish = [&](uint32_t row, float M, float MU, float L) {
+        const bool none = M == -INFINITY && L == 0.0f;
+        rows[row] = make_float2(finite_base(MU), none ? 0.0f : ex2(finite_base(MU) - finite_base(M) - wlog2) / L);
+        if (a.lse) {
+            const uint32_t flat = s.row0 + row;
+            a.lse[(uint64_t)(s.tok0 + flat / a.group) * a.q_heads + h * a.group + flat % a.group] =
+                none ? -INFINITY : (M + __log2f(L)) * LN2;
+        }
+    };
+    if (MANY) {
         for (uint32_t row = t; row < s.rows; row += threads) {
-            float *r = rows + 4 * row;
-            float M = k0 ? r[0] : -INFINITY, MU = k0 ? r[1] : -INFINITY, L = k0 ? r[2] : 0.0f;
-            const uint32_t n = min(KB, parts - k0);
-            float m = M;
-            for (uint32_t k = 0; k < n; k++) {
-                m = fmaxf(m, sh[3 * (k * RT + row)]);
-                MU = fmaxf(MU, sh[3 * (k * RT + row) + 1]);
+            float M = -INFINITY, MU = -INFINITY, L = 0.0f;
+#pragma unroll 4
+            for (uint32_t k = 0; k < parts; k++) {
+                const float4 st = __ldcg(reinterpret_cast<const float4 *>(at(k, row)));
+                const float m = fmaxf(M, st.x), b = finite_base(m);
+                L = L * ex2(M - b) + st.z * ex2(st.x - b);
+                M = m;
+                MU = fmaxf(MU, st.y);
             }
-            const float b = finite_base(m);
-            L *= ex2(M - b);
-            for (uint32_t k = 0; k < n; k++) L += sh[3 * (k * RT + row) + 2] * ex2(sh[3 * (k * RT + row)] - b);
-            r[0] = m, r[1] = MU, r[2] = L;
-            if (k0 + KB >= parts) {
-                const bool none = m == -INFINITY && L == 0.0f;
-                r[3] = none ? 0.0f : ex2(finite_base(MU) - b - wlog2) / L;
-                if (a.lse) {
-                    const uint32_t flat = s.row0 + row;
-                    a.lse[(uint64_t)(s.tok0 + flat / a.group) * a.q_heads + h * a.group + flat % a.group] =
-                        none ? -INFINITY : (m + __log2f(L)) * LN2;
+            finish(row, M, MU, L);
+        }
+    } else {
+        const uint32_t lane = t & 31;
+        for (uint32_t row = t >> 5; row < s.rows; row += threads >> 5) {
+            float M = -INFINITY, MU = -INFINITY, L = 0.0f, mu0 = -INFINITY;
+            for (uint32_t k0 = 0; k0 < parts; k0 += 32) {
+                float4 st = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
+                if (k0 + lane < parts) st = __ldcg(reinterpret_cast<const float4 *>(at(k0 + lane, row)));
+                if (k0 == 0) mu0 = st.y;
+                float m = fmaxf(M, st.x), u = st.y;
+#pragma unroll
+                for (int d = 16; d >= 1; d >>= 1) {
+                    m = fmaxf(m, __shfl_xor_sync(DGT_FULL, m, d));
+                    u = fmaxf(u, __shfl_xor_sync(DGT_FULL, u, d));
                 }
+                const float b = finite_base(m);
+                float l = st.z * ex2(st.x - b);
+#pragma unroll
+                for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(DGT_FULL, l, d);
+                L = L * ex2(M - b) + l;
+                M = m;
+                MU = fmaxf(MU, u);
             }
+            weight[lane * RT + row] = ex2(mu0 - finite_base(MU));
+            if (lane == 0) finish(row, M, MU, L);
         }
     }
     sync();
-    const bool one = parts <= KB;   // the statistics of every part are still here
-    constexpr uint32_t Q = D / 4, B = RT >= 128 ? 4 : 1, UN = RT >= 128 ? 2 : 8;   // B elements of four in flight, UN parts
+    constexpr uint32_t Q = D / 4, B = MANY ? 4 : 1, UN = MANY ? 1 : 8;   // B elements of four in flight, UN parts
     const uint32_t all = s.rows * Q;
     for (uint32_t i0 = t; i0 < all; i0 += B * threads) {
         float v[B][4] = {};
-#pragma unroll UN
-        for (uint32_t k = 0; k < parts; k++) {
-            float mu[B];
+        float2 ro[B];
+#pragma unroll
+        for (uint32_t b = 0; b < B; b++) ro[b] = rows[min(i0 + b * threads, all - 1) / Q];
+        // the parts' loads stand together: no branch between them
+        auto add = [&](uint32_t k, bool known) {
+            float f[B];
             float4 x[B];
 #pragma unroll
             for (uint32_t b = 0; b < B; b++) {
                 const uint32_t i = min(i0 + b * threads, all - 1), row = i / Q;
                 const float *p = at(k, row);
-                mu[b] = one ? sh[3 * (k * RT + row) + 1] : __ldcg(p + 1);
                 x[b] = __ldcg(reinterpret_cast<const float4 *>(p + 4 + (i % Q) * 4));
+                f[b] = known ? weight[k * RT + row] : ex2(__ldcg(p + 1) - ro[b].x);
             }
 #pragma unroll
-            for (uint32_t b = 0; b < B; b++) {
-                const float f = ex2(mu[b] - finite_base(rows[4 * (min(i0 + b * threads, all - 1) / Q) + 1]));
-                v[b][0] += x[b].x * f, v[b][1] += x[b].y * f, v[b][2] += x[b].z * f, v[b][3] += x[b].w * f;
-            }
+            for (uint32_t b = 0; b < B; b++)
+                v[b][0] += x[b].x * f[b], v[b][1] += x[b].y * f[b], v[b][2] += x[b].z * f[b], v[b][3] += x[b].w * f[b];
+        };
+        uint32_t k = 0;
+        if constexpr (!MANY) {
+            const uint32_t known = min(parts, JOIN_PARTS);
+#pragma unroll UN
+            for (; k < known; k++) add(k, true);
         }
+#pragma unroll 2
+        for (; k < parts; k++) add(k, false);
 #pragma unroll
         for (uint32_t b = 0; b < B; b++) {
             const uint32_t i = i0 + b * threads;
             if (i >= all) break;
-            const float quot = rows[4 * (i / Q) + 3];
             const uint32_t flat = s.row0 + i / Q;
             const uint64_t o = (uint64_t)(s.tok0 + flat / a.group) * a.q_heads + h * a.group + flat % a.group;
             *reinterpret_cast<uint2 *>(a.out + o * D + (i % Q) * 4) =
-                make_uint2(bf16x2(v[b][0] * quot, v[b][1] * quot), bf16x2(v[b][2] * quot, v[b][3] * quot));
+                make_uint2(bf16x2(v[b][0] * ro[b].y, v[b][1] * ro[b].y), bf16x2(v[b][2] * ro[b].y, v[b][3] * ro[b].y));
         }
     }
     sync();   // sh and the parts are done with
+}
+
+// A CTA's arrival at a segment's counter, after a barrier behind its part's
+// stores: true for the last of `parts` to arrive, which then sees all parts
+// (behind another barrier for the other threads).
+__device__ __forceinline__ bool arrive_last(int32_t *count, uint32_t parts) {
+    int32_t was;
+    asm volatile("atom.add.acq_rel.gpu.s32 %0, [%1], 1;" : "=r"(was) : "l"(count) : "memory");
+    if (was != (int32_t)(parts - 1)) return false;
+    *count = 0;
+    return true;
 }
 
 }  // namespace dgt

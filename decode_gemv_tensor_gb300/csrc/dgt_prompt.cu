@@ -91,10 +91,10 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
     __shared__ __align__(8) uint64_t kfull[KS], kfree[KS], vfull[VS], vfree[VS], wfull[WS], wfree[WS];
     __shared__ __align__(8) uint64_t sfull[4], pfull[4], ofull[2], ofin[2], qfull[2], mfull[PR_META], drained;
     __shared__ PageMeta meta[PR_META];
-    __shared__ float joined[join_floats(RT)];
+    __shared__ __align__(8) float joined[join_floats(RT)];
     __shared__ Slot slots[AT_CHUNK];
+    __shared__ uint32_t fits[16];
     __shared__ uint64_t usum[PR_WARPS];
-    __shared__ uint32_t wsum[PR_WARPS];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag, last_flag;
     // the warp's number out of a shuffle: the compiler then knows that it is the warp's
@@ -130,11 +130,10 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
     const uint32_t tm = tmem_slot;
     volatile int *abortp = &abort_flag;
 
-    uint32_t tot = describe<PR_WARPS>(a, RT, 0, slots, wsum);
-    const uint64_t U = a.slots <= AT_CHUNK ? tot : all_units<PR_WARPS>(a, RT, usum);
-    const uint64_t most = (U + a.min_units - 1) / a.min_units;
-    const uint64_t C = most < gridDim.x ? most : gridDim.x;
-    const uint64_t ua = C ? blockIdx.x * U / C : 0, ub = blockIdx.x < C ? (blockIdx.x + 1) * U / C : 0;
+    Units here = describe<PR_WARPS>(a, RT, 0, slots, usum);
+    const Units all = a.slots <= AT_CHUNK ? here : all_units<PR_WARPS>(a, RT, usum);
+    const Cuts cut = cut_plan(a, all, slots, gridDim.x, fits);
+    const uint64_t ub = blockIdx.x >= cut.C ? 0 : cut.parts ? cut.U : cut.raw(blockIdx.x + 1);
 
     bool dead = false;   // a wait ran out, here or elsewhere in the CTA: no more work from this warp
     // a whole warp's wait: mostly the phase has ended already
@@ -157,15 +156,15 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
 
     uint64_t base0 = 0;
     for (uint32_t s0 = 0; s0 < a.slots && base0 < ub; s0 += AT_CHUNK) {
-        if (s0) tot = describe<PR_WARPS>(a, RT, s0, slots, wsum);
-        const uint64_t first = base0 > ua ? base0 : ua, end = base0 + tot < ub ? base0 + tot : ub;
-        const uint32_t u0 = (uint32_t)(first - base0), u1 = end > first ? (uint32_t)(end - base0) : u0;
-        const uint64_t chunk_base = base0;
+        if (s0) here = describe<PR_WARPS>(a, RT, s0, slots, usum);
+        const uint32_t tot = (uint32_t)here.units();
         const uint32_t nslots = min(AT_CHUNK, a.slots - s0);
+        const uint64_t chunk_base = base0;
         base0 += tot;
-        for (uint32_t u = u0, hint = 0; u < u1;) {
-            const Run r = run_at(slots, nslots, u, u1, hint);
-            hint = r.slot;
+        uint32_t u0, u1;
+        cut.share(slots, nslots, chunk_base, tot, u0, u1);
+        for (uint32_t u = u0; u < u1;) {
+            const Run r = run_at(slots, nslots, u, u1);
             u += r.pe - r.pa;
             const Slot &s = slots[r.slot];
             const uint32_t n = s.per_head();
@@ -311,7 +310,8 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                     const uint32_t src = base + Cfg::v + (c % VS) * PB, dst = base + Cfg::w + (c % WS) * PB * 2;
                     const bool used = meta[c % PR_META].used != 0;
                     // 16 bytes a thread: row at / 4, its tokens 16 (at % 4) ..
-                    constexpr uint32_t B = 4;
+                    constexpr uint32_t B = D * 4 / PR_CONV < 4 ? D * 4 / PR_CONV : 4;
+                    static_assert(D * 4 % (B * PR_CONV) == 0, "a page's pieces divide evenly over the threads");
 #pragma unroll 1
                     for (uint32_t i0 = ct; i0 < D * 4; i0 += B * PR_CONV) {
                         uint4 x[B];
@@ -507,8 +507,7 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                             tmem_ld32(tm + tl + t * D + d0, o);
                             tmem_wait_ld();
                         }
-                        if (!live) continue;
-                        if (complete) {
+                        if (live && complete) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 8) {
                                 uint32_t w[4];
@@ -517,11 +516,12 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                                     w[e] = bf16x2(__uint_as_float(o[i + 2 * e]) * quot, __uint_as_float(o[i + 2 * e + 1]) * quot);
                                 *reinterpret_cast<uint4 *>(a.out + at * D + d0 + i) = make_uint4(w[0], w[1], w[2], w[3]);
                             }
-                        } else {
+                        } else if (live) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 4)
                                 *reinterpret_cast<uint4 *>(part + 4 + d0 + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                         }
+                        __syncwarp();   // the next load is the whole warp's
                     }
                     if (live && complete && a.lse) a.lse[at] = none ? -INFINITY : (m + __log2f(l)) * LN2;
                     if (live && !complete) *reinterpret_cast<float4 *>(part) = make_float4(m, mu, l, 0.0f);
@@ -530,15 +530,10 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                 if (!complete) {
                     // the last CTA of the segment to arrive adds its parts in page order
                     const uint64_t sa = chunk_base + s.base + (uint64_t)r.h * n, sb = sa + n;
-                    const uint64_t c0 = ((sa + 1) * C - 1) / U, c1 = (sb * C - 1) / U;
+                    uint32_t c0, c1;
+                    cut.holders(sa, sb, c0, c1);
                     bar_rows();
-                    if (tid == 0) {
-                        __threadfence();   // what the rows' threads wrote, the barrier before it, is seen with the arrival
-                        const int32_t was = atomicAdd(&a.count[c0], 1);
-                        last_flag = was == (int32_t)(c1 - c0);
-                        if (last_flag) a.count[c0] = 0;
-                        __threadfence();
-                    }
+                    if (tid == 0) last_flag = arrive_last(&a.count[c0], c1 - c0 + 1);
                     bar_rows();
                     if (last_flag)
                         join_parts<D, Cfg::PART, RT>(a, s, r.h, c0, c1, tid, 256, PR_W_LOG2, joined, bar_rows);
@@ -580,7 +575,7 @@ static int prompt_launch_d(const AttnArgs &a, cudaStream_t st) {
             return DGT_ERR_CUDA;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    const unsigned grid = (unsigned)di.sms < AT_MAX_CTAS ? (unsigned)di.sms : AT_MAX_CTAS;
+    const unsigned grid = (unsigned)di.sms < PR_MAX_CTAS ? (unsigned)di.sms : PR_MAX_CTAS;
     return launch_pdl(fn, dim3(grid), dim3(PR_WARPS * 32), PromptCfg<D>::bytes, st, a) == cudaSuccess ? DGT_OK
                                                                                                       : DGT_ERR_CUDA;
 }
