@@ -68,7 +68,6 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) k_kv_attention(AttnArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bar[AT_WARPS][NS];
     __shared__ Slot slots[AT_CHUNK];
-    __shared__ uint32_t fits[16];
     __shared__ float stat[AT_WARPS][RT][3];
     __shared__ float rowstat[RT][3];
     __shared__ float rowfac[RT];
@@ -84,13 +83,15 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) k_kv_attention(AttnArgs a) {
     // ---- the CTA's units
     Units here = describe<AT_WARPS>(a, RT, 0, slots, usum);
     const Units all = a.slots <= AT_CHUNK ? here : all_units<AT_WARPS>(a, RT, usum);
-    const Cuts cut = cut_plan(a, all, slots, gridDim.x, fits);
+    const Cuts cut = cut_plan(a, all, slots, gridDim.x);
     if (blockIdx.x >= cut.C) return;
     const uint64_t ub = cut.parts ? cut.U : cut.raw(blockIdx.x + 1);
 
     const uint32_t ring = smem_u32(smem) + warp * NS * IB;
     float *scratch = reinterpret_cast<float *>(smem + Cfg::scratch);
     const uint32_t qs = smem_u32(smem + Cfg::q);
+    // pages are read once: they leave L2 first, tables, lengths and queries stay
+    const uint64_t once = l2_evict_first();
     uint32_t issued = 0, taken = 0;   // items of this warp's ring
     bool dead = false;                // a wait ran out: no more work from this warp
 
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) k_kv_attention(AttnArgs a) {
                     const uint32_t st = issued % NS, fb = smem_u32(&bar[warp][st]);
                     fence_proxy_async_smem();
                     mbar_arrive_expect_tx(fb, IB);
-                    bulk_g2s(ring + st * IB, src, IB, fb);
+                    bulk_g2s_once(ring + st * IB, src, IB, fb, once);
                 }
                 issued++;
                 if (++ik == IPP) {

@@ -246,15 +246,16 @@ struct Cuts {
 // `slack` pages above an even share, because a second segment in a CTA costs a
 // segment's end (statistics, stores, the counter, the join: about what twelve
 // pages of 128 dimensions cost).  Otherwise even shares, whose cuts move by an
-// eighth of a share at most.  All warps call it; `fits` is shared memory.
-__device__ __forceinline__ Cuts cut_plan(const AttnArgs &a, Units all, const Slot *slots, uint32_t grid, uint32_t *fits) {
+// eighth of a share at most.
+__device__ __forceinline__ Cuts cut_plan(const AttnArgs &a, Units all, const Slot *slots, uint32_t grid) {
     const uint64_t U = all.units(), S = (uint64_t)all.tiles() * a.c.kv_heads;
-    const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, heads = a.c.kv_heads;
+    const uint32_t lane = lane_id(), heads = a.c.kv_heads;
     Cuts k;
     k.U = U;
     k.C = (uint32_t)min((uint64_t)grid, U);   // shares of one unit at least: cuts inside a segment are distinct
-    k.tol = k.C ? (U < (1u << 30) ? min((uint32_t)U / k.C / 8, 16u) : 16u) : 0u;
-    k.parts = a.slots <= AT_CHUNK && S <= grid && U && U < (1u << 30);
+    k.tol = (uint32_t)min(U / (8 * grid), (uint64_t)16);
+    // (U below 2^22: a segment's pages and T then are below 2^23)
+    k.parts = a.slots <= AT_CHUNK && S <= grid && U && U < (1u << 22);
     if (!k.parts) return k;
     // two tiles a lane
     uint32_t n[2], p[2];
@@ -265,25 +266,27 @@ __device__ __forceinline__ Cuts cut_plan(const AttnArgs &a, Units all, const Slo
         const uint32_t next = s + 1 < a.slots ? slots[s + 1].base : (uint32_t)U;
         n[i] = s < a.slots && next > slots[s].base ? slots[s].per_head() : 0;
     }
-    const uint32_t T0 = max(((uint32_t)U + grid - 1) / grid, a.min_units), step = max(a.slack / 15, 1u);
-    if (warp < 4) {
+    auto pieces = [](uint32_t x, uint32_t T, float inv) {   // ceil(x / T), x below 2^23
+        x += T - 1;
+        uint32_t q = (uint32_t)((float)x * inv);
+        if (q * T > x) q--;
+        if ((q + 1) * T <= x) q++;
+        return q;
+    };
+    const uint32_t T0 = max(((uint32_t)U + grid - 1) / grid, a.min_units);
+    uint32_t T = 0;
 #pragma unroll
-        for (uint32_t i = 0; i < 4; i++) {
-            const uint32_t T = T0 + (4 * i + warp) * step;
-            const uint32_t sum = ((n[0] + T - 1) / T + (n[1] + T - 1) / T) * heads;
-            const uint32_t cnt = __reduce_add_sync(DGT_FULL, sum);
-            if (lane == 0) fits[4 * i + warp] = cnt <= grid;
-        }
+    for (uint32_t i = 0; i < 6; i++) {
+        const uint32_t t = T0 + a.slack * (5 - i) / 5;
+        const float inv = 1.0f / (float)t;
+        const uint32_t p0 = pieces(n[0], t, inv), p1 = pieces(n[1], t, inv);
+        // the least that fits comes last
+        if (__reduce_add_sync(DGT_FULL, (p0 + p1) * heads) <= grid) T = t, p[0] = p0, p[1] = p1;
     }
-    __syncthreads();
-    const uint32_t ok = __ballot_sync(DGT_FULL, lane < 16 && fits[lane & 15]);
-    if (!ok) {
+    if (!T) {
         k.parts = false;
         return k;
     }
-    const uint32_t T = T0 + (__ffs(ok) - 1) * step;
-#pragma unroll
-    for (int i = 0; i < 2; i++) p[i] = (n[i] + T - 1) / T;
     uint32_t cnt;
     const uint32_t ex = warp_excl_scan((p[0] + p[1]) * heads, &cnt);
     k.C = cnt;
@@ -361,62 +364,75 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, const Slot &s, uin
             finish(row, M, MU, L);
         }
     } else {
-        const uint32_t lane = t & 31;
-        for (uint32_t row = t >> 5; row < s.rows; row += threads >> 5) {
-            float M = -INFINITY, MU = -INFINITY, L = 0.0f, mu0 = -INFINITY;
-            for (uint32_t k0 = 0; k0 < parts; k0 += 32) {
-                float4 st = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
-                if (k0 + lane < parts) st = __ldcg(reinterpret_cast<const float4 *>(at(k0 + lane, row)));
-                if (k0 == 0) mu0 = st.y;
-                float m = fmaxf(M, st.x), u = st.y;
+        // RPW rows a warp, their loads together
+        constexpr uint32_t RPW = MANY ? 1 : RT / 4;
+        const uint32_t lane = t & 31, warp = t >> 5;
+        float M[RPW], MU[RPW], L[RPW], mu0[RPW];
+#pragma unroll
+        for (uint32_t i = 0; i < RPW; i++) M[i] = MU[i] = -INFINITY, L[i] = 0.0f;
+        for (uint32_t k0 = 0; k0 < parts; k0 += 32) {
+            float4 st[RPW];
+#pragma unroll
+            for (uint32_t i = 0; i < RPW; i++) {
+                st[i] = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
+                if (k0 + lane < parts && warp + 4 * i < s.rows)
+                    st[i] = __ldcg(reinterpret_cast<const float4 *>(at(k0 + lane, warp + 4 * i)));
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < RPW; i++) {
+                if (k0 == 0) mu0[i] = st[i].y;
+                float m = fmaxf(M[i], st[i].x), u = st[i].y;
 #pragma unroll
                 for (int d = 16; d >= 1; d >>= 1) {
                     m = fmaxf(m, __shfl_xor_sync(DGT_FULL, m, d));
                     u = fmaxf(u, __shfl_xor_sync(DGT_FULL, u, d));
                 }
                 const float b = finite_base(m);
-                float l = st.z * ex2(st.x - b);
+                float l = st[i].z * ex2(st[i].x - b);
 #pragma unroll
                 for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(DGT_FULL, l, d);
-                L = L * ex2(M - b) + l;
-                M = m;
-                MU = fmaxf(MU, u);
+                L[i] = L[i] * ex2(M[i] - b) + l;
+                M[i] = m;
+                MU[i] = fmaxf(MU[i], u);
             }
-            weight[lane * RT + row] = ex2(mu0 - finite_base(MU));
-            if (lane == 0) finish(row, M, MU, L);
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < RPW; i++) {
+            const uint32_t row = warp + 4 * i;
+            if (row >= s.rows) break;
+            weight[lane * RT + row] = ex2(mu0[i] - finite_base(MU[i]));
+            if (lane == 0) finish(row, M[i], MU[i], L[i]);
         }
     }
     sync();
-    constexpr uint32_t Q = D / 4, B = MANY ? 4 : 1, UN = MANY ? 1 : 8;   // B elements of four in flight, UN parts
+    constexpr uint32_t Q = D / 4, B = MANY ? 4 : RT / 8, UN = MANY ? 2 : RT <= 8 ? 8 : 4;   // B elements of four in flight, UN parts
     const uint32_t all = s.rows * Q;
     for (uint32_t i0 = t; i0 < all; i0 += B * threads) {
         float v[B][4] = {};
         float2 ro[B];
 #pragma unroll
         for (uint32_t b = 0; b < B; b++) ro[b] = rows[min(i0 + b * threads, all - 1) / Q];
-        // the parts' loads stand together: no branch between them
-        auto add = [&](uint32_t k, bool known) {
-            float f[B];
-            float4 x[B];
+        // UN parts' loads together; past the last part the last again, with weight 0
+        for (uint32_t k0 = 0; k0 < parts; k0 += UN) {
+            float f[UN][B];
+            float4 x[UN][B];
 #pragma unroll
-            for (uint32_t b = 0; b < B; b++) {
-                const uint32_t i = min(i0 + b * threads, all - 1), row = i / Q;
-                const float *p = at(k, row);
-                x[b] = __ldcg(reinterpret_cast<const float4 *>(p + 4 + (i % Q) * 4));
-                f[b] = known ? weight[k * RT + row] : ex2(__ldcg(p + 1) - ro[b].x);
-            }
+            for (uint32_t j = 0; j < UN; j++)
 #pragma unroll
-            for (uint32_t b = 0; b < B; b++)
-                v[b][0] += x[b].x * f[b], v[b][1] += x[b].y * f[b], v[b][2] += x[b].z * f[b], v[b][3] += x[b].w * f[b];
-        };
-        uint32_t k = 0;
-        if constexpr (!MANY) {
-            const uint32_t known = min(parts, JOIN_PARTS);
-#pragma unroll UN
-            for (; k < known; k++) add(k, true);
+                for (uint32_t b = 0; b < B; b++) {
+                    const uint32_t i = min(i0 + b * threads, all - 1), row = i / Q, k = min(k0 + j, parts - 1);
+                    const float *p = at(k, row);
+                    x[j][b] = __ldcg(reinterpret_cast<const float4 *>(p + 4 + (i % Q) * 4));
+                    f[j][b] = !MANY && k0 < JOIN_PARTS ? weight[k * RT + row] : __ldcg(p + 1) - ro[b].x;
+                }
+#pragma unroll
+            for (uint32_t j = 0; j < UN; j++)
+#pragma unroll
+                for (uint32_t b = 0; b < B; b++) {
+                    const float w = k0 + j >= parts ? 0.0f : !MANY && k0 < JOIN_PARTS ? f[j][b] : ex2(f[j][b]);
+                    v[b][0] += x[j][b].x * w, v[b][1] += x[j][b].y * w, v[b][2] += x[j][b].z * w, v[b][3] += x[j][b].w * w;
+                }
         }
-#pragma unroll 2
-        for (; k < parts; k++) add(k, false);
 #pragma unroll
         for (uint32_t b = 0; b < B; b++) {
             const uint32_t i = i0 + b * threads;

@@ -93,7 +93,6 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
     __shared__ PageMeta meta[PR_META];
     __shared__ __align__(8) float joined[join_floats(RT)];
     __shared__ Slot slots[AT_CHUNK];
-    __shared__ uint32_t fits[16];
     __shared__ uint64_t usum[PR_WARPS];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag, last_flag;
@@ -132,7 +131,7 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
 
     Units here = describe<PR_WARPS>(a, RT, 0, slots, usum);
     const Units all = a.slots <= AT_CHUNK ? here : all_units<PR_WARPS>(a, RT, usum);
-    const Cuts cut = cut_plan(a, all, slots, gridDim.x, fits);
+    const Cuts cut = cut_plan(a, all, slots, gridDim.x);
     const uint64_t ub = blockIdx.x >= cut.C ? 0 : cut.parts ? cut.U : cut.raw(blockIdx.x + 1);
 
     bool dead = false;   // a wait ran out, here or elsewhere in the CTA: no more work from this warp
