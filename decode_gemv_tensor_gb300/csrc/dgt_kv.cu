@@ -1,11 +1,13 @@
 // dgt_kv.cu -- the paged 8-bit cache: quantising append, reading back, and the
 // page operations (copy, fork, reserve with copy on write, free, compact).
 //
-// An append is a pass over the new rows: the block's largest magnitude gives
-// the power-of-two scale, the codes follow by one multiplication and one
-// rounding (exact scaling, so the result depends on no order).  Page copies
-// move whole pages, bytes untouched.  Page bookkeeping is integer work on a
-// few words per sequence, done by one CTA in the order of the list.
+// An append reads the new rows of a block once, into registers: the largest
+// magnitude (of the bf16 bits, two at a time) gives the power-of-two scale, the
+// codes follow by one multiplication and one rounding (exact scaling, so the
+// result depends on no order).  Values are transposed four by four through
+// shared memory.  Page copies move whole pages, bytes untouched.  Page
+// bookkeeping is integer work on a few words per sequence, done by one CTA in
+// the order of the list.
 #include "dgt_kv.cuh"
 
 #include "dgt_device.cuh"
@@ -31,12 +33,28 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint16_t c) {
     return __half22float2(__half2(h));
 }
 
-__device__ __forceinline__ float finite_or_zero(float x, bool &bad) {
-    if ((__float_as_uint(x) & 0x7F800000u) == 0x7F800000u) {
-        bad = true;
-        return 0.0f;
-    }
-    return x;
+// A bf16 pair with what is not finite set to zero.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
+    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
+    return w;
+}
+
+// Value tiles in shared memory, 64 tokens of D / 4 words (four dimensions
+// each): the words of a row permuted by its sixteen-token quarter, so that the
+// four quarters of a word, read together, fall into different banks.
+__device__ __forceinline__ uint32_t tile_word(uint32_t D, uint32_t t, uint32_t w) {
+    return t * (D / 4) + (w ^ (8 * ((t >> 4) & (D >= 128 ? 3 : 1))));
+}
+
+// Four words of four bytes, transposed.
+__device__ __forceinline__ void transpose4(uint32_t (&x)[4]) {
+    const uint32_t a = prmt(x[0], x[1], 0x5140u), b = prmt(x[2], x[3], 0x5140u);   // bytes 0 and 1 of each pair
+    const uint32_t c = prmt(x[0], x[1], 0x7362u), d = prmt(x[2], x[3], 0x7362u);   // bytes 2 and 3
+    x[0] = prmt(a, b, 0x5410u);
+    x[1] = prmt(a, b, 0x7632u);
+    x[2] = prmt(c, d, 0x5410u);
+    x[3] = prmt(c, d, 0x7632u);
 }
 
 struct AppendArgs {
@@ -53,9 +71,8 @@ constexpr uint32_t AP_THREADS = 128;
 // One CTA: (block item, head, keys or values).
 template <uint32_t D>
 __global__ void __launch_bounds__(AP_THREADS) k_kv_append(AppendArgs a) {
-    __shared__ float red[AP_THREADS / 32];
-    __shared__ int redbad[AP_THREADS / 32];
-    __shared__ __align__(16) uint8_t tile[KV_P * (D + 4)];
+    __shared__ uint32_t red[AP_THREADS / 32];
+    __shared__ __align__(16) uint32_t tile[KV_P * D / 4];
     pdl_trigger();
     pdl_wait();
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -91,35 +108,55 @@ __global__ void __launch_bounds__(AP_THREADS) k_kv_append(AppendArgs a) {
     uint8_t *dst = (side ? a.c.v : a.c.k) + bi * (KV_P * D);
     float *scale_p = (side ? a.c.v_scale : a.c.k_scale) + bi;
 
-    // the new rows' largest magnitude
-    constexpr uint32_t CH = D / 16;   // 16-element chunks of a row
+    // the new rows, and their largest magnitude
+    constexpr uint32_t CH = D / 16;                          // 16-element chunks of a row
+    constexpr uint32_t N = KV_P * CH / AP_THREADS;           // chunks of a thread
     const uint32_t chunks = (hi - lo) * CH;
-    float amax = 0.0f;
-    bool bad = false;
-    for (uint32_t i = tid; i < chunks; i += AP_THREADS) {
-        const uint16_t *p = src + (int64_t)(i / CH) * x.token_stride + (i % CH) * 16;
-        const uint4 u0 = *reinterpret_cast<const uint4 *>(p), u1 = *reinterpret_cast<const uint4 *>(p + 8);
-        const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+    uint4 u[N][2];
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            amax = fmaxf(amax, fabsf(finite_or_zero(bf16lo(w[j]), bad)));
-            amax = fmaxf(amax, fabsf(finite_or_zero(bf16hi(w[j]), bad)));
+    for (uint32_t k = 0; k < N; k++) {
+        const uint32_t i = tid + k * AP_THREADS;
+        u[k][0] = u[k][1] = make_uint4(0, 0, 0, 0);
+        if (i < chunks) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(src + (int64_t)(i / CH) * x.token_stride + (i % CH) * 16);
+            u[k][0] = p[0];
+            u[k][1] = p[1];
         }
     }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(DGT_FULL, amax, d));
-    bad = __any_sync(DGT_FULL, bad);
-    if (lane == 0) {
-        red[warp] = amax;
-        redbad[warp] = bad;
-    }
     const float s_old = lo ? *scale_p : 0.0f;   // read by all before thread 0 writes it
-    __syncthreads();
+    auto largest = [&]() {
+        uint32_t m = 0;
 #pragma unroll
-    for (uint32_t i = 0; i < AP_THREADS / 32; i++) {
-        amax = fmaxf(amax, red[i]);
-        bad = bad || redbad[i];
+        for (uint32_t k = 0; k < N; k++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const uint4 v = u[k][e];
+                m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                         __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+            }
+        m = __reduce_max_sync(DGT_FULL, max(m & 0xFFFFu, m >> 16));
+        if (lane == 0) red[warp] = m;
+        __syncthreads();
+        m = 0;
+#pragma unroll
+        for (uint32_t i = 0; i < AP_THREADS / 32; i++) m = max(m, red[i]);
+        return m;
+    };
+    uint32_t top = largest();
+    bool bad = top >= 0x7F80u;
+    if (bad) {
+        // a value that is not finite: the block's scale will say so; its finite values as ever
+#pragma unroll
+        for (uint32_t k = 0; k < N; k++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                uint4 &v = u[k][e];
+                v = make_uint4(finite_pair(v.x), finite_pair(v.y), finite_pair(v.z), finite_pair(v.w));
+            }
+        __syncthreads();
+        top = largest();
     }
+    const float amax = __uint_as_float(top << 16);
     int e = scale_exp(amax);
     bool grow = false;
     float down = 1.0f;
@@ -165,40 +202,53 @@ __global__ void __launch_bounds__(AP_THREADS) k_kv_append(AppendArgs a) {
         __syncthreads();   // a value word may hold old and new tokens
     }
 
-    // the new rows
-    for (uint32_t i = tid; i < chunks; i += AP_THREADS) {
+    // codes: a chunk of keys is 16 bytes of its row; values go through the tile
+#pragma unroll
+    for (uint32_t k = 0; k < N; k++) {
+        const uint32_t i = tid + k * AP_THREADS;
+        if (i >= chunks) break;
         const uint32_t r = i / CH, c = i % CH;
-        const uint16_t *p = src + (int64_t)r * x.token_stride + c * 16;
-        const uint4 u0 = *reinterpret_cast<const uint4 *>(p), u1 = *reinterpret_cast<const uint4 *>(p + 8);
-        const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
         uint32_t o[4];
-        bool ignore = false;
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            const float f0 = finite_or_zero(bf16lo(w[2 * j]), ignore) * inv;
-            const float f1 = finite_or_zero(bf16hi(w[2 * j]), ignore) * inv;
-            const float f2 = finite_or_zero(bf16lo(w[2 * j + 1]), ignore) * inv;
-            const float f3 = finite_or_zero(bf16hi(w[2 * j + 1]), ignore) * inv;
-            o[j] = (uint32_t)e4m3x2(f0, f1) | (uint32_t)e4m3x2(f2, f3) << 16;
+            const uint4 v = u[k][j / 2];
+            const uint32_t w0 = j & 1 ? v.z : v.x, w1 = j & 1 ? v.w : v.y;
+            o[j] = (uint32_t)e4m3x2(bf16lo(w0) * inv, bf16hi(w0) * inv) |
+                   (uint32_t)e4m3x2(bf16lo(w1) * inv, bf16hi(w1) * inv) << 16;
         }
-        if (side == 0) {
+        if (side == 0)
             *reinterpret_cast<uint4 *>(dst + kv_k_off(D, lo + r, c * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
-        } else {
-            uint32_t *tp = reinterpret_cast<uint32_t *>(tile + (lo + r) * (D + 4) + c * 16);
-#pragma unroll
-            for (int j = 0; j < 4; j++) tp[j] = o[j];
-        }
+        else
+            *reinterpret_cast<uint4 *>(&tile[tile_word(D, lo + r, 4 * c)]) = make_uint4(o[0], o[1], o[2], o[3]);
     }
     if (side == 0) return;
     __syncthreads();
-    // values: transposed out of shared memory, a word of four tokens at a time
-    const uint32_t w0 = lo / 4, w1 = (hi + 3) / 4;
-    for (uint32_t i = tid; i < D * (w1 - w0); i += AP_THREADS) {
-        const uint32_t d = i / (w1 - w0), t = (w0 + i % (w1 - w0)) * 4;
+    if (lo == 0 && hi == KV_P) {
+        // four dimensions by sixteen tokens a thread, four rows of 16 bytes out
+        for (uint32_t i = tid; i < D; i += AP_THREADS) {
+            const uint32_t q = i & 3, w = i >> 2;
+            uint32_t y[4][4];   // [word of four tokens][dimension]
+#pragma unroll
+            for (uint32_t j = 0; j < 4; j++) {
+#pragma unroll
+                for (uint32_t t = 0; t < 4; t++) y[j][t] = tile[tile_word(D, 16 * q + 4 * j + t, w)];
+                transpose4(y[j]);
+            }
+#pragma unroll
+            for (uint32_t d = 0; d < 4; d++)
+                *reinterpret_cast<uint4 *>(dst + kv_v_off(16 * q, 4 * w + d)) = make_uint4(y[0][d], y[1][d], y[2][d], y[3][d]);
+        }
+        return;
+    }
+    // a part of a block: whole words of four tokens where they are new, bytes at the ends
+    const uint8_t *tb = reinterpret_cast<const uint8_t *>(tile);
+    const uint32_t w0 = lo / 4, nw = (hi + 3) / 4 - w0;
+    for (uint32_t i = tid; i < D * nw; i += AP_THREADS) {
+        const uint32_t d = i / nw, t = (w0 + i % nw) * 4;
+        uint8_t *q = dst + kv_v_off(t, d);
         uint32_t w = 0;
 #pragma unroll
-        for (uint32_t j = 0; j < 4; j++) w |= (uint32_t)tile[(t + j) * (D + 4) + d] << (8 * j);
-        uint8_t *q = dst + kv_v_off(t, d);
+        for (uint32_t j = 0; j < 4; j++) w |= (uint32_t)tb[4 * tile_word(D, t + j, d / 4) + d % 4] << (8 * j);
         if (t >= lo && t + 4 <= hi) {
             *reinterpret_cast<uint32_t *>(q) = w;
         } else {
@@ -219,14 +269,19 @@ struct ReadArgs {
 
 constexpr uint32_t RD_THREADS = 128;
 
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-    return (uint32_t)f32_to_bf16_rne(lo) | (uint32_t)f32_to_bf16_rne(hi) << 16;
+// Four codes of a word, times the scale, to four bf16 (exact).
+__device__ __forceinline__ uint2 decode4(uint32_t w, float s) {
+    const float2 a = e4m3x2_f32((uint16_t)w), b = e4m3x2_f32((uint16_t)(w >> 16));
+    uint2 r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r.x) : "f"(a.y * s), "f"(a.x * s));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r.y) : "f"(b.y * s), "f"(b.x * s));
+    return r;
 }
 
 // One CTA: (block item, head, layer and keys or values).
 template <uint32_t D>
 __global__ void __launch_bounds__(RD_THREADS) k_kv_read(ReadArgs a) {
-    __shared__ __align__(16) uint8_t tile[D * (KV_P + 4)];
+    __shared__ __align__(16) uint32_t tile[KV_P * D / 4];
     pdl_trigger();
     pdl_wait();
     const uint32_t tid = threadIdx.x;
@@ -262,33 +317,34 @@ __global__ void __launch_bounds__(RD_THREADS) k_kv_read(ReadArgs a) {
     uint16_t *out = a.out[side] + (((uint64_t)(layer - a.layer0) * a.tokens + row0 + (t0 + lo - (uint32_t)first)) *
                                        a.c.kv_heads + head) * D;
     if (side) {
-        for (uint32_t i = tid; i < D * KV_P / 16; i += RD_THREADS) {
-            const uint4 u = reinterpret_cast<const uint4 *>(src)[i];
-            uint32_t *tp = reinterpret_cast<uint32_t *>(tile + (i / 4) * (KV_P + 4) + (i % 4) * 16);
-            tp[0] = u.x, tp[1] = u.y, tp[2] = u.z, tp[3] = u.w;
+        // rows of tokens out of rows of dimensions: four dimensions by sixteen tokens a thread
+        for (uint32_t i = tid; i < D; i += RD_THREADS) {
+            const uint32_t q = i & 3, w = i >> 2;
+            uint4 v[4];
+#pragma unroll
+            for (uint32_t d = 0; d < 4; d++) v[d] = *reinterpret_cast<const uint4 *>(src + kv_v_off(16 * q, 4 * w + d));
+#pragma unroll
+            for (uint32_t j = 0; j < 4; j++) {
+                uint32_t y[4];
+#pragma unroll
+                for (uint32_t d = 0; d < 4; d++) y[d] = j == 0 ? v[d].x : j == 1 ? v[d].y : j == 2 ? v[d].z : v[d].w;
+                transpose4(y);
+#pragma unroll
+                for (uint32_t t = 0; t < 4; t++) tile[tile_word(D, 16 * q + 4 * j + t, w)] = y[t];
+            }
         }
         __syncthreads();
     }
-    constexpr uint32_t CH = D / 8;
+    constexpr uint32_t CH = D / 16;
+#pragma unroll 2
     for (uint32_t i = tid; i < (hi - lo) * CH; i += RD_THREADS) {
-        const uint32_t r = i / CH, c = (i % CH) * 8;
-        uint32_t w[2];
-        if (side) {
-            w[0] = w[1] = 0;
-#pragma unroll
-            for (uint32_t j = 0; j < 8; j++)
-                w[j / 4] |= (uint32_t)tile[(c + j) * (KV_P + 4) + lo + r] << (8 * (j & 3));
-        } else {
-            const uint2 u = *reinterpret_cast<const uint2 *>(src + kv_k_off(D, lo + r, c));
-            w[0] = u.x, w[1] = u.y;
-        }
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const float2 f = e4m3x2_f32((uint16_t)(w[j / 2] >> (16 * (j & 1))));
-            o[j] = bf16_pair(f.x * s, f.y * s);
-        }
-        *reinterpret_cast<uint4 *>(out + (uint64_t)r * a.c.kv_heads * D + c) = make_uint4(o[0], o[1], o[2], o[3]);
+        const uint32_t r = i / CH, c = (i % CH) * 16;
+        const uint4 w = side ? *reinterpret_cast<const uint4 *>(&tile[tile_word(D, lo + r, c / 4)])
+                             : *reinterpret_cast<const uint4 *>(src + kv_k_off(D, lo + r, c));
+        const uint2 a0 = decode4(w.x, s), a1 = decode4(w.y, s), a2 = decode4(w.z, s), a3 = decode4(w.w, s);
+        uint4 *o = reinterpret_cast<uint4 *>(out + (uint64_t)r * a.c.kv_heads * D + c);
+        o[0] = make_uint4(a0.x, a0.y, a1.x, a1.y);
+        o[1] = make_uint4(a2.x, a2.y, a3.x, a3.y);
     }
 }
 
@@ -327,7 +383,17 @@ __global__ void __launch_bounds__(CP_THREADS) k_kv_copy(CopyArgs a) {
         float *sc = side ? a.c.v_scale : a.c.k_scale;
         const uint4 *from = reinterpret_cast<const uint4 *>(base + bs * (KV_P * a.c.head_dim));
         uint4 *to = reinterpret_cast<uint4 *>(base + bd * (KV_P * a.c.head_dim));
-        for (uint32_t q = threadIdx.x; q < quads; q += CP_THREADS) to[q] = from[q];
+        // eight loads in flight (a page of one layer and side is a multiple of 4 KB)
+        constexpr uint32_t UN = 8;
+        uint32_t q = threadIdx.x;
+        for (; q + (UN - 1) * CP_THREADS < quads; q += UN * CP_THREADS) {
+            uint4 v[UN];
+#pragma unroll
+            for (uint32_t i = 0; i < UN; i++) v[i] = ldg_stream16(from + q + i * CP_THREADS);
+#pragma unroll
+            for (uint32_t i = 0; i < UN; i++) to[q + i * CP_THREADS] = v[i];
+        }
+        for (; q < quads; q += CP_THREADS) to[q] = from[q];
         for (uint32_t h = threadIdx.x; h < a.c.kv_heads; h += CP_THREADS) sc[bd + h] = sc[bs + h];
     }
 }
