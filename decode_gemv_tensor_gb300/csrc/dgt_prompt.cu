@@ -56,20 +56,25 @@ struct PageMeta {
     uint32_t used;
 };
 
-// Two fp32 operations an instruction.
-__device__ __forceinline__ void fma2(float a0, float a1, float b, float c, float &d0, float &d1) {
-    asm("{\n\t.reg .b64 x, y, z, r;\n\t"
-        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %5};\n\t"
-        "fma.rn.f32x2 r, x, y, z;\n\tmov.b64 {%0, %1}, r;\n\t}"
-        : "=f"(d0), "=f"(d1)
-        : "f"(a0), "f"(a1), "f"(b), "f"(c));
+// Pairs of fp32, two operations an instruction.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
 }
-__device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1) {
-    asm("{\n\t.reg .b64 x, y;\n\t"
-        "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
-        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "+f"(d0), "+f"(d1)
-        : "f"(a0), "f"(a1));
+__device__ __forceinline__ void unpack2(f32x2 x, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 __device__ __forceinline__ void bar_rows() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -89,7 +94,7 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                        KS = Cfg::KS, VS = Cfg::VS, WS = Cfg::WS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t kfull[KS], kfree[KS], vfull[VS], vfree[VS], wfull[WS], wfree[WS];
-    __shared__ __align__(8) uint64_t sfull[4], pfull[4], ofull[2], ofin[2], qfull[2], mfull[PR_META], drained;
+    __shared__ __align__(8) uint64_t sfull[4], pfull[4], ofull[2], ofin[2], qfull[2], drained;
     __shared__ PageMeta meta[PR_META];
     __shared__ __align__(8) float joined[join_floats(RT)];
     __shared__ Slot slots[AT_CHUNK];
@@ -104,7 +109,7 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
         for (uint32_t i = 0; i < VS; i++) mbar_init(smem_u32(&vfull[i]), 1), mbar_init(smem_u32(&vfree[i]), PR_CONV / 32);
         for (uint32_t i = 0; i < WS; i++) mbar_init(smem_u32(&wfull[i]), PR_CONV / 32), mbar_init(smem_u32(&wfree[i]), NSTR);
         for (uint32_t i = 0; i < 4; i++) {
-            mbar_init(smem_u32(&sfull[i]), 1);
+            mbar_init(smem_u32(&sfull[i]), 2);
             mbar_init(smem_u32(&pfull[i]), 4);
         }
         for (uint32_t i = 0; i < 2; i++) {
@@ -112,7 +117,6 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
             mbar_init(smem_u32(&ofin[i]), 1);
             mbar_init(smem_u32(&qfull[i]), 4);
         }
-        for (uint32_t i = 0; i < PR_META; i++) mbar_init(smem_u32(&mfull[i]), 1);
         mbar_init(smem_u32(&drained), NSTR);
         abort_flag = 0;
         fence_mbarrier_init();
@@ -135,17 +139,21 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
     const uint64_t ub = blockIdx.x >= cut.C ? 0 : cut.parts ? cut.U : cut.raw(blockIdx.x + 1);
 
     bool dead = false;   // a wait ran out, here or elsewhere in the CTA: no more work from this warp
-    // a whole warp's wait: mostly the phase has ended already
-    auto wait_at = [&](uint32_t bar, uint32_t parity) {
-        if (__all_sync(DGT_FULL, !dead && a.spin && mbar_try_wait(bar, parity))) return true;
-        if (!dead && !__any_sync(DGT_FULL, wait_or_abort(bar, parity, abortp, a.spin))) {
-            dead = true;
-            if (lane == 0) set_status(a.status, DGT_ERR_TIMEOUT);
-            *abortp = 1;
+    // a whole warp's wait for two phases (or one, given twice): the tries overlap
+    auto wait_both = [&](uint32_t bar, uint32_t parity, uint32_t bar2, uint32_t parity2) {
+        if (dead) return false;
+        for (uint32_t i = 0; i < a.spin; i++) {
+            bool ok = mbar_try_wait(bar, parity);
+            if (bar2 != bar) ok &= mbar_try_wait(bar2, parity2);
+            if (__all_sync(DGT_FULL, ok)) return true;
+            if ((i & 63) == 63 && *abortp) break;
         }
-        __syncwarp();   // the lane that saw the phase end has seen it for all
-        return !dead;
+        dead = true;
+        if (lane == 0) set_status(a.status, DGT_ERR_TIMEOUT);
+        *abortp = 1;
+        return false;
     };
+    auto wait_at = [&](uint32_t bar, uint32_t parity) { return wait_both(bar, parity, bar, parity); };
     auto wait = [&](uint64_t &bar, uint32_t parity) { return wait_at(smem_u32(&bar), parity); };
     Ring kr{0, 0}, wr{0, 0};       // the matrix instructions' next stages of keys and fp16 values
     uint32_t it = 0;               // pages so far, the same in every role
@@ -198,7 +206,6 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                     if (lane == 0) {
                         PageMeta &m = meta[c % PR_META];
                         m.ks = id < 0 ? 1.0f : kk, m.vs = id < 0 ? 1.0f : vv, m.used = id >= 0;
-                        mbar_arrive(smem_u32(&mfull[c % PR_META]));
                         if (id >= 0) {
                             mbar_arrive_expect_tx(kb, PB);
                             bulk_g2s(base + Cfg::k + (c % KS) * PB, a.c.k + bi * PB, PB, kb);
@@ -251,6 +258,8 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                                              kd + (st * PB + pan * KV_P * RB) / 16 + 2 * i, idesc_s,
                                              part + pan + i > 0 ? 1u : 0u);
                     commit(sf0 + 8 * n);
+                    // the page's scales, seen here with its keys, are seen behind this barrier too
+                    if (leader) mbar_arrive(sf0 + 8 * n);
                     commit(kf0 + 8 * st);
                 };
                 if (t < ns) {
@@ -267,7 +276,8 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                         const uint32_t n = sc[t] + j;
                         const uint32_t x = __shfl_sync(DGT_FULL, kr.st | wr.st << 8 | (n & 1) << 16 | (j ? 1u << 24 : 0u), 0);
                         const uint32_t ks = x & 255, ws = x >> 8 & 255, nb = x >> 16 & 1, more = x >> 24;
-                        if ((j + 2 < T && !wait_at(kb0 + 8 * ks, kr.ph)) || !wait_at(wb0 + 8 * ws, wr.ph) ||
+                        const uint32_t wbar = wb0 + 8 * ws;
+                        if (!wait_both(j + 2 < T ? kb0 + 8 * ks : wbar, j + 2 < T ? kr.ph : wr.ph, wbar, wr.ph) ||
                             !wait_at(pf0 + 8 * nb, (n >> 1) & 1u))
                             break;
                         tc_fence_after();
@@ -304,26 +314,28 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                 const uint32_t ct = tid - 256;
                 for (uint32_t j = 0; j < T && !dead; j++) {
                     const uint32_t c = it + j;
-                    if (!wait(vfull[c % VS], (c / VS) & 1u)) break;
-                    if (c >= WS && !wait(wfree[c % WS], (c / WS - 1) & 1u)) break;
+                    const uint32_t vb = smem_u32(&vfull[c % VS]), wb = smem_u32(&wfree[c % WS]);
+                    if (!wait_both(vb, (c / VS) & 1u, c >= WS ? wb : vb, c >= WS ? (c / WS - 1) & 1u : 0u)) break;
                     const uint32_t src = base + Cfg::v + (c % VS) * PB, dst = base + Cfg::w + (c % WS) * PB * 2;
                     const bool used = meta[c % PR_META].used != 0;
-                    // 16 bytes a thread: row at / 4, its tokens 16 (at % 4) ..
+                    // 16 bytes a thread: row ct / 4 (and every 32nd from there), tokens 16 (ct % 4) ..
                     constexpr uint32_t B = D * 4 / PR_CONV < 4 ? D * 4 / PR_CONV : 4;
                     static_assert(D * 4 % (B * PR_CONV) == 0, "a page's pieces divide evenly over the threads");
-#pragma unroll 1
-                    for (uint32_t i0 = ct; i0 < D * 4; i0 += B * PR_CONV) {
+                    const uint32_t row = ct >> 2, q = ct & 3, o0 = dst + row * 128 + (((2 * q) ^ (row & 7)) << 4);
+                    const uint32_t o1 = dst + row * 128 + (((2 * q + 1) ^ (row & 7)) << 4);
+#pragma unroll
+                    for (uint32_t i0 = 0; i0 < D * 4 / PR_CONV; i0 += B) {
                         uint4 x[B];
 #pragma unroll
                         for (uint32_t i = 0; i < B; i++) {
                             x[i] = make_uint4(0, 0, 0, 0);
-                            if (used) x[i] = lds128(src + (i0 + i * PR_CONV) * 16);
+                            if (used) x[i] = lds128(src + ct * 16 + (i0 + i) * PR_CONV * 16);
                         }
 #pragma unroll
                         for (uint32_t i = 0; i < B; i++) {
-                            const uint32_t at = i0 + i * PR_CONV, row = at >> 2, q = at & 3, o = dst + row * 128;
-                            sts128(o + (((2 * q) ^ (row & 7)) << 4), e4m3_lo(x[i].x), e4m3_hi(x[i].x), e4m3_lo(x[i].y), e4m3_hi(x[i].y));
-                            sts128(o + (((2 * q + 1) ^ (row & 7)) << 4), e4m3_lo(x[i].z), e4m3_hi(x[i].z), e4m3_lo(x[i].w), e4m3_hi(x[i].w));
+                            const uint32_t k = (i0 + i) * (PR_CONV / 4) * 128;
+                            sts128(o0 + k, e4m3_lo(x[i].x), e4m3_hi(x[i].x), e4m3_lo(x[i].y), e4m3_hi(x[i].y));
+                            sts128(o1 + k, e4m3_lo(x[i].z), e4m3_hi(x[i].z), e4m3_lo(x[i].w), e4m3_hi(x[i].w));
                         }
                     }
                     fence_proxy_async_smem();
@@ -389,7 +401,7 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                 const int32_t pl = s.pos0 + (int32_t)((s.row0 + s.rows - 1) / a.group);
                 for (uint32_t j = 0; mine && j < T && !dead; j++) {
                     const uint32_t c = it + j, sn = sc[t] + j, sb = 2 * t + (sn & 1);
-                    if (!wait(mfull[c % PR_META], (c / PR_META) & 1u) || !wait(sfull[sb], (sn >> 1) & 1u)) break;
+                    if (!wait(sfull[sb], (sn >> 1) & 1u)) break;
                     tc_fence_after();
                     const uint32_t st = tm + tl + Cfg::SCOL + sb * KV_P;
                     uint32_t sv[64];
@@ -439,34 +451,40 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                     const float lc = bm + ev - bu + PR_W_LOG2;
                     const bool fast = __all_sync(DGT_FULL, fabsf(lc) < 40.0f && vs == vs && f == f);
                     const float bb = fast ? lc - bm : -bm;
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const f32x2 f2 = pack2(f, f), b2 = pack2(bb, bb);
+                    f32x2 sum[2] = {0ull, 0ull};
+                    uint32_t pk[32];
 #pragma unroll
                     for (int i = 0; i < 32; i++) {
-                        float u, v;
-                        fma2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]), f, bb, u, v);
-                        sv[2 * i] = __float_as_uint(ex2(u));
-                        sv[2 * i + 1] = __float_as_uint(ex2(v));
+                        float x, y;
+                        unpack2(fma2(pack2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), f2, b2), x, y);
+                        x = ex2(x);
+                        y = ex2(y);
+                        sv[2 * i] = __float_as_uint(x);
+                        sv[2 * i + 1] = __float_as_uint(y);
+                        sum[i & 1] = add2(sum[i & 1], pack2(x, y));
+                        pk[i] = f16_pair(x, y);
                     }
-                    if (fast) {
-#pragma unroll
-                        for (int i = 0; i < 32; i++)
-                            add2(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], __uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
-                    } else {
+                    float all;
+                    {
+                        float x, y;
+                        unpack2(add2(sum[0], sum[1]), x, y);
+                        all = x + y;
+                    }
+                    if (!fast) {
                         // scales that are not finite or far apart: weights and their sum one by one, and none
                         // for a token that the row does not see, whatever its scales are
                         const float cw = vs != vs ? vs : ex2(fminf(lc, 126.0f));
+                        all = 0.0f;
 #pragma unroll
-                        for (int i = 0; i < 64; i++) {
-                            const bool v = (see >> i) & 1u;
-                            if (v) sum[i & 3] += __uint_as_float(sv[i]);
-                            sv[i] = v ? __float_as_uint(__uint_as_float(sv[i]) * cw) : 0u;
+                        for (int i = 0; i < 32; i++) {
+                            const float x = (see >> (2 * i)) & 1u ? __uint_as_float(sv[2 * i]) : 0.0f;
+                            const float y = (see >> (2 * i + 1)) & 1u ? __uint_as_float(sv[2 * i + 1]) : 0.0f;
+                            all += x + y;
+                            pk[i] = f16_pair((see >> (2 * i)) & 1u ? x * cw : 0.0f, (see >> (2 * i + 1)) & 1u ? y * cw : 0.0f);
                         }
                     }
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int i = 0; i < 32; i++) pk[i] = f16_pair(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
                     tmem_st32(st, pk);
-                    const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     l += fast ? all * ex2(-lc) : all;
                     if (j > 0 && __any_sync(DGT_FULL, grow)) {
                         // The accumulators may move once the products of the page before are done.  Those of
