@@ -13,7 +13,8 @@ add_rmsnorm, silu_mul, silu_mul_rows, repeat, weighted_sum, exponent_stats,
 rotate, kv_append, kv_read, kv_attention, kv_reserve, kv_fork, kv_free,
 kv_copy_pages, kv_compact, read_status; Rotary and KvCache hold a rotation's
 frequencies and a paged 8-bit cache; DecodeStep and MoeDecodeStep compose a
-batch-1 decode step from them and capture it in a CUDA graph.
+batch-1 decode step from them, with a StepAttention over a cache or without,
+and capture it in a CUDA graph.
 """
 from __future__ import annotations
 
@@ -896,6 +897,49 @@ def repeat(v, n_out, out=None, stream=None):
 DENSE_PROJ = ("q", "k", "v", "o", "gate", "up", "down")
 
 
+class StepAttention:
+    """The attention of a batch-1 decode step: the new token's q and k turned to
+    its position, its k and v appended to sequence `seq` of a KvCache (layer l
+    of the step is layer l of the cache), and attention over what the sequence
+    holds, with an optional window and first tokens that stay visible.  For
+    DecodeStep and MoeDecodeStep; the query heads have the cache's head_dim,
+    their count a multiple of its kv_heads.  Positions and lengths live on the
+    device, so a captured step moves on by one token with every replay.
+    self.status (int32 [1]) reports a pool or a table without room
+    (DGT_ERR_FULL: nothing is appended) and bad pages."""
+
+    def __init__(self, cache: KvCache, rotary: Rotary, seq: int = 0, window: int = 0, sinks: int = 0, scale=None):
+        import torch
+        if rotary.axes != 1:
+            raise ValueError("rotary: one axis")
+        i32 = lambda v: torch.tensor([v], dtype=torch.int32, device=cache.k.device)
+        self.cache, self.rotary, self.window, self.sinks, self.scale = cache, rotary, window, sinks, scale
+        self.seq, self.one, self.start, self.status = i32(seq), i32(1), i32(0), i32(0)
+        self.ws = None
+
+    def prepare(self, q_width: int, depth: int):
+        """Workspace for steps of this query width; checks that the cache has room for the layers."""
+        c = self.cache
+        if q_width % (c.head_dim * c.kv_heads) or depth > c.layers:
+            raise ValueError("the cache's heads or layers do not fit the step's")
+        self.q_heads = q_width // c.head_dim
+        self.ws = kv_attention_workspace(c, self.q_heads, 1, 1)
+
+    def begin(self, stream=None):
+        """Room for the step's token; its position to self.start."""
+        kv_reserve(self.cache, self.seq, self.one, start=self.start, status=self.status, stream=stream)
+
+    def __call__(self, layer: int, q, k, v, out, stream=None):
+        """One layer: bf16 vectors q, k, v of the projections (q and k are
+        rotated in place), out bf16 of q's width."""
+        c = self.cache
+        q, k, v = (x.view(1, -1, c.head_dim) for x in (q, k, v))
+        rotate(self.rotary, q, self.start, k=k, q_out=q, k_out=k, stream=stream)
+        kv_append(c, layer, k, v, self.seq, self.start, status=self.status, stream=stream)
+        kv_attention(c, layer, q, self.seq, scale=self.scale, window=self.window, sinks=self.sinks,
+                     out=out.view(1, self.q_heads, c.head_dim), ws=self.ws, status=self.status, stream=stream)
+
+
 class DecodeStep:
     """One batch-1 decode step through a stack of dense decoder layers, every
     op a kernel of this library.  Per layer, with the fp32 residual stream x:
@@ -904,9 +948,10 @@ class DecodeStep:
         a = repeat(v, rows of Wq);  x += Wo a
         h = rmsnorm(x, g2);  m = silu(Wgate h) * (Wup h);  x += Wdown m
 
-    and a final h = rmsnorm(x, g_final).  Attention itself is not part of the
-    step: the output projection reads the value vector repeated over the query
-    heads.  layers: list of dicts proj -> R4 (or bf16 tensors [rows, cols] for
+    and a final h = rmsnorm(x, g_final).  Without `attention` the output
+    projection reads the value vector repeated over the query heads, as above;
+    with a StepAttention a is the attention of the new token over its cache,
+    and every step appends one token.  layers: list of dicts proj -> R4 (or bf16 tensors [rows, cols] for
     the twin), either q, k, v, o, gate, up, down, or the stacked form qkv
     (rows of q, then k, then v; k and v of equal size), o, gate_up (rows of
     gate, then up) and down, which computes the same step with one product
@@ -916,8 +961,9 @@ class DecodeStep:
     The R4 step and the BF16 step over the same weights give bit-identical
     outputs."""
 
-    def __init__(self, layers, gammas, depth=None, eps=1e-5, device=None):
+    def __init__(self, layers, gammas, depth=None, eps=1e-5, device=None, attention=None):
         import torch
+        self.attention = attention
         self.layers, self.gammas, self.eps = layers, gammas, eps
         self.depth = depth or len(layers)
         w0 = layers[0]
@@ -937,16 +983,19 @@ class DecodeStep:
         self.ffn = shape(w0["down"])[1]
         if self.fused:
             nkv = (dims["qkv"] - nq) // 2
+            self.q16, self.k16 = self.y["qkv"][0][:nq], self.y["qkv"][0][nq:nq + nkv]
             self.v16 = self.y["qkv"][0][nq + nkv:nq + 2 * nkv]
             self.g32 = self.y["gate_up"][1][:self.ffn]
             self.u32 = self.y["gate_up"][1][self.ffn:]
         else:
-            self.v16 = self.y["v"][0]
+            self.q16, self.k16, self.v16 = (self.y[p][0] for p in ("q", "k", "v"))
             self.g32, self.u32 = self.y["gate"][1], self.y["up"][1]
         self.a = b16(nq)
         self.m = b16(self.ffn)
         self.out = b16(hidden)
         self._graph = None
+        if attention is not None:
+            attention.prepare(nq, self.depth)
         # the step streams its weights before each product's dependency wait
         # (DGT_GEMV_STATIC_WEIGHTS): everything that wrote them must be done
         torch.cuda.synchronize(dev)
@@ -964,6 +1013,8 @@ class DecodeStep:
         """Queue the step on `stream` (self.x holds the input, then the output
         residual stream; self.out the final normed vector)."""
         gi = 0
+        if self.attention is not None:
+            self.attention.begin(stream)
         for l in range(self.depth):
             W = self.layers[l % len(self.layers)]
             add_rmsnorm(self.x, self.gammas[gi % (len(self.gammas) - 1)], self.eps, self.h,
@@ -971,7 +1022,10 @@ class DecodeStep:
             gi += 1
             for p in (("qkv",) if self.fused else ("q", "k", "v")):
                 self._gemv(W[p], self.h, p, stream)
-            repeat(self.v16, self.a.numel(), self.a, stream)
+            if self.attention is not None:
+                self.attention(l, self.q16, self.k16, self.v16, self.a, stream)
+            else:
+                repeat(self.v16, self.a.numel(), self.a, stream)
             self._gemv(W["o"], self.a, "o", stream)
             add_rmsnorm(self.x, self.gammas[gi % (len(self.gammas) - 1)], self.eps, self.h, self.y["o"][1], stream)
             gi += 1
@@ -1040,11 +1094,13 @@ class MoeDecodeStep:
     gate_up stacks expert e's gate rows and then its up rows as expert e's
     block ([E * 2 ffn, hidden]): one product for q, k, v and one gather for
     gate and up.  routes: per layer (ids int32 [topk], p float32 [topk]) on
-    the device; layer l uses layers[l % len] and routes[l % len].  The R4 step
-    and the BF16 step give bit-identical outputs."""
+    the device; layer l uses layers[l % len] and routes[l % len].  attention: a
+    StepAttention, as in DecodeStep.  The R4 step and the BF16 step give
+    bit-identical outputs."""
 
-    def __init__(self, layers, gammas, routes, n_experts, depth=None, eps=1e-5):
+    def __init__(self, layers, gammas, routes, n_experts, depth=None, eps=1e-5, attention=None):
         import torch
+        self.attention = attention
         self.layers, self.gammas, self.routes, self.E, self.eps = layers, gammas, routes, n_experts, eps
         self.depth = depth or len(layers)
         w0 = layers[0]
@@ -1064,10 +1120,11 @@ class MoeDecodeStep:
         nq = shape(w0["o"])[1]
         if self.fused:
             nkv = (shape(w0["qkv"])[0] - nq) // 2
+            self.q16, self.k16 = self.y["qkv"][0][:nq], self.y["qkv"][0][nq:nq + nkv]
             self.v16 = self.y["qkv"][0][nq + nkv:nq + 2 * nkv]
             self.ygu = f32(1, topk, 2 * ffn)
         else:
-            self.v16 = self.y["v"][0]
+            self.q16, self.k16, self.v16 = (self.y[p][0] for p in ("q", "k", "v"))
             self.yg, self.yu = f32(1, topk, ffn), f32(1, topk, ffn)
         self.a = b16(nq)
         self.m = b16(topk, ffn)
@@ -1079,6 +1136,8 @@ class MoeDecodeStep:
         self.ws_u = torch.empty(max(nb_up, 256), dtype=torch.uint8, device=dev)
         self.ws_d = torch.empty(max(nb_dn, 256), dtype=torch.uint8, device=dev)
         self._graph = None
+        if attention is not None:
+            attention.prepare(nq, self.depth)
         torch.cuda.synchronize(dev)     # the products stream weights before their dependency wait
 
     def _gemv(self, W, x, p, stream):
@@ -1094,13 +1153,18 @@ class MoeDecodeStep:
 
     def launch(self, stream=None):
         ng = len(self.gammas) - 1
+        if self.attention is not None:
+            self.attention.begin(stream)
         for l in range(self.depth):
             W = self.layers[l % len(self.layers)]
             ids, p = self.routes[l % len(self.routes)]
             add_rmsnorm(self.x, self.gammas[(2 * l) % ng], self.eps, self.h, None if l == 0 else self.comb, stream)
             for pr in (("qkv",) if self.fused else ("q", "k", "v")):
                 self._gemv(W[pr], self.h, pr, stream)
-            repeat(self.v16, self.a.numel(), self.a, stream)
+            if self.attention is not None:
+                self.attention(l, self.q16, self.k16, self.v16, self.a, stream)
+            else:
+                repeat(self.v16, self.a.numel(), self.a, stream)
             self._gemv(W["o"], self.a, "o", stream)
             add_rmsnorm(self.x, self.gammas[(2 * l + 1) % ng], self.eps, self.h, self.y["o"][1], stream)
             ids1 = ids.view(1, self.topk)

@@ -253,7 +253,7 @@ __device__ __forceinline__ Cuts cut_plan(const AttnArgs &a, Units all, const Slo
     Cuts k;
     k.U = U;
     k.C = (uint32_t)min((uint64_t)grid, U);   // shares of one unit at least: cuts inside a segment are distinct
-    k.tol = (uint32_t)min(U / (8 * grid), (uint64_t)16);
+    k.tol = (uint32_t)min(U / (8 * grid), (uint64_t)4);
     // (U below 2^22: a segment's pages and T then are below 2^23)
     k.parts = a.slots <= AT_CHUNK && S <= grid && U && U < (1u << 22);
     if (!k.parts) return k;

@@ -247,20 +247,22 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                 const uint64_t wd = sw128_desc(base + Cfg::w);
                 // scores with the keys' stage st into buffer n
                 auto scores = [&](uint32_t st, uint32_t n) {
+                    const uint64_t k0 = kd + st * (PB / 16);
+                    const uint32_t col = scol + n * KV_P;
+                    if (leader) {
 #pragma unroll
-                    for (uint32_t part = 0; part < 2; part++)
+                        for (uint32_t part = 0; part < 2; part++)
 #pragma unroll
-                        for (uint32_t pan = 0; pan < PAN; pan++)
+                            for (uint32_t pan = 0; pan < PAN; pan++)
 #pragma unroll
-                            for (uint32_t i = 0; i < RB / 32; i++)
-                                if (leader)
-                                    mma_e4m3(scol + n * KV_P, qd + (part * QP + pan * 128 * RB) / 16 + 2 * i,
-                                             kd + (st * PB + pan * KV_P * RB) / 16 + 2 * i, idesc_s,
-                                             part + pan + i > 0 ? 1u : 0u);
-                    commit(sf0 + 8 * n);
-                    // the page's scales, seen here with its keys, are seen behind this barrier too
-                    if (leader) mbar_arrive(sf0 + 8 * n);
-                    commit(kf0 + 8 * st);
+                                for (uint32_t i = 0; i < RB / 32; i++)
+                                    mma_e4m3(col, qd + (part * QP + pan * 128 * RB) / 16 + 2 * i,
+                                             k0 + pan * KV_P * RB / 16 + 2 * i, idesc_s, part + pan + i > 0 ? 1u : 0u);
+                        mma_commit(sf0 + 8 * n);
+                        // the page's scales, seen here with its keys, are seen behind this barrier too
+                        mbar_arrive(sf0 + 8 * n);
+                        mma_commit(kf0 + 8 * st);
+                    }
                 };
                 if (t < ns) {
                     // The pipe runs a warp's instructions in order: a buffer's next scores are issued behind
