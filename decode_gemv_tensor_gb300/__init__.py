@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import numpy as np
 
@@ -67,6 +68,9 @@ class HeadsStruct(C.Structure):
                 ("reserved", C.c_uint32)]
 
 
+_pack_heads = struct.Struct("=QqqII").pack     # the same as bytes, which ctypes passes by address
+
+
 class RotaryStruct(C.Structure):
     _fields_ = [("rot_dim", C.c_uint32), ("axes", C.c_uint32), ("interleaved", C.c_uint32), ("reserved", C.c_uint32),
                 ("d_freq", C.c_void_p), ("d_axis", C.c_void_p)]
@@ -91,7 +95,7 @@ def lib():
                               "`python -c 'import __graft_entry__ as g; g.build()'`")
         L = C.CDLL(LIB_PATH)
         vp, u64, i32 = C.c_void_p, C.c_uint64, C.c_int
-        hp, kp = C.POINTER(HeadsStruct), C.POINTER(KvCacheStruct)
+        hp = kp = vp     # dgt_heads as packed bytes, dgt_kv_cache by address: half the cost of a pointer type
         sig = {
             "dgt_status_string": (C.c_char_p, [i32]),
             "dgt_version": (i32, []),
@@ -142,7 +146,7 @@ def lib():
             "dgt_repeat": (i32, [vp, u64, u64, vp, vp]),
             "dgt_weighted_sum": (i32, [vp, vp, C.c_uint32, u64, vp, vp]),
             "dgt_rotary_freqs": (i32, [C.c_double, C.c_uint32, vp]),
-            "dgt_rotate": (i32, [C.POINTER(RotaryStruct), hp, hp, hp, hp, C.c_uint32, u64, vp, vp]),
+            "dgt_rotate": (i32, [vp, hp, hp, hp, hp, C.c_uint32, u64, vp, vp]),
             "dgt_kv_append": (i32, [kp, C.c_uint32, hp, hp, u64, vp, vp, vp, C.c_uint32, vp, vp]),
             "dgt_kv_read": (i32, [kp, C.c_int32, vp, vp, vp, C.c_uint32, u64, vp, vp, vp, vp]),
             "dgt_kv_attention_workspace_bytes": (C.c_size_t, [kp, C.c_uint32, C.c_uint32, u64]),
@@ -619,20 +623,20 @@ def gemm_rebuild(W: R4, X, scratch=None, plan=None, Y32=None, Y=None, ws=None, s
 # rotary positions
 # ---------------------------------------------------------------------------
 def _heads(x, name):
-    """The dgt_heads view of a bf16 tensor [tokens, heads, dim] on the device."""
+    """The dgt_heads view of a bf16 tensor [tokens, heads, dim] on the device (packed)."""
     import torch
-    if x.dim() != 3 or x.dtype != torch.bfloat16 or not x.is_cuda:
+    if x.dtype is not torch.bfloat16 or not x.is_cuda or x.dim() != 3:
         raise ValueError(f"{name}: a CUDA bfloat16 tensor [tokens, heads, dim]")
     (n, h, _), (ts, hs, es) = x.shape, x.stride()
     if es != 1 and x.numel():
         raise ValueError(f"{name}: a contiguous last dimension")
     # a stride that no element uses may be anything
-    return HeadsStruct(x.data_ptr(), ts if n > 1 else 0, hs if h > 1 else 0, h, 0)
+    return _pack_heads(x.data_ptr(), ts if n > 1 else 0, hs if h > 1 else 0, h, 0)
 
 
 def _i32(x, name, n=None):
     import torch
-    if x.dtype != torch.int32 or not x.is_cuda or not x.is_contiguous() or (n is not None and x.numel() != n):
+    if x.dtype is not torch.int32 or not x.is_cuda or not x.is_contiguous() or (n is not None and x.numel() != n):
         raise ValueError(f"{name}: a contiguous CUDA int32 tensor" + ("" if n is None else f" of {n} elements"))
     return x.data_ptr()
 
@@ -672,6 +676,7 @@ class Rotary:
         self.axis = torch.tensor(axis, dtype=torch.uint8, device=device)
         self.s = RotaryStruct(rot_dim, self.axes, int(self.interleaved), 0, self.freq.data_ptr(),
                               self.axis.data_ptr())
+        self.ptr = C.addressof(self.s)
 
 
 def rotate(rotary: Rotary, q, pos, k=None, q_out=None, k_out=None, stream=None):
@@ -684,9 +689,11 @@ def rotate(rotary: Rotary, q, pos, k=None, q_out=None, k_out=None, stream=None):
     hq, hk, ok = _heads(q, "q"), None, None
     if q_out is None:
         q_out = torch.empty((tokens, nq, dim), dtype=torch.bfloat16, device=q.device)
-        oq = HeadsStruct(q_out.data_ptr(), nq * dim, dim, nq, 0)
+        oq = _pack_heads(q_out.data_ptr(), nq * dim, dim, nq, 0)
     else:
         oq = _heads(q_out, "q_out")
+        if q_out.shape != q.shape:
+            raise ValueError("q_out: the shape of q")
     if k is None:
         k_out = None
     else:
@@ -695,14 +702,12 @@ def rotate(rotary: Rotary, q, pos, k=None, q_out=None, k_out=None, stream=None):
             raise ValueError("k: the same tokens and head size as q")
         if k_out is None:
             k_out = torch.empty((tokens, nk, dim), dtype=torch.bfloat16, device=q.device)
-            ok = HeadsStruct(k_out.data_ptr(), nk * dim, dim, nk, 0)
+            ok = _pack_heads(k_out.data_ptr(), nk * dim, dim, nk, 0)
         else:
             ok = _heads(k_out, "k_out")
             if k_out.shape != k.shape:
                 raise ValueError("k_out: the shape of k")
-    if q_out.shape != q.shape:
-        raise ValueError("q_out: the shape of q")
-    _check(lib().dgt_rotate(rotary.s, hq, hk, oq, ok, dim, tokens, p, _stream_on(q, stream)), "dgt_rotate")
+    _check(lib().dgt_rotate(rotary.ptr, hq, hk, oq, ok, dim, tokens, p, _stream_on(q, stream)), "dgt_rotate")
     return q_out, k_out
 
 
@@ -735,7 +740,8 @@ class KvCache:
         self.s = KvCacheStruct(layers, pages, kv_heads, head_dim, max_seqs, max_pages,
                                *(t.data_ptr() for t in (self.k, self.v, self.k_scale, self.v_scale, self.refs,
                                                         self.table, self.lens)))
-        self.ws = torch.empty(max(int(lib().dgt_kv_pages_workspace_bytes(C.byref(self.s))), 256), dtype=torch.uint8,
+        self.ptr = C.addressof(self.s)
+        self.ws = torch.empty(max(int(lib().dgt_kv_pages_workspace_bytes(self.ptr)), 256), dtype=torch.uint8,
                               device=device)   # of the page operations
 
 
@@ -747,7 +753,7 @@ def kv_append(cache: KvCache, layer: int, k, v, seqs, start, cu=None, status=Non
     tokens, batch = k.shape[0], seqs.numel()
     if k.shape != v.shape or tuple(k.shape[1:]) != (cache.kv_heads, cache.head_dim):
         raise ValueError("k, v: [tokens, kv_heads, head_dim]")
-    _check(lib().dgt_kv_append(cache.s, layer, _heads(k, "k"), _heads(v, "v"), tokens,
+    _check(lib().dgt_kv_append(cache.ptr, layer, _heads(k, "k"), _heads(v, "v"), tokens,
                                _i32(seqs, "seqs"), _i32(start, "start", batch),
                                None if cu is None else _i32(cu, "cu", batch + 1), batch, _ptr(status),
                                _stream_on(cache.k, stream)), "dgt_kv_append")
@@ -764,7 +770,7 @@ def kv_read(cache: KvCache, layer, seqs, first, cu, tokens: int, status=None, st
         shape = (cache.layers, *shape)
     dev = cache.k.device
     out = [torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in range(2)]
-    _check(lib().dgt_kv_read(cache.s, -1 if layer is None else layer, _i32(seqs, "seqs"),
+    _check(lib().dgt_kv_read(cache.ptr, -1 if layer is None else layer, _i32(seqs, "seqs"),
                              _i32(first, "first", batch), None if cu is None else _i32(cu, "cu", batch + 1), batch,
                              tokens, _ptr(out[0]), _ptr(out[1]), _ptr(status), _stream_on(cache.k, stream)), "dgt_kv_read")
     return out
@@ -773,7 +779,7 @@ def kv_read(cache: KvCache, layer, seqs, first, cu, tokens: int, status=None, st
 def kv_attention_workspace(cache: KvCache, q_heads: int, batch: int, tokens: int):
     """A workspace for kv_attention calls of these sizes (zeroed, as its first use wants it)."""
     import torch
-    nb = int(lib().dgt_kv_attention_workspace_bytes(cache.s, q_heads, batch, tokens))
+    nb = int(lib().dgt_kv_attention_workspace_bytes(cache.ptr, q_heads, batch, tokens))
     return torch.zeros(max(nb, 256), dtype=torch.uint8, device=cache.k.device)
 
 
@@ -801,7 +807,7 @@ def kv_attention(cache: KvCache, layer: int, q, seqs, cu=None, scale=None, windo
         raise ValueError("lse: a contiguous float32 tensor [tokens, q_heads]")
     if ws is None:
         ws = kv_attention_workspace(cache, heads, batch, tokens)
-    _check(lib().dgt_kv_attention_ex(cache.s, layer, _heads(q, "q"), tokens, _i32(seqs, "seqs"),
+    _check(lib().dgt_kv_attention_ex(cache.ptr, layer, _heads(q, "q"), tokens, _i32(seqs, "seqs"),
                                      None if cu is None else _i32(cu, "cu", batch + 1), batch,
                                      dim ** -0.5 if scale is None else scale, window, sinks, _ptr(out), _ptr(lse),
                                      _ptr(ws), ws.numel(), _ptr(status), test_wait_flags(test_wait_polls),
@@ -817,7 +823,7 @@ def kv_reserve(cache: KvCache, seqs, count, start=None, status=None, stream=None
     n = seqs.numel()
     if start is None:
         start = torch.empty(n, dtype=torch.int32, device=seqs.device)
-    _check(lib().dgt_kv_reserve(cache.s, _i32(seqs, "seqs"), _i32(count, "count", n), n,
+    _check(lib().dgt_kv_reserve(cache.ptr, _i32(seqs, "seqs"), _i32(count, "count", n), n,
                                 _i32(start, "start", n), _ptr(cache.ws), cache.ws.numel(), _ptr(status),
                                 _stream_on(cache.k, stream)), "dgt_kv_reserve")
     return start
@@ -825,26 +831,26 @@ def kv_reserve(cache: KvCache, seqs, count, start=None, status=None, stream=None
 
 def kv_fork(cache: KvCache, src, dst, status=None, stream=None):
     """dgt_kv_fork: sequences dst[i] become copies of src[i] that share its pages."""
-    _check(lib().dgt_kv_fork(cache.s, _i32(src, "src"), _i32(dst, "dst", src.numel()), src.numel(),
+    _check(lib().dgt_kv_fork(cache.ptr, _i32(src, "src"), _i32(dst, "dst", src.numel()), src.numel(),
                              _ptr(status), _stream_on(cache.k, stream)), "dgt_kv_fork")
 
 
 def kv_free(cache: KvCache, seqs, status=None, stream=None):
     """dgt_kv_free: the sequences give up their pages."""
-    _check(lib().dgt_kv_free(cache.s, _i32(seqs, "seqs"), seqs.numel(), _ptr(status), _stream_on(cache.k, stream)),
+    _check(lib().dgt_kv_free(cache.ptr, _i32(seqs, "seqs"), seqs.numel(), _ptr(status), _stream_on(cache.k, stream)),
            "dgt_kv_free")
 
 
 def kv_copy_pages(cache: KvCache, src, dst, status=None, stream=None):
     """dgt_kv_copy_pages: pages src[i] -> dst[i] (int32 on the device) in every layer."""
-    _check(lib().dgt_kv_copy_pages(cache.s, _i32(src, "src"), _i32(dst, "dst", src.numel()), src.numel(),
+    _check(lib().dgt_kv_copy_pages(cache.ptr, _i32(src, "src"), _i32(dst, "dst", src.numel()), src.numel(),
                                    _ptr(status), _stream_on(cache.k, stream)), "dgt_kv_copy_pages")
 
 
 def kv_compact(cache: KvCache, live=None, status=None, stream=None):
     """dgt_kv_compact: the used pages move to the lowest numbers; live (int32
     [1] on the device) gets their count."""
-    _check(lib().dgt_kv_compact(cache.s, None if live is None else _i32(live, "live", 1), _ptr(cache.ws),
+    _check(lib().dgt_kv_compact(cache.ptr, None if live is None else _i32(live, "live", 1), _ptr(cache.ws),
                                 cache.ws.numel(), _ptr(status), _stream_on(cache.k, stream)), "dgt_kv_compact")
 
 
