@@ -571,16 +571,23 @@ static int attn_launch(const AttnArgs &a, cudaStream_t st) {
 }
 
 // Rows of a tile, by an entry's rows (the mean of a batch): in n-tiles of
-// eight, as many as they fill, up to what the registers hold beside D
-// accumulators a row; from PROMPT_ROWS on the tensor-core tiles.
-constexpr uint64_t PROMPT_ROWS = 64;
+// eight, as many as they fill, while the accumulators of D dimensions a row fit
+// the registers beside them; more rows go to the tensor-core tiles.  Measured
+// on both sides, n-tiles of eight first:
+//   64 dimensions, 28 rows: 31 and 41 us (8 sequences of up to 8003 tokens),
+//     53 and 69 us (32 of 4000), but 21 and 13 us (1 of 500);
+//   128 dimensions, 24 rows: 35 and 44 us (8 of 8003), 73 and 79 us (2 of
+//     60000); 28 rows: 45 and 45 us, 97 and 80 us, and 28 and 15 us (1 of 500);
+//   256 dimensions, 12 rows: 55 and 61 us (8 of 8003), 108 and 104 us (2 of
+//     60000); 18 rows: 64 and 63 us, 140 and 108 us.
 struct Plan {
     uint32_t nt, RT;   // nt 0: tensor-core tiles
 };
 static Plan attn_plan(uint32_t head_dim, uint32_t group, uint32_t batch, uint64_t tokens) {
     const uint64_t rows = group * ((tokens + batch - 1) / batch);
-    if (rows >= PROMPT_ROWS) return {0, prompt_rows(head_dim)};
-    const uint32_t nt = rows <= 8 ? 1 : rows <= 16 || head_dim == 256 ? 2 : rows <= 24 ? 3 : 4;
+    const uint64_t most = head_dim == 64 ? 32 : head_dim == 128 ? 24 : 16;
+    if (rows > most) return {0, prompt_rows(head_dim)};
+    const uint32_t nt = (uint32_t)((rows + 7) / 8);
     return {nt, 8 * nt};
 }
 static uint64_t slot_count(uint32_t RT, uint32_t group, uint32_t batch, uint64_t tokens, bool ragged) {
@@ -645,10 +652,7 @@ extern "C" int dgt_kv_attention_ex(const dgt_kv_cache *cache, uint32_t layer, co
                    : nt == 3 ? attn_launch<64, 3>(a, st)
                              : attn_launch<64, 4>(a, st);
         case 128:
-            return nt == 1   ? attn_launch<128, 1>(a, st)
-                   : nt == 2 ? attn_launch<128, 2>(a, st)
-                   : nt == 3 ? attn_launch<128, 3>(a, st)
-                             : attn_launch<128, 4>(a, st);
+            return nt == 1 ? attn_launch<128, 1>(a, st) : nt == 2 ? attn_launch<128, 2>(a, st) : attn_launch<128, 3>(a, st);
         default: return nt == 1 ? attn_launch<256, 1>(a, st) : attn_launch<256, 2>(a, st);
     }
 }

@@ -509,6 +509,7 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&pfull[sb]));
                 }
+                tmem_wait_st();   // weights of a page whose wait ran out
 
                 // ---- the segment's end: this row's quotient, or its part
                 const bool complete = r.pa == 0 && r.pe == n;

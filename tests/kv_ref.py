@@ -84,7 +84,7 @@ def attention(q, k, v, first, window, sinks, scale):
             out[i, h] = w @ vv / w.sum()
             mag[i, h] = w @ np.abs(vv) / w.sum()
             lse[i, h] = m + np.log(w.sum())
-            big[i, h] = (np.abs(kk) @ np.abs(q[i, h])).max() * scale
+            big[i, h] = (np.abs(kk) @ np.abs(q[i, h])).max() * abs(scale)
     return out, lse, mag, big
 
 

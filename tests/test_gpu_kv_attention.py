@@ -191,6 +191,89 @@ def test_value_scales_far_apart(dgt):
         assert (np.abs(y - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * mag).all()
 
 
+@pytest.mark.parametrize("hq,hk,dim", HEADS[:3])
+@pytest.mark.parametrize("longest", [70, 900])
+def test_more_sequences_than_are_described_at_a_time(dgt, hq, hk, dim, longest):
+    g = np.random.default_rng(longest + dim)
+    lens = g.integers(0, longest + 1, size=170).tolist()
+    s = Setup(dgt, g, lens, hk, dim)
+    s.check(rand(g, 170, hq, dim), [1] * 170)
+    s.check(rand(g, 170, hq, dim), [1] * 170, 65, 2)
+
+
+@pytest.mark.parametrize("hq,hk,dim", HEADS[:3])
+def test_more_prompts_than_are_described_at_a_time(dgt, hq, hk, dim):
+    # some of them without rows, some without tokens, some with more rows than tokens
+    g = np.random.default_rng(dim + 1)
+    counts = g.integers(0, 120, size=90).tolist()
+    lens = [int(n) + int(x) for n, x in zip(counts, g.integers(-20, 300, size=90))]
+    lens = [max(n, 0) for n in lens]
+    s = Setup(dgt, g, lens, hk, dim)
+    s.check(rand(g, sum(counts), hq, dim), counts, rows=[0, 19, 20, 21, 63, 64, 100])
+    s.check(rand(g, sum(counts), hq, dim), counts, 70, 3, rows=[0, 20, 64, 100])
+
+
+def test_a_prompt_of_many_tiles(dgt):
+    g = np.random.default_rng(77)
+    s = Setup(dgt, g, [6100], 1, 128)
+    q = rand(g, 6000, 3, 128)
+    s.check(q, [6000], rows=[0, 85, 86, 2047, 2048, 5461, 5462, 5999])
+    s.check(q, [6000], 500, 66, rows=[0, 85, 86, 2047, 2048, 5461, 5462, 5999])
+
+
+@pytest.mark.parametrize("hq,hk,dim", HEADS[:3])
+def test_a_prompt_before_the_sequence_begins(dgt, hq, hk, dim):
+    g = np.random.default_rng(dim + 2)
+    s = Setup(dgt, g, [3, 100, 0], hk, dim)
+    s.check(rand(g, 450, hq, dim), [200, 150, 100])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 100])
+def test_a_scale_below_zero(dgt, dim, rows):
+    g = np.random.default_rng(dim + rows)
+    s = Setup(dgt, g, [300], 2, dim)
+    s.check(rand(g, rows, 4, dim), [rows], scale=-0.06)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_a_prompt_of_queries_of_any_size(dgt, dim):
+    # many rows keep a query to 2^-17 of the row's largest element: that, times the sum of |k|, is what a score
+    # may be off besides its sums
+    g = np.random.default_rng(dim + 5)
+    s = Setup(dgt, g, [200], 1, dim)
+    q = rand(g, 100, 4, dim)
+    q[:, 0] *= 2.0 ** -120
+    q[:, 1] *= 2.0 ** 10
+    q[:, 2] = 0
+    q[:, 3, ::2] *= 2.0 ** -14
+    scale = dim ** -0.5 * torch.tensor([1, 2.0 ** -10, 1, 1], dtype=torch.float64)
+    for h in range(4):
+        part = q[:, h:h + 1].contiguous()
+        lse = torch.empty(100, 1, device="cuda")
+        out = dgt.kv_attention(s.c, 0, part, i32([0]), cu=i32([0, 100]), scale=float(scale[h]), lse=lse)
+        ref, lref, mag, big = R.attention(f64(part), *s.kv[0], 100, 0, 0, float(scale[h]))
+        keys = np.abs(s.kv[0][0]).sum(2).max() * float(scale[h])
+        off = dim * 2.0 ** -24 * big + 2.0 ** -17 * np.abs(f64(part)).max(2) * keys
+        assert (np.abs(f64(lse) - lref) <= off + 2.0 ** -18).all()
+        assert (np.abs(f64(out) - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -10 + 2 * off[..., None]) * mag).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_rows_of_a_prompt_that_are_not_finite(dgt, dim):
+    g = np.random.default_rng(dim + 8)
+    s = Setup(dgt, g, [230], 1, dim)
+    q = rand(g, 100, 4, dim)
+    clean = dgt.kv_attention(s.c, 0, q, i32([0]), cu=i32([0, 100]))
+    for bad in (float("nan"), float("-inf")):
+        p = q.clone()
+        p[40, 1, 5] = bad
+        got = dgt.kv_attention(s.c, 0, p, i32([0]), cu=i32([0, 100]))
+        assert torch.isnan(got[40, 1]).all()
+        got[40, 1] = clean[40, 1]
+        assert torch.equal(got, clean)
+
+
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("side", [0, 1])
 def test_what_a_row_does_not_see_adds_nothing(dgt, dim, side):
@@ -313,7 +396,7 @@ def test_offsets_past_32_bits(dgt):
 
 
 @pytest.mark.parametrize("polls", [0, 1])
-@pytest.mark.parametrize("dim,rows", [(64, 1), (128, 1), (256, 1), (128, 9)])
+@pytest.mark.parametrize("dim,rows", [(64, 1), (128, 1), (256, 1), (128, 9), (64, 100), (128, 100), (256, 100)])
 def test_a_wait_that_runs_out_is_reported(dgt, dim, rows, polls):
     # the test hook: waits give up after `polls` polls, the status says so, and the next call is as ever
     g = np.random.default_rng(dim)
