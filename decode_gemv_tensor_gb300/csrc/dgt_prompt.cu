@@ -382,18 +382,24 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                     fac = bad ? __uint_as_float(0x7FC00000u) : ldexpf(fabsf(a.scale_log2), -up);
                     const uint32_t rr = row & 127, q0 = base + Cfg::q + 2 * t * QP + rr * RB;
                     const uint32_t sw = RB == 128 ? rr & 7 : (rr >> 1) & 3;
-                    // 16 elements at a time, again from the cache: kept rolled, the code runs once a segment
+                    // again from the cache, 64 elements' loads in flight (16: 256 dimensions, 2048 tokens 335 us, so 293)
 #pragma unroll 1
-                    for (uint32_t i = 0; i < D / 16; i++) {
-                        uint4 x[2] = {};
-                        if (live && !bad) x[0] = qp[2 * i], x[1] = qp[2 * i + 1];
-                        const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-                        uint32_t hi[8], lo[8];
+                    for (uint32_t i0 = 0; i0 < D / 16; i0 += 4) {
+                        uint4 x[8];
 #pragma unroll
-                        for (int e = 0; e < 8; e++) split2(w[e], f0, f1, hi[e], lo[e]);
-                        const uint32_t at = q0 + i / (RB / 16) * 128 * RB + (((i % (RB / 16)) ^ sw) << 4);
-                        sts128(at, hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
-                        sts128(at + QP, lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
+                        for (uint32_t e = 0; e < 8; e++) x[e] = live && !bad ? qp[2 * i0 + e] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (uint32_t k = 0; k < 4; k++) {
+                            const uint32_t i = i0 + k;
+                            const uint32_t w[8] = {x[2 * k].x, x[2 * k].y, x[2 * k].z, x[2 * k].w,
+                                                   x[2 * k + 1].x, x[2 * k + 1].y, x[2 * k + 1].z, x[2 * k + 1].w};
+                            uint32_t hi[8], lo[8];
+#pragma unroll
+                            for (int e = 0; e < 8; e++) split2(w[e], f0, f1, hi[e], lo[e]);
+                            const uint32_t at = q0 + i / (RB / 16) * 128 * RB + (((i % (RB / 16)) ^ sw) << 4);
+                            sts128(at, hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
+                            sts128(at + QP, lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
