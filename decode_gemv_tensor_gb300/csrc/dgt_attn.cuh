@@ -329,11 +329,10 @@ __device__ __forceinline__ void write_none(const AttnArgs &a, const Slot &s, uin
 // elements at a time are weighted and added, the parts' loads in flight
 // together.
 constexpr uint32_t JOIN_PARTS = 32;
-__host__ __device__ constexpr uint32_t join_floats(uint32_t RT) { return RT >= 128 ? 2 * RT : (JOIN_PARTS + 2) * RT; }
+__host__ __device__ constexpr uint32_t join_floats(uint32_t RT) { return (JOIN_PARTS + 2) * RT; }
 template <uint32_t D, uint32_t PART, uint32_t RT, typename Sync>
 __device__ __forceinline__ void join_parts(const AttnArgs &a, const Slot &s, uint32_t h, uint32_t c0, uint32_t c1,
                                            uint32_t t, uint32_t threads, float wlog2, float *sh, Sync sync) {
-    constexpr bool MANY = RT >= 128;   // many rows, few parts: a thread per row, weights found again
     float2 *rows = reinterpret_cast<float2 *>(sh);   // per row MU, the quotient's factor
     float *weight = sh + 2 * RT;                     // per part and row
     const uint32_t parts = c1 - c0 + 1;
@@ -350,62 +349,47 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, const Slot &s, uin
                 none ? -INFINITY : (M + __log2f(L)) * LN2;
         }
     };
-    if (MANY) {
-        for (uint32_t row = t; row < s.rows; row += threads) {
-            float M = -INFINITY, MU = -INFINITY, L = 0.0f;
-#pragma unroll 4
-            for (uint32_t k = 0; k < parts; k++) {
-                const float4 st = __ldcg(reinterpret_cast<const float4 *>(at(k, row)));
-                const float m = fmaxf(M, st.x), b = finite_base(m);
-                L = L * ex2(M - b) + st.z * ex2(st.x - b);
-                M = m;
-                MU = fmaxf(MU, st.y);
-            }
-            finish(row, M, MU, L);
-        }
-    } else {
-        // RPW rows a warp, their loads together
-        constexpr uint32_t RPW = MANY ? 1 : RT / 4;
-        const uint32_t lane = t & 31, warp = t >> 5;
-        float M[RPW], MU[RPW], L[RPW], mu0[RPW];
+    // RPW rows a warp, their loads together
+    constexpr uint32_t RPW = RT / 4;
+    const uint32_t lane = t & 31, warp = t >> 5;
+    float M[RPW], MU[RPW], L[RPW], mu0[RPW];
 #pragma unroll
-        for (uint32_t i = 0; i < RPW; i++) M[i] = MU[i] = -INFINITY, L[i] = 0.0f;
-        for (uint32_t k0 = 0; k0 < parts; k0 += 32) {
-            float4 st[RPW];
+    for (uint32_t i = 0; i < RPW; i++) M[i] = MU[i] = -INFINITY, L[i] = 0.0f;
+    for (uint32_t k0 = 0; k0 < parts; k0 += 32) {
+        float4 st[RPW];
 #pragma unroll
-            for (uint32_t i = 0; i < RPW; i++) {
-                st[i] = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
-                if (k0 + lane < parts && warp + 4 * i < s.rows)
-                    st[i] = __ldcg(reinterpret_cast<const float4 *>(at(k0 + lane, warp + 4 * i)));
-            }
-#pragma unroll
-            for (uint32_t i = 0; i < RPW; i++) {
-                if (k0 == 0) mu0[i] = st[i].y;
-                float m = fmaxf(M[i], st[i].x), u = st[i].y;
-#pragma unroll
-                for (int d = 16; d >= 1; d >>= 1) {
-                    m = fmaxf(m, __shfl_xor_sync(DGT_FULL, m, d));
-                    u = fmaxf(u, __shfl_xor_sync(DGT_FULL, u, d));
-                }
-                const float b = finite_base(m);
-                float l = st[i].z * ex2(st[i].x - b);
-#pragma unroll
-                for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(DGT_FULL, l, d);
-                L[i] = L[i] * ex2(M[i] - b) + l;
-                M[i] = m;
-                MU[i] = fmaxf(MU[i], u);
-            }
+        for (uint32_t i = 0; i < RPW; i++) {
+            st[i] = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
+            if (k0 + lane < parts && warp + 4 * i < s.rows)
+                st[i] = __ldcg(reinterpret_cast<const float4 *>(at(k0 + lane, warp + 4 * i)));
         }
 #pragma unroll
         for (uint32_t i = 0; i < RPW; i++) {
-            const uint32_t row = warp + 4 * i;
-            if (row >= s.rows) break;
-            weight[lane * RT + row] = ex2(mu0[i] - finite_base(MU[i]));
-            if (lane == 0) finish(row, M[i], MU[i], L[i]);
+            if (k0 == 0) mu0[i] = st[i].y;
+            float m = fmaxf(M[i], st[i].x), u = st[i].y;
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) {
+                m = fmaxf(m, __shfl_xor_sync(DGT_FULL, m, d));
+                u = fmaxf(u, __shfl_xor_sync(DGT_FULL, u, d));
+            }
+            const float b = finite_base(m);
+            float l = st[i].z * ex2(st[i].x - b);
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(DGT_FULL, l, d);
+            L[i] = L[i] * ex2(M[i] - b) + l;
+            M[i] = m;
+            MU[i] = fmaxf(MU[i], u);
         }
     }
+#pragma unroll
+    for (uint32_t i = 0; i < RPW; i++) {
+        const uint32_t row = warp + 4 * i;
+        if (row >= s.rows) break;
+        weight[lane * RT + row] = ex2(mu0[i] - finite_base(MU[i]));
+        if (lane == 0) finish(row, M[i], MU[i], L[i]);
+    }
     sync();
-    constexpr uint32_t Q = D / 4, B = MANY ? 4 : RT / 8, UN = MANY ? 2 : RT <= 8 ? 8 : 4;   // B elements of four in flight, UN parts
+    constexpr uint32_t Q = D / 4, B = RT / 8, UN = RT <= 8 ? 8 : 4;   // B elements of four in flight, UN parts
     const uint32_t all = s.rows * Q;
     for (uint32_t i0 = t; i0 < all; i0 += B * threads) {
         float v[B][4] = {};
@@ -423,13 +407,13 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, const Slot &s, uin
                     const uint32_t i = min(i0 + b * threads, all - 1), row = i / Q, k = min(k0 + j, parts - 1);
                     const float *p = at(k, row);
                     x[j][b] = __ldcg(reinterpret_cast<const float4 *>(p + 4 + (i % Q) * 4));
-                    f[j][b] = !MANY && k0 < JOIN_PARTS ? weight[k * RT + row] : __ldcg(p + 1) - ro[b].x;
+                    f[j][b] = k0 < JOIN_PARTS ? weight[k * RT + row] : __ldcg(p + 1) - ro[b].x;
                 }
 #pragma unroll
             for (uint32_t j = 0; j < UN; j++)
 #pragma unroll
                 for (uint32_t b = 0; b < B; b++) {
-                    const float w = k0 + j >= parts ? 0.0f : !MANY && k0 < JOIN_PARTS ? f[j][b] : ex2(f[j][b]);
+                    const float w = k0 + j >= parts ? 0.0f : k0 < JOIN_PARTS ? f[j][b] : ex2(f[j][b]);
                     v[b][0] += x[j][b].x * w, v[b][1] += x[j][b].y * w, v[b][2] += x[j][b].z * w, v[b][3] += x[j][b].w * w;
                 }
         }

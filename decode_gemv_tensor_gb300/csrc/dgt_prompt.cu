@@ -71,6 +71,11 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
     f32x2 r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -79,12 +84,44 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
 
 __device__ __forceinline__ void bar_rows() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// Two query elements, scaled, to their two e4m3 parts (the low 16 bits).
-__device__ __forceinline__ void split2(uint32_t bits, float f0, float f1, uint32_t &hi, uint32_t &lo) {
-    const float x = bf16lo(bits) * f0 * f1, y = bf16hi(bits) * f0 * f1;
-    hi = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
-    const float2 z = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));
-    lo = __nv_cvt_float2_to_fp8x2(make_float2(x - z.x, y - z.y), __NV_SATFINITE, __NV_E4M3);
+// Two query elements times f0 and f1, to their two e4m3 parts (16 bits each).
+// The scaled pair is exact in fp16, down to 2^-31 of the row's largest element.
+__device__ __forceinline__ void split2(uint32_t bits, f32x2 f0, f32x2 f1, uint32_t &hi, uint32_t &lo) {
+    float x, y;
+    unpack2(mul2(mul2(pack2(bf16lo(bits), bf16hi(bits)), f0), f1), x, y);
+    const uint32_t h = f16_pair(x, y);
+    asm("{\n\t.reg .b16 c, e;\n\t.reg .b32 b, d;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 c, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 b, c;\n\t"
+        "sub.rn.f16x2 d, %2, b;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 e, d;\n\t"
+        "cvt.u32.u16 %0, c;\n\t"
+        "cvt.u32.u16 %1, e;\n\t}"
+        : "=r"(hi), "=r"(lo)
+        : "r"(h));
+}
+
+// A lane's N words of a row, and to shared memory N halfwords.
+template <uint32_t N>
+__device__ __forceinline__ void load_words(const uint16_t *p, uint32_t (&x)[N]) {
+    if constexpr (N == 1) {
+        x[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        x[0] = v.x, x[1] = v.y;
+    } else {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    }
+}
+template <uint32_t N>
+__device__ __forceinline__ void store_halves(uint32_t addr, const uint32_t (&x)[N]) {
+    if constexpr (N == 1)
+        asm volatile("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tst.shared.b16 [%0], h;\n\t}" ::"r"(addr), "r"(x[0]) : "memory");
+    else if constexpr (N == 2)
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(x[0] | x[1] << 16) : "memory");
+    else
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(x[0] | x[1] << 16), "r"(x[2] | x[3] << 16) : "memory");
 }
 
 template <uint32_t D>
@@ -96,7 +133,6 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
     __shared__ __align__(8) uint64_t kfull[KS], kfree[KS], vfull[VS], vfree[VS], wfull[WS], wfree[WS];
     __shared__ __align__(8) uint64_t sfull[4], pfull[4], ofull[2], ofin[2], qfull[2], drained;
     __shared__ PageMeta meta[PR_META];
-    __shared__ __align__(8) float joined[join_floats(RT)];
     __shared__ Slot slots[AT_CHUNK];
     __shared__ uint64_t usum[PR_WARPS];
     __shared__ uint32_t tmem_slot;
@@ -356,51 +392,57 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                 const uint32_t flat = s.row0 + row;
                 const int32_t pos = live ? s.pos0 + (int32_t)(flat / a.group) : -1;
                 float m = -INFINITY, mu = -INFINITY, l = 0.0f, fac = 0.0f;
+                const uint32_t qt = base + Cfg::q + 2 * t * QP;   // the row tile's operand, later its output
                 if (mine && T) {
-                    const uint4 *qp = reinterpret_cast<const uint4 *>(
-                        a.q.data + (int64_t)(s.tok0 + flat / a.group) * a.q.token_stride +
-                        (int64_t)(r.h * a.group + flat % a.group) * a.q.head_stride);
-                    uint32_t top = 0;
+                    // A row by the whole warp, so that a load touches one row's lines (a thread per row: as many
+                    // lines a load as lanes, 5 us a segment; so 2 us), IN rows in flight.
+                    constexpr uint32_t W = D / 64, IN = 32 / W;
+                    const uint32_t first = t * 128 + quad * 32, f0 = s.row0 + first;
+                    const uint32_t count = s.rows > first ? min(s.rows - first, 32u) : 0;
+                    uint32_t head = f0 % a.group, mytop = 0;
+                    const uint16_t *qp = a.q.data + (int64_t)(s.tok0 + f0 / a.group) * a.q.token_stride +
+                                         (int64_t)(r.h * a.group + head) * a.q.head_stride + lane * 2 * W;
+                    const int64_t wrap = a.q.token_stride - (int64_t)(a.group - 1) * a.q.head_stride;
+                    const uint32_t d = lane * 2 * W, chunk = (d % RB) / 16;   // the lane's first dimension
+                    const uint32_t col = qt + d / RB * 128 * RB + d % 16;
 #pragma unroll 1
-                    for (uint32_t i0 = 0; i0 < D / 8; i0 += 8) {
-                        uint4 x[8];
+                    for (uint32_t i0 = 0; i0 < 32; i0 += IN) {
+                        uint32_t x[IN][W];
 #pragma unroll
-                        for (uint32_t i = 0; i < 8; i++) x[i] = live ? qp[i0 + i] : make_uint4(0, 0, 0, 0);
+                        for (uint32_t i = 0; i < IN; i++) {
+                            if (i0 + i < count) {
+                                load_words<W>(qp, x[i]);
+                                const bool last = ++head == a.group;
+                                qp += last ? wrap : a.q.head_stride;
+                                if (last) head = 0;
+                            } else {
 #pragma unroll
-                        for (uint32_t i = 0; i < 8; i++) {
-                            top = max(top, max(max(x[i].x & 0x7FFFu, x[i].x >> 16 & 0x7FFFu), max(x[i].y & 0x7FFFu, x[i].y >> 16 & 0x7FFFu)));
-                            top = max(top, max(max(x[i].z & 0x7FFFu, x[i].z >> 16 & 0x7FFFu), max(x[i].w & 0x7FFFu, x[i].w >> 16 & 0x7FFFu)));
+                                for (uint32_t k = 0; k < W; k++) x[i][k] = 0;
+                            }
+                        }
+#pragma unroll
+                        for (uint32_t i = 0; i < IN; i++) {
+                            uint32_t top = x[i][0] & 0x7FFF7FFFu;
+#pragma unroll
+                            for (uint32_t k = 1; k < W; k++) top = __vmaxu2(top, x[i][k] & 0x7FFF7FFFu);
+                            top = __reduce_max_sync(DGT_FULL, max(top & 0xFFFFu, top >> 16)) >> 7;
+                            if (lane == i0 + i) mytop = top;
+                            // the largest element to [2^7, 2^8); one that is not finite: the row's factor says so
+                            const int up = 7 + 127 - (int)top, up0 = min(up, 100);
+                            float a0 = __uint_as_float((uint32_t)(up0 + 127) << 23);
+                            const float a1 = __uint_as_float((uint32_t)(up - up0 + 127) << 23);
+                            if (a.scale_log2 < 0.0f) a0 = -a0;
+                            const f32x2 m0 = pack2(a0, a0), m1 = pack2(a1, a1);
+                            uint32_t hi[W], lo[W];
+#pragma unroll
+                            for (uint32_t k = 0; k < W; k++) split2(top == 255 ? 0u : x[i][k], m0, m1, hi[k], lo[k]);
+                            const uint32_t rr = quad * 32 + i0 + i, sw = RB == 128 ? rr & 7 : (rr >> 1) & 3;
+                            const uint32_t at = col + rr * RB + ((chunk ^ sw) << 4);
+                            store_halves<W>(at, hi);
+                            store_halves<W>(at + QP, lo);
                         }
                     }
-                    top >>= 7;
-                    // the largest element to [2^7, 2^8); one that is not finite: the row's factor says so
-                    const bool bad = top == 255;
-                    const int up = 7 + 127 - (int)top, up0 = min(up, 100);
-                    float f0 = __uint_as_float((uint32_t)(up0 + 127) << 23);
-                    const float f1 = __uint_as_float((uint32_t)(up - up0 + 127) << 23);
-                    if (a.scale_log2 < 0.0f) f0 = -f0;
-                    fac = bad ? __uint_as_float(0x7FC00000u) : ldexpf(fabsf(a.scale_log2), -up);
-                    const uint32_t rr = row & 127, q0 = base + Cfg::q + 2 * t * QP + rr * RB;
-                    const uint32_t sw = RB == 128 ? rr & 7 : (rr >> 1) & 3;
-                    // again from the cache, 64 elements' loads in flight (16: 256 dimensions, 2048 tokens 335 us, so 293)
-#pragma unroll 1
-                    for (uint32_t i0 = 0; i0 < D / 16; i0 += 4) {
-                        uint4 x[8];
-#pragma unroll
-                        for (uint32_t e = 0; e < 8; e++) x[e] = live && !bad ? qp[2 * i0 + e] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                        for (uint32_t k = 0; k < 4; k++) {
-                            const uint32_t i = i0 + k;
-                            const uint32_t w[8] = {x[2 * k].x, x[2 * k].y, x[2 * k].z, x[2 * k].w,
-                                                   x[2 * k + 1].x, x[2 * k + 1].y, x[2 * k + 1].z, x[2 * k + 1].w};
-                            uint32_t hi[8], lo[8];
-#pragma unroll
-                            for (int e = 0; e < 8; e++) split2(w[e], f0, f1, hi[e], lo[e]);
-                            const uint32_t at = q0 + i / (RB / 16) * 128 * RB + (((i % (RB / 16)) ^ sw) << 4);
-                            sts128(at, hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
-                            sts128(at + QP, lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
-                        }
-                    }
+                    fac = mytop == 255 ? __uint_as_float(0x7FC00000u) : ldexpf(fabsf(a.scale_log2), (int)mytop - 134);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&qfull[t]));
@@ -521,48 +563,106 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                 const bool complete = r.pa == 0 && r.pe == n;
                 if (mine && T) wait(ofin[t], qc[t] & 1u);
                 tc_fence_after();
-                float *part = a.part + (2 * (uint64_t)blockIdx.x + (r.pa == 0 ? 1 : 0)) * Cfg::PART + row * (D + 4);
                 const bool none = m == -INFINITY && l == 0.0f;
-                const uint64_t at = (uint64_t)(s.tok0 + flat / a.group) * a.q_heads + r.h * a.group + flat % a.group;
-                const float quot = none ? 0.0f : ex2(finite_base(mu) - finite_base(m) - PR_W_LOG2) / l;
+                const uint32_t orow = (s.tok0 + flat / a.group) * a.q_heads + r.h * a.group + flat % a.group;
+                // Output rows pass through the warp's 32 rows of the operand, which nothing reads any more, and
+                // leave it a row's lines at a time.
+                const uint32_t rr = quad * 32 + lane, sw = RB == 128 ? rr & 7 : (rr >> 1) & 3;
+                auto put = [&](uint32_t d0, const float (&o)[32], float f) {
+#pragma unroll
+                    for (uint32_t i = 0; i < 4; i++) {
+                        const uint32_t e = d0 / 8 + i, c = e % (RB / 16);
+                        sts128(qt + e / (RB / 16) * 128 * RB + rr * RB + ((c ^ sw) << 4),
+                               bf16x2(o[8 * i] * f, o[8 * i + 1] * f), bf16x2(o[8 * i + 2] * f, o[8 * i + 3] * f),
+                               bf16x2(o[8 * i + 4] * f, o[8 * i + 5] * f), bf16x2(o[8 * i + 6] * f, o[8 * i + 7] * f));
+                    }
+                };
+                auto put_out = [&]() {
+                    __syncwarp();
+#pragma unroll 4
+                    for (uint32_t k = 0; k < D / 8; k++) {
+                        const uint32_t i = (k * 32 + lane) / (D / 8), e = (k * 32 + lane) % (D / 8);
+                        const uint32_t ri = quad * 32 + i, c = (e % (RB / 16)) ^ (RB == 128 ? ri & 7 : (ri >> 1) & 3);
+                        const uint32_t o = __shfl_sync(DGT_FULL, orow, i);
+                        const uint4 x = lds128(qt + e / (RB / 16) * 128 * RB + ri * RB + (c << 4));
+                        if (t * 128 + ri < s.rows) reinterpret_cast<uint4 *>(a.out + (uint64_t)o * D)[e] = x;
+                    }
+                    __syncwarp();
+                };
+                // A part: four dimensions of all rows after four, then M, MU, L of all rows.
+                float4 *part = reinterpret_cast<float4 *>(a.part + (2 * (uint64_t)blockIdx.x + (r.pa == 0 ? 1 : 0)) * Cfg::PART) + row;
                 if (mine && !dead) {
+                    const float quot = none ? 0.0f : ex2(finite_base(mu) - finite_base(m) - PR_W_LOG2) / l;
 #pragma unroll 1
                     for (uint32_t d0 = 0; d0 < D; d0 += 32) {
-                        uint32_t o[32] = {};
+                        float o[32] = {};
                         if (T) {
-                            tmem_ld32(tm + tl + t * D + d0, o);
+                            uint32_t w[32];
+                            tmem_ld32(tm + tl + t * D + d0, w);
                             tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; i++) o[i] = __uint_as_float(w[i]);
                         }
-                        if (live && complete) {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 8) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int e = 0; e < 4; e++)
-                                    w[e] = bf16x2(__uint_as_float(o[i + 2 * e]) * quot, __uint_as_float(o[i + 2 * e + 1]) * quot);
-                                *reinterpret_cast<uint4 *>(a.out + at * D + d0 + i) = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
+                        if (complete) {
+                            put(d0, o, quot);
                         } else if (live) {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<uint4 *>(part + 4 + d0 + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                            for (int i = 0; i < 8; i++)
+                                part[(d0 / 4 + i) * RT] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                         }
                         __syncwarp();   // the next load is the whole warp's
                     }
-                    if (live && complete && a.lse) a.lse[at] = none ? -INFINITY : (m + __log2f(l)) * LN2;
-                    if (live && !complete) *reinterpret_cast<float4 *>(part) = make_float4(m, mu, l, 0.0f);
+                    if (complete) put_out();
+                    if (live && complete && a.lse) a.lse[orow] = none ? -INFINITY : (m + __log2f(l)) * LN2;
+                    if (live && !complete) part[D / 4 * RT] = make_float4(m, mu, l, 0.0f);
                 }
                 tc_fence_before();
                 if (!complete) {
-                    // the last CTA of the segment to arrive adds its parts in page order
+                    // the last CTA of the segment to arrive adds its parts in page order, a thread per row
                     const uint64_t sa = chunk_base + s.base + (uint64_t)r.h * n, sb = sa + n;
                     uint32_t c0, c1;
                     cut.holders(sa, sb, c0, c1);
                     bar_rows();
                     if (tid == 0) last_flag = arrive_last(&a.count[c0], c1 - c0 + 1);
                     bar_rows();
-                    if (last_flag)
-                        join_parts<D, Cfg::PART, RT>(a, s, r.h, c0, c1, tid, 256, PR_W_LOG2, joined, bar_rows);
+                    if (last_flag && mine) {
+                        // part 0 is the one that begins the segment, at the end of its CTA's work
+                        const float4 *p0 = reinterpret_cast<const float4 *>(a.part + (2 * (uint64_t)c0 + 1) * Cfg::PART) + (live ? row : 0);
+                        const float4 *p1 = reinterpret_cast<const float4 *>(a.part + 2 * ((uint64_t)c0 + 1) * Cfg::PART) + (live ? row : 0);
+                        const uint32_t parts = c1 - c0 + 1;
+                        auto at = [&](uint32_t k) { return k ? p1 + (uint64_t)(k - 1) * (2 * Cfg::PART / 4) : p0; };
+                        float M = -INFINITY, MU = -INFINITY, L = 0.0f;
+#pragma unroll 4
+                        for (uint32_t k = 0; k < parts; k++) {
+                            const float4 st = __ldcg(at(k) + D / 4 * RT);
+                            const float mn = fmaxf(M, st.x), bm = finite_base(mn);
+                            L = L * ex2(M - bm) + st.z * ex2(st.x - bm);
+                            M = mn;
+                            MU = fmaxf(MU, st.y);
+                        }
+                        const bool nothing = M == -INFINITY && L == 0.0f;
+                        const float bu = finite_base(MU), quot = nothing ? 0.0f : ex2(bu - finite_base(M) - PR_W_LOG2) / L;
+                        if (live && a.lse) a.lse[orow] = nothing ? -INFINITY : (M + __log2f(L)) * LN2;
+#pragma unroll 1
+                        for (uint32_t d0 = 0; d0 < D; d0 += 32) {
+                            float o[32] = {};
+#pragma unroll 2
+                            for (uint32_t k = 0; k < parts; k++) {
+                                const float4 *p = at(k);
+                                float4 x[8];
+#pragma unroll
+                                for (uint32_t i = 0; i < 8; i++) x[i] = __ldcg(p + (d0 / 4 + i) * RT);
+                                const float w = ex2(__ldcg(p + D / 4 * RT).y - bu);
+#pragma unroll
+                                for (uint32_t i = 0; i < 8; i++) {
+                                    o[4 * i] += x[i].x * w, o[4 * i + 1] += x[i].y * w;
+                                    o[4 * i + 2] += x[i].z * w, o[4 * i + 3] += x[i].w * w;
+                                }
+                            }
+                            put(d0, o, quot);
+                        }
+                        put_out();
+                    }
                 }
             }
             it += T;
