@@ -2,7 +2,8 @@
 // how the work is cut.
 //
 // Work is cut evenly over the CTAs whatever the lengths.  A segment is one tile
-// of query rows and one kv head, its units are the pages that the tile sees.
+// of query rows and one kv head, its units are the pages that the tile sees and
+// `end` more, which come first, for what a segment costs besides its pages.
 // Where that comes out even enough, every segment is cut into equal parts, a
 // CTA for each; otherwise CTA c of C takes units [c U / C, (c + 1) U / C) of
 // all U, a cut close to a segment's border moved there.  A segment that ends up
@@ -33,13 +34,15 @@ struct AttnArgs {
     int32_t *count;     // workspace: arrivals at the segment that CTA c begins and others end, zero between calls
     float *part;        // workspace: two partial results per CTA
     int32_t *status;
-    uint32_t min_units, slack, spin;   // pages of a part at least; pages that parts may be above an even share
+    uint32_t min_units, slack;   // pages of a part at least; pages that parts may be above an even share
+    uint32_t end;                // what a segment costs besides its pages, in pages
+    uint32_t spin;
 };
 
 // A tile of query rows: rows [row0, row0 + rows) of its entry's flattened
 // (token, head of the group) rows, at positions pos0 + row / group.
 struct Slot {
-    uint32_t base, np;          // first unit (of the chunk's), pages per head (0: none is seen)
+    uint32_t base, np;          // first unit (of the chunk's), pages per head (0: none is seen, counted as one)
     uint32_t sp, wp;            // pages seen before the window's, the window's first page
     int32_t seq, pos0;          // table row; position of the entry's first row
     uint32_t tok0, row0, rows;  // entry's first token row, tile's first flattened row, row count
@@ -99,7 +102,7 @@ __device__ __forceinline__ Slot slot_info(const AttnArgs &a, uint32_t slot, uint
     if (first >= all) return s;
     s.row0 = (uint32_t)first;
     s.rows = (uint32_t)min((uint64_t)RT, all - first);
-    *units = a.c.kv_heads;
+    *units = a.c.kv_heads * (1 + a.end);
     s.seq = a.seqs[b];
     int32_t len = 0;
     if (s.seq < 0 || (uint32_t)s.seq >= a.c.max_seqs) {
@@ -119,7 +122,7 @@ __device__ __forceinline__ Slot slot_info(const AttnArgs &a, uint32_t slot, uint
     s.wp = lo / KV_P;
     s.sp = min((min(a.sinks, lo) + KV_P - 1) / KV_P, s.wp);
     s.np = s.sp + (uint32_t)pl / KV_P - s.wp + 1;
-    *units = a.c.kv_heads * s.np;
+    *units = a.c.kv_heads * (s.np + a.end);
     return s;
 }
 
@@ -182,12 +185,12 @@ __device__ __forceinline__ Units describe(const AttnArgs &a, uint32_t RT, uint32
     return u;
 }
 
-// A run of pages [pa, pe) of head h's segment of a described tile, beginning
-// at unit u and ending by unit u1.
+// A run of pages [pa, pe) of head h's segment of a described tile: `units`
+// units from u on, ending by unit u1.
 struct Run {
-    uint32_t u, slot, h, pa, pe;
+    uint32_t u, units, slot, h, pa, pe;
 };
-__device__ __forceinline__ Run run_at(const Slot *slots, uint32_t nslots, uint32_t u, uint32_t u1) {
+__device__ __forceinline__ Run run_at(const Slot *slots, uint32_t nslots, uint32_t end, uint32_t u, uint32_t u1) {
     uint32_t lo = 0, hi = nslots;   // the last tile that begins at or before u
     while (hi - lo > 1) {
         const uint32_t mid = (lo + hi) >> 1;
@@ -196,16 +199,17 @@ __device__ __forceinline__ Run run_at(const Slot *slots, uint32_t nslots, uint32
     }
     Run r;
     const Slot &s = slots[lo];
-    const uint32_t n = s.per_head();
-    r.u = u, r.slot = lo, r.h = (u - s.base) / n, r.pa = (u - s.base) % n;
-    r.pe = min(n, r.pa + (u1 - u));
+    const uint32_t n = s.per_head() + end, from = (u - s.base) % n, to = min(n, from + (u1 - u));
+    r.u = u, r.units = to - from, r.slot = lo, r.h = (u - s.base) / n;
+    r.pa = from > end ? from - end : 0;
+    r.pe = to > end ? to - end : 0;
     return r;
 }
 
 // Where the CTAs' shares begin.
 struct Cuts {
     uint64_t U;
-    uint32_t C, tol;          // CTA c at unit c U / C, or at a segment's border within tol of that
+    uint32_t C, tol, end;     // CTA c at unit c U / C, or at a segment's border within tol of that
     bool parts;               // or: one part of one segment, units [u0, u1) of the only chunk,
     uint32_t u0, u1, c0, c1;  // the segment's other parts with the CTAs c0..c1
     __device__ __forceinline__ uint64_t raw(uint32_t c) const {
@@ -213,10 +217,9 @@ struct Cuts {
     }
     // unit u of a described chunk, moved to a segment's border
     __device__ __forceinline__ uint32_t snap(const Slot *slots, uint32_t nslots, uint32_t u) const {
-        if (tol == 0) return u;
-        const Run r = run_at(slots, nslots, u, u + 1);
-        const uint32_t n = slots[r.slot].per_head(), below = r.pa, above = n - r.pa;
-        return below <= tol || above <= tol ? (below <= above ? u - below : u + above) : u;
+        const Run r = run_at(slots, nslots, end, u, u + 1);
+        const uint32_t n = slots[r.slot].per_head() + end, below = (u - slots[r.slot].base) % n, above = n - below;
+        return below <= end + tol || above <= tol ? (below <= end + above ? u - below : u + above) : u;
     }
     // this CTA's units of the chunk [base, base + tot)
     __device__ __forceinline__ void share(const Slot *slots, uint32_t nslots, uint64_t base, uint32_t tot, uint32_t &a,
@@ -235,8 +238,8 @@ struct Cuts {
             first = c0, last = c1;
             return;
         }
-        // cuts c with sa + tol < raw(c) < sb - tol stay inside
-        first = (uint32_t)(((sa + tol + 1) * C + U - 1) / U) - 1;
+        // cuts c with sa + end + tol < raw(c) < sb - tol stay inside
+        first = (uint32_t)(((sa + end + tol + 1) * C + U - 1) / U) - 1;
         last = sb <= tol ? 0u : (uint32_t)(((sb - tol) * C + U - 1) / U) - 1;
     }
 };
@@ -244,16 +247,16 @@ struct Cuts {
 // How a call is cut over `grid` CTAs.  Parts: of at most T pages, T the least
 // for which all parts have a CTA, and min_units; taken while T is no more than
 // `slack` pages above an even share, because a second segment in a CTA costs a
-// segment's end (statistics, stores, the counter, the join: about what twelve
-// pages of 128 dimensions cost).  Otherwise even shares, whose cuts move by an
-// eighth of a share at most.
+// segment's end.  Otherwise even shares, whose cuts move by an eighth of a
+// share at most, or past the units that stand for the segment's end.
 __device__ __forceinline__ Cuts cut_plan(const AttnArgs &a, Units all, const Slot *slots, uint32_t grid) {
-    const uint64_t U = all.units(), S = (uint64_t)all.tiles() * a.c.kv_heads;
+    const uint64_t U = all.units(), S = (uint64_t)all.tiles() * a.c.kv_heads, P = U - S * a.end;
     const uint32_t lane = lane_id(), heads = a.c.kv_heads;
     Cuts k;
     k.U = U;
     k.C = (uint32_t)min((uint64_t)grid, U);   // shares of one unit at least: cuts inside a segment are distinct
     k.tol = (uint32_t)min(U / (8 * grid), (uint64_t)4);
+    k.end = a.end;
     // (U below 2^22: a segment's pages and T then are below 2^23)
     k.parts = a.slots <= AT_CHUNK && S <= grid && U && U < (1u << 22);
     if (!k.parts) return k;
@@ -273,7 +276,7 @@ __device__ __forceinline__ Cuts cut_plan(const AttnArgs &a, Units all, const Slo
         if ((q + 1) * T <= x) q++;
         return q;
     };
-    const uint32_t T0 = max(((uint32_t)U + grid - 1) / grid, a.min_units);
+    const uint32_t T0 = max(((uint32_t)P + grid - 1) / grid, a.min_units);
     uint32_t T = 0;
 #pragma unroll
     for (uint32_t i = 0; i < 6; i++) {
@@ -302,9 +305,9 @@ __device__ __forceinline__ Cuts cut_plan(const AttnArgs &a, Units all, const Slo
     const uint32_t first = __shfl_sync(DGT_FULL, second ? mid : ex, src);
     const uint32_t parts = __shfl_sync(DGT_FULL, second ? p[1] : p[0], src), pages = __shfl_sync(DGT_FULL, second ? n[1] : n[0], src);
     const uint32_t slot = 2 * src + __shfl_sync(DGT_FULL, (uint32_t)second, src);
-    const uint32_t h = (cta - first) / parts, j = (cta - first) % parts, at = slots[slot].base + h * pages;
-    k.u0 = at + j * pages / parts;
-    k.u1 = at + (j + 1) * pages / parts;
+    const uint32_t h = (cta - first) / parts, j = (cta - first) % parts, at = slots[slot].base + h * (pages + a.end);
+    k.u0 = at + (j ? a.end + j * pages / parts : 0);
+    k.u1 = at + a.end + (j + 1) * pages / parts;
     k.c0 = first + h * parts;
     k.c1 = k.c0 + parts - 1;
     return k;

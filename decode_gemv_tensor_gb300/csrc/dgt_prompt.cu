@@ -207,8 +207,8 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
         uint32_t u0, u1;
         cut.share(slots, nslots, chunk_base, tot, u0, u1);
         for (uint32_t u = u0; u < u1;) {
-            const Run r = run_at(slots, nslots, u, u1);
-            u += r.pe - r.pa;
+            const Run r = run_at(slots, nslots, a.end, u, u1);
+            u += r.units;
             const Slot &s = slots[r.slot];
             const uint32_t n = s.per_head();
             const uint32_t T = s.np ? r.pe - r.pa : 0;
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                 tc_fence_before();
                 if (!complete) {
                     // the last CTA of the segment to arrive adds its parts in page order, a thread per row
-                    const uint64_t sa = chunk_base + s.base + (uint64_t)r.h * n, sb = sa + n;
+                    const uint64_t sa = chunk_base + s.base + (uint64_t)r.h * (n + a.end), sb = sa + n + a.end;
                     uint32_t c0, c1;
                     cut.holders(sa, sb, c0, c1);
                     bar_rows();
