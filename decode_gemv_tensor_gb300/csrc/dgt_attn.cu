@@ -53,8 +53,8 @@ struct AttnCfg {
     static constexpr uint32_t IB = KV_P * PD, IPP = 2 * PAN;
     static constexpr uint32_t NS = D == 64 ? 4 : 2;      // deeper rings were no faster (16 KB a warp in flight is enough)
     static constexpr uint32_t RT = 8 * NT;
-    static constexpr uint32_t KSTEPS = D / 16;           // k-steps of the first product
-    static constexpr bool QREG = NT * D <= 256;          // query fragments in registers
+    static constexpr uint32_t KSTEPS = D / 16;           // k-steps of the first product; their operands stay in registers
+    static_assert(NT * D <= 256, "which more rows would not");
     static constexpr uint32_t RS = D + 4;                // row of the merge scratch, padded
     static constexpr uint32_t ring = 0, scratch = AT_WARPS * NS * IB, q = scratch + AT_WARPS * 8 * RS * 4,
                               bytes = q + KSTEPS * NT * 256;
@@ -269,16 +269,10 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) k_kv_attention(AttnArgs a) {
             __syncthreads();
 
             at_hand = false;
-            uint2 qf[Cfg::QREG ? Cfg::KSTEPS * NT : 1];
-            auto load_q = [&](uint32_t i) {
-                uint2 v;
-                asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(qs + (i * 32 + lane) * 8));
-                return v;
-            };
-            if (Cfg::QREG) {
+            uint2 qf[Cfg::KSTEPS * NT];
 #pragma unroll
-                for (uint32_t i = 0; i < (Cfg::QREG ? Cfg::KSTEPS * NT : 1); i++) qf[i] = load_q(i);
-            }
+            for (uint32_t i = 0; i < Cfg::KSTEPS * NT; i++)
+                asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(qf[i].x), "=r"(qf[i].y) : "r"(qs + (i * 32 + lane) * 8));
             // per column (query row 8 nt + 2 c + e): factor, position, window start, maxima, sum
             float fac[NT][2], m[NT][2], mu[NT][2], l[NT][2];
             float o[D / 16][NT][4];
@@ -342,8 +336,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 2) k_kv_attention(AttnArgs a) {
                                     const uint32_t a1 = e4m3_lo(wb[w]), a3 = e4m3_hi(wb[w]);
 #pragma unroll
                                     for (uint32_t nt = 0; nt < NT; nt++) {
-                                        const uint32_t qi = (pan * 8 + i * 4 + w) * NT + nt;
-                                        const uint2 b = Cfg::QREG ? qf[Cfg::QREG ? qi : 0] : load_q(qi);
+                                        const uint2 b = qf[(pan * 8 + i * 4 + w) * NT + nt];
                                         mma16816(sc[t][nt], a0, a1, a2, a3, b.x, b.y);
                                     }
                                 }
@@ -571,21 +564,20 @@ static int attn_launch(const AttnArgs &a, cudaStream_t st) {
 }
 
 // Rows of a tile, by an entry's rows (the mean of a batch): in n-tiles of
-// eight, as many as they fill, while the accumulators of D dimensions a row fit
-// the registers beside them; more rows go to the tensor-core tiles.  Measured
-// on both sides, n-tiles of eight first:
-//   64 dimensions, 28 rows: 31 and 41 us (8 sequences of up to 8003 tokens),
-//     53 and 69 us (32 of 4000), but 21 and 13 us (1 of 500);
-//   128 dimensions, 24 rows: 35 and 44 us (8 of 8003), 73 and 79 us (2 of
-//     60000); 28 rows: 45 and 45 us, 97 and 80 us, and 28 and 15 us (1 of 500);
-//   256 dimensions, 12 rows: 55 and 61 us (8 of 8003), 108 and 104 us (2 of
-//     60000); 18 rows: 64 and 63 us, 140 and 108 us.
+// eight, as many as they fill, while that is the faster form; more rows go to
+// the tensor-core tiles.  Measured on both sides, n-tiles of eight first (1
+// sequence of 500 tokens, 8 of up to 8003 with 4 kv heads, 2 of 60000):
+//   64 dimensions, 24 rows: 15 and 13, 24 and 28, 44 and 42 us; 32 rows: 21
+//     and 13, 33 and 28, 56 and 43 us;
+//   128 dimensions, 16 rows: 13 and 14, 24 and 29, 58 and 44 us; 24 rows: 20
+//     and 14, 35 and 29, 73 and 45 us;
+//   256 dimensions, 10 rows: 20 and 18, 41 and 39, 94 and 56 us.
 struct Plan {
     uint32_t nt, RT;   // nt 0: tensor-core tiles
 };
 static Plan attn_plan(uint32_t head_dim, uint32_t group, uint32_t batch, uint64_t tokens) {
     const uint64_t rows = group * ((tokens + batch - 1) / batch);
-    const uint64_t most = head_dim == 64 ? 32 : head_dim == 128 ? 24 : 16;
+    const uint64_t most = head_dim == 64 ? 24 : head_dim == 128 ? 16 : 8;
     if (rows > most) return {0, prompt_rows(head_dim)};
     const uint32_t nt = (uint32_t)((rows + 7) / 8);
     return {nt, 8 * nt};
@@ -649,14 +641,9 @@ extern "C" int dgt_kv_attention_ex(const dgt_kv_cache *cache, uint32_t layer, co
     cudaStream_t st = (cudaStream_t)stream;
     if (nt == 0) return prompt_launch(a, st);
     switch (cache->head_dim) {
-        case 64:
-            return nt == 1   ? attn_launch<64, 1>(a, st)
-                   : nt == 2 ? attn_launch<64, 2>(a, st)
-                   : nt == 3 ? attn_launch<64, 3>(a, st)
-                             : attn_launch<64, 4>(a, st);
-        case 128:
-            return nt == 1 ? attn_launch<128, 1>(a, st) : nt == 2 ? attn_launch<128, 2>(a, st) : attn_launch<128, 3>(a, st);
-        default: return nt == 1 ? attn_launch<256, 1>(a, st) : attn_launch<256, 2>(a, st);
+        case 64: return nt == 1 ? attn_launch<64, 1>(a, st) : nt == 2 ? attn_launch<64, 2>(a, st) : attn_launch<64, 3>(a, st);
+        case 128: return nt == 1 ? attn_launch<128, 1>(a, st) : attn_launch<128, 2>(a, st);
+        default: return attn_launch<256, 1>(a, st);
     }
 }
 

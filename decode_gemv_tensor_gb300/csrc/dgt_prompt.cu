@@ -567,25 +567,25 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                 const uint32_t orow = (s.tok0 + flat / a.group) * a.q_heads + r.h * a.group + flat % a.group;
                 // Output rows pass through the warp's 32 rows of the operand, which nothing reads any more, and
                 // leave it a row's lines at a time.
-                const uint32_t rr = quad * 32 + lane, sw = RB == 128 ? rr & 7 : (rr >> 1) & 3;
-                auto put = [&](uint32_t d0, const float (&o)[32], float f) {
+                auto chunk_at = [&](uint32_t row, uint32_t e) {   // 16 bytes of output row `row` of the tile
+                    const uint32_t rr = row & 127, c = (e % (RB / 16)) ^ (RB == 128 ? rr & 7 : (rr >> 1) & 3);
+                    return base + Cfg::q + row / 128 * 2 * QP + e / (RB / 16) * 128 * RB + rr * RB + (c << 4);
+                };
+                auto put = [&](uint32_t row, uint32_t d0, const float (&o)[32], float f) {
 #pragma unroll
-                    for (uint32_t i = 0; i < 4; i++) {
-                        const uint32_t e = d0 / 8 + i, c = e % (RB / 16);
-                        sts128(qt + e / (RB / 16) * 128 * RB + rr * RB + ((c ^ sw) << 4),
-                               bf16x2(o[8 * i] * f, o[8 * i + 1] * f), bf16x2(o[8 * i + 2] * f, o[8 * i + 3] * f),
-                               bf16x2(o[8 * i + 4] * f, o[8 * i + 5] * f), bf16x2(o[8 * i + 6] * f, o[8 * i + 7] * f));
-                    }
+                    for (uint32_t i = 0; i < 4; i++)
+                        sts128(chunk_at(row, d0 / 8 + i), bf16x2(o[8 * i] * f, o[8 * i + 1] * f),
+                               bf16x2(o[8 * i + 2] * f, o[8 * i + 3] * f), bf16x2(o[8 * i + 4] * f, o[8 * i + 5] * f),
+                               bf16x2(o[8 * i + 6] * f, o[8 * i + 7] * f));
                 };
                 auto put_out = [&]() {
                     __syncwarp();
 #pragma unroll 4
                     for (uint32_t k = 0; k < D / 8; k++) {
-                        const uint32_t i = (k * 32 + lane) / (D / 8), e = (k * 32 + lane) % (D / 8);
-                        const uint32_t ri = quad * 32 + i, c = (e % (RB / 16)) ^ (RB == 128 ? ri & 7 : (ri >> 1) & 3);
+                        const uint32_t i = (k * 32 + lane) / (D / 8), e = (k * 32 + lane) % (D / 8), ri = t * 128 + quad * 32 + i;
                         const uint32_t o = __shfl_sync(DGT_FULL, orow, i);
-                        const uint4 x = lds128(qt + e / (RB / 16) * 128 * RB + ri * RB + (c << 4));
-                        if (t * 128 + ri < s.rows) reinterpret_cast<uint4 *>(a.out + (uint64_t)o * D)[e] = x;
+                        const uint4 x = lds128(chunk_at(ri, e));
+                        if (ri < s.rows) reinterpret_cast<uint4 *>(a.out + (uint64_t)o * D)[e] = x;
                     }
                     __syncwarp();
                 };
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                             for (int i = 0; i < 32; i++) o[i] = __uint_as_float(w[i]);
                         }
                         if (complete) {
-                            put(d0, o, quot);
+                            put(row, d0, o, quot);
                         } else if (live) {
 #pragma unroll
                             for (int i = 0; i < 8; i++)
@@ -618,21 +618,29 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                 }
                 tc_fence_before();
                 if (!complete) {
-                    // the last CTA of the segment to arrive adds its parts in page order, a thread per row
+                    // The last CTA of the segment to arrive adds its parts in page order: GR threads a row, each
+                    // for D / GR of its dimensions, as many as the tile's rows leave.
                     const uint64_t sa = chunk_base + s.base + (uint64_t)r.h * (n + a.end), sb = sa + n + a.end;
                     uint32_t c0, c1;
                     cut.holders(sa, sb, c0, c1);
                     bar_rows();
                     if (tid == 0) last_flag = arrive_last(&a.count[c0], c1 - c0 + 1);
                     bar_rows();
-                    if (last_flag && mine) {
+                    if (last_flag) {
+                        const uint32_t lrows = s.rows > 128 ? 8 : s.rows > 64 ? 7 : s.rows > 32 ? 6 : 5;   // log2 of rows, padded
+                        const uint32_t jr = tid & ((1u << lrows) - 1), gr = tid >> lrows, groups = 256u >> lrows;
+                        const bool jlive = jr < s.rows;
                         // part 0 is the one that begins the segment, at the end of its CTA's work
-                        const float4 *p0 = reinterpret_cast<const float4 *>(a.part + (2 * (uint64_t)c0 + 1) * Cfg::PART) + (live ? row : 0);
-                        const float4 *p1 = reinterpret_cast<const float4 *>(a.part + 2 * ((uint64_t)c0 + 1) * Cfg::PART) + (live ? row : 0);
+                        const float4 *p0 = reinterpret_cast<const float4 *>(a.part + (2 * (uint64_t)c0 + 1) * Cfg::PART) + (jlive ? jr : 0);
+                        const float4 *p1 = reinterpret_cast<const float4 *>(a.part + 2 * ((uint64_t)c0 + 1) * Cfg::PART) + (jlive ? jr : 0);
                         const uint32_t parts = c1 - c0 + 1;
                         auto at = [&](uint32_t k) { return k ? p1 + (uint64_t)(k - 1) * (2 * Cfg::PART / 4) : p0; };
+                        auto out_row = [&](uint32_t row) {
+                            const uint32_t f = s.row0 + row;
+                            return (uint64_t)(s.tok0 + f / a.group) * a.q_heads + r.h * a.group + f % a.group;
+                        };
                         float M = -INFINITY, MU = -INFINITY, L = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
                         for (uint32_t k = 0; k < parts; k++) {
                             const float4 st = __ldcg(at(k) + D / 4 * RT);
                             const float mn = fmaxf(M, st.x), bm = finite_base(mn);
@@ -642,9 +650,9 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                         }
                         const bool nothing = M == -INFINITY && L == 0.0f;
                         const float bu = finite_base(MU), quot = nothing ? 0.0f : ex2(bu - finite_base(M) - PR_W_LOG2) / L;
-                        if (live && a.lse) a.lse[orow] = nothing ? -INFINITY : (M + __log2f(L)) * LN2;
+                        if (jlive && gr == 0 && a.lse) a.lse[out_row(jr)] = nothing ? -INFINITY : (M + __log2f(L)) * LN2;
 #pragma unroll 1
-                        for (uint32_t d0 = 0; d0 < D; d0 += 32) {
+                        for (uint32_t d0 = gr * 32; jlive && d0 < D; d0 += groups * 32) {
                             float o[32] = {};
 #pragma unroll 2
                             for (uint32_t k = 0; k < parts; k++) {
@@ -659,9 +667,14 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                                     o[4 * i + 2] += x[i].z * w, o[4 * i + 3] += x[i].w * w;
                                 }
                             }
-                            put(d0, o, quot);
+                            put(jr, d0, o, quot);
                         }
-                        put_out();
+                        bar_rows();
+                        for (uint32_t i = tid; i < s.rows * (D / 8); i += 256) {
+                            const uint32_t row = i / (D / 8), e = i % (D / 8);
+                            reinterpret_cast<uint4 *>(a.out + out_row(row) * D)[e] = lds128(chunk_at(row, e));
+                        }
+                        bar_rows();   // the rows' places are free for the next queries
                     }
                 }
             }
