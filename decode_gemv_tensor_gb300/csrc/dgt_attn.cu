@@ -11,6 +11,12 @@
 // scale) (the numerator sums codes times exp2(t + log2 vs - mu)).  Then no
 // page's weight is lost to another page's scale, and the quotient is
 // exp2(mu - m) * numerator / l.
+//
+// What bounds it: with many long sequences HBM (48 of up to 6007 tokens, 8 kv
+// heads of 128: 62 us, 5.8 TB/s, 87 % of the measured copy rate; two of 131072
+// and 93523, 8 heads of 256: 138 us, 99 %); with few pages a warp the chain of
+// dependent steps from the tables to the join (one sequence of 778 tokens: 9.6
+// us, of which its bytes are 0.2).
 #include "dgt_attn.cuh"
 
 namespace dgt {
@@ -634,8 +640,9 @@ extern "C" int dgt_kv_attention_ex(const dgt_kv_cache *cache, uint32_t layer, co
     a.part = (float *)((uint8_t *)d_ws + AT_COUNT_BYTES);
     a.min_units = nt ? 4 : 8;   // a page a warp
     a.slack = nt ? 12 : 16;
-    // Measured against shares of equal pages: 100 sequences of up to 300 tokens 28 and 22 us, 200 of 1000 65 and
-    // 52 us (12 instead of 8: the same within 2%); a prompt of 8192 rows 770 and 379 us (6: 439, 15: 389).
+    // Measured against shares of equal pages: 100 sequences of up to 300 tokens (64 dimensions) 28 and 22 us, 200
+    // of 1000 65 and 52 us (12 instead of 8: the same within 4%); a prompt of 8192 rows (128 dimensions) 770 and
+    // 379 us (6: 439, 15: 389).
     a.end = nt ? 8 : 10;
     a.spin = wait_limit_from_flags(flags);
     cudaStream_t st = (cudaStream_t)stream;

@@ -655,14 +655,17 @@ int dgt_kv_read(const dgt_kv_cache *cache, int32_t layer, const int32_t *d_seqs,
  * multiple of kv_heads, at most 64 times it), strides multiples of 8, data
  * 16-byte aligned.  d_out: device bf16 [tokens, q_heads, head_dim],
  * contiguous, 16-byte aligned; d_lse: device float [tokens, q_heads] or NULL.
- * q is scaled to its row's exponent and kept in fp16 (exact to 2^-31 of the
- * row's largest element), the weights exp(t_j - max) are rounded to fp16
- * (2^-11 relative), every sum is fp32.
+ * A row of q is scaled to its largest element's exponent and kept exactly, but
+ * for elements below 2^-9 of the largest: with few rows an entry (at most 24,
+ * 16 or 8 rows of a kv head, for head_dim 64, 128 and 256; the mean of the
+ * batch) those are kept to 2^-31 of it, with more to 2^-17.  The weights
+ * exp(t_j - max) are rounded to fp16 (2^-11 relative), every sum is fp32.
  * d_ws: device, dgt_kv_attention_workspace_bytes(...) bytes, 256-byte aligned,
  * zeroed before its first use: it begins with arrival counters that every
  * call, of whatever sizes, leaves at zero; the rest need not be kept.  Calls
- * that may overlap need one each.  The results do not depend on timing.  DGT_ERR_TIMEOUT in the status: a bounded wait ran
- * out, the outputs are then unspecified.  flags: 0, or the failure-path test
+ * that may overlap need one each.  The results do not depend on timing.
+ * DGT_ERR_TIMEOUT in the status: a bounded wait ran out, the outputs are then
+ * unspecified.  flags: 0, or the failure-path test
  * hook DGT_TEST_SHORT_WAITS | DGT_TEST_WAIT_POLLS(n); others DGT_ERR_ARG.
  */
 size_t dgt_kv_attention_workspace_bytes(const dgt_kv_cache *cache, uint32_t q_heads, uint32_t batch,
