@@ -255,11 +255,15 @@ __device__ __forceinline__ Cuts cut_plan(const AttnArgs &a, Units all, const Slo
     Cuts k;
     k.U = U;
     k.C = (uint32_t)min((uint64_t)grid, U);   // shares of one unit at least: cuts inside a segment are distinct
-    k.tol = (uint32_t)min(U / (8 * grid), (uint64_t)4);
     k.end = a.end;
     // (U below 2^22: a segment's pages and T then are below 2^23)
     k.parts = a.slots <= AT_CHUNK && S <= grid && U && U < (1u << 22);
-    if (!k.parts) return k;
+    auto shares = [&]() {
+        k.parts = false;
+        k.tol = U >= 32ull * grid ? 4u : (uint32_t)U / (8 * grid);
+        return k;
+    };
+    if (!k.parts) return shares();
     // two tiles a lane
     uint32_t n[2], p[2];
 #pragma unroll
@@ -277,19 +281,16 @@ __device__ __forceinline__ Cuts cut_plan(const AttnArgs &a, Units all, const Slo
         return q;
     };
     const uint32_t T0 = max(((uint32_t)P + grid - 1) / grid, a.min_units);
-    uint32_t T = 0;
-#pragma unroll
-    for (uint32_t i = 0; i < 6; i++) {
-        const uint32_t t = T0 + a.slack * (5 - i) / 5;
-        const float inv = 1.0f / (float)t;
-        const uint32_t p0 = pieces(n[0], t, inv), p1 = pieces(n[1], t, inv);
-        // the least that fits comes last
-        if (__reduce_add_sync(DGT_FULL, (p0 + p1) * heads) <= grid) T = t, p[0] = p0, p[1] = p1;
+    // rolled, and left at the first T that fits: the code runs once a call, from a cold instruction cache
+    uint32_t i = 0;
+#pragma unroll 1
+    for (; i < 6; i++) {
+        const uint32_t t = T0 + a.slack * i / 5;
+        const float inv = __fdividef(1.0f, (float)t);
+        p[0] = pieces(n[0], t, inv), p[1] = pieces(n[1], t, inv);
+        if (__reduce_add_sync(DGT_FULL, (p[0] + p[1]) * heads) <= grid) break;
     }
-    if (!T) {
-        k.parts = false;
-        return k;
-    }
+    if (i == 6) return shares();
     uint32_t cnt;
     const uint32_t ex = warp_excl_scan((p[0] + p[1]) * heads, &cnt);
     k.C = cnt;

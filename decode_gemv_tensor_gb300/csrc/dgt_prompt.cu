@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
     __shared__ Slot slots[AT_CHUNK];
     __shared__ uint64_t usum[PR_WARPS];
     __shared__ uint32_t tmem_slot;
+    __shared__ Cuts shared_cut;
     __shared__ int abort_flag, last_flag;
     // the warp's number out of a shuffle: the compiler then knows that it is the warp's
     const uint32_t tid = threadIdx.x, warp = __shfl_sync(DGT_FULL, tid >> 5, 0), lane = tid & 31;
@@ -177,7 +178,13 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
 
     Units here = describe<PR_WARPS>(a, RT, 0, slots, usum);
     const Units all = a.slots <= AT_CHUNK ? here : all_units<PR_WARPS>(a, RT, usum);
-    const Cuts cut = cut_plan(a, all, slots, gridDim.x);
+    // found by one warp, and kept in shared memory: registers are short here
+    if (warp == 0) {
+        const Cuts k = cut_plan(a, all, slots, gridDim.x);
+        if (lane == 0) shared_cut = k;
+    }
+    __syncthreads();
+    const Cuts &cut = shared_cut;
     const uint64_t ub = blockIdx.x >= cut.C ? 0 : cut.parts ? cut.U : cut.raw(blockIdx.x + 1);
 
     bool dead = false;   // a wait ran out, here or elsewhere in the CTA: no more work from this warp
