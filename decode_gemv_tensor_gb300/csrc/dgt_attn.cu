@@ -53,11 +53,19 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 // Every warp works alone on its share of a CTA's pages with its own ring of
 // bulk copies (one item: 64 tokens by up to 128 dimensions of one side), and
 // looks ahead into the CTA's next segment; warps meet only at a segment's end.
+
+// CTAs an SM: what the registers allow without spills.  64 dimensions and up to
+// eight rows, three against two: 48 sequences of up to 6000 tokens, 4 kv heads
+// 24 and 29 us, 200 of 300 20 and 23 us, one of 500 9.1 and 8.8 us; with 16
+// rows, spilling, 37 and 39, 30 and 32, 12.0 and 11.2 us, 2 of 60000 33 and 29.
+__host__ __device__ constexpr uint32_t attn_ctas(uint32_t D, uint32_t nt) { return D == 64 && nt == 1 ? 3 : 2; }
+
 template <uint32_t D, uint32_t NT>
 struct AttnCfg {
     static constexpr uint32_t PD = D < 128 ? D : 128, PAN = D / PD;
     static constexpr uint32_t IB = KV_P * PD, IPP = 2 * PAN;
-    static constexpr uint32_t NS = D == 64 ? 4 : 2;      // deeper rings were no faster (16 KB a warp in flight is enough)
+    static constexpr uint32_t CTAS = attn_ctas(D, NT);
+    static constexpr uint32_t NS = D == 64 ? (CTAS == 3 ? 3 : 4) : 2;   // deeper rings were no faster
     static constexpr uint32_t RT = 8 * NT;
     static constexpr uint32_t KSTEPS = D / 16;           // k-steps of the first product; their operands stay in registers
     static_assert(NT * D <= 256, "which more rows would not");
@@ -68,7 +76,7 @@ struct AttnCfg {
 };
 
 template <uint32_t D, uint32_t NT>
-__global__ void __launch_bounds__(AT_WARPS * 32, 2) k_kv_attention(AttnArgs a) {
+__global__ void __launch_bounds__(AT_WARPS * 32, attn_ctas(D, NT)) k_kv_attention(AttnArgs a) {
     using Cfg = AttnCfg<D, NT>;
     constexpr uint32_t RT = Cfg::RT, NS = Cfg::NS, IB = Cfg::IB, PD = Cfg::PD, PAN = Cfg::PAN, IPP = Cfg::IPP;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -565,7 +573,7 @@ static int attn_launch(const AttnArgs &a, cudaStream_t st) {
             return DGT_ERR_CUDA;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    const unsigned grid = 2u * di.sms < AT_MAX_CTAS ? 2u * di.sms : AT_MAX_CTAS;
+    const unsigned grid = AttnCfg<D, NT>::CTAS * std::min((unsigned)di.sms, AT_MAX_SMS);
     return launch_pdl(fn, dim3(grid), dim3(AT_WARPS * 32), smem, st, a) == cudaSuccess ? DGT_OK : DGT_ERR_CUDA;
 }
 
@@ -598,12 +606,12 @@ static uint64_t slot_count(uint32_t RT, uint32_t group, uint32_t batch, uint64_t
 using namespace dgt;
 
 // Arrival counters, then two partial results per CTA.
-constexpr size_t AT_COUNT_BYTES = (AT_MAX_CTAS * 4 + 255) / 256 * 256;
+constexpr size_t AT_COUNT_BYTES = (3 * AT_MAX_SMS * 4 + 255) / 256 * 256;   // a counter a CTA
 extern "C" size_t dgt_kv_attention_workspace_bytes(const dgt_kv_cache *cache, uint32_t q_heads, uint32_t batch,
                                                    uint64_t tokens) {
     if (!cache || cache->kv_heads == 0 || batch == 0 || q_heads < cache->kv_heads) return 0;
     const Plan p = attn_plan(cache->head_dim, q_heads / cache->kv_heads, batch, tokens);
-    return AT_COUNT_BYTES + (size_t)(p.nt ? AT_MAX_CTAS : PR_MAX_CTAS) * 2 * p.RT * (cache->head_dim + 4) * 4;
+    return AT_COUNT_BYTES + (size_t)AT_MAX_SMS * (p.nt ? attn_ctas(cache->head_dim, p.nt) : 1) * 2 * p.RT * (cache->head_dim + 4) * 4;
 }
 
 extern "C" int dgt_kv_attention_ex(const dgt_kv_cache *cache, uint32_t layer, const dgt_heads *q, uint64_t tokens,

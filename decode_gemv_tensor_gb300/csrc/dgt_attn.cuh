@@ -11,6 +11,8 @@
 // last adds them in page order, so results do not depend on timing.  Lengths
 // are read on the device: a captured graph follows them.
 #pragma once
+#include <algorithm>
+
 #include "dgt_kv.cuh"
 
 #include "dgt_device.cuh"
@@ -20,7 +22,7 @@ namespace dgt {
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr uint32_t AT_CHUNK = 64;      // row tiles described in shared memory at a time
-constexpr uint32_t AT_MAX_CTAS = 320, PR_MAX_CTAS = 160;
+constexpr uint32_t AT_MAX_SMS = 160;   // a workspace has room for so many
 
 struct AttnArgs {
     dgt_kv_cache c;

@@ -728,7 +728,7 @@ static int prompt_launch_d(const AttnArgs &a, cudaStream_t st) {
             return DGT_ERR_CUDA;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    const unsigned grid = (unsigned)di.sms < PR_MAX_CTAS ? (unsigned)di.sms : PR_MAX_CTAS;
+    const unsigned grid = std::min((unsigned)di.sms, AT_MAX_SMS);
     return launch_pdl(fn, dim3(grid), dim3(PR_WARPS * 32), PromptCfg<D>::bytes, st, a) == cudaSuccess ? DGT_OK
                                                                                                       : DGT_ERR_CUDA;
 }
