@@ -38,6 +38,7 @@ struct AttnArgs {
     int32_t *status;
     uint32_t min_units, slack;   // pages of a part at least; pages that parts may be above an even share
     uint32_t end;                // what a segment costs besides its pages, in pages
+    float join;                  // what a part costs the join, in pages
     uint32_t spin;
 };
 
@@ -247,7 +248,8 @@ struct Cuts {
 };
 
 // How a call is cut over `grid` CTAs.  Parts: of at most T pages, T the least
-// for which all parts have a CTA, and min_units; taken while T is no more than
+// for which all parts have a CTA, min_units, and what balances a part's pages
+// against the join of many parts; taken while T is no more than
 // `slack` pages above an even share, because a second segment in a CTA costs a
 // segment's end.  Otherwise even shares, whose cuts move by an eighth of a
 // share at most, or past the units that stand for the segment's end.
@@ -282,7 +284,9 @@ __device__ __forceinline__ Cuts cut_plan(const AttnArgs &a, Units all, const Slo
         if ((q + 1) * T <= x) q++;
         return q;
     };
-    const uint32_t T0 = max(((uint32_t)P + grid - 1) / grid, a.min_units);
+    // T pages take T, their n / T parts' join n / T times the cost of a part: least at the root
+    const uint32_t nmax = __reduce_max_sync(DGT_FULL, max(n[0], n[1]));
+    const uint32_t T0 = max(max(((uint32_t)P + grid - 1) / grid, a.min_units), (uint32_t)sqrtf(a.join * (float)nmax));
     // rolled, and left at the first T that fits: the code runs once a call, from a cold instruction cache
     uint32_t i = 0;
 #pragma unroll 1
