@@ -580,12 +580,13 @@ static int attn_launch(const AttnArgs &a, cudaStream_t st) {
 // Rows of a tile, by an entry's rows (the mean of a batch): in n-tiles of
 // eight, as many as they fill, while that is the faster form; more rows go to
 // the tensor-core tiles.  Measured on both sides, n-tiles of eight first (1
-// sequence of 500 tokens, 8 of up to 8003 with 4 kv heads, 2 of 60000):
-//   64 dimensions, 24 rows: 15 and 13, 24 and 28, 44 and 42 us; 32 rows: 21
-//     and 13, 33 and 28, 56 and 43 us;
-//   128 dimensions, 16 rows: 13 and 14, 24 and 29, 58 and 44 us; 24 rows: 20
-//     and 14, 35 and 29, 73 and 45 us;
-//   256 dimensions, 10 rows: 20 and 18, 41 and 39, 94 and 56 us.
+// sequence of 500 tokens, 8 of up to 8003 with 4 kv heads):
+//   64 dimensions, 24 rows: 14 and 12, 23 and 27 us (2 of 60000: 32 and 41);
+//     32 rows: 21 and 13, 33 and 28 us;
+//   128 dimensions, 16 rows: 13 and 13, 23 and 29 us (2 of 60000: 37 and 42);
+//     24 rows: 20 and 14, 35 and 29 us;
+//   256 dimensions, 8 rows: 14 and 18, 26 and 38 us; 10 rows: 20 and 18, 41
+//     and 39 us.
 struct Plan {
     uint32_t nt, RT;   // nt 0: tensor-core tiles
 };
