@@ -647,7 +647,11 @@ extern "C" int dgt_kv_attention_ex(const dgt_kv_cache *cache, uint32_t layer, co
     a.per_entry = (a.group + RT - 1) / RT;
     a.count = (int32_t *)d_ws;
     a.part = (float *)((uint8_t *)d_ws + AT_COUNT_BYTES);
-    a.min_units = nt ? 4 : 8;   // a page a warp
+    // A page a warp (64 dimensions, 4001 tokens: 10.6 us; 2 or 8 pages 11.6); in prompts eight pages (200 rows of 128
+    // dimensions over 500 tokens 18.2 us; 4 pages 21.4).
+    a.min_units = nt ? 4 : 8;
+    // 30 sequences of up to 1501 tokens, 8 kv heads of 128: 17.1 us (24 pages 18.5); 4 prompts of up to 300 rows over
+    // 2300 tokens 42 us (10 pages 46, 24 pages 44).
     a.slack = nt ? 12 : 16;
     // Measured against min_units alone, one sequence of 60000 tokens, one kv head of 64, 128 and 256 dimensions: 4
     // rows 28 and 19, 29 and 20, 49 and 31 us (0.5: 21, 22, 35); 240 rows over 120020 tokens 104 and 76, 218 and

@@ -21,7 +21,7 @@
 // What bounds it: the row threads' exponentials and conversions and the
 // dependent steps of a page (issue slots 49 % used, tensor pipe 47 %).  Two
 // prompts of 2048 and 1461 rows over 7048 and 5028 tokens, 24 heads of 128:
-// 212 us, 1.08 PFLOP/s by what causality leaves of the two products, 55 % of
+// 213 us, 1.07 PFLOP/s by what causality leaves of the two products, 55 % of
 // the measured bf16 peak.  One of 8192 rows from an empty cache: 373 us.
 #include "dgt_attn.cuh"
 
