@@ -202,6 +202,24 @@ def _stream_on(x, stream):
     return _raw_stream(x.device.index)
 
 
+def _new(shape, dtype, device, stream=None, zero=False, temp=False):
+    """A tensor that a call allocates for its work on `stream` (None: the
+    current stream).  With a stream given, memory and fill are that stream's: a
+    block of the current stream's may still be written by work queued there,
+    and nothing would order a fill there before the kernel.  temp: released
+    when the call returns, to the stream that uses it; otherwise the current
+    stream may read it too until it is released."""
+    import torch
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=device)
+    if not temp:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 # ---------------------------------------------------------------------------
 # host: pack / unpack / container
 # ---------------------------------------------------------------------------
@@ -776,11 +794,15 @@ def kv_read(cache: KvCache, layer, seqs, first, cu, tokens: int, status=None, st
     return out
 
 
-def kv_attention_workspace(cache: KvCache, q_heads: int, batch: int, tokens: int):
-    """A workspace for kv_attention calls of these sizes (zeroed, as its first use wants it)."""
+def _attention_workspace(cache, q_heads, batch, tokens, stream, temp):
     import torch
     nb = int(lib().dgt_kv_attention_workspace_bytes(cache.ptr, q_heads, batch, tokens))
-    return torch.zeros(max(nb, 256), dtype=torch.uint8, device=cache.k.device)
+    return _new(max(nb, 256), torch.uint8, cache.k.device, stream, zero=True, temp=temp)
+
+
+def kv_attention_workspace(cache: KvCache, q_heads: int, batch: int, tokens: int, stream=None):
+    """A workspace for kv_attention calls of these sizes on `stream` (zeroed, as its first use wants it)."""
+    return _attention_workspace(cache, q_heads, batch, tokens, stream, False)
 
 
 def kv_attention(cache: KvCache, layer: int, q, seqs, cu=None, scale=None, window: int = 0, sinks: int = 0, out=None,
@@ -806,7 +828,7 @@ def kv_attention(cache: KvCache, layer: int, q, seqs, cu=None, scale=None, windo
     if lse is not None and (lse.numel() != tokens * heads or lse.dtype != torch.float32 or not lse.is_contiguous()):
         raise ValueError("lse: a contiguous float32 tensor [tokens, q_heads]")
     if ws is None:
-        ws = kv_attention_workspace(cache, heads, batch, tokens)
+        ws = _attention_workspace(cache, heads, batch, tokens, stream, True)
     _check(lib().dgt_kv_attention_ex(cache.ptr, layer, _heads(q, "q"), tokens, _i32(seqs, "seqs"),
                                      None if cu is None else _i32(cu, "cu", batch + 1), batch,
                                      dim ** -0.5 if scale is None else scale, window, sinks, _ptr(out), _ptr(lse),

@@ -1,0 +1,55 @@
+"""Calls on a stream of their own while the current stream is busy, without a
+workspace or outputs given."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def dgt():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import decode_gemv_tensor_gb300 as d
+    d.lib()
+    return d
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def rand(seed, *shape):
+    g = np.random.default_rng(seed)
+    return torch.from_numpy(g.normal(size=shape).astype(np.float32)).cuda().bfloat16()
+
+
+def busy(nbytes):
+    """The current stream with some ten milliseconds of work before it, and memory of this size that it has
+    released and is still to write."""
+    torch.cuda.synchronize()
+    junk = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    torch.cuda._sleep(20_000_000)
+    junk.fill_(255)
+
+
+def test_attention_without_a_workspace(dgt):
+    # 20011 tokens: parts that the last CTA to arrive joins, by counters in the workspace
+    c = dgt.KvCache(1, 320, 2, 128, max_seqs=1, max_pages=320)
+    c.table[0] = torch.arange(320, dtype=torch.int32, device="cuda")
+    c.lens[0] = 20011
+    k, v, q, seqs = rand(1, 20011, 2, 128), rand(2, 20011, 2, 128), rand(3, 1, 6, 128), i32([0])
+    dgt.kv_append(c, 0, k, v, seqs, i32([0]), cu=i32([0, 20011]))
+    want = dgt.kv_attention(c, 0, q, seqs)
+    side = torch.cuda.Stream()
+    n = dgt.kv_attention_workspace(c, 6, 1, 1).numel()
+    for _ in range(3):
+        busy(n)
+        got = dgt.kv_attention(c, 0, q, seqs, stream=side)
+        other = dgt.kv_attention(c, 0, q, seqs, stream=side)
+        side.synchronize()
+        assert torch.equal(got, want) and torch.equal(other, want)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(other, want)
