@@ -363,16 +363,16 @@ class R4:
     """R4 runtime tensor: torch device buffers (nib, esc, seg; sm aliases the
     packed upload) and the dgt_r4 descriptor."""
 
-    def __init__(self, dev: DevicePacked):
+    def __init__(self, dev: DevicePacked, stream=None):
         import torch
         v = dev.view
         nb, eb, sb = C.c_uint64(), C.c_uint64(), C.c_uint64()
         _check(lib().dgt_r4_sizes(v.rows, v.cols, v.n_esc15, C.byref(nb), C.byref(eb), C.byref(sb)),
                "dgt_r4_sizes")
         d = dev.tensors["sm"].device
-        self.nib = torch.empty(max(nb.value, 16), dtype=torch.uint8, device=d)
-        self.esc = torch.empty(max(eb.value, 16), dtype=torch.uint8, device=d)
-        self.seg = torch.empty(max(sb.value // 4, 4), dtype=torch.int32, device=d)
+        self.nib = _new(max(nb.value, 16), torch.uint8, d, stream)
+        self.esc = _new(max(eb.value, 16), torch.uint8, d, stream)
+        self.seg = _new(max(sb.value // 4, 4), torch.int32, d, stream)
         self.sm = dev.tensors["sm"]
         self.dev = dev
         self.s = R4Struct()
@@ -400,7 +400,7 @@ class R4:
 
 def load_r4(dev: DevicePacked, status=None, stream=None) -> R4:
     """dgt_load_r4: transcode the uploaded format-1/2 tensor into R4 on the GPU."""
-    r4 = R4(dev)
+    r4 = R4(dev, stream)
     _check(lib().dgt_load_r4(C.byref(dev.view), C.byref(r4.s), _ptr(status), _stream(stream)), "dgt_load_r4")
     return r4
 
@@ -421,7 +421,7 @@ def r4_to_bf16(r4: R4, out=None, status=None, stream=None):
     """dgt_r4_to_bf16: rebuild the bf16 matrix on the GPU (torch.bfloat16 [rows, cols])."""
     import torch
     if out is None:
-        out = torch.empty((r4.rows, r4.cols), dtype=torch.bfloat16, device=r4.sm.device)
+        out = _new((r4.rows, r4.cols), torch.bfloat16, r4.sm.device, stream)
     _check(lib().dgt_r4_to_bf16(C.byref(r4.s), _ptr(out), _ptr(status), _stream(stream)), "dgt_r4_to_bf16")
     return out
 
@@ -456,9 +456,9 @@ def gemv(W: R4, x, y=None, y32=None, status=None, stream=None, static_weights=Fa
     import torch
     dev = W.sm.device
     if y is None:
-        y = torch.empty(W.rows, dtype=torch.bfloat16, device=dev)
+        y = _new(W.rows, torch.bfloat16, dev, stream)
     if y32 is None:
-        y32 = torch.empty(W.rows, dtype=torch.float32, device=dev)
+        y32 = _new(W.rows, torch.float32, dev, stream)
     flags = (STATIC_WEIGHTS if static_weights else 0) | test_wait_flags(test_wait_polls)
     _check(lib().dgt_gemv_ex(C.byref(W.s), _ptr(x), _ptr(y), _ptr(y32), _ptr(status), flags, _stream(stream)),
            "dgt_gemv")
@@ -470,9 +470,9 @@ def gemv_bf16(W, x, y=None, y32=None, status=None, stream=None, static_weights=F
     import torch
     rows, cols = W.shape
     if y is None:
-        y = torch.empty(rows, dtype=torch.bfloat16, device=W.device)
+        y = _new(rows, torch.bfloat16, W.device, stream)
     if y32 is None:
-        y32 = torch.empty(rows, dtype=torch.float32, device=W.device)
+        y32 = _new(rows, torch.float32, W.device, stream)
     flags = (STATIC_WEIGHTS if static_weights else 0) | test_wait_flags(test_wait_polls)
     _check(lib().dgt_gemv_bf16_ex(_ptr(W), rows, cols, _ptr(x), _ptr(y), _ptr(y32), _ptr(status), flags,
                                   _stream(stream)), "dgt_gemv_bf16")
@@ -483,14 +483,14 @@ def moe_workspace_bytes(n_experts: int, expert_rows: int, cols: int, tokens: int
     return int(lib().dgt_moe_workspace_bytes(n_experts, expert_rows, cols, tokens, topk))
 
 
-def _moe_outputs(tokens, topk, ne, dev, want_y, want_out, y32, out, out32):
+def _moe_outputs(tokens, topk, ne, dev, want_y, want_out, y32, out, out32, stream):
     import torch
     if want_y and y32 is None:
-        y32 = torch.empty((tokens, topk, ne), dtype=torch.float32, device=dev)
+        y32 = _new((tokens, topk, ne), torch.float32, dev, stream)
     if want_out and out is None:
-        out = torch.empty((tokens, ne), dtype=torch.bfloat16, device=dev)
+        out = _new((tokens, ne), torch.bfloat16, dev, stream)
     if want_out and out32 is None:
-        out32 = torch.empty((tokens, ne), dtype=torch.float32, device=dev)
+        out32 = _new((tokens, ne), torch.float32, dev, stream)
     return y32, out, out32
 
 
@@ -503,10 +503,10 @@ def moe_gemv(W: R4, n_experts: int, ids, p, x, ws=None, y32=None, out=None, out3
     tokens, topk = ids.shape
     ne = W.rows // n_experts
     dev = W.sm.device
-    y32, out, out32 = _moe_outputs(tokens, topk, ne, dev, want_y, p is not None, y32, out, out32)
+    y32, out, out32 = _moe_outputs(tokens, topk, ne, dev, want_y, p is not None, y32, out, out32, stream)
     nb = moe_workspace_bytes(n_experts, ne, W.cols, tokens, topk)
     if ws is None:
-        ws = torch.empty(max(nb, 256), dtype=torch.uint8, device=dev)
+        ws = _new(max(nb, 256), torch.uint8, dev, stream, temp=True)
     _check(lib().dgt_moe_gemv_ex(C.byref(W.s), n_experts, _ptr(ids), _ptr(p), tokens, topk, _ptr(x), _ptr(y32),
                                  _ptr(out), _ptr(out32), _ptr(ws), ws.numel(), _ptr(status),
                                  test_wait_flags(test_wait_polls), _stream(stream)), "dgt_moe_gemv")
@@ -520,10 +520,10 @@ def moe_gemv_bf16(W, n_experts: int, ids, p, x, ws=None, y32=None, out=None, out
     tokens, topk = ids.shape
     rows, cols = W.shape
     ne = rows // n_experts
-    y32, out, out32 = _moe_outputs(tokens, topk, ne, W.device, want_y, p is not None, y32, out, out32)
+    y32, out, out32 = _moe_outputs(tokens, topk, ne, W.device, want_y, p is not None, y32, out, out32, stream)
     nb = moe_workspace_bytes(n_experts, ne, cols, tokens, topk)
     if ws is None:
-        ws = torch.empty(max(nb, 256), dtype=torch.uint8, device=W.device)
+        ws = _new(max(nb, 256), torch.uint8, W.device, stream, temp=True)
     _check(lib().dgt_moe_gemv_bf16(_ptr(W), rows, cols, n_experts, _ptr(ids), _ptr(p), tokens, topk, _ptr(x),
                                    _ptr(y32), _ptr(out), _ptr(out32), _ptr(ws), ws.numel(), _ptr(status),
                                    _stream(stream)), "dgt_moe_gemv_bf16")
@@ -544,10 +544,10 @@ def moe_gemm(W: R4, n_experts: int, ids, p, X, ws=None, y32=None, out=None, out3
     tokens, topk = ids.shape
     ne = W.rows // n_experts
     dev = W.sm.device
-    y32, out, out32 = _moe_outputs(tokens, topk, ne, dev, True, p is not None, y32, out, out32)
+    y32, out, out32 = _moe_outputs(tokens, topk, ne, dev, True, p is not None, y32, out, out32, stream)
     nb = moe_gemm_workspace_bytes(n_experts, ne, W.cols, tokens, topk)
     if ws is None:
-        ws = torch.empty(max(nb, 256), dtype=torch.uint8, device=dev)
+        ws = _new(max(nb, 256), torch.uint8, dev, stream, temp=True)
     _check(lib().dgt_moe_gemm(C.byref(W.s), n_experts, _ptr(ids), _ptr(p), _ptr(X), tokens, topk, _ptr(y32),
                               _ptr(out), _ptr(out32), _ptr(ws), ws.numel(), _ptr(status), _stream(stream)),
            "dgt_moe_gemm")
@@ -561,10 +561,10 @@ def moe_gemm_bf16(W, n_experts: int, ids, p, X, ws=None, y32=None, out=None, out
     tokens, topk = ids.shape
     rows, cols = W.shape
     ne = rows // n_experts
-    y32, out, out32 = _moe_outputs(tokens, topk, ne, W.device, True, p is not None, y32, out, out32)
+    y32, out, out32 = _moe_outputs(tokens, topk, ne, W.device, True, p is not None, y32, out, out32, stream)
     nb = moe_gemm_workspace_bytes(n_experts, ne, cols, tokens, topk)
     if ws is None:
-        ws = torch.empty(max(nb, 256), dtype=torch.uint8, device=W.device)
+        ws = _new(max(nb, 256), torch.uint8, W.device, stream, temp=True)
     _check(lib().dgt_moe_gemm_bf16(_ptr(W), rows, cols, n_experts, _ptr(ids), _ptr(p), _ptr(X), tokens, topk,
                                    _ptr(y32), _ptr(out), _ptr(out32), _ptr(ws), ws.numel(), _ptr(status),
                                    _stream(stream)), "dgt_moe_gemm_bf16")
@@ -587,15 +587,15 @@ def gemm_plan(M: int, N: int, K: int, m_tile=None, split_k=None, test_wait_polls
     return p
 
 
-def _gemm_out(M, N, dev, Y32, Y, plan, ws):
+def _gemm_out(M, N, dev, Y32, Y, plan, ws, stream):
     import torch
     if Y32 is None:
-        Y32 = torch.empty((M, N), dtype=torch.float32, device=dev)
+        Y32 = _new((M, N), torch.float32, dev, stream)
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        Y = _new((M, N), torch.bfloat16, dev, stream)
     nb = int(lib().dgt_gemm_workspace_bytes(M, N, C.byref(plan)))
     if ws is None and nb:
-        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        ws = _new(nb, torch.uint8, dev, stream, temp=True)
     return Y32, Y, ws
 
 
@@ -604,7 +604,7 @@ def gemm(W: R4, X, plan=None, Y32=None, Y=None, ws=None, status=None, stream=Non
     M, K = X.shape
     N = W.rows
     plan = plan or gemm_plan(M, N, K)
-    Y32, Y, ws = _gemm_out(M, N, W.sm.device, Y32, Y, plan, ws)
+    Y32, Y, ws = _gemm_out(M, N, W.sm.device, Y32, Y, plan, ws, stream)
     _check(lib().dgt_gemm(C.byref(W.s), _ptr(X), M, _ptr(Y32), _ptr(Y), C.byref(plan), _ptr(ws),
                           0 if ws is None else ws.numel(), _ptr(status), _stream(stream)), "dgt_gemm")
     return Y32, Y
@@ -615,7 +615,7 @@ def gemm_bf16(W, X, plan=None, Y32=None, Y=None, ws=None, status=None, stream=No
     M, K = X.shape
     N = W.shape[0]
     plan = plan or gemm_plan(M, N, K)
-    Y32, Y, ws = _gemm_out(M, N, W.device, Y32, Y, plan, ws)
+    Y32, Y, ws = _gemm_out(M, N, W.device, Y32, Y, plan, ws, stream)
     _check(lib().dgt_gemm_bf16(_ptr(W), N, K, _ptr(X), M, _ptr(Y32), _ptr(Y), C.byref(plan), _ptr(ws),
                                0 if ws is None else ws.numel(), _ptr(status), _stream(stream)), "dgt_gemm_bf16")
     return Y32, Y
@@ -629,8 +629,8 @@ def gemm_rebuild(W: R4, X, scratch=None, plan=None, Y32=None, Y=None, ws=None, s
     N = W.rows
     plan = plan or gemm_plan(M, N, K)
     if scratch is None:
-        scratch = torch.empty((N, K), dtype=torch.bfloat16, device=W.sm.device)
-    Y32, Y, ws = _gemm_out(M, N, W.sm.device, Y32, Y, plan, ws)
+        scratch = _new((N, K), torch.bfloat16, W.sm.device, stream, temp=True)
+    Y32, Y, ws = _gemm_out(M, N, W.sm.device, Y32, Y, plan, ws, stream)
     _check(lib().dgt_gemm_rebuild(C.byref(W.s), _ptr(X), M, _ptr(Y32), _ptr(Y), C.byref(plan), _ptr(scratch),
                                   _ptr(ws), 0 if ws is None else ws.numel(), _ptr(status), _stream(stream)),
            "dgt_gemm_rebuild")
@@ -706,7 +706,7 @@ def rotate(rotary: Rotary, q, pos, k=None, q_out=None, k_out=None, stream=None):
     p = _i32(pos, "pos", rotary.axes * tokens)
     hq, hk, ok = _heads(q, "q"), None, None
     if q_out is None:
-        q_out = torch.empty((tokens, nq, dim), dtype=torch.bfloat16, device=q.device)
+        q_out = _new((tokens, nq, dim), torch.bfloat16, q.device, stream)
         oq = _pack_heads(q_out.data_ptr(), nq * dim, dim, nq, 0)
     else:
         oq = _heads(q_out, "q_out")
@@ -719,7 +719,7 @@ def rotate(rotary: Rotary, q, pos, k=None, q_out=None, k_out=None, stream=None):
         if k.shape[0] != tokens or k.shape[2] != dim:
             raise ValueError("k: the same tokens and head size as q")
         if k_out is None:
-            k_out = torch.empty((tokens, nk, dim), dtype=torch.bfloat16, device=q.device)
+            k_out = _new((tokens, nk, dim), torch.bfloat16, q.device, stream)
             ok = _pack_heads(k_out.data_ptr(), nk * dim, dim, nk, 0)
         else:
             ok = _heads(k_out, "k_out")
@@ -787,7 +787,7 @@ def kv_read(cache: KvCache, layer, seqs, first, cu, tokens: int, status=None, st
     if layer is None:
         shape = (cache.layers, *shape)
     dev = cache.k.device
-    out = [torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    out = [_new(shape, torch.bfloat16, dev, stream) for _ in range(2)]
     _check(lib().dgt_kv_read(cache.ptr, -1 if layer is None else layer, _i32(seqs, "seqs"),
                              _i32(first, "first", batch), None if cu is None else _i32(cu, "cu", batch + 1), batch,
                              tokens, _ptr(out[0]), _ptr(out[1]), _ptr(status), _stream_on(cache.k, stream)), "dgt_kv_read")
@@ -822,7 +822,7 @@ def kv_attention(cache: KvCache, layer: int, q, seqs, cu=None, scale=None, windo
     if window < 0 or sinks < 0:
         raise ValueError("window and sinks: not negative")
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=q.device)
+        out = _new((tokens, heads, dim), torch.bfloat16, q.device, stream)
     elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
         raise ValueError("out: a contiguous bfloat16 tensor of q's shape")
     if lse is not None and (lse.numel() != tokens * heads or lse.dtype != torch.float32 or not lse.is_contiguous()):
@@ -844,7 +844,7 @@ def kv_reserve(cache: KvCache, seqs, count, start=None, status=None, stream=None
     import torch
     n = seqs.numel()
     if start is None:
-        start = torch.empty(n, dtype=torch.int32, device=seqs.device)
+        start = _new(n, torch.int32, seqs.device, stream)
     _check(lib().dgt_kv_reserve(cache.ptr, _i32(seqs, "seqs"), _i32(count, "count", n), n,
                                 _i32(start, "start", n), _ptr(cache.ws), cache.ws.numel(), _ptr(status),
                                 _stream_on(cache.k, stream)), "dgt_kv_reserve")
@@ -885,7 +885,7 @@ def add_rmsnorm(x32, gamma, eps, h=None, y32=None, stream=None):
     import torch
     n = x32.numel()
     if h is None:
-        h = torch.empty(n, dtype=torch.bfloat16, device=x32.device)
+        h = _new(n, torch.bfloat16, x32.device, stream)
     _check(lib().dgt_add_rmsnorm(_ptr(x32), _ptr(y32), _ptr(gamma), n, C.c_float(eps), _ptr(h), _stream(stream)),
            "dgt_add_rmsnorm")
     return h
@@ -896,7 +896,7 @@ def silu_mul(g32, u32, out=None, stream=None):
     import torch
     n = g32.numel()
     if out is None:
-        out = torch.empty(n, dtype=torch.bfloat16, device=g32.device)
+        out = _new(n, torch.bfloat16, g32.device, stream)
     _check(lib().dgt_silu_mul(_ptr(g32), _ptr(u32), n, _ptr(out), _stream(stream)), "dgt_silu_mul")
     return out
 
@@ -908,7 +908,7 @@ def silu_mul_rows(gu32, out=None, stream=None):
     rows, n2 = gu32.shape
     n = n2 // 2
     if out is None:
-        out = torch.empty((rows, n), dtype=torch.bfloat16, device=gu32.device)
+        out = _new((rows, n), torch.bfloat16, gu32.device, stream)
     _check(lib().dgt_silu_mul_rows(_ptr(gu32), rows, n, _ptr(out), _stream(stream)), "dgt_silu_mul_rows")
     return out
 
@@ -917,7 +917,7 @@ def repeat(v, n_out, out=None, stream=None):
     """dgt_repeat: out[i] = v[i mod len(v)] (bf16)."""
     import torch
     if out is None:
-        out = torch.empty(n_out, dtype=torch.bfloat16, device=v.device)
+        out = _new(n_out, torch.bfloat16, v.device, stream)
     _check(lib().dgt_repeat(_ptr(v), v.numel(), n_out, _ptr(out), _stream(stream)), "dgt_repeat")
     return out
 
@@ -1097,7 +1097,7 @@ def weighted_sum(y32, p, out=None, stream=None):
     slots = p.numel()
     n = y32.numel() // slots
     if out is None:
-        out = torch.empty(n, dtype=torch.float32, device=y32.device)
+        out = _new(n, torch.float32, y32.device, stream)
     _check(lib().dgt_weighted_sum(_ptr(y32), _ptr(p), slots, n, _ptr(out), _stream(stream)), "dgt_weighted_sum")
     return out
 
@@ -1241,10 +1241,10 @@ def exponent_stats(w, tile=128, stream=None):
     import torch
     n = w.numel()
     dev = w.device
-    hist = torch.empty(256, dtype=torch.int64, device=dev)
+    hist = _new(256, torch.int64, dev, stream)
     # an invalid tile gets a 1-element buffer; the C call rejects it
-    tb = torch.empty(max((n + tile - 1) // tile, 1) if tile > 0 else 1, dtype=torch.float64, device=dev)
-    tot = torch.empty(2, dtype=torch.float64, device=dev)
+    tb = _new(max((n + tile - 1) // tile, 1) if tile > 0 else 1, torch.float64, dev, stream)
+    tot = _new(2, torch.float64, dev, stream, temp=True)
     _check(lib().dgt_exponent_stats(_ptr(w), n, tile, _ptr(hist), _ptr(tb), _ptr(tot), _stream(stream)),
            "dgt_exponent_stats")
     t = tot.cpu()
