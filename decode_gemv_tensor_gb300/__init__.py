@@ -1247,6 +1247,7 @@ def exponent_stats(w, tile=128, stream=None):
     tot = _new(2, torch.float64, dev, stream, temp=True)
     _check(lib().dgt_exponent_stats(_ptr(w), n, tile, _ptr(hist), _ptr(tb), _ptr(tot), _stream(stream)),
            "dgt_exponent_stats")
-    t = tot.cpu()
+    with torch.cuda.stream(stream):
+        t = tot.cpu()
     return hist, tb, float(t[0]), float(t[1])
 

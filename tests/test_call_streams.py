@@ -33,6 +33,8 @@ class Allocations:
     @contextlib.contextmanager
     def within(self, stream):
         was, self.stream = self.stream, stream
+        if stream is None:
+            self.stream = was
         yield
         self.stream = was
 
@@ -129,3 +131,12 @@ def test_an_attention_workspace_made_for_a_stream(seen):
     log.made.clear()
     ws = dgt.kv_attention_workspace(cache, 2, 1, 1, stream=side)
     assert log.made == [(1000, side)] and log.kept == [(ws.data_ptr(), "current")]
+
+
+def test_exponent_stats_reads_its_totals_behind_its_kernels(seen, monkeypatch):
+    _, side, log = seen
+    read = []
+    cpu = torch.Tensor.cpu
+    monkeypatch.setattr(torch.Tensor, "cpu", lambda t: read.append(log.stream) or cpu(t))
+    dgt.exponent_stats(torch.ones(256, dtype=BF16), stream=side)
+    assert read == [side] and all(s is side for _, s in log.made)

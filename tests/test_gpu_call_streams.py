@@ -73,3 +73,11 @@ def test_outputs_and_temporary_memory(dgt):
         torch.cuda.synchronize()
         for a, b in zip(got, want + tuple(back)):
             assert torch.equal(a, b)
+
+
+def test_exponent_stats(dgt):
+    w = rand(8, 4096, 4096)
+    _, _, bits, entropy = dgt.exponent_stats(w)
+    busy(1 << 20)
+    _, _, b2, e2 = dgt.exponent_stats(w, stream=torch.cuda.Stream())
+    assert (b2, e2) == (bits, entropy)
