@@ -932,7 +932,9 @@ class StepAttention:
     holds, with an optional window and first tokens that stay visible.  For
     DecodeStep and MoeDecodeStep; the query heads have the cache's head_dim,
     their count a multiple of its kv_heads.  Positions and lengths live on the
-    device, so a captured step moves on by one token with every replay.
+    device, so a captured step moves on by one token with every replay.  Several
+    steps may share one, if they run one after the other: the tokens of each
+    follow those of the others.
     self.status (int32 [1]) reports a pool or a table without room
     (DGT_ERR_FULL: nothing is appended) and bad pages."""
 
@@ -943,15 +945,16 @@ class StepAttention:
         i32 = lambda v: torch.tensor([v], dtype=torch.int32, device=cache.k.device)
         self.cache, self.rotary, self.window, self.sinks, self.scale = cache, rotary, window, sinks, scale
         self.seq, self.one, self.start, self.status = i32(seq), i32(1), i32(0), i32(0)
-        self.ws = None
+        self.ws = {}     # by query heads; kept, because captured steps hold their addresses
 
     def prepare(self, q_width: int, depth: int):
         """Workspace for steps of this query width; checks that the cache has room for the layers."""
         c = self.cache
         if q_width % (c.head_dim * c.kv_heads) or depth > c.layers:
             raise ValueError("the cache's heads or layers do not fit the step's")
-        self.q_heads = q_width // c.head_dim
-        self.ws = kv_attention_workspace(c, self.q_heads, 1, 1)
+        heads = q_width // c.head_dim
+        if heads not in self.ws:
+            self.ws[heads] = kv_attention_workspace(c, heads, 1, 1)
 
     def begin(self, stream=None):
         """Room for the step's token; its position to self.start."""
@@ -965,7 +968,7 @@ class StepAttention:
         rotate(self.rotary, q, self.start, k=k, q_out=q, k_out=k, stream=stream)
         kv_append(c, layer, k, v, self.seq, self.start, status=self.status, stream=stream)
         kv_attention(c, layer, q, self.seq, scale=self.scale, window=self.window, sinks=self.sinks,
-                     out=out.view(1, self.q_heads, c.head_dim), ws=self.ws, status=self.status, stream=stream)
+                     out=out.view(q.shape), ws=self.ws[q.shape[1]], status=self.status, stream=stream)
 
 
 class DecodeStep:
