@@ -932,7 +932,8 @@ class StepAttention:
     holds, with an optional window and first tokens that stay visible.  For
     DecodeStep and MoeDecodeStep; the query heads have the cache's head_dim,
     their count a multiple of its kv_heads.  Positions and lengths live on the
-    device, so a captured step moves on by one token with every replay.  Several
+    device, so a captured step moves on by one token with every replay, and
+    every eager step appends its token too.  Several
     steps may share one, if they run one after the other: the tokens of each
     follow those of the others.
     self.status (int32 [1]) reports a pool or a table without room
@@ -1073,8 +1074,10 @@ class DecodeStep:
         return self.x, self.out
 
     def capture(self):
-        """Capture launch() in a CUDA graph (run the step once eagerly first);
-        replay() then runs the step on the current contents of self.x."""
+        """Capture launch() in a CUDA graph; replay() then runs the step on the
+        current contents of self.x.  Nothing runs here and no eager step is
+        needed before: with an attention that would leave a token in its
+        sequence."""
         import torch
         g = torch.cuda.CUDAGraph()
         s = torch.cuda.Stream()
@@ -1216,6 +1219,7 @@ class MoeDecodeStep:
         return self.x, self.out
 
     def capture(self):
+        """As DecodeStep.capture."""
         import torch
         g = torch.cuda.CUDAGraph()
         s = torch.cuda.Stream()

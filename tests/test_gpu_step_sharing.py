@@ -33,7 +33,7 @@ def attention(dgt, held):
     g = np.random.default_rng(held)
     i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
     start = dgt.kv_reserve(c, i32([1]), i32([held]))
-    for l in range(2):
+    for l in range(2 if held else 0):
         k, v = (torch.from_numpy(g.normal(size=(held, NKV // DIM, DIM)).astype(np.float32)).cuda().bfloat16()
                 for _ in range(2))
         dgt.kv_append(c, l, k, v, i32([1]), start, cu=i32([0, held]))
@@ -65,3 +65,41 @@ def test_a_captured_step_after_another_was_built(dgt):
     assert all((j == 255).all() for j in junk)
     other(x[0])
     assert att.status.item() == 0 and att.cache.lens.tolist() == [0, 1007]
+
+
+def as_r4(dgt, w):
+    return [{p: dgt.load_r4(dgt.upload(dgt.pack(t.view(torch.int16).cpu().numpy().view(np.uint16)))) for p, t in l.items()}
+            for l in w]
+
+
+def moe(dgt, w, gam, att):
+    """Two experts in every layer, gate, up and down stacked."""
+    e = [{p: torch.cat([t, t.flip(0)]) if p in ("gate", "up", "down") else t for p, t in l.items()} for l in w]
+    r = [(torch.tensor([1, 0], dtype=torch.int32, device="cuda"), torch.tensor([0.25, 0.75], device="cuda"))]
+    return dgt.MoeDecodeStep(e, gam, r, 2, attention=att)
+
+
+STEPS = {"bf16": lambda dgt, w, gam, att: dgt.DecodeStep(w, gam, attention=att),
+         "r4": lambda dgt, w, gam, att: dgt.DecodeStep(as_r4(dgt, w), gam, attention=att), "moe": moe}
+
+
+@pytest.mark.parametrize("held", [0, 70])
+@pytest.mark.parametrize("form", list(STEPS))
+def test_a_step_is_captured_without_a_token_of_its_own(dgt, form, held):
+    # a prompt of `held` tokens in the cache; the first token that the step appends is the first that is replayed
+    w, gam = layers(2, 2)
+    x = inputs(4)
+    att = attention(dgt, held)
+    before = [t.clone() for t in (att.cache.k, att.cache.v, att.cache.table, att.cache.refs)]
+    step = STEPS[form](dgt, w, gam, att)
+    step.x.copy_(x[0])
+    step.capture()
+    assert torch.equal(step.x, x[0]) and att.status.item() == 0
+    assert att.cache.lens.tolist() == [0, held]
+    for a, b in zip((att.cache.k, att.cache.v, att.cache.table, att.cache.refs), before):
+        assert torch.equal(a, b)
+    got = [step.replay()[0].clone()] + [step.replay(v)[0].clone() for v in x[1:]]
+    alone = STEPS[form](dgt, w, gam, attention(dgt, held))
+    want = [alone(v)[0].clone() for v in x]
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
