@@ -1069,7 +1069,9 @@ class DecodeStep:
 
     def __call__(self, x0, stream=None):
         """Eager step from the fp32 input x0: returns (x, out)."""
-        self.x.copy_(x0)
+        import torch
+        with torch.cuda.stream(stream):
+            self.x.copy_(x0)
         self.launch(stream)
         return self.x, self.out
 
@@ -1214,7 +1216,9 @@ class MoeDecodeStep:
         add_rmsnorm(self.x, self.gammas[-1], self.eps, self.out, self.comb, stream)
 
     def __call__(self, x0, stream=None):
-        self.x.copy_(x0)
+        import torch
+        with torch.cuda.stream(stream):
+            self.x.copy_(x0)
         self.launch(stream)
         return self.x, self.out
 

@@ -31,3 +31,24 @@ def test_a_second_step_leaves_the_first_ones_workspace(monkeypatch):
     assert q == out == (1, 2, 64) and other is not ws
     got, q, out = step(4)
     assert got is ws and q == out == (1, 4, 64)
+
+
+@pytest.mark.parametrize("kind", [dgt.DecodeStep, dgt.MoeDecodeStep])
+def test_a_steps_input_is_copied_on_its_stream(monkeypatch, kind):
+    # an eager step on a stream of its own reads its input there: the copy belongs to the same stream
+    import contextlib
+    now, seen = ["current"], []
+
+    @contextlib.contextmanager
+    def within(stream):
+        was = now[0]
+        now[0] = was if stream is None else stream
+        yield
+        now[0] = was
+    monkeypatch.setattr(torch.cuda, "stream", within)
+    step = kind.__new__(kind)
+    step.x = types.SimpleNamespace(copy_=lambda x0: seen.append(now[0]))
+    step.out, step.launch = None, lambda stream: seen.append("current" if stream is None else stream)
+    step("x0", "side")
+    step("x0")
+    assert seen == ["side", "side", "current", "current"]
