@@ -783,6 +783,8 @@ def kv_read(cache: KvCache, layer, seqs, first, cu, tokens: int, status=None, st
     ...].  cu int32 [batch + 1] (None: one position each), tokens: their sum."""
     import torch
     batch = seqs.numel()
+    if layer is not None and layer < 0:
+        raise ValueError("layer: None or 0..layers - 1")
     shape = (tokens, cache.kv_heads, cache.head_dim)
     if layer is None:
         shape = (cache.layers, *shape)
