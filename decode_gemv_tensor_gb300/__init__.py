@@ -659,6 +659,15 @@ def _i32(x, name, n=None):
     return x.data_ptr()
 
 
+def _status(x):
+    import torch
+    if x is None:
+        return None
+    if x.dtype is not torch.int32 or not x.is_cuda or x.numel() == 0:
+        raise ValueError("status: a CUDA int32 tensor")
+    return x.data_ptr()
+
+
 class Rotary:
     """What a rotation turns and by how much (dgt_rotary), its tables on the
     device.  The first rot_dim dimensions of a head are turned; pair i is
@@ -773,7 +782,7 @@ def kv_append(cache: KvCache, layer: int, k, v, seqs, start, cu=None, status=Non
         raise ValueError("k, v: [tokens, kv_heads, head_dim]")
     _check(lib().dgt_kv_append(cache.ptr, layer, _heads(k, "k"), _heads(v, "v"), tokens,
                                _i32(seqs, "seqs"), _i32(start, "start", batch),
-                               None if cu is None else _i32(cu, "cu", batch + 1), batch, _ptr(status),
+                               None if cu is None else _i32(cu, "cu", batch + 1), batch, _status(status),
                                _stream_on(cache.k, stream)), "dgt_kv_append")
 
 
@@ -792,7 +801,7 @@ def kv_read(cache: KvCache, layer, seqs, first, cu, tokens: int, status=None, st
     out = [_new(shape, torch.bfloat16, dev, stream) for _ in range(2)]
     _check(lib().dgt_kv_read(cache.ptr, -1 if layer is None else layer, _i32(seqs, "seqs"),
                              _i32(first, "first", batch), None if cu is None else _i32(cu, "cu", batch + 1), batch,
-                             tokens, _ptr(out[0]), _ptr(out[1]), _ptr(status), _stream_on(cache.k, stream)), "dgt_kv_read")
+                             tokens, _ptr(out[0]), _ptr(out[1]), _status(status), _stream_on(cache.k, stream)), "dgt_kv_read")
     return out
 
 
@@ -825,16 +834,19 @@ def kv_attention(cache: KvCache, layer: int, q, seqs, cu=None, scale=None, windo
         raise ValueError("window and sinks: not negative")
     if out is None:
         out = _new((tokens, heads, dim), torch.bfloat16, q.device, stream)
-    elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
-        raise ValueError("out: a contiguous bfloat16 tensor of q's shape")
-    if lse is not None and (lse.numel() != tokens * heads or lse.dtype != torch.float32 or not lse.is_contiguous()):
-        raise ValueError("lse: a contiguous float32 tensor [tokens, q_heads]")
+    elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_cuda or not out.is_contiguous():
+        raise ValueError("out: a contiguous CUDA bfloat16 tensor of q's shape")
+    if lse is not None and (lse.numel() != tokens * heads or lse.dtype != torch.float32 or not lse.is_cuda or
+                            not lse.is_contiguous()):
+        raise ValueError("lse: a contiguous CUDA float32 tensor [tokens, q_heads]")
+    if ws is not None and not (ws.is_cuda and ws.is_contiguous()):
+        raise ValueError("ws: a contiguous CUDA tensor (kv_attention_workspace)")
     if ws is None:
         ws = _attention_workspace(cache, heads, batch, tokens, stream, True)
     _check(lib().dgt_kv_attention_ex(cache.ptr, layer, _heads(q, "q"), tokens, _i32(seqs, "seqs"),
                                      None if cu is None else _i32(cu, "cu", batch + 1), batch,
                                      dim ** -0.5 if scale is None else scale, window, sinks, _ptr(out), _ptr(lse),
-                                     _ptr(ws), ws.numel(), _ptr(status), test_wait_flags(test_wait_polls),
+                                     _ptr(ws), ws.numel(), _status(status), test_wait_flags(test_wait_polls),
                                      _stream_on(cache.k, stream)), "dgt_kv_attention")
     return out
 
@@ -848,7 +860,7 @@ def kv_reserve(cache: KvCache, seqs, count, start=None, status=None, stream=None
     if start is None:
         start = _new(n, torch.int32, seqs.device, stream)
     _check(lib().dgt_kv_reserve(cache.ptr, _i32(seqs, "seqs"), _i32(count, "count", n), n,
-                                _i32(start, "start", n), _ptr(cache.ws), cache.ws.numel(), _ptr(status),
+                                _i32(start, "start", n), _ptr(cache.ws), cache.ws.numel(), _status(status),
                                 _stream_on(cache.k, stream)), "dgt_kv_reserve")
     return start
 
@@ -856,26 +868,26 @@ def kv_reserve(cache: KvCache, seqs, count, start=None, status=None, stream=None
 def kv_fork(cache: KvCache, src, dst, status=None, stream=None):
     """dgt_kv_fork: sequences dst[i] become copies of src[i] that share its pages."""
     _check(lib().dgt_kv_fork(cache.ptr, _i32(src, "src"), _i32(dst, "dst", src.numel()), src.numel(),
-                             _ptr(status), _stream_on(cache.k, stream)), "dgt_kv_fork")
+                             _status(status), _stream_on(cache.k, stream)), "dgt_kv_fork")
 
 
 def kv_free(cache: KvCache, seqs, status=None, stream=None):
     """dgt_kv_free: the sequences give up their pages."""
-    _check(lib().dgt_kv_free(cache.ptr, _i32(seqs, "seqs"), seqs.numel(), _ptr(status), _stream_on(cache.k, stream)),
+    _check(lib().dgt_kv_free(cache.ptr, _i32(seqs, "seqs"), seqs.numel(), _status(status), _stream_on(cache.k, stream)),
            "dgt_kv_free")
 
 
 def kv_copy_pages(cache: KvCache, src, dst, status=None, stream=None):
     """dgt_kv_copy_pages: pages src[i] -> dst[i] (int32 on the device) in every layer."""
     _check(lib().dgt_kv_copy_pages(cache.ptr, _i32(src, "src"), _i32(dst, "dst", src.numel()), src.numel(),
-                                   _ptr(status), _stream_on(cache.k, stream)), "dgt_kv_copy_pages")
+                                   _status(status), _stream_on(cache.k, stream)), "dgt_kv_copy_pages")
 
 
 def kv_compact(cache: KvCache, live=None, status=None, stream=None):
     """dgt_kv_compact: the used pages move to the lowest numbers; live (int32
     [1] on the device) gets their count."""
     _check(lib().dgt_kv_compact(cache.ptr, None if live is None else _i32(live, "live", 1), _ptr(cache.ws),
-                                cache.ws.numel(), _ptr(status), _stream_on(cache.k, stream)), "dgt_kv_compact")
+                                cache.ws.numel(), _status(status), _stream_on(cache.k, stream)), "dgt_kv_compact")
 
 
 # ---------------------------------------------------------------------------

@@ -63,10 +63,10 @@ def rows(n, heads):
 
 def test_attention_allocates_its_workspace_on_its_stream(seen):
     cache, side, log = seen
-    q, seqs, out = rows(1, 2), torch.ones(1, dtype=torch.int32), rows(1, 2)
+    q, seqs = rows(1, 2), torch.ones(1, dtype=torch.int32)
     log.made.clear()
-    dgt.kv_attention(cache, 0, q, seqs, out=out, stream=side)
-    assert log.made == [(1000, side)]
+    dgt.kv_attention(cache, 0, q, seqs, stream=side)
+    assert (1000, side) in log.made and all(s is side for _, s in log.made)
 
 
 F32, BF16 = torch.float32, torch.bfloat16

@@ -33,3 +33,50 @@ def test_read_of_a_layer_below_zero(kv):
     assert not kv.calls
     k, v = dgt.kv_read(kv.cache, None, kv.one, kv.one, None, 1)
     assert k.shape == v.shape == (3, 1, 1, 64) and kv.calls[-1][1][1] == -1
+
+
+class Device:
+    """A host tensor that says it is on the device."""
+
+    def __init__(self, *shape, dtype=torch.bfloat16, cuda=True):
+        self.t, self.is_cuda = torch.zeros(shape, dtype=dtype), cuda
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+BAD_TENSORS = {
+    "out on the host": dict(out=Device(1, 2, 64, cuda=False)),
+    "out of another type": dict(out=Device(1, 2, 64, dtype=torch.float16)),
+    "out of another shape": dict(out=Device(1, 64, 2)),
+    "lse on the host": dict(lse=Device(1, 2, dtype=torch.float32, cuda=False)),
+    "lse of another size": dict(lse=Device(1, 1, dtype=torch.float32)),
+    "ws on the host": dict(ws=Device(4096, dtype=torch.uint8, cuda=False)),
+    "status on the host": dict(status=Device(1, dtype=torch.int32, cuda=False)),
+    "status of another type": dict(status=Device(1, dtype=torch.int64)),
+    "an empty status": dict(status=Device(0, dtype=torch.int32)),
+}
+
+
+@pytest.mark.parametrize("what", list(BAD_TENSORS))
+def test_attention_refuses(kv, what):
+    good = dict(out=Device(1, 2, 64), lse=Device(1, 2, dtype=torch.float32), ws=Device(4096, dtype=torch.uint8),
+                status=Device(1, dtype=torch.int32))
+    dgt.kv_attention(kv.cache, 0, Device(1, 2, 64), kv.one, **good)
+    assert len(kv.calls) == 1
+    with pytest.raises(ValueError):
+        dgt.kv_attention(kv.cache, 0, Device(1, 2, 64), kv.one, **{**good, **BAD_TENSORS[what]})
+    assert len(kv.calls) == 1
+
+
+@pytest.mark.parametrize("bad", [Device(1, dtype=torch.int32, cuda=False), Device(1, dtype=torch.int64)])
+def test_every_call_checks_its_status(kv, bad):
+    c, one, row = kv.cache, kv.one, Device(1, 1, 64)
+    for call in (lambda: dgt.kv_append(c, 0, row, row, one, one, status=bad),
+                 lambda: dgt.kv_read(c, 0, one, one, None, 1, status=bad),
+                 lambda: dgt.kv_reserve(c, one, one, status=bad), lambda: dgt.kv_fork(c, one, one, status=bad),
+                 lambda: dgt.kv_free(c, one, status=bad), lambda: dgt.kv_copy_pages(c, one, one, status=bad),
+                 lambda: dgt.kv_compact(c, status=bad)):
+        with pytest.raises(ValueError):
+            call()
+    assert not kv.calls
