@@ -845,7 +845,8 @@ def kv_attention(cache: KvCache, layer: int, q, seqs, cu=None, scale=None, windo
         ws = _attention_workspace(cache, heads, batch, tokens, stream, True)
     _check(lib().dgt_kv_attention_ex(cache.ptr, layer, _heads(q, "q"), tokens, _i32(seqs, "seqs"),
                                      None if cu is None else _i32(cu, "cu", batch + 1), batch,
-                                     dim ** -0.5 if scale is None else scale, window, sinks, _ptr(out), _ptr(lse),
+                                     dim ** -0.5 if scale is None else scale, min(window, 1 << 30), min(sinks, 1 << 30),
+                                     _ptr(out), _ptr(lse),
                                      _ptr(ws), ws.numel(), _status(status), test_wait_flags(test_wait_polls),
                                      _stream_on(cache.k, stream)), "dgt_kv_attention")
     return out

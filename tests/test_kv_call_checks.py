@@ -80,3 +80,12 @@ def test_every_call_checks_its_status(kv, bad):
         with pytest.raises(ValueError):
             call()
     assert not kv.calls
+
+
+@pytest.mark.parametrize("size", [2 ** 30, 2 ** 32, 2 ** 32 + 5, 2 ** 40])
+def test_a_window_past_every_position_stays_one(kv, size):
+    # the library takes 32 bits; from 2^30 on a window is none, and first tokens are all
+    dgt.kv_attention(kv.cache, 0, Device(1, 2, 64), kv.one, out=Device(1, 2, 64), ws=Device(4096, dtype=torch.uint8),
+                     window=size, sinks=size)
+    window, sinks = kv.calls[0][1][8:10]
+    assert 2 ** 30 <= window < 2 ** 32 and 2 ** 30 <= sinks < 2 ** 32
