@@ -84,6 +84,10 @@ __global__ void __launch_bounds__(AP_THREADS) k_kv_append(AppendArgs a) {
     const uint32_t head = blockIdx.y, side = blockIdx.z;
     uint32_t b = blockIdx.x, blk = 0, row0 = blockIdx.x, n = 1;
     if (a.cu) {
+        if (a.cu[0] != 0) {   // the numbering below begins at the first entry's rows
+            if (tid == 0) set_status(a.status, DGT_ERR_ARG);
+            return;
+        }
         b = item_entry(a.cu, a.batch, blockIdx.x, KV_P, 2);
         blk = blockIdx.x - item_base(a.cu, b, KV_P, 2);
         row0 = (uint32_t)a.cu[b];
@@ -294,6 +298,10 @@ __global__ void __launch_bounds__(RD_THREADS) k_kv_read(ReadArgs a) {
     if (!a.out[side]) return;
     uint32_t b = blockIdx.x, blk = 0, row0 = blockIdx.x, n = 1;
     if (a.cu) {
+        if (a.cu[0] != 0) {   // the numbering below begins at the first entry's rows
+            if (tid == 0) set_status(a.status, DGT_ERR_ARG);
+            return;
+        }
         b = item_entry(a.cu, a.batch, blockIdx.x, KV_P, 2);
         blk = blockIdx.x - item_base(a.cu, b, KV_P, 2);
         row0 = (uint32_t)a.cu[b];

@@ -617,8 +617,9 @@ typedef struct dgt_kv_cache {
  * to d_cu[b + 1] (device int32 [batch + 1], d_cu[0] = 0, not decreasing,
  * d_cu[batch] = tokens); d_cu NULL: one row each.  What the device finds
  * wrong is reported in d_status (int32 or NULL, never cleared by the call)
- * and skipped: a slot, page number or position outside its range is
- * DGT_ERR_ARG.  tokens <= 2^24, batch <= 65536.  All asynchronous.
+ * and skipped: a slot, page number or position outside its range, and a d_cu
+ * of an append or a read that does not begin at 0, is DGT_ERR_ARG.  tokens <=
+ * 2^24, batch <= 65536.  All asynchronous.
  *
  * dgt_kv_append: writes token rows k and v (heads = kv_heads) of entry b at
  * positions d_start[b], d_start[b] + 1, ... of its sequence in `layer`.  Pages
