@@ -54,7 +54,7 @@ static inline int heads_check(const dgt_heads *x, uint32_t heads) {
 
 static inline int batch_check(uint64_t tokens, uint32_t batch, const int32_t *cu) {
     if (tokens > KV_MAX_TOKENS || batch > KV_MAX_BATCH) return DGT_ERR_SHAPE;
-    if (!cu && tokens != batch) return DGT_ERR_ARG;
+    if ((!cu || batch == 0) && tokens != batch) return DGT_ERR_ARG;
     return DGT_OK;
 }
 
