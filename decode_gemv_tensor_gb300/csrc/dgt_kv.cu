@@ -480,13 +480,15 @@ struct ReserveArgs {
     dgt_kv_cache c;
     const int32_t *seqs, *count;
     uint32_t n;
-    int32_t *start, *src, *dst, *free;   // workspace: copy pairs [n], free pages found
+    int32_t *start, *src, *dst, *free, *old;   // workspace: copy pairs [n], free pages found and what they replace
     int32_t *status;
 };
 
 // Copy on write in list order: of the listed sequences that share a partly
 // filled last page, the k-th (from 0) finds refs - k references left, and
-// copies it when that is more than its own.
+// copies it when that is more than its own.  Pages that a row lists past its
+// length (it was lowered) and that no other row does serve again; the others
+// are replaced like empty entries, and lose this row's reference.
 __global__ void __launch_bounds__(PG_THREADS) k_kv_reserve(ReserveArgs a) {
     __shared__ int32_t seq_s[PG_MAX], last_s[PG_MAX];
     __shared__ uint32_t part[32];
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(PG_THREADS) k_kv_reserve(ReserveArgs a) {
     const uint32_t t = threadIdx.x;
     const dgt_kv_cache &c = a.c;
     int32_t seq = -1, len = 0, cnt = 0, last = -1;
-    uint32_t have = 0, add = 0, bad = 0, full = 0;
+    uint32_t have = 0, add = 0, need = 0, bad = 0, full = 0, listed = 0;   // listed: pages past the length
     if (t < a.n) {
         seq = a.seqs[t];
         cnt = a.count[t];
@@ -510,7 +512,15 @@ __global__ void __launch_bounds__(PG_THREADS) k_kv_reserve(ReserveArgs a) {
                 have = ((uint32_t)len + KV_P - 1) / KV_P;
                 const uint64_t want = ((uint64_t)len + (uint32_t)cnt + KV_P - 1) / KV_P;
                 if (want > c.max_pages) full = 1;
-                else add = (uint32_t)want - have;
+                else need = add = (uint32_t)want - have;
+                const int32_t *row = c.table + (uint64_t)seq * c.max_pages + have;
+                for (uint32_t i = 0; i < add; i++) {
+                    const int32_t p = row[i];
+                    if (p < 0) continue;
+                    listed = 1;
+                    if ((uint32_t)p >= c.pages) bad = 1;
+                    else if (c.refs[p] == 1) need--;
+                }
                 if (have) {
                     const int32_t p = c.table[(uint64_t)seq * c.max_pages + have - 1];
                     if (p < 0 || (uint32_t)p >= c.pages) bad = 1;
@@ -533,8 +543,9 @@ __global__ void __launch_bounds__(PG_THREADS) k_kv_reserve(ReserveArgs a) {
     const uint32_t copy = last >= 0 && c.refs[last] - (int32_t)rank > 1 ? 1u : 0u;
     const uint32_t anybad = __syncthreads_or(bad);
     const uint32_t anyfull = __syncthreads_or(full);
+    const uint32_t anylisted = __syncthreads_or(listed);
     uint32_t total;
-    const uint32_t base = cta_excl_scan(bad || full ? 0 : add + copy, &total, part);
+    const uint32_t base = cta_excl_scan(bad || full ? 0 : need + copy, &total, part);
     // the lowest free pages, in order
     uint32_t found = 0;
     if (!anybad && !anyfull && total <= c.pages) {
@@ -566,7 +577,23 @@ __global__ void __launch_bounds__(PG_THREADS) k_kv_reserve(ReserveArgs a) {
             c.lens[seq] = len + cnt;
             int32_t *row = c.table + (uint64_t)seq * c.max_pages;
             uint32_t at = base;
-            if (copy) {
+            if (anylisted) {
+                // references change below, when every row has been read
+                if (copy) {
+                    const int32_t p = a.free[at];
+                    a.src[t] = last;
+                    a.dst[t] = p;
+                    row[have - 1] = p;
+                    a.old[at++] = last;
+                }
+                for (uint32_t i = 0; i < add; i++) {
+                    const int32_t p = row[have + i], r = p < 0 ? 0 : c.refs[p];
+                    if (r == 1) continue;
+                    row[have + i] = a.free[at];
+                    a.old[at++] = r > 1 ? p : -1;
+                }
+                add = 0;
+            } else if (copy) {
                 const int32_t p = a.free[at++];
                 a.src[t] = last;
                 a.dst[t] = p;
@@ -579,6 +606,13 @@ __global__ void __launch_bounds__(PG_THREADS) k_kv_reserve(ReserveArgs a) {
                 row[have + i] = p;
                 c.refs[p] = 1;
             }
+        }
+    }
+    if (ok && anylisted) {
+        __syncthreads();
+        for (uint32_t k = t; k < total; k += PG_THREADS) {
+            c.refs[a.free[k]] = 1;
+            if (a.old[k] >= 0) atomicSub(&c.refs[a.old[k]], 1);
         }
     }
     if (!ok && t == 0) set_status(a.status, anybad ? DGT_ERR_ARG : DGT_ERR_FULL);
@@ -715,11 +749,11 @@ extern "C" int dgt_kv_free(const dgt_kv_cache *cache, const int32_t *d_seqs, uin
     return launched(launch_pdl(k_kv_free, dim3(n), dim3(256), 0, (cudaStream_t)stream, *cache, d_seqs, d_status));
 }
 
-// Workspace: a reserve's copy pairs and free list, or a compaction's moves, map
-// and count.
+// Workspace: a reserve's copy pairs, free list and what it replaces, or a
+// compaction's moves, map and count.
 extern "C" size_t dgt_kv_pages_workspace_bytes(const dgt_kv_cache *cache) {
     if (!cache) return 0;
-    const size_t reserve = 2 * (size_t)PG_MAX + cache->pages, compact = 3 * (size_t)cache->pages + 1;
+    const size_t reserve = 2 * (size_t)PG_MAX + 2 * (size_t)cache->pages, compact = 3 * (size_t)cache->pages + 1;
     return 4 * (reserve > compact ? reserve : compact);
 }
 
@@ -731,7 +765,8 @@ extern "C" int dgt_kv_reserve(const dgt_kv_cache *cache, const int32_t *d_seqs, 
     if (n == 0) return DGT_OK;
     if (!d_seqs || !d_count || !d_start || !d_ws || ws_bytes < dgt_kv_pages_workspace_bytes(cache)) return DGT_ERR_ARG;
     int32_t *w = (int32_t *)d_ws;
-    const ReserveArgs a{*cache, d_seqs, d_count, n, d_start, w, w + PG_MAX, w + 2 * PG_MAX, d_status};
+    const ReserveArgs a{*cache, d_seqs, d_count, n, d_start, w, w + PG_MAX, w + 2 * PG_MAX,
+                        w + 2 * PG_MAX + cache->pages, d_status};
     rc = launched(launch_pdl(k_kv_reserve, dim3(1), dim3(PG_THREADS), 0, (cudaStream_t)stream, a));
     if (rc != DGT_OK) return rc;
     return copy_launch(CopyArgs{*cache, a.src, a.dst, nullptr, n, d_status}, (cudaStream_t)stream);

@@ -695,7 +695,10 @@ int dgt_kv_attention_ex(const dgt_kv_cache *cache, uint32_t layer, const dgt_hea
  * (n <= 1024, each sequence once) and moves lens on; d_start[i] gets the
  * length before.  In the order of the list: a partly filled last page that
  * another sequence shares is copied to a free page (copy on write), then free
- * pages are added; always the lowest free page number first.  When the pool
+ * pages are added; always the lowest free page number first.  lens may have
+ * been lowered by the caller (tokens given back): pages that the table row
+ * still lists past it serve again, but for one that another sequence shares,
+ * which is given up and replaced.  When the pool
  * or a table row has too little room, nothing changes, every d_start[i] is -1
  * and the status is DGT_ERR_FULL.  The same, with DGT_ERR_ARG, for a slot out
  * of range, one that occurs twice, a negative count or a table that does not
