@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(AP_THREADS) k_kv_append(AppendArgs a) {
         }
     }
     const float s_old = lo ? *scale_p : 0.0f;   // read by all before thread 0 writes it
+    const int32_t holders = a.c.refs[page];
     auto largest = [&]() {
         uint32_t m = 0;
 #pragma unroll
@@ -152,6 +153,10 @@ __global__ void __launch_bounds__(AP_THREADS) k_kv_append(AppendArgs a) {
         return m;
     };
     uint32_t top = largest();
+    if (holders > 1) {   // other sequences read this page
+        if (tid == 0) set_status(a.status, DGT_ERR_ARG);
+        return;
+    }
     bool bad = top >= 0x7F80u;
     if (bad) {
         // a value that is not finite: the block's scale will say so; its finite values as ever

@@ -623,7 +623,9 @@ typedef struct dgt_kv_cache {
  *
  * dgt_kv_append: writes token rows k and v (heads = kv_heads) of entry b at
  * positions d_start[b], d_start[b] + 1, ... of its sequence in `layer`.  Pages
- * must be there (dgt_kv_reserve) and be the sequence's own.  A block whose
+ * must be there (dgt_kv_reserve) and be the sequence's own: one that several
+ * table rows hold (refs above 1) is not written, with DGT_ERR_ARG in the
+ * status.  Two entries of a call do not write the same page.  A block whose
  * first token is written is begun anew; one that already holds tokens keeps
  * its scale unless the new tokens need a larger one, and then its codes are
  * rounded (nearest, ties to even) to that.  lens is not read or written.
