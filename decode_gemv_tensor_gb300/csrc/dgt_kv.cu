@@ -83,19 +83,17 @@ __global__ void __launch_bounds__(AP_THREADS) k_kv_append(AppendArgs a) {
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t head = blockIdx.y, side = blockIdx.z;
     uint32_t b = blockIdx.x, blk = 0, row0 = blockIdx.x, n = 1;
+    int32_t cu0 = 0;
     if (a.cu) {
-        if (a.cu[0] != 0) {   // the numbering below begins at the first entry's rows
-            if (tid == 0) set_status(a.status, DGT_ERR_ARG);
-            return;
-        }
+        cu0 = a.cu[0];   // the numbering begins at the first entry's rows: 0
         b = item_entry(a.cu, a.batch, blockIdx.x, KV_P, 2);
         blk = blockIdx.x - item_base(a.cu, b, KV_P, 2);
         row0 = (uint32_t)a.cu[b];
         n = (uint32_t)(a.cu[b + 1] - a.cu[b]);
     }
-    if (n == 0) return;
+    if (n == 0 && cu0 == 0) return;
     const int32_t seq = a.seqs[b], start = a.start[b];
-    if ((uint64_t)row0 + n > a.tokens || seq < 0 || (uint32_t)seq >= a.c.max_seqs || start < 0 ||
+    if (cu0 != 0 || (uint64_t)row0 + n > a.tokens || seq < 0 || (uint32_t)seq >= a.c.max_seqs || start < 0 ||
         (uint64_t)start + n > (uint64_t)a.c.max_pages * KV_P) {
         if (tid == 0) set_status(a.status, DGT_ERR_ARG);
         return;
@@ -302,19 +300,17 @@ __global__ void __launch_bounds__(RD_THREADS) k_kv_read(ReadArgs a) {
     const uint32_t head = blockIdx.y, side = blockIdx.z & 1, layer = a.layer0 + blockIdx.z / 2;
     if (!a.out[side]) return;
     uint32_t b = blockIdx.x, blk = 0, row0 = blockIdx.x, n = 1;
+    int32_t cu0 = 0;
     if (a.cu) {
-        if (a.cu[0] != 0) {   // the numbering below begins at the first entry's rows
-            if (tid == 0) set_status(a.status, DGT_ERR_ARG);
-            return;
-        }
+        cu0 = a.cu[0];   // the numbering begins at the first entry's rows: 0
         b = item_entry(a.cu, a.batch, blockIdx.x, KV_P, 2);
         blk = blockIdx.x - item_base(a.cu, b, KV_P, 2);
         row0 = (uint32_t)a.cu[b];
         n = (uint32_t)(a.cu[b + 1] - a.cu[b]);
     }
-    if (n == 0) return;
+    if (n == 0 && cu0 == 0) return;
     const int32_t seq = a.seqs[b], first = a.first[b];
-    if ((uint64_t)row0 + n > a.tokens || seq < 0 || (uint32_t)seq >= a.c.max_seqs || first < 0 ||
+    if (cu0 != 0 || (uint64_t)row0 + n > a.tokens || seq < 0 || (uint32_t)seq >= a.c.max_seqs || first < 0 ||
         (uint64_t)first + n > (uint64_t)a.c.max_pages * KV_P) {
         if (tid == 0) set_status(a.status, DGT_ERR_ARG);
         return;
