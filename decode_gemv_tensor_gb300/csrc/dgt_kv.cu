@@ -374,6 +374,18 @@ struct CopyArgs {
 
 constexpr uint32_t CP_THREADS = 256;
 
+// A load that is not kept in L1.  Not the read-only path: the grid may have
+// started before the kernel that writes these pages has ended, and writes to
+// the same pool itself.
+__device__ __forceinline__ uint4 ld_once16(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // Item: (pair, layer, keys or values), one page of one layer and side, the
 // scales with it.  CTAs walk the items.
 __global__ void __launch_bounds__(CP_THREADS) k_kv_copy(CopyArgs a) {
@@ -403,7 +415,7 @@ __global__ void __launch_bounds__(CP_THREADS) k_kv_copy(CopyArgs a) {
         for (; q + (UN - 1) * CP_THREADS < quads; q += UN * CP_THREADS) {
             uint4 v[UN];
 #pragma unroll
-            for (uint32_t i = 0; i < UN; i++) v[i] = ldg_stream16(from + q + i * CP_THREADS);
+            for (uint32_t i = 0; i < UN; i++) v[i] = ld_once16(from + q + i * CP_THREADS);
 #pragma unroll
             for (uint32_t i = 0; i < UN; i++) to[q + i * CP_THREADS] = v[i];
         }

@@ -75,3 +75,29 @@ def test_an_append_into_a_page_that_others_share(dgt, held):
     want, _ = dgt.kv_read(c, 0, i32([0]), i32([0]), i32([0, held]), held, status=st)
     assert torch.equal(k[:held], want) and dgt.read_status(st) == 0
     assert ((k[-1].float() - new[0].float()).abs() <= 2.0 ** -4 * new[0].float().abs().amax()).all()
+
+
+def test_copies_right_behind_what_writes_their_pages(dgt):
+    # pages copied back and forth between appends, every kernel launched while the one before may still run
+    c = dgt.KvCache(1, 130, 8, 128, max_seqs=1, max_pages=64)
+    c.table[0] = torch.arange(64, dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = [torch.randn(64 * 64, 8, 128, device="cuda", generator=g).bfloat16() for _ in range(2)]
+    seq, zero, cu = i32([0]), i32([0]), i32([0, 64 * 64])
+    here, there = torch.arange(64, dtype=torch.int32, device="cuda"), torch.arange(64, 128, dtype=torch.int32, device="cuda")
+    want = []
+    for v in x:
+        dgt.kv_append(c, 0, v, v, seq, zero, cu=cu)
+        torch.cuda.synchronize()
+        want.append((c.k[:, :64].clone(), c.v[:, :64].clone()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i, v in enumerate(x):
+            dgt.kv_append(c, 0, v, v, seq, zero, cu=cu)
+            dgt.kv_copy_pages(c, here, there)
+            dgt.kv_append(c, 0, x[1 - i], x[1 - i], seq, zero, cu=cu)
+            got = c.k[:, 64:128].clone(), c.v[:, 64:128].clone()
+            dgt.kv_copy_pages(c, there, here)
+            back = c.k[:, :64].clone(), c.v[:, :64].clone()
+            for a in (got, back):
+                assert torch.equal(a[0], want[i][0]) and torch.equal(a[1], want[i][1])
