@@ -662,7 +662,10 @@ int dgt_kv_read(const dgt_kv_cache *cache, int32_t layer, const int32_t *d_seqs,
  * for elements below 2^-9 of the largest: with few rows an entry (at most 24,
  * 16 or 8 rows of a kv head, for head_dim 64, 128 and 256; the mean of the
  * batch) those are kept to 2^-31 of it, with more to 2^-17.  The weights
- * exp(t_j - max) are rounded to fp16 (2^-11 relative), every sum is fp32.
+ * exp(t_j - max) are rounded to fp16, every sum is fp32: a weight is held to
+ * 2^-11 of itself, and weight times the value scale of its page (what the
+ * rounding sees) to 2^-37 of the row's largest such product with few rows, to
+ * 2^-29 with many; below half of that a weight is lost to the numerator.
  * d_ws: device, dgt_kv_attention_workspace_bytes(...) bytes, 256-byte aligned,
  * zeroed before its first use: it begins with arrival counters that every
  * call, of whatever sizes, leaves at zero; the rest need not be kept.  Calls
