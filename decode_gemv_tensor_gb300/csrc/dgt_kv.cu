@@ -526,18 +526,18 @@ __global__ void __launch_bounds__(PG_THREADS) k_kv_reserve(ReserveArgs a) {
                 const uint64_t want = ((uint64_t)len + (uint32_t)cnt + KV_P - 1) / KV_P;
                 if (want > c.max_pages) full = 1;
                 else need = add = (uint32_t)want - have;
-                const int32_t *row = c.table + (uint64_t)seq * c.max_pages + have;
+                const int32_t *row = c.table + (uint64_t)seq * c.max_pages;
+                const int32_t end = have ? row[have - 1] : -1;   // on its way with the entries behind it
                 for (uint32_t i = 0; i < add; i++) {
-                    const int32_t p = row[i];
+                    const int32_t p = row[have + i];
                     if (p < 0) continue;
                     listed = 1;
                     if ((uint32_t)p >= c.pages) bad = 1;
                     else if (c.refs[p] == 1) need--;
                 }
                 if (have) {
-                    const int32_t p = c.table[(uint64_t)seq * c.max_pages + have - 1];
-                    if (p < 0 || (uint32_t)p >= c.pages) bad = 1;
-                    else if (((uint32_t)len & (KV_P - 1)) && cnt > 0) last = p;
+                    if (end < 0 || (uint32_t)end >= c.pages) bad = 1;
+                    else if (((uint32_t)len & (KV_P - 1)) && cnt > 0) last = end;
                 }
             }
         }
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(PG_THREADS) k_kv_reserve(ReserveArgs a) {
         seq_s[t] = seq;
         last_s[t] = last;
     }
-    __syncthreads();
+    const bool anylisted = __syncthreads_or(listed);
     uint32_t rank = 0;
     if (t < a.n)
         for (uint32_t j = 0; j < t; j++) {
@@ -556,7 +556,6 @@ __global__ void __launch_bounds__(PG_THREADS) k_kv_reserve(ReserveArgs a) {
     const uint32_t copy = last >= 0 && c.refs[last] - (int32_t)rank > 1 ? 1u : 0u;
     const uint32_t anybad = __syncthreads_or(bad);
     const uint32_t anyfull = __syncthreads_or(full);
-    const uint32_t anylisted = __syncthreads_or(listed);
     uint32_t total;
     const uint32_t base = cta_excl_scan(bad || full ? 0 : need + copy, &total, part);
     // the lowest free pages, in order
@@ -590,7 +589,7 @@ __global__ void __launch_bounds__(PG_THREADS) k_kv_reserve(ReserveArgs a) {
             c.lens[seq] = len + cnt;
             int32_t *row = c.table + (uint64_t)seq * c.max_pages;
             uint32_t at = base;
-            if (anylisted) {
+            if (__builtin_expect(anylisted, 0)) {
                 // references change below, when every row has been read
                 if (copy) {
                     const int32_t p = a.free[at];
@@ -621,7 +620,7 @@ __global__ void __launch_bounds__(PG_THREADS) k_kv_reserve(ReserveArgs a) {
             }
         }
     }
-    if (ok && anylisted) {
+    if (__builtin_expect(ok && anylisted, 0)) {
         __syncthreads();
         for (uint32_t k = t; k < total; k += PG_THREADS) {
             c.refs[a.free[k]] = 1;
