@@ -15,7 +15,7 @@
 // What bounds it: with many long sequences HBM (48 of up to 6007 tokens, 8 kv
 // heads of 128: 62 us, 5.8 TB/s, 87 % of the measured copy rate; two of 131072
 // and 93523, 8 heads of 256: 138 us, 99 %); with few pages a warp the chain of
-// dependent steps from the tables to the join (one sequence of 778 tokens: 9.0
+// dependent steps from the tables to the join (one sequence of 778 tokens: 9.1
 // us, of which its bytes are 0.2).
 #include "dgt_attn.cuh"
 

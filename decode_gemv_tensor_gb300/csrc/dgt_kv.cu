@@ -9,10 +9,10 @@
 // bookkeeping is integer work on a few words per sequence, done by one CTA in
 // the order of the list.
 //
-// Bounds: a step's append is latency (16 sequences, append and read back 7.2
+// Bounds: a step's append is latency (16 sequences, append and read back 7.3
 // us); a prompt's the loads in flight (three of up to 3001 rows, 8 heads of
-// 256, append and read back 35.5 us, 56 % of the measured copy rate); copies
-// HBM (160 pages of 28 layers, 1.17 GB: 187 us, 94 %).
+// 256, append and read back 35.8 us, 55 % of the measured copy rate); copies
+// HBM (160 pages of 28 layers, 1.17 GB: 184 us, 95 %).
 #include "dgt_kv.cuh"
 
 #include "dgt_device.cuh"

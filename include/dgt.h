@@ -598,8 +598,9 @@ int dgt_rotate(const dgt_rotary *rot, const dgt_heads *q, const dgt_heads *k, co
  * page p (0: free).  A new cache has every byte of k and v zero, refs and
  * lens zero and table -1; the scales need no initial value.
  * Everything is device memory, caller-owned; k and v 16-byte aligned.
- * head_dim 64, 128 or 256; kv_heads 1..256; layers >= 1; pages 1..2^22;
- * max_seqs 1..2^20; max_pages 1..2^16 (else DGT_ERR_SHAPE).
+ * head_dim 64, 128 or 256; kv_heads 1..256; layers 1..2^16 (at most 32767 in
+ * a dgt_kv_read of every layer); pages 1..2^22; max_seqs 1..2^20; max_pages
+ * 1..2^16 (else DGT_ERR_SHAPE).
  */
 #define DGT_KV_PAGE 64
 typedef struct dgt_kv_cache {
@@ -661,7 +662,9 @@ int dgt_kv_read(const dgt_kv_cache *cache, int32_t layer, const int32_t *d_seqs,
  * A row of q is scaled to its largest element's exponent and kept exactly, but
  * for elements below 2^-9 of the largest: with few rows an entry (at most 24,
  * 16 or 8 rows of a kv head, for head_dim 64, 128 and 256; the mean of the
- * batch) those are kept to 2^-31 of it, with more to 2^-17.  The weights
+ * batch) those are kept to 2^-31 of it, with more to 2^-17 (while scale times
+ * the largest element is at least 2^-100; smaller products lose bits to fp32's
+ * range).  The weights
  * exp(t_j - max) are rounded to fp16, every sum is fp32: a weight is held to
  * 2^-11 of itself, and weight times the value scale of its page (what the
  * rounding sees) to 2^-37 of the row's largest such product with few rows, to
@@ -669,7 +672,10 @@ int dgt_kv_read(const dgt_kv_cache *cache, int32_t layer, const int32_t *d_seqs,
  * d_ws: device, dgt_kv_attention_workspace_bytes(...) bytes, 256-byte aligned,
  * zeroed before its first use: it begins with arrival counters that every
  * call, of whatever sizes, leaves at zero; the rest need not be kept.  Calls
- * that may overlap need one each.  The results do not depend on timing.
+ * that may overlap need one each.  The results do not depend on timing.  They
+ * do on the rest of the batch and the device's SM count: the mean of the
+ * entries' rows chooses the row tile, and all lengths where the work is cut, so
+ * that another batch may add a sequence's sums in another order.
  * DGT_ERR_TIMEOUT in the status: a bounded wait ran out, the outputs are then
  * unspecified.  flags: 0, or the failure-path test
  * hook DGT_TEST_SHORT_WAITS | DGT_TEST_WAIT_POLLS(n); others DGT_ERR_ARG.
