@@ -161,8 +161,7 @@ extern "C" int dgt_rotate(const dgt_rotary *rot, const dgt_heads *q, const dgt_h
     // Four tokens a CTA where one leaves most of its threads without a piece (a piece a thread is 16 elements) and
     // there are CTAs enough.  One and four, 4096 tokens: 576 elements a token 6.6 and 5.0 us, 1152 7.4 and 6.5, 1536
     // 7.4 and 7.0, 2048 8.5 and 9.2, 4096 14.3 and 16.8, 6144 20.6 and 22.9; 2048 tokens of 1536 4.5 and 4.3, 1024 2.8
-    // and 3.6.  From there to 3072 elements one is faster by 6 to 12% at 4096 tokens and four by 0 to 6% at
-    // 12873.
+    // and 3.6.  Between 1536 and 3072 elements one is faster by 6 to 12% at 4096 tokens, four by up to 6% at 12873.
     const bool four = tokens >= 2048 && a.heads * head_dim <= 1536;
     auto fn = rot->interleaved ? (four ? k_rotate<true, 4> : k_rotate<true, 1>)
                                : (four ? k_rotate<false, 4> : k_rotate<false, 1>);
