@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(PG_THREADS) k_kv_reserve(ReserveArgs a) {
                 const int32_t end = have ? row[have - 1] : -1;   // on its way with the entries behind it
                 for (uint32_t i = 0; i < add; i++) {
                     const int32_t p = row[have + i];
-                    if (p < 0) continue;
+                    if (p < 0) break;   // a row's pages stand together
                     listed = 1;
                     if ((uint32_t)p >= c.pages) bad = 1;
                     else if (c.refs[p] == 1) need--;
@@ -598,8 +598,10 @@ __global__ void __launch_bounds__(PG_THREADS) k_kv_reserve(ReserveArgs a) {
                     row[have - 1] = p;
                     a.old[at++] = last;
                 }
+                bool more = true;
                 for (uint32_t i = 0; i < add; i++) {
-                    const int32_t p = row[have + i], r = p < 0 ? 0 : c.refs[p];
+                    const int32_t p = more ? row[have + i] : -1, r = p < 0 ? 0 : c.refs[p];
+                    more = p >= 0;
                     if (r == 1) continue;
                     row[have + i] = a.free[at];
                     a.old[at++] = r > 1 ? p : -1;
