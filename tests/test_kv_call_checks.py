@@ -11,12 +11,15 @@ import decode_gemv_tensor_gb300 as dgt  # noqa: E402
 
 @pytest.fixture
 def kv(monkeypatch):
-    """A cache, and a library whose calls are counted and succeed."""
+    """A cache, and a library whose cache calls are counted and succeed (others go through: what earlier tests
+    left may be freed meanwhile)."""
     cache = dgt.KvCache(3, 2, 1, 64, max_seqs=1, max_pages=2, device="cpu")
-    calls = []
+    calls, real = [], dgt.lib()
 
     class Library:
         def __getattr__(self, name):
+            if not name.startswith("dgt_kv_"):
+                return getattr(real, name)
             return lambda *a: 1000 if name.endswith("_bytes") else calls.append((name, a)) or 0
     monkeypatch.setattr(dgt, "_lib", Library())
     monkeypatch.setattr(dgt, "_raw_stream", lambda i: 0)
