@@ -69,6 +69,8 @@ class HeadsStruct(C.Structure):
 
 
 _pack_heads = struct.Struct("=QqqII").pack     # the same as bytes, which ctypes passes by address
+_pack_norm = struct.Struct("=7Q5q2I").pack     # dgt_norm
+_pack_router = struct.Struct("=8IfIQ").pack    # dgt_router
 
 
 class RotaryStruct(C.Structure):
@@ -145,6 +147,11 @@ def lib():
             "dgt_silu_mul_rows": (i32, [vp, C.c_uint32, u64, vp, vp]),
             "dgt_repeat": (i32, [vp, u64, u64, vp, vp]),
             "dgt_weighted_sum": (i32, [vp, vp, C.c_uint32, u64, vp, vp]),
+            "dgt_block_norm": (i32, [vp, u64, C.c_uint32, C.c_float, C.c_float, C.c_float, C.c_float, vp]),
+            "dgt_route": (i32, [vp, vp, C.c_int64, u64, vp, vp, vp]),
+            "dgt_beam_workspace_bytes": (C.c_size_t, [C.c_uint32] * 4),
+            "dgt_beam_select": (i32, [vp, C.c_uint32, C.c_int64, vp, vp, C.c_int32, C.c_uint32, C.c_uint32,
+                                      C.c_uint32, C.c_uint32, vp, vp, vp, vp, vp, C.c_size_t, vp]),
             "dgt_rotary_freqs": (i32, [C.c_double, C.c_uint32, vp]),
             "dgt_rotate": (i32, [vp, hp, hp, hp, hp, C.c_uint32, u64, vp, vp]),
             "dgt_kv_append": (i32, [kp, C.c_uint32, hp, hp, u64, vp, vp, vp, C.c_uint32, vp, vp]),
@@ -158,6 +165,7 @@ def lib():
             "dgt_kv_copy_pages": (i32, [kp, vp, vp, C.c_uint32, vp, vp]),
             "dgt_kv_fork": (i32, [kp, vp, vp, C.c_uint32, vp, vp]),
             "dgt_kv_reserve": (i32, [kp, vp, vp, C.c_uint32, vp, vp, C.c_size_t, vp, vp]),
+            "dgt_kv_reorder": (i32, [kp, vp, vp, vp, C.c_uint32, C.c_uint32, vp, vp]),
             "dgt_kv_free": (i32, [kp, vp, C.c_uint32, vp, vp]),
             "dgt_kv_compact": (i32, [kp, vp, vp, C.c_size_t, vp, vp]),
             "dgt_exponent_stats": (i32, [vp, u64, C.c_uint32, vp, vp, vp, vp]),
@@ -638,6 +646,180 @@ def gemm_rebuild(W: R4, X, scratch=None, plan=None, Y32=None, Y=None, ws=None, s
 
 
 # ---------------------------------------------------------------------------
+# norms around a block, routing, beams
+# ---------------------------------------------------------------------------
+def _here(x, name):
+    """x is on the current device, where its kernels are launched."""
+    import torch
+    if not x.is_cuda or x.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: a tensor on the current CUDA device")
+
+
+def _float_rows(x, name, shape=None, bf16=False):
+    """(address, row stride, is fp32) of fp32 or bf16 rows [rows, n] or of one row [n]."""
+    import torch
+    f32 = x.dtype is torch.float32 and not bf16
+    if not (f32 or x.dtype is torch.bfloat16) or not x.is_cuda or x.dim() not in (1, 2):
+        raise ValueError(f"{name}: a CUDA {'' if bf16 else 'float32 or '}bfloat16 tensor [rows, n] or [n]")
+    if shape is not None and x.shape != shape:
+        raise ValueError(f"{name}: the shape of x")
+    if x.stride(-1) != 1 and x.shape[-1] > 1 and x.numel():
+        raise ValueError(f"{name}: a contiguous last dimension")
+    return x.data_ptr(), x.stride(0) if x.dim() == 2 and x.shape[0] > 1 else x.shape[-1], f32
+
+
+def block_norm(x, y=None, pre=None, post=None, gate=None, scale: float = 1.0, residual: float = 1.0,
+               offset: float = 0.0, eps: float = 1e-5, x_out=None, h=None, stream=None):
+    """dgt_block_norm: the norm after a block (weights post), its gate, the
+    residual add and the norm before the next block (weights pre), row by row:
+    u = y r(y) (offset + post) gate, x' = residual x + scale u, h = x' r(x')
+    (offset + pre), r(v) = (mean v^2 + eps)^-1/2.  x, y: float32 or bfloat16
+    [rows, n] or [n]; pre, post: bfloat16 [n]; gate: bfloat16 [n] or of x's
+    shape; None is left out (pre: then there is no h).  x_out: of x's type,
+    may be x itself.  Returns (x', of x's type, and h bfloat16 or None)."""
+    import torch
+    _here(x, "x")
+    px, sx, fx = _float_rows(x, "x")
+    n = x.shape[-1]
+    rows = x.shape[0] if x.dim() == 2 else 1
+    if x_out is None:
+        x_out = _new(x.shape, x.dtype, x.device, stream)
+    elif x_out.dtype != x.dtype:
+        raise ValueError("x_out: the type of x")
+    po, so, _ = _float_rows(x_out, "x_out", x.shape)
+    if x_out.dim() == 2 and rows > 1 and abs(so) < n:
+        raise ValueError("x_out: rows that do not overlap")
+    py, sy, fy = (0, 0, False) if y is None else _float_rows(y, "y", x.shape)
+    vec = lambda w, name: 0 if w is None else _bf16_vector(w, name, n)
+    pp, pq = vec(pre, "pre"), vec(post, "post")
+    ph = pg = sh = sg = 0
+    if pre is not None:
+        if h is None:
+            h = _new(x.shape, torch.bfloat16, x.device, stream)
+        ph, sh, _ = _float_rows(h, "h", x.shape, bf16=True)
+        if h.dim() == 2 and rows > 1 and abs(sh) < n:
+            raise ValueError("h: rows that do not overlap")
+    else:
+        h = None
+    if gate is not None:
+        if gate.shape == x.shape and gate.dim() == 2:
+            pg, sg, _ = _float_rows(gate, "gate", x.shape, bf16=True)
+        else:
+            pg = _bf16_vector(gate, "gate", n)
+    if (post is not None or gate is not None) and y is None:
+        raise ValueError("post and gate: of y")
+    _check(lib().dgt_block_norm(_pack_norm(px, po, py, ph, pp, pq, pg, sx, so, sy, sh, sg, fx, fy), rows, n, scale,
+                                residual, offset, eps, _stream_on(x, stream)), "dgt_block_norm")
+    return x_out, h
+
+
+def _bf16_vector(w, name, n):
+    import torch
+    if w.dtype is not torch.bfloat16 or not w.is_cuda or w.numel() != n or not w.is_contiguous():
+        raise ValueError(f"{name}: a contiguous CUDA bfloat16 tensor [n]")
+    return w.data_ptr()
+
+
+def route(logits, topk: int, score: str = "softmax", bias=None, groups: int = 1, group_topk: int = 1,
+          group_best: int = 2, renorm: bool = True, scale: float = 1.0, ids=None, p=None, stream=None):
+    """dgt_route: a router's choice of experts from its logits, float32 or
+    bfloat16 [tokens, experts].  score: "softmax" or "sigmoid"; bias: float32
+    [experts], added to the scores for the choice alone; groups > 1: of so many
+    equal groups of experts the group_topk stay whose group_best (1 or 2)
+    greatest values sum to most; renorm: the chosen scores divided by their
+    sum; scale: of the weights.  Returns (ids int32, p float32), both [tokens,
+    topk], greatest first: what the expert products take."""
+    import torch
+    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits: a float32 or bfloat16 tensor [tokens, experts]")
+    _here(logits, "logits")
+    tokens, experts = logits.shape
+    if logits.stride(1) != 1 and experts > 1 and tokens:
+        raise ValueError("logits: a contiguous last dimension")
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError("score: softmax or sigmoid")
+    if min(topk, groups, group_topk) < 1 or group_best not in (1, 2):
+        raise ValueError("topk, groups, group_topk: at least 1; group_best: 1 or 2")
+    pb = 0
+    if bias is not None:
+        if bias.dtype is not torch.float32 or not bias.is_cuda or bias.numel() != experts or not bias.is_contiguous():
+            raise ValueError("bias: a contiguous CUDA float32 tensor [experts]")
+        pb = bias.data_ptr()
+    shape = (tokens, topk)
+    if ids is None:
+        ids = _new(shape, torch.int32, logits.device, stream)
+    elif ids.shape != shape:
+        raise ValueError("ids: [tokens, topk]")
+    if p is None:
+        p = _new(shape, torch.float32, logits.device, stream)
+    elif p.shape != shape or p.dtype is not torch.float32 or not p.is_cuda or not p.is_contiguous():
+        raise ValueError("p: a contiguous CUDA float32 tensor [tokens, topk]")
+    _check(lib().dgt_route(_pack_router(experts, topk, groups, group_topk, group_best, logits.dtype is torch.float32,
+                                        score == "sigmoid", bool(renorm), scale, 0, pb),
+                           logits.data_ptr(), logits.stride(0) if tokens > 1 else experts, tokens, _i32(ids, "ids"),
+                           p.data_ptr(), _stream_on(logits, stream)), "dgt_route")
+    return ids, p
+
+
+def _beam_workspace(batch, beams, vocab, n, device, stream, temp):
+    import torch
+    nb = int(lib().dgt_beam_workspace_bytes(batch, beams, vocab, n))
+    return _new(max(nb, 256), torch.uint8, device, stream, zero=True, temp=temp)
+
+
+def beam_workspace(batch: int, beams: int, vocab: int, n: int, device="cuda", stream=None):
+    """A workspace for beam_select calls of these sizes on `stream` (zeroed, as its first use wants it)."""
+    return _beam_workspace(batch, beams, vocab, n, device, stream, False)
+
+
+def beam_select(logits, scores, n: int, eos: int = -1, done=None, parent=None, token=None, total=None, done_out=None,
+                ws=None, stream=None):
+    """dgt_beam_select: the n best continuations of the beams of each entry.
+    logits: float32 or bfloat16 [batch * beams, vocab]; scores: float32 [batch,
+    beams], sums of log probabilities (-inf: a beam that is not there); done:
+    uint8 [batch, beams], beams at their end, which offer token eos at their
+    own score.  Returns (parent int32, token int32, total float32), all [batch,
+    n], greatest total first, and done_out uint8 when done is given; -1, -1,
+    -inf (and 0) where there are fewer candidates.  The outputs may be given."""
+    import torch
+    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits: a float32 or bfloat16 tensor [batch * beams, vocab]")
+    _here(logits, "logits")
+    rows, vocab = logits.shape
+    if logits.stride(1) != 1 and vocab > 1 and rows:
+        raise ValueError("logits: a contiguous last dimension")
+    if scores.dim() != 2 or scores.dtype is not torch.float32 or not scores.is_cuda or not scores.is_contiguous() or \
+            scores.numel() != rows:
+        raise ValueError("scores: a contiguous CUDA float32 tensor [batch, beams] of the logits' rows")
+    batch, beams = scores.shape
+    if n < 1:
+        raise ValueError("n: at least 1")
+    if done is not None and (done.dtype is not torch.uint8 or not done.is_cuda or done.numel() != rows or
+                             not done.is_contiguous()):
+        raise ValueError("done: a contiguous CUDA uint8 tensor [batch, beams]")
+    if done is None and done_out is not None:
+        raise ValueError("done_out: with done")
+    outs = []
+    for x, dt, name in ((parent, torch.int32, "parent"), (token, torch.int32, "token"), (total, torch.float32, "total"),
+                        (done_out, torch.uint8, "done_out"))[:3 if done is None else 4]:
+        if x is None:
+            x = _new((batch, n), dt, logits.device, stream)
+        elif x.shape != (batch, n) or x.dtype is not dt or not x.is_cuda or not x.is_contiguous():
+            raise ValueError(f"{name}: a contiguous CUDA tensor [batch, n] of its type")
+        outs.append(x)
+    if ws is None:
+        ws = _beam_workspace(batch, beams, vocab, n, logits.device, stream, True)
+    elif not (ws.is_cuda and ws.is_contiguous()):
+        raise ValueError("ws: a contiguous CUDA tensor (beam_workspace)")
+    _check(lib().dgt_beam_select(logits.data_ptr(), logits.dtype is torch.float32,
+                                 logits.stride(0) if rows > 1 else vocab, scores.data_ptr(), _ptr(done), eos, batch,
+                                 beams, vocab, n, outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(),
+                                 outs[3].data_ptr() if done is not None else None, ws.data_ptr(),
+                                 ws.numel() * ws.element_size(), _stream_on(logits, stream)), "dgt_beam_select")
+    return tuple(outs)
+
+
+# ---------------------------------------------------------------------------
 # rotary positions
 # ---------------------------------------------------------------------------
 def _heads(x, name):
@@ -870,6 +1052,18 @@ def kv_fork(cache: KvCache, src, dst, status=None, stream=None):
     """dgt_kv_fork: sequences dst[i] become copies of src[i] that share its pages."""
     _check(lib().dgt_kv_fork(cache.ptr, _i32(src, "src"), _i32(dst, "dst", src.numel()), src.numel(),
                              _status(status), _stream_on(cache.k, stream)), "dgt_kv_fork")
+
+
+def kv_reorder(cache: KvCache, seqs, parent, dst=None, status=None, stream=None):
+    """dgt_kv_reorder: with seqs and parent int32 [groups, beams], sequence
+    dst[g, j] (None: seqs[g, j]) becomes what sequence seqs[g, parent[g, j]]
+    was, sharing its pages; all at once.  parent -1: it becomes empty."""
+    if seqs.dim() not in (1, 2):
+        raise ValueError("seqs: [groups, beams] or [beams]")
+    n, beams = seqs.numel(), seqs.shape[-1]
+    _check(lib().dgt_kv_reorder(cache.ptr, _i32(seqs, "seqs"), _i32(parent, "parent", n),
+                                None if dst is None else _i32(dst, "dst", n), n // beams if beams else 0, beams,
+                                _status(status), _stream_on(cache.k, stream)), "dgt_kv_reorder")
 
 
 def kv_free(cache: KvCache, seqs, status=None, stream=None):

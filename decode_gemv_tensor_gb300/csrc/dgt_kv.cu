@@ -13,6 +13,8 @@
 // us); a prompt's the loads in flight (three of up to 3001 rows, 8 heads of
 // 256, append and read back 35.8 us, 55 % of the measured copy rate); copies
 // HBM (160 pages of 28 layers, 1.17 GB: 184 us, 95 %).
+#include <algorithm>
+
 #include "dgt_kv.cuh"
 
 #include "dgt_device.cuh"
@@ -452,6 +454,75 @@ __global__ void __launch_bounds__(256) k_kv_fork(dgt_kv_cache c, const int32_t *
     if (threadIdx.x == 0) c.lens[t] = c.lens[f];
 }
 
+// Sequences dst[i] become what seqs[group of i][parent[i]] were before, all at
+// once.  A CTA takes RO_COLS columns of the tables (the last CTA the lengths):
+// every new entry of them is read before the first is written.
+constexpr uint32_t RO_COLS = 32, RO_MAX = 1024;   // sequences of one call
+__global__ void __launch_bounds__(1024) k_kv_reorder(dgt_kv_cache c, const int32_t *seqs, const int32_t *parent,
+                                                    const int32_t *dst, uint32_t n, uint32_t beams, int32_t *status) {
+    __shared__ __align__(16) int32_t to[RO_MAX];
+    __shared__ int32_t from[RO_MAX];   // -1: emptied, -2: left alone
+    pdl_trigger();
+    pdl_wait();
+    const uint32_t padded = (n + 3) / 4 * 4;
+    for (uint32_t i = threadIdx.x; i < padded; i += blockDim.x) to[i] = i < n ? dst[i] : -1;
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) {
+        const int32_t p = parent[i], t = to[i];
+        bool ok = t >= 0 && (uint32_t)t < c.max_seqs && p >= -1 && p < (int32_t)beams;
+        int32_t f = -1;
+        if (ok && p >= 0) {
+            f = seqs[i / beams * beams + (uint32_t)p];
+            ok = f >= 0 && (uint32_t)f < c.max_seqs;
+        }
+        // a target that the list holds twice is left alone
+        uint32_t same = 0;
+        for (uint32_t j = 0; j < padded; j += 4) {
+            const int4 x = *reinterpret_cast<const int4 *>(&to[j]);
+            same += (x.x == t) + (x.y == t) + (x.z == t) + (x.w == t);
+        }
+        if (!ok || same != 1) {
+            f = -2;
+            if (blockIdx.x == 0) set_status(status, DGT_ERR_ARG);
+        }
+        from[i] = f;
+    }
+    __syncthreads();
+    constexpr uint32_t PER = RO_MAX / 32;
+    int32_t now[PER];
+    if (blockIdx.x == gridDim.x - 1) {
+        if (threadIdx.x < n) now[0] = from[threadIdx.x] >= 0 ? c.lens[from[threadIdx.x]] : 0;
+        __syncthreads();
+        if (threadIdx.x < n && from[threadIdx.x] != -2) c.lens[to[threadIdx.x]] = now[0];
+        return;
+    }
+    const uint32_t col = blockIdx.x * RO_COLS + lane_id(), step = blockDim.x / 32;
+    const bool in = col < c.max_pages;
+#pragma unroll
+    for (uint32_t j = 0; j < PER; j++) {
+        const uint32_t i = threadIdx.x / 32 + j * step;
+        now[j] = -1;
+        if (i < n && in && from[i] >= 0) now[j] = c.table[(uint64_t)from[i] * c.max_pages + col];
+    }
+    __syncthreads();
+#pragma unroll
+    for (uint32_t j = 0; j < PER; j++) {
+        const uint32_t i = threadIdx.x / 32 + j * step;
+        if (i >= n || !in || from[i] == -2) continue;
+        int32_t *at = c.table + (uint64_t)to[i] * c.max_pages + col;
+        const int32_t was = *at;
+        int32_t is = now[j];
+        if (is < -1 || is >= (int32_t)c.pages) {
+            set_status(status, DGT_ERR_ARG);
+            is = -1;
+        }
+        if (was == is) continue;
+        *at = is;
+        if (is >= 0) atomicAdd(&c.refs[is], 1);
+        if (was >= 0 && (uint32_t)was < c.pages) atomicSub(&c.refs[was], 1);
+    }
+}
+
 // One CTA per sequence.
 __global__ void __launch_bounds__(256) k_kv_free(dgt_kv_cache c, const int32_t *seqs, int32_t *status) {
     pdl_trigger();
@@ -752,6 +823,20 @@ extern "C" int dgt_kv_fork(const dgt_kv_cache *cache, const int32_t *d_from, con
     if (n == 0) return DGT_OK;
     if (!d_from || !d_to) return DGT_ERR_ARG;
     return launched(launch_pdl(k_kv_fork, dim3(n), dim3(256), 0, (cudaStream_t)stream, *cache, d_from, d_to, d_status));
+}
+
+extern "C" int dgt_kv_reorder(const dgt_kv_cache *cache, const int32_t *d_seqs, const int32_t *d_parent,
+                              const int32_t *d_dst, uint32_t groups, uint32_t beams, int32_t *d_status, void *stream) {
+    const int rc = kv_check(cache);
+    if (rc != DGT_OK) return rc;
+    const uint64_t n = (uint64_t)groups * beams;
+    if (n > RO_MAX) return DGT_ERR_SHAPE;
+    if (n == 0) return DGT_OK;
+    if (!d_seqs || !d_parent) return DGT_ERR_ARG;
+    const uint32_t threads = (uint32_t)std::min<uint64_t>(n, 32) * 32;
+    const uint32_t grid = (cache->max_pages + RO_COLS - 1) / RO_COLS + 1;
+    return launched(launch_pdl(k_kv_reorder, dim3(grid), dim3(threads), 0, (cudaStream_t)stream, *cache, d_seqs,
+                               d_parent, d_dst ? d_dst : d_seqs, (uint32_t)n, beams, d_status));
 }
 
 extern "C" int dgt_kv_free(const dgt_kv_cache *cache, const int32_t *d_seqs, uint32_t n, int32_t *d_status,

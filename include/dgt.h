@@ -523,6 +523,93 @@ int dgt_silu_mul_rows(const float *d_gu, uint32_t rows, uint64_t n, uint16_t *d_
 int dgt_repeat(const uint16_t *d_v, uint64_t n_in, uint64_t n_out, uint16_t *d_out, void *stream);
 int dgt_weighted_sum(const float *d_y, const float *d_p, uint32_t slots, uint64_t n, float *d_out, void *stream);
 
+/*
+ * The norm after a block, its gate, the residual add and the norm before the
+ * next block, for rows of n elements:
+ *   u = y;  u = u * r(u) * (offset + post);  u = u * gate;
+ *   x' = residual * x + scale * u;  h = x' * r(x') * (offset + pre),
+ * with r(v) = 1 / sqrt(mean v^2 + eps), every step in fp32, x' and h each
+ * rounded once (h from x' before its rounding).  What is NULL is left out: y
+ * (then post and gate are NULL too), post, gate, x_out, or h with pre.
+ * x, x_out and y are fp32 where x_f32 / y_f32 is 1 and bf16 where it is 0;
+ * h, pre, post and gate are bf16.  Strides are elements between rows; 0 is
+ * allowed for what is read (one gate for all rows).  x_out may be x itself;
+ * apart from that no output overlaps another buffer.  n 1..32768, rows <=
+ * 2^24 (else DGT_ERR_SHAPE); eps >= 0; pointers aligned to their elements
+ * (else DGT_ERR_ARG).  Rows are read in 16-byte pieces where n and all strides
+ * are multiples of 8 and all pointers of 16 bytes.  Asynchronous.
+ */
+typedef struct dgt_norm {
+    const void *x;
+    void *x_out;
+    const void *y;
+    uint16_t *h;
+    const uint16_t *pre, *post, *gate;
+    int64_t x_stride, xo_stride, y_stride, h_stride, gate_stride;
+    uint32_t x_f32, y_f32;
+} dgt_norm;
+int dgt_block_norm(const dgt_norm *io, uint64_t rows, uint32_t n, float scale, float residual, float offset, float eps,
+                   void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Routing                                                                  */
+/* ------------------------------------------------------------------------ */
+/*
+ * Which experts a token goes to, and with which weights: the ids and p of the
+ * expert products, from a router's logits (fp32 where f32 is 1, else bf16;
+ * token t's at element t * stride).
+ *   s = softmax(logits), or 1 / (1 + e^-l) where sigmoid is 1;
+ *   c = s + d_bias (fp32 [experts], or NULL: none);
+ *   with groups > 1 (equal runs of neighbouring experts) the group_topk groups
+ *   stay whose sum of the group_best (1 or 2) greatest c is greatest;
+ *   ids: the topk experts of greatest c, greatest first (without a bias: of
+ *   greatest logit), equal ones and equal groups by the lower number;
+ *   p = s of them, with renorm divided by their sum, times scale.
+ * Values are compared as 64-bit floats.  A logit of -inf has score 0, a NaN
+ * score 0 and the last place.  Where every score is 0 (all logits -inf) p is
+ * 0; renormalised scores below fp32's range keep their quotients.
+ * d_ids int32 and d_p float [tokens, topk].  experts 1..1024, topk 1..32,
+ * groups 1..32 and a divisor of experts, topk at most the experts of
+ * group_topk groups, tokens <= 2^24 (else DGT_ERR_SHAPE).  Asynchronous.
+ */
+typedef struct dgt_router {
+    uint32_t experts, topk, groups, group_topk, group_best;
+    uint32_t f32, sigmoid, renorm;
+    float scale;
+    uint32_t reserved;
+    const float *d_bias;
+} dgt_router;
+int dgt_route(const dgt_router *router, const void *d_logits, int64_t stride, uint64_t tokens, int32_t *d_ids,
+              float *d_p, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Beams                                                                    */
+/* ------------------------------------------------------------------------ */
+/*
+ * The best continuations of the beams of each entry: with row r = entry *
+ * beams + b of the logits l (fp32 where f32 is 1, else bf16; row r at element
+ * r * stride) the n candidates (b, v), v < vocab, of greatest
+ *   total = d_scores[r] + l[r, v] - log sum_w e^l[r, w],
+ * greatest first, equal totals by the lower beam, then the lower v: d_parent
+ * and d_token int32, d_total float [batch, n].  Totals are compared as if in
+ * 64 bits (to 2^-32; beams whose rows hold the same logits have the same sum).  A logit of -inf is no candidate; a beam whose
+ * score is not finite, or whose logits hold a NaN or +inf, has none, and its
+ * row is not read where the score says so.  d_done (uint8 [batch, beams] or
+ * NULL): a beam at its end has one candidate, token eos with its own score as
+ * the total, and its row is not read; d_done_out (uint8 [batch, n] or NULL):
+ * whether the candidate's beam was, or its token is eos.  Where there are
+ * fewer candidates than n the rest is parent -1, token -1, total -inf, done 0.
+ * d_ws: dgt_beam_workspace_bytes(...) bytes, 256-byte aligned, zeroed before
+ * its first use: it begins with arrival counters that every call, of whatever
+ * sizes, leaves at zero; the rest need not be kept.  Calls that may overlap
+ * need one each.  Outputs do not overlap inputs.  beams and n 1..64, beams * n <= 2048, vocab 1..2^24,
+ * batch <= 65536 (else DGT_ERR_SHAPE).  Asynchronous.
+ */
+size_t dgt_beam_workspace_bytes(uint32_t batch, uint32_t beams, uint32_t vocab, uint32_t n);
+int dgt_beam_select(const void *d_logits, uint32_t f32, int64_t stride, const float *d_scores, const uint8_t *d_done,
+                    int32_t eos, uint32_t batch, uint32_t beams, uint32_t vocab, uint32_t n, int32_t *d_parent,
+                    int32_t *d_token, float *d_total, uint8_t *d_done_out, void *d_ws, size_t ws_bytes, void *stream);
+
 /* ------------------------------------------------------------------------ */
 /* Rotary positions                                                         */
 /* ------------------------------------------------------------------------ */
@@ -715,6 +802,14 @@ int dgt_kv_attention_ex(const dgt_kv_cache *cache, uint32_t layer, const dgt_hea
  * of range, one that occurs twice, a negative count or a table that does not
  * hold lens.  d_ws: dgt_kv_pages_workspace_bytes() bytes, 256-byte aligned.
  *
+ * dgt_kv_reorder: for i = g * beams + j (j < beams, g < groups) sequence
+ * d_dst[i] (NULL: d_seqs[i]) becomes what sequence d_seqs[g * beams +
+ * d_parent[i]] was before the call, its pages shared, or empty where d_parent[i]
+ * is -1; all at once, so that d_dst may be d_seqs.  What the targets held is
+ * given up.  device int32 [groups * beams] each, at most 1024.  A target that
+ * occurs twice, and slots and parents out of range, are skipped, with
+ * DGT_ERR_ARG in the status.
+ *
  * dgt_kv_free: the sequences give up their pages; length 0.
  *
  * dgt_kv_compact: the pages in use move to the lowest numbers (the k-th used
@@ -727,6 +822,8 @@ int dgt_kv_copy_pages(const dgt_kv_cache *cache, const int32_t *d_src, const int
                       int32_t *d_status, void *stream);
 int dgt_kv_fork(const dgt_kv_cache *cache, const int32_t *d_from, const int32_t *d_to, uint32_t n, int32_t *d_status,
                 void *stream);
+int dgt_kv_reorder(const dgt_kv_cache *cache, const int32_t *d_seqs, const int32_t *d_parent, const int32_t *d_dst,
+                   uint32_t groups, uint32_t beams, int32_t *d_status, void *stream);
 int dgt_kv_reserve(const dgt_kv_cache *cache, const int32_t *d_seqs, const int32_t *d_count, uint32_t n,
                    int32_t *d_start, void *d_ws, size_t ws_bytes, int32_t *d_status, void *stream);
 int dgt_kv_free(const dgt_kv_cache *cache, const int32_t *d_seqs, uint32_t n, int32_t *d_status, void *stream);
