@@ -161,6 +161,9 @@ def lib():
                                        C.c_uint32, vp, vp, vp, C.c_size_t, vp, vp]),
             "dgt_kv_attention_ex": (i32, [kp, C.c_uint32, hp, u64, vp, vp, C.c_uint32, C.c_float, C.c_uint32,
                                           C.c_uint32, vp, vp, vp, C.c_size_t, vp, C.c_uint, vp]),
+            "dgt_kv_attention_shared_workspace_bytes": (C.c_size_t, [kp, C.c_uint32, C.c_uint32, C.c_uint32, u64]),
+            "dgt_kv_attention_shared": (i32, [kp, C.c_uint32, hp, u64, vp, vp, C.c_uint32, vp, vp, vp, C.c_uint32,
+                                              C.c_float, vp, vp, vp, C.c_size_t, vp, C.c_uint, vp]),
             "dgt_kv_pages_workspace_bytes": (C.c_size_t, [kp]),
             "dgt_kv_copy_pages": (i32, [kp, vp, vp, C.c_uint32, vp, vp]),
             "dgt_kv_fork": (i32, [kp, vp, vp, C.c_uint32, vp, vp]),
@@ -1031,6 +1034,58 @@ def kv_attention(cache: KvCache, layer: int, q, seqs, cu=None, scale=None, windo
                                      _ptr(out), _ptr(lse),
                                      _ptr(ws), ws.numel(), _status(status), test_wait_flags(test_wait_polls),
                                      _stream_on(cache.k, stream)), "dgt_kv_attention")
+    return out
+
+
+def _shared_workspace(cache, q_heads, groups, batch, tokens, stream, temp):
+    import torch
+    nb = int(lib().dgt_kv_attention_shared_workspace_bytes(cache.ptr, q_heads, groups, batch, tokens))
+    return _new(max(nb, 256), torch.uint8, cache.k.device, stream, zero=True, temp=temp)
+
+
+def kv_attention_shared_workspace(cache: KvCache, q_heads: int, groups: int, batch: int, tokens: int, stream=None):
+    """A workspace for kv_attention_shared calls of these sizes on `stream` (zeroed, as its first use wants it)."""
+    return _shared_workspace(cache, q_heads, groups, batch, tokens, stream, False)
+
+
+def kv_attention_shared(cache: KvCache, layer: int, q, seqs, prefix, shared, groups=None, cu=None, scale=None, out=None,
+                        lse=None, ws=None, status=None, stream=None, test_wait_polls=None):
+    """dgt_kv_attention_shared: kv_attention (without a window) of sequences that
+    share their first pages, which are read once for a group.  groups int32 [G +
+    1]: where each group of neighbouring sequences begins in `seqs`, 0 first and
+    the batch last (None: one group); prefix int32 [G]: the sequence that holds
+    a group's shared tokens; shared int32 [G]: how many they are (whole pages of
+    them are shared, what is behind comes from each sequence's own pages).  The
+    sequences of a group list the same pages for them, as kv_fork and kv_reserve
+    leave them, and their new rows are behind them.  Returns out, bf16 [tokens,
+    q_heads, head_dim]."""
+    import torch
+    tokens, heads, dim = q.shape
+    batch, n = seqs.numel(), shared.numel()
+    if dim != cache.head_dim:
+        raise ValueError("q: [tokens, q_heads, head_dim] with the cache's head_dim")
+    if groups is None and n != 1:
+        raise ValueError("groups: where each of several groups begins")
+    _here(cache.k, "cache")
+    if out is None:
+        out = _new((tokens, heads, dim), torch.bfloat16, q.device, stream)
+    elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_cuda or not out.is_contiguous():
+        raise ValueError("out: a contiguous CUDA bfloat16 tensor of q's shape")
+    if lse is not None and (lse.numel() != tokens * heads or lse.dtype != torch.float32 or not lse.is_cuda or
+                            not lse.is_contiguous()):
+        raise ValueError("lse: a contiguous CUDA float32 tensor [tokens, q_heads]")
+    if ws is not None and not (ws.is_cuda and ws.is_contiguous()):
+        raise ValueError("ws: a contiguous CUDA tensor (kv_attention_shared_workspace)")
+    if ws is None:
+        ws = _shared_workspace(cache, heads, n, batch, tokens, stream, True)
+    _check(lib().dgt_kv_attention_shared(cache.ptr, layer, _heads(q, "q"), tokens, _i32(seqs, "seqs"),
+                                         None if cu is None else _i32(cu, "cu", batch + 1), batch,
+                                         _i32(prefix, "prefix", n), _i32(shared, "shared"),
+                                         None if groups is None else _i32(groups, "groups", n + 1), n,
+                                         dim ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(ws),
+                                         ws.numel() * ws.element_size(), _status(status),
+                                         test_wait_flags(test_wait_polls), _stream_on(cache.k, stream)),
+           "dgt_kv_attention_shared")
     return out
 
 

@@ -75,7 +75,7 @@ struct AttnCfg {
     static constexpr uint32_t PART = RT * (D + 4);       // floats of a partial result
 };
 
-template <uint32_t D, uint32_t NT>
+template <uint32_t D, uint32_t NT, int PART = AT_ALL>
 __global__ void __launch_bounds__(AT_WARPS * 32, attn_ctas(D, NT)) k_kv_attention(AttnArgs a) {
     using Cfg = AttnCfg<D, NT>;
     constexpr uint32_t RT = Cfg::RT, NS = Cfg::NS, IB = Cfg::IB, PD = Cfg::PD, PAN = Cfg::PAN, IPP = Cfg::IPP;
@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(AT_WARPS * 32, attn_ctas(D, NT)) k_kv_attentio
     pdl_wait();
 
     // ---- the CTA's units
-    Units here = describe<AT_WARPS>(a, RT, 0, slots, usum);
-    const Units all = a.slots <= AT_CHUNK ? here : all_units<AT_WARPS>(a, RT, usum);
+    Units here = describe<AT_WARPS, PART>(a, RT, 0, slots, usum);
+    const Units all = a.slots <= AT_CHUNK ? here : all_units<AT_WARPS, PART>(a, RT, usum);
     const Cuts cut = cut_plan(a, all, slots, gridDim.x);
     if (blockIdx.x >= cut.C) return;
     const uint64_t ub = cut.parts ? cut.U : cut.raw(blockIdx.x + 1);
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, attn_ctas(D, NT)) k_kv_attentio
     uint64_t base0 = 0;
     for (uint32_t s0 = 0; s0 < a.slots && base0 < ub; s0 += AT_CHUNK) {
         // ---- describe the next row tiles
-        if (s0) here = describe<AT_WARPS>(a, RT, s0, slots, usum);
+        if (s0) here = describe<AT_WARPS, PART>(a, RT, s0, slots, usum);
         const uint32_t tot = (uint32_t)here.units();
         const uint32_t nslots = min(AT_CHUNK, a.slots - s0);
         const uint64_t chunk_base = base0;
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, attn_ctas(D, NT)) k_kv_attentio
             const Slot s = slots[r.slot];
 
             if (s.np == 0) {
-                write_none<D>(a, s, r.h, tid, AT_WARPS * 32);
+                write_none<D, PART>(a, s, r.h, tid, AT_WARPS * 32);
                 at_hand = false;
                 continue;
             }
@@ -531,11 +531,26 @@ __global__ void __launch_bounds__(AT_WARPS * 32, attn_ctas(D, NT)) k_kv_attentio
                     const float *st = rowstat[row];
                     if (complete) {
                         const bool none = st[0] == -INFINITY && st[2] == 0.0f;
-                        const float q = none ? 0.0f : ex2(finite_base(st[1]) - finite_base(st[0]) - W_LOG2) / st[2];
+                        float q = none ? 0.0f : ex2(finite_base(st[1]) - finite_base(st[0]) - W_LOG2) / st[2];
                         const uint32_t flat = s.row0 + row;
                         const uint64_t at = (uint64_t)(s.tok0 + flat / a.group) * a.q_heads + r.h * a.group + flat % a.group;
+                        if (PART == AT_FRONT) {
+                            *reinterpret_cast<float4 *>(a.front + at * D + d) = make_float4(v.x * q, v.y * q, v.z * q, v.w * q);
+                            if (d == 0) a.front_lse[at] = none ? -INFINITY : st[0] + __log2f(st[2]);
+                            continue;
+                        }
+                        if (PART == AT_TAIL) {
+                            const TailJoin tj = tail_join(a, s, at, none ? -INFINITY : st[0] + __log2f(st[2]));
+                            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            if (s.joins) x = *reinterpret_cast<const float4 *>(a.front + at * D + d);
+                            q *= tj.tail;
+                            v.x = fmaf(v.x, q, x.x * tj.front), v.y = fmaf(v.y, q, x.y * tj.front);
+                            v.z = fmaf(v.z, q, x.z * tj.front), v.w = fmaf(v.w, q, x.w * tj.front);
+                            q = 1.0f;
+                            if (a.lse && d == 0) a.lse[at] = tj.lse * LN2;
+                        }
                         *reinterpret_cast<uint2 *>(a.out + at * D + d) = make_uint2(bf16x2(v.x * q, v.y * q), bf16x2(v.z * q, v.w * q));
-                        if (a.lse && d == 0) a.lse[at] = none ? -INFINITY : (st[0] + __log2f(st[2])) * LN2;
+                        if (PART == AT_ALL && a.lse && d == 0) a.lse[at] = none ? -INFINITY : (st[0] + __log2f(st[2])) * LN2;
                     } else {
                         float *pr = part + row * (D + 4);
                         *reinterpret_cast<float4 *>(pr + 4 + d) = v;
@@ -553,18 +568,18 @@ __global__ void __launch_bounds__(AT_WARPS * 32, attn_ctas(D, NT)) k_kv_attentio
             if (tid == 0) last_flag = arrive_last(&a.count[c0], c1 - c0 + 1);
             __syncthreads();
             if (!last_flag) continue;
-            join_parts<D, Cfg::PART, RT>(a, s, r.h, c0, c1, tid, AT_WARPS * 32, W_LOG2, scratch, [] { __syncthreads(); });
+            join_parts<D, Cfg::PART, RT, PART>(a, s, r.h, c0, c1, tid, AT_WARPS * 32, W_LOG2, scratch, [] { __syncthreads(); });
         }
         more = false;   // everything of this chunk has been taken
     }
 }
 
-template <uint32_t D, uint32_t NT>
-static int attn_launch(const AttnArgs &a, cudaStream_t st) {
+template <uint32_t D, uint32_t NT, int PART>
+static int attn_launch_part(const AttnArgs &a, cudaStream_t st) {
     DeviceInfo di;
     if (device_info(&di) != DGT_OK) return DGT_ERR_CUDA;
     constexpr uint32_t smem = AttnCfg<D, NT>::bytes;
-    auto fn = k_kv_attention<D, NT>;
+    auto fn = k_kv_attention<D, NT, PART>;
     static std::atomic<uint64_t> ready;   // devices that allow the shared memory
     const uint64_t bit = di.device < 64 ? 1ull << di.device : 0;
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
@@ -575,6 +590,13 @@ static int attn_launch(const AttnArgs &a, cudaStream_t st) {
     }
     const unsigned grid = AttnCfg<D, NT>::CTAS * std::min((unsigned)di.sms, AT_MAX_SMS);
     return launch_pdl(fn, dim3(grid), dim3(AT_WARPS * 32), smem, st, a) == cudaSuccess ? DGT_OK : DGT_ERR_CUDA;
+}
+
+template <uint32_t D, uint32_t NT>
+static int attn_launch(const AttnArgs &a, AttnPart part, cudaStream_t st) {
+    return part == AT_ALL     ? attn_launch_part<D, NT, AT_ALL>(a, st)
+           : part == AT_FRONT ? attn_launch_part<D, NT, AT_FRONT>(a, st)
+                              : attn_launch_part<D, NT, AT_TAIL>(a, st);
 }
 
 // Rows of a tile, by an entry's rows (the mean of a batch): in n-tiles of
@@ -600,6 +622,37 @@ static Plan attn_plan(uint32_t head_dim, uint32_t group, uint32_t batch, uint64_
 static uint64_t slot_count(uint32_t RT, uint32_t group, uint32_t batch, uint64_t tokens, bool ragged) {
     if (!ragged) return (uint64_t)batch * ((group + RT - 1) / RT);
     return tokens * group / RT + batch;
+}
+
+// The row tile and how the work is cut, and the launch.
+static int attn_run(AttnArgs &a, AttnPart part, cudaStream_t st) {
+    const uint32_t head_dim = a.c.head_dim;
+    const Plan plan = attn_plan(head_dim, a.group, a.batch, a.tokens);
+    const uint32_t nt = plan.nt, RT = plan.RT;
+    a.slots = (uint32_t)slot_count(RT, a.group, a.batch, a.tokens, part == AT_FRONT || a.cu != nullptr);
+    a.per_entry = (a.group + RT - 1) / RT;
+    // A page a warp (64 dimensions, 4001 tokens: 10.6 us; 2 or 8 pages 11.6); in prompts eight pages (200 rows of 128
+    // dimensions over 500 tokens 18.2 us; 4 pages 21.4).
+    a.min_units = nt ? 4 : 8;
+    // 30 sequences of up to 1501 tokens, 8 kv heads of 128: 17.1 us (24 pages 18.5); 4 prompts of up to 300 rows over
+    // 2300 tokens 42 us (10 pages 46, 24 pages 44).
+    a.slack = nt ? 12 : 16;
+    // Measured against min_units alone, one sequence of 60000 tokens, one kv head of 64, 128 and 256 dimensions: 4
+    // rows 28 and 19, 29 and 20, 49 and 31 us (0.5: 21, 22, 35); 240 rows over 120020 tokens 104 and 76, 218 and
+    // 107, 143 and 108 us (0.75: 72, 113, 114).
+    a.join = nt ? 0.25f : 1.5f;
+    // Measured against shares of equal pages: 100 sequences of up to 300 tokens (64 dimensions) 28 and 22 us, 200
+    // of 1000 65 and 52 us (12 instead of 8: the same within 4%); a prompt of 8192 rows (128 dimensions) 770 and
+    // 379 us (6: 439, 15: 389).
+    a.end = nt ? 8 : 10;
+    if (nt == 0) return prompt_launch(a, part, st);
+    switch (head_dim) {
+        case 64:
+            return nt == 1 ? attn_launch<64, 1>(a, part, st)
+                           : nt == 2 ? attn_launch<64, 2>(a, part, st) : attn_launch<64, 3>(a, part, st);
+        case 128: return nt == 1 ? attn_launch<128, 1>(a, part, st) : attn_launch<128, 2>(a, part, st);
+        default: return attn_launch<256, 1>(a, part, st);
+    }
 }
 
 }  // namespace dgt
@@ -640,35 +693,10 @@ extern "C" int dgt_kv_attention_ex(const dgt_kv_cache *cache, uint32_t layer, co
     a.group = q->heads / cache->kv_heads;
     a.q = *q, a.seqs = d_seqs, a.cu = d_cu, a.scale_log2 = scale * LOG2E, a.out = d_out, a.lse = d_lse;
     a.status = d_status;
-    const Plan plan = attn_plan(cache->head_dim, a.group, batch, tokens);
-    const uint32_t nt = plan.nt, RT = plan.RT;
-    const uint64_t slots = slot_count(RT, a.group, batch, tokens, d_cu != nullptr);
-    a.slots = (uint32_t)slots;
-    a.per_entry = (a.group + RT - 1) / RT;
     a.count = (int32_t *)d_ws;
     a.part = (float *)((uint8_t *)d_ws + AT_COUNT_BYTES);
-    // A page a warp (64 dimensions, 4001 tokens: 10.6 us; 2 or 8 pages 11.6); in prompts eight pages (200 rows of 128
-    // dimensions over 500 tokens 18.2 us; 4 pages 21.4).
-    a.min_units = nt ? 4 : 8;
-    // 30 sequences of up to 1501 tokens, 8 kv heads of 128: 17.1 us (24 pages 18.5); 4 prompts of up to 300 rows over
-    // 2300 tokens 42 us (10 pages 46, 24 pages 44).
-    a.slack = nt ? 12 : 16;
-    // Measured against min_units alone, one sequence of 60000 tokens, one kv head of 64, 128 and 256 dimensions: 4
-    // rows 28 and 19, 29 and 20, 49 and 31 us (0.5: 21, 22, 35); 240 rows over 120020 tokens 104 and 76, 218 and
-    // 107, 143 and 108 us (0.75: 72, 113, 114).
-    a.join = nt ? 0.25f : 1.5f;
-    // Measured against shares of equal pages: 100 sequences of up to 300 tokens (64 dimensions) 28 and 22 us, 200
-    // of 1000 65 and 52 us (12 instead of 8: the same within 4%); a prompt of 8192 rows (128 dimensions) 770 and
-    // 379 us (6: 439, 15: 389).
-    a.end = nt ? 8 : 10;
     a.spin = wait_limit_from_flags(flags);
-    cudaStream_t st = (cudaStream_t)stream;
-    if (nt == 0) return prompt_launch(a, st);
-    switch (cache->head_dim) {
-        case 64: return nt == 1 ? attn_launch<64, 1>(a, st) : nt == 2 ? attn_launch<64, 2>(a, st) : attn_launch<64, 3>(a, st);
-        case 128: return nt == 1 ? attn_launch<128, 1>(a, st) : attn_launch<128, 2>(a, st);
-        default: return attn_launch<256, 1>(a, st);
-    }
+    return attn_run(a, AT_ALL, (cudaStream_t)stream);
 }
 
 extern "C" int dgt_kv_attention(const dgt_kv_cache *cache, uint32_t layer, const dgt_heads *q, uint64_t tokens,
@@ -677,4 +705,58 @@ extern "C" int dgt_kv_attention(const dgt_kv_cache *cache, uint32_t layer, const
                                 size_t ws_bytes, int32_t *d_status, void *stream) {
     return dgt_kv_attention_ex(cache, layer, q, tokens, d_seqs, d_cu, batch, scale, window, sinks, d_out, d_lse, d_ws,
                                ws_bytes, d_status, 0, stream);
+}
+
+// Shared pages.  Workspace: the counters of both launches, the front's
+// logarithms and quotients, then the partial results of each.
+struct SharedSpace {
+    size_t front_lse, front, front_part, tail_part, bytes;
+    SharedSpace(const dgt_kv_cache *c, uint32_t q_heads, uint32_t groups, uint32_t batch, uint64_t tokens) {
+        const uint64_t rows = tokens * q_heads;
+        const size_t tail = dgt_kv_attention_workspace_bytes(c, q_heads, batch, tokens);
+        front_lse = 2 * AT_COUNT_BYTES;
+        front = front_lse + (rows * 4 + 255) / 256 * 256;
+        front_part = front + rows * c->head_dim * 4;
+        tail_part = front_part + dgt_kv_attention_workspace_bytes(c, q_heads, groups, tokens) - AT_COUNT_BYTES;
+        bytes = tail_part + tail - AT_COUNT_BYTES;
+    }
+};
+
+extern "C" size_t dgt_kv_attention_shared_workspace_bytes(const dgt_kv_cache *cache, uint32_t q_heads, uint32_t groups,
+                                                          uint32_t batch, uint64_t tokens) {
+    if (!cache || cache->kv_heads == 0 || batch == 0 || groups == 0 || tokens == 0 || q_heads < cache->kv_heads) return 0;
+    return SharedSpace(cache, q_heads, groups, batch, tokens).bytes;
+}
+
+extern "C" int dgt_kv_attention_shared(const dgt_kv_cache *cache, uint32_t layer, const dgt_heads *q, uint64_t tokens,
+                                       const int32_t *d_seqs, const int32_t *d_cu, uint32_t batch,
+                                       const int32_t *d_prefix, const int32_t *d_shared, const int32_t *d_groups,
+                                       uint32_t groups, float scale, uint16_t *d_out, float *d_lse, void *d_ws,
+                                       size_t ws_bytes, int32_t *d_status, unsigned flags, void *stream) {
+    int rc = kv_check(cache);
+    if (rc != DGT_OK) return rc;
+    if (!q || layer >= cache->layers) return DGT_ERR_ARG;
+    if (flags & ~(DGT_TEST_SHORT_WAITS | DGT_TEST_WAIT_POLLS(0xFFFF))) return DGT_ERR_ARG;
+    if ((rc = batch_check(tokens, batch, d_cu)) != DGT_OK) return rc;
+    if (groups > KV_MAX_BATCH) return DGT_ERR_SHAPE;
+    if (tokens == 0 || batch == 0) return DGT_OK;
+    if (groups == 0 || (!d_groups && groups != 1) || !d_prefix || !d_shared) return DGT_ERR_ARG;
+    if (!d_seqs || !d_out || !aligned16(d_out)) return DGT_ERR_ARG;
+    if (q->heads == 0 || q->heads % cache->kv_heads || q->heads / cache->kv_heads > 64) return DGT_ERR_SHAPE;
+    if ((rc = heads_check(q, q->heads)) != DGT_OK) return rc;
+    const SharedSpace at(cache, q->heads, groups, batch, tokens);
+    if (!d_ws || ((uintptr_t)d_ws & 255) || ws_bytes < at.bytes) return DGT_ERR_ARG;
+    AttnArgs a{};
+    a.c = *cache;
+    a.layer = layer, a.q_heads = q->heads, a.tokens = tokens, a.group = q->heads / cache->kv_heads;
+    a.q = *q, a.cu = d_cu, a.scale_log2 = scale * LOG2E, a.out = d_out, a.lse = d_lse, a.status = d_status;
+    a.spin = wait_limit_from_flags(flags);
+    a.group_at = d_groups, a.prefix = d_prefix, a.shared = d_shared, a.groups = groups, a.entries = batch;
+    uint8_t *w = (uint8_t *)d_ws;
+    a.front_lse = (float *)(w + at.front_lse), a.front = (float *)(w + at.front);
+    AttnArgs f = a;
+    f.batch = groups, f.count = (int32_t *)w, f.part = (float *)(w + at.front_part);
+    if ((rc = attn_run(f, AT_FRONT, (cudaStream_t)stream)) != DGT_OK) return rc;
+    a.batch = batch, a.seqs = d_seqs, a.count = (int32_t *)(w + AT_COUNT_BYTES), a.part = (float *)(w + at.tail_part);
+    return attn_run(a, AT_TAIL, (cudaStream_t)stream);
 }

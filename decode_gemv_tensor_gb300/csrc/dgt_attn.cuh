@@ -10,6 +10,11 @@
 // in several CTAs leaves partial sums in the workspace; the CTA that arrives
 // last adds them in page order, so results do not depend on timing.  Lengths
 // are read on the device: a captured graph follows them.
+//
+// Sequences that share their first pages: one launch takes these pages once
+// for all rows of a group (front) and leaves quotients and logarithms of the
+// sums in fp32, the next the pages behind them for each sequence (tail) and
+// joins the two.
 #pragma once
 #include <algorithm>
 
@@ -23,6 +28,8 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr uint32_t AT_CHUNK = 64;      // row tiles described in shared memory at a time
 constexpr uint32_t AT_MAX_SMS = 160;   // a workspace has room for so many
+
+enum AttnPart { AT_ALL, AT_FRONT, AT_TAIL };
 
 struct AttnArgs {
     dgt_kv_cache c;
@@ -40,7 +47,37 @@ struct AttnArgs {
     uint32_t end;                // what a segment costs besides its pages, in pages
     float join;                  // what a part costs the join, in pages
     uint32_t spin;
+    // front and tail: the groups' first entries (NULL: one group), the sequences whose first tokens are shared, and
+    // how many are; a front's entries are the groups
+    const int32_t *group_at, *prefix, *shared;
+    uint32_t groups, entries;
+    float *front, *front_lse;    // [tokens, q_heads, head_dim], and log2 of the sums
 };
+
+// Where group g begins among the entries, and its shared pages.
+__device__ __forceinline__ uint32_t group_entry(const AttnArgs &a, uint32_t g) {
+    if (!a.group_at) return g ? a.entries : 0;
+    const int32_t e = a.group_at[g];
+    if (e >= 0 && (uint32_t)e <= a.entries) return (uint32_t)e;
+    set_status(a.status, DGT_ERR_ARG);
+    return a.entries;
+}
+__device__ __forceinline__ uint32_t front_pages(const AttnArgs &a, uint32_t g) {
+    const int32_t s = a.prefix[g], n = a.shared[g];
+    if (s >= 0 && (uint32_t)s < a.c.max_seqs && n >= 0 && n <= a.c.lens[s] && (uint64_t)n <= (uint64_t)a.c.max_pages * KV_P)
+        return (uint32_t)n / KV_P;
+    set_status(a.status, DGT_ERR_ARG);
+    return 0;
+}
+// The first token row of an entry.
+template <int PART>
+__device__ __forceinline__ uint32_t entry_row(const AttnArgs &a, uint32_t b) {
+    if (PART == AT_FRONT) {
+        const uint32_t e = group_entry(a, b);
+        return a.cu ? (uint32_t)a.cu[e] : e;
+    }
+    return (uint32_t)a.cu[b];
+}
 
 // A tile of query rows: rows [row0, row0 + rows) of its entry's flattened
 // (token, head of the group) rows, at positions pos0 + row / group.
@@ -49,6 +86,7 @@ struct Slot {
     uint32_t sp, wp;            // pages seen before the window's, the window's first page
     int32_t seq, pos0;          // table row; position of the entry's first row
     uint32_t tok0, row0, rows;  // entry's first token row, tile's first flattened row, row count
+    uint32_t joins;             // tail: there are shared pages before
     __device__ __forceinline__ uint32_t per_head() const { return np ? np : 1; }
     __device__ __forceinline__ uint32_t page_index(uint32_t i) const { return i < sp ? i : wp + i - sp; }
 };
@@ -83,15 +121,24 @@ __device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
     return r;
 }
 // The row tile of number `slot`, RT rows each; units 0 for an empty number.
+template <int PART = AT_ALL>
 __device__ __forceinline__ Slot slot_info(const AttnArgs &a, uint32_t slot, uint32_t RT, uint32_t *units) {
     Slot s{};
     uint32_t b, rt, n = 1;
     *units = 0;
-    if (a.cu) {
-        b = item_entry(a.cu, a.batch, slot, RT, 1, a.group);
-        rt = slot - item_base(a.cu, b, RT, 1, a.group);
-        s.tok0 = (uint32_t)a.cu[b];
-        n = (uint32_t)(a.cu[b + 1] - a.cu[b]);
+    if (PART == AT_FRONT || a.cu) {
+        // as item_entry and item_base
+        auto base = [&](uint32_t i) { return (uint32_t)((uint64_t)entry_row<PART>(a, i) * a.group / RT) + i; };
+        uint32_t lo = 0, hi = a.batch;
+        while (hi - lo > 1) {
+            const uint32_t mid = (lo + hi) >> 1;
+            if (base(mid) <= slot) lo = mid;
+            else hi = mid;
+        }
+        b = lo;
+        rt = slot - base(b);
+        s.tok0 = entry_row<PART>(a, b);
+        n = entry_row<PART>(a, b + 1) - s.tok0;
         if ((uint64_t)s.tok0 + n > a.tokens) {
             set_status(a.status, DGT_ERR_ARG);
             return s;
@@ -106,6 +153,13 @@ __device__ __forceinline__ Slot slot_info(const AttnArgs &a, uint32_t slot, uint
     s.row0 = (uint32_t)first;
     s.rows = (uint32_t)min((uint64_t)RT, all - first);
     *units = a.c.kv_heads * (1 + a.end);
+    if (PART == AT_FRONT) {
+        s.seq = a.prefix[b];
+        s.np = front_pages(a, b);
+        s.pos0 = s.np * KV_P;   // behind every shared token
+        *units = a.c.kv_heads * (s.per_head() + a.end);
+        return s;
+    }
     s.seq = a.seqs[b];
     int32_t len = 0;
     if (s.seq < 0 || (uint32_t)s.seq >= a.c.max_seqs) {
@@ -120,6 +174,29 @@ __device__ __forceinline__ Slot slot_info(const AttnArgs &a, uint32_t slot, uint
     s.pos0 = len > 0 ? len - (int32_t)n : -0x40000000;
     const int32_t pf = s.pos0 + (int32_t)(s.row0 / a.group);
     const int32_t pl = s.pos0 + (int32_t)((s.row0 + s.rows - 1) / a.group);
+    if (PART == AT_TAIL) {
+        if (len == 0) return s;
+        uint32_t lo = 0, hi = a.groups;
+        while (hi - lo > 1) {
+            const uint32_t mid = (lo + hi) >> 1;
+            if (group_entry(a, mid) <= b) lo = mid;
+            else hi = mid;
+        }
+        uint32_t front = 0;
+        if (group_entry(a, lo) <= b && b < group_entry(a, lo + 1)) front = front_pages(a, lo);
+        else set_status(a.status, DGT_ERR_ARG);
+        if (front && s.pos0 < (int32_t)(front * KV_P)) {
+            // new rows inside the shared pages
+            set_status(a.status, DGT_ERR_ARG);
+            return s;
+        }
+        if (pl < 0) return s;
+        s.joins = front;
+        s.wp = front;
+        s.np = (uint32_t)pl / KV_P - front + 1;
+        *units = a.c.kv_heads * (s.np + a.end);
+        return s;
+    }
     if (pl < 0) return s;
     const uint32_t lo = a.window && pf >= 0 && (uint32_t)pf >= a.window ? (uint32_t)pf - a.window + 1 : 0;
     s.wp = lo / KV_P;
@@ -129,9 +206,22 @@ __device__ __forceinline__ Slot slot_info(const AttnArgs &a, uint32_t slot, uint
     return s;
 }
 
+// A row's sum over its tail (log2) and its front's, as the factors of the two
+// quotients and log2 of both sums.
+struct TailJoin {
+    float tail, front, lse;
+};
+__device__ __forceinline__ TailJoin tail_join(const AttnArgs &a, const Slot &s, uint64_t at, float own) {
+    if (!s.joins) return {1.0f, 0.0f, own};
+    const float f = a.front_lse[at], m = fmaxf(own, f), b = finite_base(m);
+    const float wt = ex2(own - b), wf = ex2(f - b), sum = wt + wf;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    return {wt * inv, wf * inv, m == -INFINITY ? m : m + __log2f(sum)};
+}
+
 // Many rows (dgt_prompt.cu): the rows of its tile, and its launch.
 uint32_t prompt_rows(uint32_t head_dim);
-int prompt_launch(const AttnArgs &a, cudaStream_t st);
+int prompt_launch(const AttnArgs &a, AttnPart part, cudaStream_t st);
 
 // Units and row tiles that hold rows, counted together.
 struct Units {
@@ -141,12 +231,12 @@ struct Units {
 };
 
 // All of a call's, summed by a CTA of WARPS warps.
-template <uint32_t WARPS>
+template <uint32_t WARPS, int PART = AT_ALL>
 __device__ __forceinline__ Units all_units(const AttnArgs &a, uint32_t RT, uint64_t *usum) {
     uint64_t sum = 0;
     uint32_t units;
     for (uint32_t s = threadIdx.x; s < a.slots; s += WARPS * 32) {
-        slot_info(a, s, RT, &units);
+        slot_info<PART>(a, s, RT, &units);
         if (units) sum += units + (1ull << 40);
     }
 #pragma unroll
@@ -160,14 +250,14 @@ __device__ __forceinline__ Units all_units(const AttnArgs &a, uint32_t RT, uint6
 }
 
 // The row tiles s0 .. s0 + AT_CHUNK - 1 into shared memory; returns their units.
-template <uint32_t WARPS>
+template <uint32_t WARPS, int PART = AT_ALL>
 __device__ __forceinline__ Units describe(const AttnArgs &a, uint32_t RT, uint32_t s0, Slot *slots, uint64_t *usum) {
     const uint32_t tid = threadIdx.x, warp = tid >> 5;
     __syncthreads();   // the tiles described before are done with
     Slot s{};
     uint32_t units = 0, before = 0;
     if (warp < AT_CHUNK / 32) {
-        if (s0 + tid < a.slots) s = slot_info(a, s0 + tid, RT, &units);
+        if (s0 + tid < a.slots) s = slot_info<PART>(a, s0 + tid, RT, &units);
         uint32_t wtot;
         before = warp_excl_scan(units, &wtot);
         const uint32_t tiles = __popc(__ballot_sync(DGT_FULL, units != 0));
@@ -320,9 +410,10 @@ __device__ __forceinline__ Cuts cut_plan(const AttnArgs &a, Units all, const Slo
     return k;
 }
 
-// Rows that see nothing: out 0, lse -inf.
-template <uint32_t D>
+// Rows that see nothing: out 0, lse -inf (a front's are not read).
+template <uint32_t D, int PART = AT_ALL>
 __device__ __forceinline__ void write_none(const AttnArgs &a, const Slot &s, uint32_t h, uint32_t t, uint32_t threads) {
+    if (PART == AT_FRONT) return;
     for (uint32_t i = t; i < s.rows * (D / 8); i += threads) {
         const uint32_t flat = s.row0 + i / (D / 8);
         const uint64_t at = (uint64_t)(s.tok0 + flat / a.group) * a.q_heads + h * a.group + flat % a.group;
@@ -339,12 +430,13 @@ __device__ __forceinline__ void write_none(const AttnArgs &a, const Slot &s, uin
 // elements at a time are weighted and added, the parts' loads in flight
 // together.
 constexpr uint32_t JOIN_PARTS = 32;
-__host__ __device__ constexpr uint32_t join_floats(uint32_t RT) { return (JOIN_PARTS + 2) * RT; }
-template <uint32_t D, uint32_t PART, uint32_t RT, typename Sync>
+__host__ __device__ constexpr uint32_t join_floats(uint32_t RT) { return (JOIN_PARTS + 3) * RT; }
+template <uint32_t D, uint32_t PART, uint32_t RT, int AP, typename Sync>
 __device__ __forceinline__ void join_parts(const AttnArgs &a, const Slot &s, uint32_t h, uint32_t c0, uint32_t c1,
                                            uint32_t t, uint32_t threads, float wlog2, float *sh, Sync sync) {
     float2 *rows = reinterpret_cast<float2 *>(sh);   // per row MU, the quotient's factor
     float *weight = sh + 2 * RT;                     // per part and row
+    float *front = weight + JOIN_PARTS * RT;         // tail: the front's factor of a row
     const uint32_t parts = c1 - c0 + 1;
     // part 0 is the one that begins the segment, at the end of its CTA's work
     auto at = [&](uint32_t k, uint32_t row) {
@@ -352,12 +444,20 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, const Slot &s, uin
     };
     auto finish = [&](uint32_t row, float M, float MU, float L) {
         const bool none = M == -INFINITY && L == 0.0f;
-        rows[row] = make_float2(finite_base(MU), none ? 0.0f : ex2(finite_base(MU) - finite_base(M) - wlog2) / L);
-        if (a.lse) {
-            const uint32_t flat = s.row0 + row;
-            a.lse[(uint64_t)(s.tok0 + flat / a.group) * a.q_heads + h * a.group + flat % a.group] =
-                none ? -INFINITY : (M + __log2f(L)) * LN2;
+        float quot = none ? 0.0f : ex2(finite_base(MU) - finite_base(M) - wlog2) / L;
+        const uint32_t flat = s.row0 + row;
+        const uint64_t at = (uint64_t)(s.tok0 + flat / a.group) * a.q_heads + h * a.group + flat % a.group;
+        if (AP == AT_FRONT) {
+            a.front_lse[at] = none ? -INFINITY : M + __log2f(L);
+        } else if (AP == AT_TAIL) {
+            const TailJoin j = tail_join(a, s, at, none ? -INFINITY : M + __log2f(L));
+            quot *= j.tail;
+            front[row] = j.front;
+            if (a.lse) a.lse[at] = j.lse * LN2;
+        } else if (a.lse) {
+            a.lse[at] = none ? -INFINITY : (M + __log2f(L)) * LN2;
         }
+        rows[row] = make_float2(finite_base(MU), quot);
     };
     // RPW rows a warp, their loads together
     constexpr uint32_t RPW = RT / 4;
@@ -433,8 +533,18 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, const Slot &s, uin
             if (i >= all) break;
             const uint32_t flat = s.row0 + i / Q;
             const uint64_t o = (uint64_t)(s.tok0 + flat / a.group) * a.q_heads + h * a.group + flat % a.group;
-            *reinterpret_cast<uint2 *>(a.out + o * D + (i % Q) * 4) =
-                make_uint2(bf16x2(v[b][0] * ro[b].y, v[b][1] * ro[b].y), bf16x2(v[b][2] * ro[b].y, v[b][3] * ro[b].y));
+            const float f = ro[b].y;
+            if (AP == AT_FRONT) {
+                reinterpret_cast<float4 *>(a.front + o * D)[i % Q] = make_float4(v[b][0] * f, v[b][1] * f, v[b][2] * f, v[b][3] * f);
+                continue;
+            }
+            float4 y = make_float4(v[b][0] * f, v[b][1] * f, v[b][2] * f, v[b][3] * f);
+            if (AP == AT_TAIL && s.joins) {
+                const float4 x = reinterpret_cast<const float4 *>(a.front + o * D)[i % Q];
+                const float w = front[i / Q];
+                y.x = fmaf(x.x, w, y.x), y.y = fmaf(x.y, w, y.y), y.z = fmaf(x.z, w, y.z), y.w = fmaf(x.w, w, y.w);
+            }
+            *reinterpret_cast<uint2 *>(a.out + o * D + (i % Q) * 4) = make_uint2(bf16x2(y.x, y.y), bf16x2(y.z, y.w));
         }
     }
     sync();   // sh and the parts are done with

@@ -130,7 +130,24 @@ __device__ __forceinline__ void store_halves(uint32_t addr, const uint32_t (&x)[
         asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(x[0] | x[1] << 16), "r"(x[2] | x[3] << 16) : "memory");
 }
 
-template <uint32_t D>
+// 32 elements of a front's row, and of a tail's row with its front's.
+__device__ __forceinline__ void put_front(const AttnArgs &a, uint64_t at, const float (&o)[32], float f) {
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        reinterpret_cast<float4 *>(a.front + at)[i] = make_float4(o[4 * i] * f, o[4 * i + 1] * f, o[4 * i + 2] * f, o[4 * i + 3] * f);
+}
+__device__ __forceinline__ void add_front(const AttnArgs &a, uint64_t at, float (&o)[32], float f, float w) {
+    float4 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) x[i] = reinterpret_cast<const float4 *>(a.front + at)[i];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        o[4 * i] = fmaf(o[4 * i], f, x[i].x * w), o[4 * i + 1] = fmaf(o[4 * i + 1], f, x[i].y * w);
+        o[4 * i + 2] = fmaf(o[4 * i + 2], f, x[i].z * w), o[4 * i + 3] = fmaf(o[4 * i + 3], f, x[i].w * w);
+    }
+}
+
+template <uint32_t D, int PART = AT_ALL>
 __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
     using Cfg = PromptCfg<D>;
     constexpr uint32_t NSTR = Cfg::NSTR, RT = Cfg::RT, RB = Cfg::RB, PAN = Cfg::PAN, PB = Cfg::PB, QP = Cfg::QP,
@@ -176,8 +193,8 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
     const uint32_t tm = tmem_slot;
     volatile int *abortp = &abort_flag;
 
-    Units here = describe<PR_WARPS>(a, RT, 0, slots, usum);
-    const Units all = a.slots <= AT_CHUNK ? here : all_units<PR_WARPS>(a, RT, usum);
+    Units here = describe<PR_WARPS, PART>(a, RT, 0, slots, usum);
+    const Units all = a.slots <= AT_CHUNK ? here : all_units<PR_WARPS, PART>(a, RT, usum);
     // found by one warp, and kept in shared memory: registers are short here
     if (warp == 0) {
         const Cuts k = cut_plan(a, all, slots, gridDim.x);
@@ -212,7 +229,7 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
 
     uint64_t base0 = 0;
     for (uint32_t s0 = 0; s0 < a.slots && base0 < ub; s0 += AT_CHUNK) {
-        if (s0) here = describe<PR_WARPS>(a, RT, s0, slots, usum);
+        if (s0) here = describe<PR_WARPS, PART>(a, RT, s0, slots, usum);
         const uint32_t tot = (uint32_t)here.units();
         const uint32_t nslots = min(AT_CHUNK, a.slots - s0);
         const uint64_t chunk_base = base0;
@@ -606,7 +623,12 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                 // A part: four dimensions of all rows after four, then M, MU, L of all rows.
                 float4 *part = reinterpret_cast<float4 *>(a.part + (2 * (uint64_t)blockIdx.x + (r.pa == 0 ? 1 : 0)) * Cfg::PART) + row;
                 if (mine && !dead) {
-                    const float quot = none ? 0.0f : ex2(finite_base(mu) - finite_base(m) - PR_W_LOG2) / l;
+                    float quot = none ? 0.0f : ex2(finite_base(mu) - finite_base(m) - PR_W_LOG2) / l;
+                    TailJoin tj{1.0f, 0.0f, none ? -INFINITY : m + __log2f(l)};
+                    if (PART == AT_TAIL && live && complete) {
+                        tj = tail_join(a, s, orow, tj.lse);
+                        quot *= tj.tail;
+                    }
 #pragma unroll 1
                     for (uint32_t d0 = 0; d0 < D; d0 += 32) {
                         float o[32] = {};
@@ -617,8 +639,15 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
 #pragma unroll
                             for (int i = 0; i < 32; i++) o[i] = __uint_as_float(w[i]);
                         }
-                        if (complete) {
-                            put(row, d0, o, quot);
+                        if (PART == AT_FRONT && complete) {
+                            if (live) put_front(a, orow * (uint64_t)D + d0, o, quot);
+                        } else if (complete) {
+                            if (PART == AT_TAIL && live && s.joins) {
+                                add_front(a, orow * (uint64_t)D + d0, o, quot, tj.front);
+                                put(row, d0, o, 1.0f);
+                            } else {
+                                put(row, d0, o, quot);
+                            }
                         } else if (live) {
 #pragma unroll
                             for (int i = 0; i < 8; i++)
@@ -626,8 +655,12 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                         }
                         __syncwarp();   // the next load is the whole warp's
                     }
-                    if (complete) put_out();
-                    if (live && complete && a.lse) a.lse[orow] = none ? -INFINITY : (m + __log2f(l)) * LN2;
+                    if (complete && PART != AT_FRONT) put_out();
+                    if (PART == AT_FRONT) {
+                        if (live && complete && T) a.front_lse[orow] = tj.lse;
+                    } else if (live && complete && a.lse) {
+                        a.lse[orow] = PART == AT_TAIL ? tj.lse * LN2 : none ? -INFINITY : (m + __log2f(l)) * LN2;
+                    }
                     if (live && !complete) part[D / 4 * RT] = make_float4(m, mu, l, 0.0f);
                 }
                 tc_fence_before();
@@ -663,8 +696,18 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                             MU = fmaxf(MU, st.y);
                         }
                         const bool nothing = M == -INFINITY && L == 0.0f;
-                        const float bu = finite_base(MU), quot = nothing ? 0.0f : ex2(bu - finite_base(M) - PR_W_LOG2) / L;
-                        if (jlive && gr == 0 && a.lse) a.lse[out_row(jr)] = nothing ? -INFINITY : (M + __log2f(L)) * LN2;
+                        const float bu = finite_base(MU);
+                        float quot = nothing ? 0.0f : ex2(bu - finite_base(M) - PR_W_LOG2) / L;
+                        TailJoin tj{1.0f, 0.0f, nothing ? -INFINITY : M + __log2f(L)};
+                        if (PART == AT_TAIL && jlive) {
+                            tj = tail_join(a, s, out_row(jr), tj.lse);
+                            quot *= tj.tail;
+                        }
+                        if (PART == AT_FRONT) {
+                            if (jlive && gr == 0) a.front_lse[out_row(jr)] = tj.lse;
+                        } else if (jlive && gr == 0 && a.lse) {
+                            a.lse[out_row(jr)] = PART == AT_TAIL ? tj.lse * LN2 : nothing ? -INFINITY : (M + __log2f(L)) * LN2;
+                        }
 #pragma unroll 1
                         for (uint32_t d0 = gr * 32; jlive && d0 < D; d0 += groups * 32) {
                             float o[32] = {};
@@ -681,12 +724,21 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
                                     o[4 * i + 2] += x[i].z * w, o[4 * i + 3] += x[i].w * w;
                                 }
                             }
-                            put(jr, d0, o, quot);
+                            if (PART == AT_FRONT) {
+                                put_front(a, out_row(jr) * D + d0, o, quot);
+                            } else if (PART == AT_TAIL && s.joins) {
+                                add_front(a, out_row(jr) * D + d0, o, quot, tj.front);
+                                put(jr, d0, o, 1.0f);
+                            } else {
+                                put(jr, d0, o, quot);
+                            }
                         }
-                        bar_rows();
-                        for (uint32_t i = tid; i < s.rows * (D / 8); i += 256) {
-                            const uint32_t row = i / (D / 8), e = i % (D / 8);
-                            reinterpret_cast<uint4 *>(a.out + out_row(row) * D)[e] = lds128(chunk_at(row, e));
+                        if (PART != AT_FRONT) {
+                            bar_rows();
+                            for (uint32_t i = tid; i < s.rows * (D / 8); i += 256) {
+                                const uint32_t row = i / (D / 8), e = i % (D / 8);
+                                reinterpret_cast<uint4 *>(a.out + out_row(row) * D)[e] = lds128(chunk_at(row, e));
+                            }
                         }
                         bar_rows();   // the rows' places are free for the next queries
                     }
@@ -715,11 +767,11 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
     if (warp == 12) tmem_dealloc(tm, 512);
 }
 
-template <uint32_t D>
-static int prompt_launch_d(const AttnArgs &a, cudaStream_t st) {
+template <uint32_t D, int PART>
+static int prompt_launch_part(const AttnArgs &a, cudaStream_t st) {
     DeviceInfo di;
     if (device_info(&di) != DGT_OK) return DGT_ERR_CUDA;
-    auto fn = k_kv_prompt<D>;
+    auto fn = k_kv_prompt<D, PART>;
     static std::atomic<uint64_t> ready;   // devices that allow the shared memory
     const uint64_t bit = di.device < 64 ? 1ull << di.device : 0;
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
@@ -733,13 +785,20 @@ static int prompt_launch_d(const AttnArgs &a, cudaStream_t st) {
                                                                                                       : DGT_ERR_CUDA;
 }
 
+template <uint32_t D>
+static int prompt_launch_d(const AttnArgs &a, AttnPart part, cudaStream_t st) {
+    return part == AT_ALL     ? prompt_launch_part<D, AT_ALL>(a, st)
+           : part == AT_FRONT ? prompt_launch_part<D, AT_FRONT>(a, st)
+                              : prompt_launch_part<D, AT_TAIL>(a, st);
+}
+
 uint32_t prompt_rows(uint32_t head_dim) { return head_dim <= 128 ? 256 : 128; }
 
-int prompt_launch(const AttnArgs &a, cudaStream_t st) {
+int prompt_launch(const AttnArgs &a, AttnPart part, cudaStream_t st) {
     switch (a.c.head_dim) {
-        case 64: return prompt_launch_d<64>(a, st);
-        case 128: return prompt_launch_d<128>(a, st);
-        default: return prompt_launch_d<256>(a, st);
+        case 64: return prompt_launch_d<64>(a, part, st);
+        case 128: return prompt_launch_d<128>(a, part, st);
+        default: return prompt_launch_d<256>(a, part, st);
     }
 }
 

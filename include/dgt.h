@@ -779,6 +779,35 @@ int dgt_kv_attention_ex(const dgt_kv_cache *cache, uint32_t layer, const dgt_hea
                         unsigned flags, void *stream);
 
 /*
+ * dgt_kv_attention_shared: dgt_kv_attention without a window, for sequences
+ * that share their first pages (forks of a prompt, beams, questions behind one
+ * document): a group's shared pages are read once for all its rows.  Groups
+ * are runs of neighbouring entries, group g those from d_groups[g] to
+ * d_groups[g + 1] (device int32 [groups + 1], 0 first, batch last; NULL: one
+ * group).  Its sequences begin with the first d_shared[g] tokens of sequence
+ * d_prefix[g] (device int32 [groups] each) and list the same whole pages for
+ * them, as dgt_kv_fork and dgt_kv_reserve leave them; what is behind the last
+ * whole page is each sequence's own.  Where they list others, which of them are
+ * read is unspecified.  Every new row is behind the shared pages; a sequence of
+ * length 0 has rows that see nothing.  A group whose prefix holds fewer than
+ * d_shared[g] tokens is an error, and so are entries of no group, both reported
+ * in d_status (their sequences then see only their pages behind none), and an
+ * entry with rows inside the shared pages (these rows: out 0, lse -inf).
+ * The precision is dgt_kv_attention's; the two parts are joined in fp32.  d_ws:
+ * dgt_kv_attention_shared_workspace_bytes(...) bytes, 256-byte aligned, zeroed
+ * before its first use, of whatever sizes later; calls that may overlap need
+ * one each.  groups <= 65536 (else DGT_ERR_SHAPE).  flags as in
+ * dgt_kv_attention_ex.
+ */
+size_t dgt_kv_attention_shared_workspace_bytes(const dgt_kv_cache *cache, uint32_t q_heads, uint32_t groups,
+                                               uint32_t batch, uint64_t tokens);
+int dgt_kv_attention_shared(const dgt_kv_cache *cache, uint32_t layer, const dgt_heads *q, uint64_t tokens,
+                            const int32_t *d_seqs, const int32_t *d_cu, uint32_t batch, const int32_t *d_prefix,
+                            const int32_t *d_shared, const int32_t *d_groups, uint32_t groups, float scale,
+                            uint16_t *d_out, float *d_lse, void *d_ws, size_t ws_bytes, int32_t *d_status,
+                            unsigned flags, void *stream);
+
+/*
  * Pages.  All in stream order, so a captured graph can hold them.
  *
  * dgt_kv_copy_pages: pages d_src[i] -> d_dst[i] (device int32 [n]) in every

@@ -111,3 +111,32 @@ def test_calls_want_cuda_tensors():
         dgt.route(x.long(), 2)
     with pytest.raises(ValueError):
         dgt.beam_select(x.view(2, 8, 8), torch.zeros(1, 2), 2)
+
+
+def test_shared_attention_refuses(lib):
+    def cache(**kw):
+        f = dict(layers=2, pages=8, kv_heads=4, head_dim=128, max_seqs=3, max_pages=4, k=P, v=P, k_scale=P, v_scale=P,
+                 refs=P, table=P, lens=P)
+        f.update(kw)
+        return C.byref(dgt.KvCacheStruct(*f.values()))
+
+    def heads(n, data=P, ts=None):
+        return C.byref(dgt.HeadsStruct(data, n * 128 if ts is None else ts, 128, n, 0))
+
+    need = int(lib.dgt_kv_attention_shared_workspace_bytes(cache(), 8, 2, 4, 4))
+    assert need > 0
+    size = lib.dgt_kv_attention_shared_workspace_bytes
+    assert size(None, 8, 1, 1, 1) == 0 and size(cache(), 2, 1, 1, 1) == 0 and size(cache(), 8, 0, 1, 1) == 0
+
+    def call(c=None, layer=0, q=heads(8), t=4, s=P, cu=None, b=4, prefix=P, shared=P, at=P, g=2, out=P, ws=P, n=need,
+             flags=0):
+        return lib.dgt_kv_attention_shared(c or cache(), layer, q, t, s, cu, b, prefix, shared, at, g, 1.0, out, None,
+                                           ws, n, None, flags, None)
+
+    assert call(c=cache(head_dim=96)) == SHAPE and call(c=cache(k=None)) == ARG and call(layer=2) == ARG
+    assert call(q=None) == ARG and call(s=None) == ARG and call(out=None) == ARG and call(out=P + 8) == ARG
+    assert call(prefix=None) == ARG and call(shared=None) == ARG and call(at=None) == ARG and call(g=0) == ARG
+    assert call(g=65537) == SHAPE and call(t=5) == ARG and call(t=(1 << 24) + 1, cu=P) == SHAPE
+    assert call(q=heads(6)) == SHAPE and call(q=heads(4 * 65)) == SHAPE and call(q=heads(8, ts=1025)) == ARG
+    assert call(ws=None) == ARG and call(ws=P + 64) == ARG and call(n=need - 1) == ARG
+    assert call(flags=1) == ARG and call(t=0, b=0) == 0
