@@ -654,21 +654,31 @@ def gemm_rebuild(W: R4, X, scratch=None, plan=None, Y32=None, Y=None, ws=None, s
 def _here(x, name):
     """x is on the current device, where its kernels are launched."""
     import torch
-    if not x.is_cuda or x.device.index != torch.cuda.current_device():
+    if x.get_device() < 0 or x.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name}: a tensor on the current CUDA device")
 
 
-def _float_rows(x, name, shape=None, bf16=False):
-    """(address, row stride, is fp32) of fp32 or bf16 rows [rows, n] or of one row [n]."""
-    import torch
-    f32 = x.dtype is torch.float32 and not bf16
-    if not (f32 or x.dtype is torch.bfloat16) or not x.is_cuda or x.dim() not in (1, 2):
-        raise ValueError(f"{name}: a CUDA {'' if bf16 else 'float32 or '}bfloat16 tensor [rows, n] or [n]")
-    if shape is not None and x.shape != shape:
-        raise ValueError(f"{name}: the shape of x")
-    if x.stride(-1) != 1 and x.shape[-1] > 1 and x.numel():
+def _empty(like, shape, dtype, stream):
+    """_new beside a tensor, without its cost where the current stream is meant."""
+    return like.new_empty(shape, dtype=dtype) if stream is None else _new(shape, dtype, like.device, stream)
+
+
+def _row_stride(x, name, shape, dev):
+    """The stride between the rows of x, [rows, n] or [n] as `shape` says, on device `dev`."""
+    if x.shape != shape or x.get_device() != dev:
+        raise ValueError(f"{name}: the shape and device of x")
+    if x.is_contiguous():
+        return shape[-1]
+    s = x.stride()
+    if s[-1] != 1 and shape[-1] > 1 and x.numel():
         raise ValueError(f"{name}: a contiguous last dimension")
-    return x.data_ptr(), x.stride(0) if x.dim() == 2 and x.shape[0] > 1 else x.shape[-1], f32
+    return s[0] if len(s) == 2 and shape[0] > 1 else shape[-1]
+
+
+def _vector(w, name, n, dtype, dev):
+    if w.dtype is not dtype or w.get_device() != dev or w.numel() != n or not w.is_contiguous():
+        raise ValueError(f"{name}: a contiguous CUDA {dtype} tensor of {n} elements on the same device")
+    return w.data_ptr()
 
 
 def block_norm(x, y=None, pre=None, post=None, gate=None, scale: float = 1.0, residual: float = 1.0,
@@ -681,46 +691,53 @@ def block_norm(x, y=None, pre=None, post=None, gate=None, scale: float = 1.0, re
     shape; None is left out (pre: then there is no h).  x_out: of x's type,
     may be x itself.  Returns (x', of x's type, and h bfloat16 or None)."""
     import torch
-    _here(x, "x")
-    px, sx, fx = _float_rows(x, "x")
-    n = x.shape[-1]
-    rows = x.shape[0] if x.dim() == 2 else 1
+    f32, bf16, shape, dtype, dev = torch.float32, torch.bfloat16, x.shape, x.dtype, x.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("x: a tensor on the current CUDA device")
+    if (dtype is not f32 and dtype is not bf16) or len(shape) not in (1, 2):
+        raise ValueError("x: a float32 or bfloat16 tensor [rows, n] or [n]")
+    n = shape[-1]
+    rows = shape[0] if len(shape) == 2 else 1
+    sx = _row_stride(x, "x", shape, dev)
     if x_out is None:
-        x_out = _new(x.shape, x.dtype, x.device, stream)
-    elif x_out.dtype != x.dtype:
-        raise ValueError("x_out: the type of x")
-    po, so, _ = _float_rows(x_out, "x_out", x.shape)
-    if x_out.dim() == 2 and rows > 1 and abs(so) < n:
-        raise ValueError("x_out: rows that do not overlap")
-    py, sy, fy = (0, 0, False) if y is None else _float_rows(y, "y", x.shape)
-    vec = lambda w, name: 0 if w is None else _bf16_vector(w, name, n)
-    pp, pq = vec(pre, "pre"), vec(post, "post")
-    ph = pg = sh = sg = 0
+        x_out, so = _empty(x, shape, dtype, stream), n
+    else:
+        so = _row_stride(x_out, "x_out", shape, dev)
+        if x_out.dtype is not dtype or (rows > 1 and abs(so) < n):
+            raise ValueError("x_out: the type of x, rows that do not overlap")
+    py = sy = ph = sh = pp = pq = pg = sg = fy = 0
+    if y is not None:
+        py, sy, fy = y.data_ptr(), _row_stride(y, "y", shape, dev), y.dtype is f32
+        if not fy and y.dtype is not bf16:
+            raise ValueError("y: float32 or bfloat16")
+    elif post is not None or gate is not None:
+        raise ValueError("post and gate: of y")
     if pre is not None:
+        pp = _vector(pre, "pre", n, bf16, dev)
         if h is None:
-            h = _new(x.shape, torch.bfloat16, x.device, stream)
-        ph, sh, _ = _float_rows(h, "h", x.shape, bf16=True)
-        if h.dim() == 2 and rows > 1 and abs(sh) < n:
-            raise ValueError("h: rows that do not overlap")
+            h, sh = _empty(x, shape, bf16, stream), n
+        else:
+            sh = _row_stride(h, "h", shape, dev)
+            if h.dtype is not bf16 or (rows > 1 and abs(sh) < n):
+                raise ValueError("h: bfloat16, rows that do not overlap")
+        ph = h.data_ptr()
     else:
         h = None
+    if post is not None:
+        pq = _vector(post, "post", n, bf16, dev)
     if gate is not None:
-        if gate.shape == x.shape and gate.dim() == 2:
-            pg, sg, _ = _float_rows(gate, "gate", x.shape, bf16=True)
+        if len(shape) == 2 and gate.shape == shape:
+            pg, sg = gate.data_ptr(), _row_stride(gate, "gate", shape, dev)
+            if gate.dtype is not bf16:
+                raise ValueError("gate: bfloat16")
         else:
-            pg = _bf16_vector(gate, "gate", n)
-    if (post is not None or gate is not None) and y is None:
-        raise ValueError("post and gate: of y")
-    _check(lib().dgt_block_norm(_pack_norm(px, po, py, ph, pp, pq, pg, sx, so, sy, sh, sg, fx, fy), rows, n, scale,
-                                residual, offset, eps, _stream_on(x, stream)), "dgt_block_norm")
+            pg = _vector(gate, "gate", n, bf16, dev)
+    rc = lib().dgt_block_norm(_pack_norm(x.data_ptr(), x_out.data_ptr(), py, ph, pp, pq, pg, sx, so, sy, sh, sg,
+                                         dtype is f32, fy), rows, n, scale, residual, offset, eps,
+                              _stream_on(x, stream))
+    if rc:
+        _check(rc, "dgt_block_norm")
     return x_out, h
-
-
-def _bf16_vector(w, name, n):
-    import torch
-    if w.dtype is not torch.bfloat16 or not w.is_cuda or w.numel() != n or not w.is_contiguous():
-        raise ValueError(f"{name}: a contiguous CUDA bfloat16 tensor [n]")
-    return w.data_ptr()
 
 
 def route(logits, topk: int, score: str = "softmax", bias=None, groups: int = 1, group_topk: int = 1,
@@ -733,34 +750,37 @@ def route(logits, topk: int, score: str = "softmax", bias=None, groups: int = 1,
     sum; scale: of the weights.  Returns (ids int32, p float32), both [tokens,
     topk], greatest first: what the expert products take."""
     import torch
-    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+    dtype, shape, dev = logits.dtype, logits.shape, logits.get_device()
+    f32 = dtype is torch.float32
+    if len(shape) != 2 or not (f32 or dtype is torch.bfloat16):
         raise ValueError("logits: a float32 or bfloat16 tensor [tokens, experts]")
-    _here(logits, "logits")
-    tokens, experts = logits.shape
-    if logits.stride(1) != 1 and experts > 1 and tokens:
-        raise ValueError("logits: a contiguous last dimension")
-    if score not in ("softmax", "sigmoid"):
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("logits: a tensor on the current CUDA device")
+    tokens, experts = shape
+    stride = _row_stride(logits, "logits", shape, dev)
+    if score != "softmax" and score != "sigmoid":
         raise ValueError("score: softmax or sigmoid")
-    if min(topk, groups, group_topk) < 1 or group_best not in (1, 2):
+    if topk < 1 or groups < 1 or group_topk < 1 or group_best not in (1, 2):
         raise ValueError("topk, groups, group_topk: at least 1; group_best: 1 or 2")
-    pb = 0
-    if bias is not None:
-        if bias.dtype is not torch.float32 or not bias.is_cuda or bias.numel() != experts or not bias.is_contiguous():
-            raise ValueError("bias: a contiguous CUDA float32 tensor [experts]")
-        pb = bias.data_ptr()
-    shape = (tokens, topk)
+    pb = 0 if bias is None else _vector(bias, "bias", experts, torch.float32, dev)
+    out = (tokens, topk)
     if ids is None:
-        ids = _new(shape, torch.int32, logits.device, stream)
-    elif ids.shape != shape:
+        ids = _empty(logits, out, torch.int32, stream)
+    elif ids.shape != out:
         raise ValueError("ids: [tokens, topk]")
+    else:
+        _vector(ids, "ids", tokens * topk, torch.int32, dev)
     if p is None:
-        p = _new(shape, torch.float32, logits.device, stream)
-    elif p.shape != shape or p.dtype is not torch.float32 or not p.is_cuda or not p.is_contiguous():
-        raise ValueError("p: a contiguous CUDA float32 tensor [tokens, topk]")
-    _check(lib().dgt_route(_pack_router(experts, topk, groups, group_topk, group_best, logits.dtype is torch.float32,
-                                        score == "sigmoid", bool(renorm), scale, 0, pb),
-                           logits.data_ptr(), logits.stride(0) if tokens > 1 else experts, tokens, _i32(ids, "ids"),
-                           p.data_ptr(), _stream_on(logits, stream)), "dgt_route")
+        p = _empty(logits, out, torch.float32, stream)
+    elif p.shape != out:
+        raise ValueError("p: [tokens, topk]")
+    else:
+        _vector(p, "p", tokens * topk, torch.float32, dev)
+    rc = lib().dgt_route(_pack_router(experts, topk, groups, group_topk, group_best, f32, score == "sigmoid",
+                                      bool(renorm), scale, 0, pb),
+                         logits.data_ptr(), stride, tokens, ids.data_ptr(), p.data_ptr(), _stream_on(logits, stream))
+    if rc:
+        _check(rc, "dgt_route")
     return ids, p
 
 
@@ -785,41 +805,47 @@ def beam_select(logits, scores, n: int, eos: int = -1, done=None, parent=None, t
     n], greatest total first, and done_out uint8 when done is given; -1, -1,
     -inf (and 0) where there are fewer candidates.  The outputs may be given."""
     import torch
-    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+    dtype, shape, dev = logits.dtype, logits.shape, logits.get_device()
+    f32 = dtype is torch.float32
+    if len(shape) != 2 or not (f32 or dtype is torch.bfloat16):
         raise ValueError("logits: a float32 or bfloat16 tensor [batch * beams, vocab]")
-    _here(logits, "logits")
-    rows, vocab = logits.shape
-    if logits.stride(1) != 1 and vocab > 1 and rows:
-        raise ValueError("logits: a contiguous last dimension")
-    if scores.dim() != 2 or scores.dtype is not torch.float32 or not scores.is_cuda or not scores.is_contiguous() or \
-            scores.numel() != rows:
-        raise ValueError("scores: a contiguous CUDA float32 tensor [batch, beams] of the logits' rows")
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("logits: a tensor on the current CUDA device")
+    rows, vocab = shape
+    stride = _row_stride(logits, "logits", shape, dev)
+    if scores.dim() != 2:
+        raise ValueError("scores: [batch, beams]")
+    ps = _vector(scores, "scores", rows, torch.float32, dev)
     batch, beams = scores.shape
     if n < 1:
         raise ValueError("n: at least 1")
-    if done is not None and (done.dtype is not torch.uint8 or not done.is_cuda or done.numel() != rows or
-                             not done.is_contiguous()):
-        raise ValueError("done: a contiguous CUDA uint8 tensor [batch, beams]")
+    pd = None if done is None else _vector(done, "done", rows, torch.uint8, dev)
     if done is None and done_out is not None:
         raise ValueError("done_out: with done")
-    outs = []
-    for x, dt, name in ((parent, torch.int32, "parent"), (token, torch.int32, "token"), (total, torch.float32, "total"),
-                        (done_out, torch.uint8, "done_out"))[:3 if done is None else 4]:
+    out = (batch, n)
+
+    def given(x, name, dt):
         if x is None:
-            x = _new((batch, n), dt, logits.device, stream)
-        elif x.shape != (batch, n) or x.dtype is not dt or not x.is_cuda or not x.is_contiguous():
-            raise ValueError(f"{name}: a contiguous CUDA tensor [batch, n] of its type")
-        outs.append(x)
+            return _empty(logits, out, dt, stream)
+        if x.shape != out:
+            raise ValueError(f"{name}: [batch, n]")
+        _vector(x, name, batch * n, dt, dev)
+        return x
+
+    parent, token = given(parent, "parent", torch.int32), given(token, "token", torch.int32)
+    total = given(total, "total", torch.float32)
+    if done is not None:
+        done_out = given(done_out, "done_out", torch.uint8)
     if ws is None:
         ws = _beam_workspace(batch, beams, vocab, n, logits.device, stream, True)
-    elif not (ws.is_cuda and ws.is_contiguous()):
-        raise ValueError("ws: a contiguous CUDA tensor (beam_workspace)")
-    _check(lib().dgt_beam_select(logits.data_ptr(), logits.dtype is torch.float32,
-                                 logits.stride(0) if rows > 1 else vocab, scores.data_ptr(), _ptr(done), eos, batch,
-                                 beams, vocab, n, outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(),
-                                 outs[3].data_ptr() if done is not None else None, ws.data_ptr(),
-                                 ws.numel() * ws.element_size(), _stream_on(logits, stream)), "dgt_beam_select")
-    return tuple(outs)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws: a contiguous CUDA tensor (beam_workspace) on the same device")
+    rc = lib().dgt_beam_select(logits.data_ptr(), f32, stride, ps, pd, eos, batch, beams, vocab, n, parent.data_ptr(),
+                               token.data_ptr(), total.data_ptr(), None if done is None else done_out.data_ptr(),
+                               ws.data_ptr(), ws.numel() * ws.element_size(), _stream_on(logits, stream))
+    if rc:
+        _check(rc, "dgt_beam_select")
+    return (parent, token, total) if done is None else (parent, token, total, done_out)
 
 
 # ---------------------------------------------------------------------------

@@ -3,13 +3,11 @@
 // over the beams b and the vocabulary v of an entry, in one pass over the
 // logits.
 //
-// A beam's row is cut into segments, a CTA each.  A CTA keeps, beside the
-// running maximum and sum of its part, the best n of its logits: within a row
-// the order of the totals is that of the logits.  The first tile gives a
-// threshold, the n-th of the threads' largest; what lies above it later is
-// rare and goes to a list in shared memory, which is cut back to its best n,
-// with a new threshold, when it is full.  The CTA that ends an entry's last
-// segment joins its parts.
+// A beam's row is cut into segments, a CTA each, whose warps go their own ways
+// through blocks of 1 KB: all they keep is the sum of e^l, and each block's
+// largest logit.  The CTA that ends an entry's last segment knows the sums, so
+// a block's largest total, and reads again only the blocks whose largest is
+// not below that of n others: a few dozen KB whatever the vocabulary.
 //
 // Totals are compared in fp64.  Sums of fp32 terms are off by up to 2^-18, so
 // where totals of two beams are closer than that and it matters, the entry's
@@ -26,11 +24,15 @@
 
 namespace dgt {
 
-constexpr uint32_t BM_THREADS = 256, BM_WARPS = BM_THREADS / 32;
+constexpr uint32_t BM_THREADS = 256, BM_WARPS = BM_THREADS / 32, BM_CTAS = 3;
 constexpr uint32_t BM_MAX_N = 64, BM_MAX_BEAMS = 64, BM_MAX_JOIN = 2048;   // the last: beams times n
-constexpr uint32_t BM_EPT = 32;                                   // elements of a tile a thread
-constexpr uint32_t BM_CAP = BM_MAX_N * BM_EPT + BM_MAX_N;         // of the list
+constexpr uint32_t BM_PIECES = 4;                                 // 16-byte pieces that a thread takes at a time
+constexpr uint32_t BM_BLOCK = 64;                                 // pieces of a block
+constexpr uint32_t BM_CAP = BM_MAX_N * BM_PIECES * 8 + BM_MAX_N;  // of the list
 constexpr float BM_LOG2E = 1.4426950408889634f;
+constexpr float BM_HUGE = 1e38f;
+constexpr float BM_OFF = 0x1p-17f;                                // totals of two beams may be off against each other
+constexpr float BM_GROW = 10.0f;                                  // logits above a thread's reference that its sum stands
 
 struct BeamArgs {
     const void *logits;
@@ -38,16 +40,14 @@ struct BeamArgs {
     const float *scores;
     const uint8_t *done;
     int32_t eos;
-    uint32_t batch, beams, vocab, n, segs, seg_pieces;
+    uint32_t batch, beams, vocab, n, segs, seg_blocks, row_blocks;
     int32_t *parent, *token;
     float *total;
     uint8_t *done_out;
     // workspace
-    int32_t *entry_count, *row_count;   // arrivals at an entry and at a row, zero between calls
-    float2 *seg_sum;                    // (maximum, sum) of a segment, and its best n
-    uint64_t *seg_keys;
-    double2 *row_sum;                   // (log of the sum, maximum) of a row, and its best n
-    uint64_t *row_keys;
+    int32_t *count;      // arrivals at an entry, zero between calls
+    float2 *sums;        // [rows, segs] (B, S) with sum e^l = S e^B
+    float *tops;         // [rows, row_blocks]
 };
 
 // A logit and its place as one whole number: greater for a greater logit, and
@@ -57,10 +57,8 @@ __device__ __forceinline__ uint32_t order_of(float v) {
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ uint64_t key_of(float v, uint32_t i) { return (uint64_t)order_of(v) << 32 | ~i; }
-__device__ __forceinline__ float key_value(uint64_t k) {
-    const uint32_t o = (uint32_t)(k >> 32);
-    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
-}
+__device__ __forceinline__ float value_of(uint32_t o) { return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o); }
+__device__ __forceinline__ float key_value(uint64_t k) { return value_of((uint32_t)(k >> 32)); }
 constexpr uint64_t BM_NONE = 0x007FFFFFull << 32 | 0xFFFFFFFFull;   // -inf at place 0: only greater keys are candidates
 
 __device__ __forceinline__ float beam_ex2(float x) {
@@ -75,15 +73,17 @@ __device__ __forceinline__ float beam_base(float m) { return m == -INFINITY ? 0.
 template <bool F32>
 struct BeamRow {
     static constexpr uint32_t V = F32 ? 4 : 8;
-    const uint8_t *base;   // the first piece, aligned
-    uint32_t off, vocab;   // elements of the first piece before the row
+    const uint8_t *base;        // the first piece, aligned
+    uint32_t off, vocab;        // elements of the first piece before the row
+    uint32_t first, inside;     // the first whole piece and how many there are
     __device__ __forceinline__ BeamRow(const void *logits, int64_t stride, uint64_t row, uint32_t vocab_) : vocab(vocab_) {
         const uintptr_t p = (uintptr_t)logits + row * stride * (F32 ? 4 : 2);
         base = (const uint8_t *)(p & ~(uintptr_t)15);
         off = (uint32_t)(p & 15) / (F32 ? 4 : 2);
+        first = off ? 1 : 0;
+        inside = (off + vocab) / V > first ? (off + vocab) / V - first : 0;
     }
     __device__ __forceinline__ uint32_t pieces() const { return (vocab + off + V - 1) / V; }
-    __device__ __forceinline__ bool whole(uint32_t c) const { return c * V >= off && (c + 1) * V <= off + vocab; }
     __device__ __forceinline__ uint4 edge(uint32_t c) const {
         uint32_t w[4];
 #pragma unroll
@@ -101,10 +101,12 @@ struct BeamRow {
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
+    // piece c, of none where c is not below end
     __device__ __forceinline__ uint4 load(uint32_t c, uint32_t end) const {
-        if (c >= end) return F32 ? make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u)
-                                 : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
-        return whole(c) ? ldg_stream16(base + (uint64_t)c * 16) : edge(c);
+        if (c - first < inside && c < end) return ldg_stream16(base + (uint64_t)c * 16);
+        if (c < end) return edge(c);
+        const uint32_t none = F32 ? 0xFF800000u : 0xFF80FF80u;
+        return make_uint4(none, none, none, none);
     }
     static __device__ __forceinline__ float value(const uint4 &x, uint32_t i) {
         const uint32_t w = F32 ? (i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w)
@@ -115,31 +117,53 @@ struct BeamRow {
     __device__ __forceinline__ uint32_t place(uint32_t c, uint32_t i) const { return c * V + i - off; }
 };
 
+constexpr uint32_t BM_MAX_BLOCKS = 1024;   // read again; more are collected row by row
+constexpr uint32_t BM_BEAM_SHIFT = 24;     // a candidate's place: its beam above the token
 struct BeamShared {
     union {
-        uint64_t list[BM_CAP];
-        struct {   // of an entry's join
-            double total[BM_MAX_JOIN], lse[BM_MAX_BEAMS];
-            uint32_t token[BM_MAX_JOIN];
-            float logit[BM_MAX_JOIN];
-            uint16_t beam[BM_MAX_JOIN];
-        };
+        uint64_t list[BM_CAP];   // of a row that is collected
+        uint32_t block[BM_MAX_BLOCKS];
+        uint64_t total[BM_MAX_JOIN];   // as whole numbers in order
     };
+    // the candidates of an entry, their order, and its beams
+    uint32_t place[BM_MAX_JOIN];
+    float logit[BM_MAX_JOIN];
+    uint16_t order[BM_MAX_JOIN];
+    double lse[BM_MAX_BEAMS];
+    float2 sum[BM_MAX_BEAMS];
+    float shift[BM_MAX_BEAMS];
     uint64_t best[BM_MAX_N];
     uint64_t top[BM_THREADS];
     float2 part[BM_WARPS];
     uint64_t thr;
-    uint32_t count, last, refine;
+    float warp_top[BM_WARPS];
+    uint32_t count, blocks, found, last, refine;
 };
 
-// The list's best n (fewer, when it has fewer) to its beginning, in order; the
-// n-th becomes the threshold.  The whole CTA.
+// The sum of (B, S) of lanes 0 .. count - 1; the same in every lane.
+__device__ __forceinline__ float2 join_sums(float2 p, uint32_t count) {
+    if (lane_id() >= count) p = make_float2(-INFINITY, 0.0f);
+    float B = p.x;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) B = fmaxf(B, __shfl_xor_sync(DGT_FULL, B, d));
+    float S = p.x == -INFINITY ? p.y : p.y * beam_ex2((p.x - B) * BM_LOG2E);   // of -inf 0, or NaN
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) S += __shfl_xor_sync(DGT_FULL, S, d);
+    return make_float2(B, S);
+}
+__device__ __forceinline__ double log_sum(float2 p) {
+    return p.y > 0.0f && p.y < INFINITY && fabsf(p.x) < INFINITY ? (double)p.x + log((double)p.y) : (double)INFINITY;
+}
+
+// The list's best n (fewer, when it has fewer) to its beginning, in order;
+// keys above the n-th are what counts from here on.  The whole CTA.
 __device__ __forceinline__ void cut_list(BeamShared &s, uint32_t n) {
     __syncthreads();
     const uint32_t count = s.count;
     for (uint32_t i = threadIdx.x; i < count; i += BM_THREADS) {
         const uint64_t k = s.list[i];
         uint32_t rank = 0;
+#pragma unroll 8
         for (uint32_t j = 0; j < count; j++) rank += s.list[j] > k;
         if (rank < n) s.best[rank] = k;
     }
@@ -148,13 +172,13 @@ __device__ __forceinline__ void cut_list(BeamShared &s, uint32_t n) {
     if (threadIdx.x < left) s.list[threadIdx.x] = s.best[threadIdx.x];
     if (threadIdx.x == 0) {
         s.count = left;
-        if (left == n) s.thr = s.best[n - 1];
+        if (left == n) s.thr = s.best[n - 1] + 1;
     }
     __syncthreads();
 }
 
-// A threshold that n keys at least reach, and n * BM_EPT at most: the n-th of
-// the threads' largest (0 counts as none).
+// A threshold that n keys at least reach, and n times a thread's keys at most:
+// the n-th of the threads' largest (0 counts as none).
 __device__ __forceinline__ uint64_t tile_threshold(BeamShared &s, uint64_t mine, uint32_t n) {
     __syncthreads();
     s.top[threadIdx.x] = mine;
@@ -170,116 +194,202 @@ __device__ __forceinline__ uint64_t tile_threshold(BeamShared &s, uint64_t mine,
     return s.top[0];
 }
 
-// The tile's elements from key `at` on to the list.
+// Pairs of fp32, two operations an instruction.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void both(f32x2 x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// The greatest of a piece, and of a thread's pieces (NaN aside).
 template <bool F32>
-__device__ __forceinline__ void push(BeamShared &s, const BeamRow<F32> &row, const uint4 (&x)[BM_EPT / BeamRow<F32>::V],
-                                     uint32_t c0, uint64_t at) {
+__device__ __forceinline__ float top_of(const uint4 &x) {
+    if (F32)
+        return fmaxf(fmaxf(__uint_as_float(x.x), __uint_as_float(x.y)), fmaxf(__uint_as_float(x.z), __uint_as_float(x.w)));
+    const uint32_t t = max_bf16x2(max_bf16x2(x.x, x.y), max_bf16x2(x.z, x.w));
+    return fmaxf(bf16lo(t), bf16hi(t));
+}
+template <bool F32>
+__device__ __forceinline__ float top_of(const uint4 (&x)[BM_PIECES]) {
+    if (F32) {
+        float t = -INFINITY;
+#pragma unroll
+        for (uint32_t u = 0; u < BM_PIECES; u++) t = fmaxf(t, top_of<F32>(x[u]));
+        return t;
+    }
+    uint32_t t = 0xFF80FF80u;
+#pragma unroll
+    for (uint32_t u = 0; u < BM_PIECES; u++)
+        t = max_bf16x2(t, max_bf16x2(max_bf16x2(x[u].x, x[u].y), max_bf16x2(x[u].z, x[u].w)));
+    return fmaxf(bf16lo(t), bf16hi(t));
+}
+
+// The elements of a thread's pieces from key `at` on to the list.
+template <bool F32>
+__device__ __forceinline__ void push(BeamShared &s, const BeamRow<F32> &row, const uint4 (&x)[BM_PIECES], uint32_t c0,
+                                     uint64_t at) {
     constexpr uint32_t V = BeamRow<F32>::V;
     const float v0 = key_value(at);
 #pragma unroll
-    for (uint32_t u = 0; u < BM_EPT / V; u++)
+    for (uint32_t u = 0; u < BM_PIECES; u++) {
+        if (!(top_of<F32>(x[u]) >= v0)) continue;
 #pragma unroll
         for (uint32_t i = 0; i < V; i++) {
             const float v = BeamRow<F32>::value(x[u], i);
             if (!(v >= v0)) continue;
             const uint64_t k = key_of(v, row.place(c0 + u * BM_THREADS + threadIdx.x, i));
-            if (k < at || k <= BM_NONE) continue;
+            if (k < at) continue;
             const uint32_t p = atomicAdd(&s.count, 1u);
             if (p < BM_CAP) s.list[p] = k;
         }
+    }
 }
 
+// The best n of a row to the list, whatever their order: a tile at a time,
+// each with a threshold of its own that bounds what it adds.
 template <bool F32>
-__device__ __forceinline__ float2 scan_segment(const BeamArgs &a, BeamShared &s, uint64_t r, uint32_t seg) {
-    constexpr uint32_t V = BeamRow<F32>::V, U = BM_EPT / V;
-    const BeamRow<F32> row(a.logits, a.stride, r, a.vocab);
-    const uint32_t c_begin = seg * a.seg_pieces, c_end = min(c_begin + a.seg_pieces, row.pieces());
-    float m = -INFINITY, sum = 0.0f, low = 0.0f;   // sum + low
-    if (threadIdx.x == 0) s.count = 0, s.thr = 0;
-    bool first = true;
-    for (uint32_t c0 = c_begin; c0 < c_end; c0 += BM_THREADS * U) {
-        uint4 x[U];
-#pragma unroll
-        for (uint32_t u = 0; u < U; u++) x[u] = row.load(c0 + u * BM_THREADS + threadIdx.x, c_end);
-        float top = -INFINITY;
-#pragma unroll
-        for (uint32_t u = 0; u < U; u++)
-#pragma unroll
-            for (uint32_t i = 0; i < V; i++) top = fmaxf(top, BeamRow<F32>::value(x[u], i));
-        const float mn = fmaxf(m, top), b = beam_base(mn);
-        float tile = 0.0f;
-#pragma unroll
-        for (uint32_t u = 0; u < U; u++)
-#pragma unroll
-            for (uint32_t i = 0; i < V; i++) tile += beam_ex2((BeamRow<F32>::value(x[u], i) - b) * BM_LOG2E);
-        const float f = m == mn ? 1.0f : beam_ex2((m - b) * BM_LOG2E);
-        sum *= f, low *= f;
-        m = mn;
-        // sum + low + tile, the error of the sum kept
-        const float t = sum + tile, back = t - sum;
-        low += (sum - (t - back)) + (tile - back);
-        sum = t;
-
-        if (first) {
-            // the thread's largest as a key: its lowest place
-            uint64_t mine = 0;
-            if (top > -INFINITY) {
-#pragma unroll
-                for (uint32_t u = 0; u < U; u++)
-#pragma unroll
-                    for (uint32_t i = 0; i < V; i++) {
-                        const uint64_t k = key_of(BeamRow<F32>::value(x[u], i), row.place(c0 + u * BM_THREADS + threadIdx.x, i));
-                        if (BeamRow<F32>::value(x[u], i) == top && k > mine) mine = k;
-                    }
-            }
-            const uint64_t at = tile_threshold(s, mine, a.n);
-            push<F32>(s, row, x, c0, at ? at : BM_NONE);
-            cut_list(s, a.n);
-            first = false;
-            continue;
-        }
-        // later places with the threshold's logit come behind it
-        const uint64_t thr = s.thr;
-        const float v0 = key_value(thr);
-        const bool above = thr ? top > v0 : top > -INFINITY;
-        if (!__syncthreads_or(above)) continue;
-        const uint32_t before = s.count;
-        __syncthreads();
-        if (above) push<F32>(s, row, x, c0, thr ? thr + 1 : BM_NONE);
-        __syncthreads();
-        if (s.count <= BM_CAP) continue;
-        // too many: cut what was there, and take the best of the tile alone
-        __syncthreads();
-        if (threadIdx.x == 0) s.count = before;
-        cut_list(s, a.n);
+__device__ __noinline__ void collect(BeamShared &s, const BeamRow<F32> &row, uint32_t n) {
+    constexpr uint32_t V = BeamRow<F32>::V;
+    const uint32_t end = row.pieces();
+    __syncthreads();
+    if (threadIdx.x == 0) s.count = 0, s.thr = BM_NONE + 1;
+    __syncthreads();
+    for (uint32_t c0 = 0; c0 < end; c0 += BM_THREADS * BM_PIECES) {
+        uint4 x[BM_PIECES];
         uint64_t mine = 0;
 #pragma unroll
-        for (uint32_t u = 0; u < U; u++)
+        for (uint32_t u = 0; u < BM_PIECES; u++) x[u] = row.load(c0 + u * BM_THREADS + threadIdx.x, end);
+#pragma unroll
+        for (uint32_t u = 0; u < BM_PIECES; u++)
 #pragma unroll
             for (uint32_t i = 0; i < V; i++) {
-                const uint64_t k = key_of(BeamRow<F32>::value(x[u], i), row.place(c0 + u * BM_THREADS + threadIdx.x, i));
-                if (BeamRow<F32>::value(x[u], i) == top && k > mine && k > BM_NONE) mine = k;
+                const float v = BeamRow<F32>::value(x[u], i);
+                if (v == v) mine = max(mine, key_of(v, row.place(c0 + u * BM_THREADS + threadIdx.x, i)));
             }
-        const uint64_t at = tile_threshold(s, mine, a.n);
-        const uint64_t from = at > s.thr ? at : s.thr + 1;
-        push<F32>(s, row, x, c0, from > BM_NONE ? from : BM_NONE);
-        cut_list(s, a.n);
+        const uint64_t from = s.thr;
+        if (!__syncthreads_or(mine >= from)) continue;
+        const uint64_t at = tile_threshold(s, mine, n);
+        push<F32>(s, row, x, c0, at > from ? at : from);
+        cut_list(s, n);
     }
-    cut_list(s, a.n);
+}
 
-    // the threads' maxima and sums to one
-    float mm = m;
+// sum 2^(v L - bl) over a thread's pieces, L = fl(log2 e).
+template <bool F32>
+__device__ __forceinline__ float sum_of(const uint4 (&x)[BM_PIECES], float bl) {
+    const f32x2 L = pair(BM_LOG2E, BM_LOG2E), B = pair(-bl, -bl);
+    f32x2 sum[2] = {0ull, 0ull};
+    auto add = [&](uint32_t i, float lo, float hi) {
+        float a, b;
+        both(fma2(pair(lo, hi), L, B), a, b);
+        sum[i & 1] = add2(sum[i & 1], pair(beam_ex2(a), beam_ex2(b)));
+    };
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(DGT_FULL, mm, d));
-    float ss = (sum + low) * beam_ex2((m - beam_base(mm)) * BM_LOG2E);
+    for (uint32_t u = 0; u < BM_PIECES; u++) {
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        if (F32) {
+            add(0, __uint_as_float(w[0]), __uint_as_float(w[1]));
+            add(1, __uint_as_float(w[2]), __uint_as_float(w[3]));
+        } else {
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) ss += __shfl_xor_sync(DGT_FULL, ss, d);
-    if (lane_id() == 0) s.part[threadIdx.x >> 5] = make_float2(mm, ss);
+            for (uint32_t i = 0; i < 4; i++) add(i, bf16lo(w[i]), bf16hi(w[i]));
+        }
+    }
+    float a, b;
+    both(add2(sum[0], sum[1]), a, b);
+    return a + b;
+}
+
+// The same where v L may be out of range: sum e^(v - base).
+template <bool F32>
+__device__ __forceinline__ float sum_of_huge(const uint4 (&x)[BM_PIECES], float base) {
+    float sum = 0.0f;
+#pragma unroll
+    for (uint32_t u = 0; u < BM_PIECES; u++)
+#pragma unroll
+        for (uint32_t i = 0; i < BeamRow<F32>::V; i++) sum += beam_ex2((BeamRow<F32>::value(x[u], i) - base) * BM_LOG2E);
+    return sum;
+}
+
+// A segment of a row: its blocks' largest logits to a.tops, and (B, S) with
+// sum e^v = S e^B.
+template <bool F32>
+__device__ __forceinline__ float2 scan_segment(const BeamArgs &a, BeamShared &s, const BeamRow<F32> &row, uint64_t r,
+                                               uint32_t seg, uint4 (&x)[BM_PIECES]) {
+    constexpr uint32_t TWO = BM_PIECES * 32 / BM_BLOCK;   // blocks of a warp at a time
+    const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, pieces = row.pieces();
+    const uint32_t end = min((seg + 1) * a.seg_blocks, (pieces + BM_BLOCK - 1) / BM_BLOCK);
+    float *tops = a.tops + r * a.row_blocks;
+    float base = -INFINITY, bl = 0.0f, sum = 0.0f, low = 0.0f;   // the sum is sum + low
+    bool huge = false;
+    for (uint32_t b = seg * a.seg_blocks + warp * TWO; b < end; b += BM_WARPS * TWO) {
+        uint4 next[BM_PIECES];
+        const uint32_t nb = b + BM_WARPS * TWO;
+        if (nb < end) {
+#pragma unroll
+            for (uint32_t u = 0; u < BM_PIECES; u++) next[u] = row.load(nb * BM_BLOCK + u * 32 + lane, pieces);
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (uint32_t h = 0; h < TWO; h++) {
+            float t = -INFINITY;
+#pragma unroll
+            for (uint32_t u = 0; u < BM_BLOCK / 32; u++) t = fmaxf(t, top_of<F32>(x[h * (BM_BLOCK / 32) + u]));
+            top = fmaxf(top, t);
+            const uint32_t all = __reduce_max_sync(DGT_FULL, order_of(t));
+            if (lane == h && b + h < end) tops[b + h] = value_of(all);
+        }
+        if (top > base + BM_GROW || (base == -INFINITY && top > base)) {
+            const bool big = fabsf(top) > BM_HUGE;
+            const float to = big ? 0.0f : top * BM_LOG2E;
+            // nothing is left of a sum that is so far below
+            const float f = big || huge || base == -INFINITY ? 0.0f : beam_ex2(bl - to);
+            sum *= f, low *= f;
+            base = top, bl = to, huge = big;
+        }
+        const float tile = huge ? sum_of_huge<F32>(x, base) : sum_of<F32>(x, bl);
+        const float t = sum + tile, back = t - sum;   // what the sum loses goes to low
+        low += (sum - (t - back)) + (tile - back);
+        sum = t;
+        if (nb < end) {
+#pragma unroll
+            for (uint32_t u = 0; u < BM_PIECES; u++) x[u] = next[u];
+        }
+    }
+    // what a row that ends early leaves of its last block's place
+    const uint32_t late = (pieces + BM_BLOCK - 1) / BM_BLOCK + threadIdx.x;
+    if (late >= seg * a.seg_blocks && late < min((seg + 1) * a.seg_blocks, a.row_blocks)) tops[late] = -INFINITY;
+    // the threads' sums to one
+    float B = base;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) B = fmaxf(B, __shfl_xor_sync(DGT_FULL, B, d));
+    float S = sum + low;
+    if (base > -INFINITY) {
+        if (!huge) S *= beam_ex2(fmaf(-base, BM_LOG2E, bl));   // what rounding base L to bl left out
+        S *= beam_ex2((base - B) * BM_LOG2E);
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) S += __shfl_xor_sync(DGT_FULL, S, d);
+    if (lane == 0) s.part[warp] = make_float2(B, S);
     __syncthreads();
-    float M = -INFINITY, S = 0.0f;
-    for (uint32_t w = 0; w < BM_WARPS; w++) M = fmaxf(M, s.part[w].x);
-    for (uint32_t w = 0; w < BM_WARPS; w++) S += s.part[w].y * beam_ex2((s.part[w].x - beam_base(M)) * BM_LOG2E);
-    return make_float2(M, S);
+    return join_sums(s.part[lane % BM_WARPS], BM_WARPS);
 }
 
 // This CTA's arrival at a counter: true for the last of `all`, which then sees
@@ -300,26 +410,16 @@ __device__ __forceinline__ bool arrive(BeamShared &s, int32_t *count, uint32_t a
     return last;
 }
 
-// The segments of a row to one: its best n to s.list, its sum.
-__device__ __forceinline__ void join_row(const BeamArgs &a, BeamShared &s, uint64_t r, float &M, double &S) {
-    if (threadIdx.x == 0) s.count = 0;
-    __syncthreads();
-    for (uint32_t i = threadIdx.x; i < a.segs * a.n; i += BM_THREADS) {
-        const uint64_t k = __ldcg(&a.seg_keys[r * a.segs * a.n + i]);
-        if (k) s.list[atomicAdd(&s.count, 1u)] = k;
+// The (B, S) of a row's segments to one, by a warp.
+__device__ __forceinline__ float2 row_sums(const BeamArgs &a, uint64_t r) {
+    float2 p = make_float2(-INFINITY, 0.0f);
+    for (uint32_t g = 0; g < a.segs; g += 32) {
+        float2 x = make_float2(-INFINITY, 0.0f);
+        if (g + lane_id() < a.segs) x = __ldcg(&a.sums[r * a.segs + g + lane_id()]);
+        x = join_sums(x, 32);
+        p = g ? join_sums(lane_id() == 0 ? p : x, 2) : x;
     }
-    cut_list(s, a.n);
-    M = -INFINITY;
-    for (uint32_t g = lane_id(); g < a.segs; g += 32) M = fmaxf(M, __ldcg(&a.seg_sum[r * a.segs + g]).x);
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(DGT_FULL, M, d));
-    S = 0.0;
-    for (uint32_t g = lane_id(); g < a.segs; g += 32) {
-        const float2 p = __ldcg(&a.seg_sum[r * a.segs + g]);
-        S += (double)(p.y * beam_ex2((p.x - beam_base(M)) * BM_LOG2E));
-    }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) S += __shfl_xor_sync(DGT_FULL, S, d);
+    return p;
 }
 
 // log sum e^l of a row: e^(l - M) = 2^(k / 32) e^r with the table of 2^(j / 32)
@@ -369,74 +469,181 @@ __device__ __forceinline__ double sum_again(const BeamArgs &a, uint64_t r, float
     return (double)M + log((double)high * 4.0 + (double)low * 0x1p-62);
 }
 
-// A total as a whole number in the same order (0: none).
-__device__ __forceinline__ uint64_t order_of(double t) {
-    const uint64_t b = (uint64_t)__double_as_longlong(t + 0.0);
-    return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+// The candidates of an entry from the blocks that can hold one.  False where
+// they are too many.  A block's largest total is in fp32, off by less than the
+// slack; a threshold that n blocks reach at least is the least of the warps'
+// k-th largest of their threads' largest, k warps >= n.
+template <bool F32>
+__device__ __forceinline__ bool read_again(const BeamArgs &a, BeamShared &s, uint64_t r0) {
+    constexpr uint32_t V = BeamRow<F32>::V, PIECES = BM_BLOCK / 32, KEEP = 16, TOGETHER = 4;
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t all = a.beams * a.row_blocks;
+    const float inv = 1.0f / (float)a.row_blocks;
+    const float *tops = a.tops + r0 * a.row_blocks;
+    auto beam_of = [&](uint32_t i) {   // i / row_blocks, i below 2^23
+        const uint32_t q = (uint32_t)((float)i * inv);
+        return q * a.row_blocks > i ? q - 1 : (q + 1) * a.row_blocks <= i ? q + 1 : q;
+    };
+    // -inf for a beam that offers nothing, whose tops were not written
+    auto total_of = [&](uint32_t i, float top) {
+        const float shift = s.shift[beam_of(i)];
+        return shift > -INFINITY ? top + shift : -INFINITY;
+    };
+    // neighbouring blocks go to different warps, a thread's first KEEP stay in registers
+    const uint32_t mine0 = lane * BM_WARPS + warp;
+    float t[KEEP], top = -INFINITY;
+#pragma unroll
+    for (uint32_t j = 0; j < KEEP; j++) t[j] = mine0 + j * BM_THREADS < all ? __ldcg(&tops[mine0 + j * BM_THREADS]) : -INFINITY;
+#pragma unroll
+    for (uint32_t j = 0; j < KEEP; j++) {
+        if (mine0 + j * BM_THREADS < all) t[j] = total_of(mine0 + j * BM_THREADS, t[j]);
+        top = fmaxf(top, t[j]);
+    }
+#pragma unroll 4
+    for (uint32_t i = mine0 + KEEP * BM_THREADS; i < all; i += BM_THREADS) top = fmaxf(top, total_of(i, __ldcg(&tops[i])));
+    uint32_t mine = order_of(top), kth = 0;
+    for (uint32_t k = 0; k < (a.n + BM_WARPS - 1) / BM_WARPS; k++) {
+        kth = __reduce_max_sync(DGT_FULL, mine);
+        if (lane == __ffs(__ballot_sync(DGT_FULL, mine == kth)) - 1) mine = 0;
+    }
+    uint32_t far = 0;
+    for (uint32_t b = lane; b < a.beams; b += 32)
+        if (s.shift[b] > -INFINITY) far = max(far, __float_as_uint(fabsf(s.shift[b])));
+    far = __reduce_max_sync(DGT_FULL, far);
+    if (lane == 0) s.warp_top[warp] = value_of(kth);
+    __syncthreads();
+    float from = s.warp_top[0];
+#pragma unroll
+    for (uint32_t w = 1; w < BM_WARPS; w++) from = fminf(from, s.warp_top[w]);
+    from -= BM_OFF + 0x1p-20f * (__uint_as_float(far) + (from > -INFINITY ? fabsf(from) : 0.0f));
+    auto take = [&](uint32_t i, float t) {
+        if (!(t >= from && t > -INFINITY)) return;
+        const uint32_t p = atomicAdd(&s.blocks, 1u);
+        if (p < BM_MAX_BLOCKS) s.block[p] = i;
+    };
+    if (top >= from) {
+#pragma unroll
+        for (uint32_t j = 0; j < KEEP; j++) take(mine0 + j * BM_THREADS, t[j]);
+        for (uint32_t i = mine0 + KEEP * BM_THREADS; i < all; i += BM_THREADS) take(i, total_of(i, __ldcg(&tops[i])));
+    }
+    __syncthreads();
+    const uint32_t blocks = s.blocks;
+    if (blocks > BM_MAX_BLOCKS) return false;
+    // TOGETHER blocks of a warp travel at a time
+    for (uint32_t i0 = warp; i0 < blocks; i0 += BM_WARPS * TOGETHER) {
+        uint4 x[TOGETHER][PIECES];
+#pragma unroll
+        for (uint32_t g = 0; g < TOGETHER; g++) {
+            const uint32_t i = s.block[min(i0 + g * BM_WARPS, blocks - 1)], beam = beam_of(i);
+            const BeamRow<F32> row(a.logits, a.stride, r0 + beam, a.vocab);
+#pragma unroll
+            for (uint32_t u = 0; u < PIECES; u++) x[g][u] = row.load((i - beam * a.row_blocks) * BM_BLOCK + u * 32 + lane, row.pieces());
+        }
+#pragma unroll
+        for (uint32_t g = 0; g < TOGETHER; g++) {
+            if (i0 + g * BM_WARPS >= blocks) break;
+            const uint32_t i = s.block[i0 + g * BM_WARPS], beam = beam_of(i);
+            const BeamRow<F32> row(a.logits, a.stride, r0 + beam, a.vocab);
+            const float shift = s.shift[beam];
+#pragma unroll
+            for (uint32_t u = 0; u < PIECES; u++) {
+                if (!(top_of<F32>(x[g][u]) + shift >= from)) continue;
+#pragma unroll
+                for (uint32_t j = 0; j < V; j++) {
+                    const float v = BeamRow<F32>::value(x[g][u], j);
+                    if (!(v + shift >= from && v > -INFINITY)) continue;
+                    const uint32_t p = atomicAdd(&s.found, 1u);
+                    if (p < BM_MAX_JOIN) {
+                        s.place[p] = beam << BM_BEAM_SHIFT | row.place((i - beam * a.row_blocks) * BM_BLOCK + u * 32 + lane, j);
+                        s.logit[p] = v;
+                    }
+                }
+            }
+        }
+    }
+    __syncthreads();
+    return s.found + a.beams <= BM_MAX_JOIN;   // beams at their end come to these
 }
 
+// The beams of an entry to its best n.
 template <bool F32>
 __device__ __forceinline__ void join_entry(const BeamArgs &a, BeamShared &s, uint32_t entry) {
-    const uint32_t tid = threadIdx.x, n = a.n;
+    const uint32_t tid = threadIdx.x, lane = tid & 31, n = a.n;
     const uint64_t r0 = (uint64_t)entry * a.beams;
-    auto reads = [&](uint32_t b) { return fabsf(a.scores[r0 + b]) < INFINITY && !(a.done && a.done[r0 + b]); };
-    if (tid == 0) s.count = 0, s.refine = 0;
+    if (tid == 0) s.blocks = 0, s.found = 0, s.refine = 0;
     // a beam without a score, without a finite sum, or at its end offers nothing of its row
-    for (uint32_t b = tid; b < a.beams; b += BM_THREADS)
-        s.lse[b] = reads(b) ? __ldcg(&a.row_sum[r0 + b]).x : (double)INFINITY;
+    for (uint32_t b = tid / 32; b < a.beams; b += BM_WARPS) {
+        float2 p = make_float2(-INFINITY, 0.0f);
+        if (fabsf(a.scores[r0 + b]) < INFINITY && !(a.done && a.done[r0 + b])) p = row_sums(a, r0 + b);
+        if (lane == 0) s.sum[b] = p;
+    }
     __syncthreads();
-    constexpr double OFF = 1.0 / (1 << 18);
-    auto candidate = [&](uint32_t c, double &t, uint32_t &b, uint32_t &v, float &x) {
-        b = c / n;
-        const double lse = s.lse[b];
-        if (!(fabs(lse) < (double)INFINITY)) return false;
-        const uint64_t k = __ldcg(&a.row_keys[r0 * n + c]);
-        v = ~(uint32_t)k;
-        x = key_value(k);
-        t = (double)a.scores[r0 + b] + ((double)x - lse);
-        return k != 0;
-    };
-    // the n-th of the threads' largest leaves out most of what cannot be among the best n
-    uint64_t mine = 0;
-    double t;
-    uint32_t b, v;
-    float x;
-    for (uint32_t c = tid; c < a.beams * n; c += BM_THREADS)
-        if (candidate(c, t, b, v, x)) mine = max(mine, order_of(t));
-    mine = mine ? (mine & ~255ull) | (255u - tid) : 0;   // distinct
-    const uint64_t at = tile_threshold(s, mine, n) & ~255ull;
-    double from = -INFINITY;
-    if (at) from = __longlong_as_double((int64_t)(at & 0x8000000000000000ull ? at ^ 0x8000000000000000ull : ~at)) - 2 * OFF;
-    auto add = [&](double t, uint32_t b, uint32_t v, float x) {
-        const uint32_t p = atomicAdd(&s.count, 1u);
-        s.total[p] = t, s.beam[p] = (uint16_t)b, s.token[p] = v, s.logit[p] = x;
-    };
-    for (uint32_t c = tid; c < a.beams * n; c += BM_THREADS)
-        if (candidate(c, t, b, v, x) && t >= from) add(t, b, v, x);
-    // a beam at its end offers its end token at its own score
-    if (a.done && tid < a.beams && a.done[r0 + tid] && fabsf(a.scores[r0 + tid]) < INFINITY)
-        add((double)a.scores[r0 + tid], tid, (uint32_t)a.eos, 0.0f);
+    // fp64 is slow here: a lane for each beam, not a warp
+    if (tid < a.beams) {
+        const double lse = log_sum(s.sum[tid]);
+        s.lse[tid] = lse;
+        s.shift[tid] = lse < (double)INFINITY ? (float)((double)a.scores[r0 + tid] - lse) : -INFINITY;
+    }
     __syncthreads();
-    const uint32_t count = s.count;
-    auto rank_of = [&](uint32_t i, bool &close) {
-        const double ti = s.total[i];
-        const uint32_t bi = s.beam[i], vi = s.token[i];
-        uint32_t rank = 0;
-        for (uint32_t j = 0; j < count; j++) {
-            const double tj = s.total[j];
-            const uint32_t bj = s.beam[j];
-            rank += tj > ti || (tj == ti && (bj < bi || (bj == bi && s.token[j] < vi)));
-            close |= bj != bi && fabs(tj - ti) <= 2 * OFF;
+    if (!read_again<F32>(a, s, r0)) {
+        // too many: the best n of each row
+        __syncthreads();
+        if (tid == 0) s.found = 0;
+        for (uint32_t b = 0; b < a.beams; b++) {
+            __syncthreads();
+            if (!(s.lse[b] < (double)INFINITY)) continue;
+            const BeamRow<F32> row(a.logits, a.stride, r0 + b, a.vocab);
+            collect<F32>(s, row, n);
+            const uint32_t at = s.found, count = s.count;
+            __syncthreads();
+            if (tid < count) s.place[at + tid] = b << BM_BEAM_SHIFT | ~(uint32_t)s.list[tid], s.logit[at + tid] = key_value(s.list[tid]);
+            if (tid == 0) s.found = at + count;
         }
-        return rank;
+        __syncthreads();
+    }
+    // a beam at its end offers its end token at its own score
+    if (a.done && tid < a.beams && a.done[r0 + tid] && fabsf(a.scores[r0 + tid]) < INFINITY) {
+        const uint32_t p = atomicAdd(&s.found, 1u);
+        s.place[p] = tid << BM_BEAM_SHIFT | (uint32_t)a.eos, s.logit[p] = 0.0f;
+    }
+    __syncthreads();
+    const uint32_t count = s.found;
+    auto total_of = [&](uint32_t i) {
+        const uint32_t b = s.place[i] >> BM_BEAM_SHIFT;
+        const double score = (double)a.scores[r0 + b], lse = s.lse[b];
+        return lse < (double)INFINITY ? score + ((double)s.logit[i] - lse) : score;
     };
-    for (uint32_t i = tid; i < count; i += BM_THREADS) {
-        bool close = false;
-        if (rank_of(i, close) < n && close) s.refine = 1;
+    auto sort = [&]() {
+        for (uint32_t i = tid; i < count; i += BM_THREADS) {
+            const uint64_t bits = (uint64_t)__double_as_longlong(total_of(i) + 0.0);
+            s.total[i] = bits ^ ((uint64_t)((int64_t)bits >> 63) | 0x8000000000000000ull);
+        }
+        __syncthreads();
+        for (uint32_t i = tid; i < count; i += BM_THREADS) {
+            const uint64_t t = s.total[i];
+            const uint32_t at = s.place[i];
+            uint32_t rank = 0;
+#pragma unroll 4
+            for (uint32_t j = 0; j < count; j++) {
+                const uint64_t o = s.total[j];
+                rank += o > t || (o == t && s.place[j] < at);
+            }
+            s.order[rank] = (uint16_t)i;
+        }
+        __syncthreads();
+    };
+    sort();
+    // Totals of two beams that may be the other way round: then two neighbours in this order are, and one of them is
+    // not further behind the n-th.
+    const double last = count > n ? total_of(s.order[n - 1]) - (double)BM_OFF : -INFINITY;
+    for (uint32_t i = tid; i + 1 < count; i += BM_THREADS) {
+        const uint32_t p = s.order[i], q = s.order[i + 1];
+        if (s.place[p] >> BM_BEAM_SHIFT == s.place[q] >> BM_BEAM_SHIFT) continue;
+        const double t = total_of(q);
+        if (t >= last && total_of(p) - t <= (double)BM_OFF) s.refine = 1;
     }
     __syncthreads();
     if (s.refine) {
-        // totals of two beams that may be the other way round
         float2 *table = reinterpret_cast<float2 *>(s.top);
         uint64_t(*scratch)[2] = reinterpret_cast<uint64_t(*)[2]>(s.top + 32);
         if (tid < 32) {
@@ -445,83 +652,79 @@ __device__ __forceinline__ void join_entry(const BeamArgs &a, BeamShared &s, uin
         }
         __syncthreads();
         for (uint32_t beam = 0; beam < a.beams; beam++) {
-            if (!(fabs(s.lse[beam]) < (double)INFINITY)) continue;
-            const double lse = sum_again<F32>(a, r0 + beam, (float)__ldcg(&a.row_sum[r0 + beam]).y, scratch, table);
-            for (uint32_t i = tid; i < count; i += BM_THREADS)
-                if (s.beam[i] == beam) s.total[i] = (double)a.scores[r0 + beam] + ((double)s.logit[i] - lse);
+            if (!(s.lse[beam] < (double)INFINITY)) continue;
+            float M = -INFINITY;
+            for (uint32_t i = lane; i < a.row_blocks; i += 32) M = fmaxf(M, __ldcg(&a.tops[(r0 + beam) * a.row_blocks + i]));
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(DGT_FULL, M, d));
+            const double lse = sum_again<F32>(a, r0 + beam, M, scratch, table);
+            __syncthreads();
+            if (tid == 0) s.lse[beam] = lse;
         }
         __syncthreads();
+        sort();
     }
     const uint64_t o = (uint64_t)entry * n;
-    for (uint32_t i = tid; i < count; i += BM_THREADS) {
-        bool close;
-        const uint32_t rank = rank_of(i, close);
-        if (rank >= n) continue;
-        a.parent[o + rank] = (int32_t)s.beam[i];
-        a.token[o + rank] = (int32_t)s.token[i];
-        a.total[o + rank] = (float)s.total[i];
-        if (a.done_out) a.done_out[o + rank] = a.done[r0 + s.beam[i]] || (int32_t)s.token[i] == a.eos;
-    }
-    for (uint32_t i = count + tid; i < n; i += BM_THREADS) {
-        a.parent[o + i] = -1;
-        a.token[o + i] = -1;
-        a.total[o + i] = -INFINITY;
-        if (a.done_out) a.done_out[o + i] = 0;
+    for (uint32_t i = tid; i < n; i += BM_THREADS) {
+        uint32_t at = 0xFFFFFFFFu;
+        float total = -INFINITY;
+        if (i < count) at = s.place[s.order[i]], total = (float)total_of(s.order[i]);
+        const int32_t beam = at == 0xFFFFFFFFu ? -1 : (int32_t)(at >> BM_BEAM_SHIFT);
+        const int32_t token = at == 0xFFFFFFFFu ? -1 : (int32_t)(at & ((1u << BM_BEAM_SHIFT) - 1));
+        a.parent[o + i] = beam;
+        a.token[o + i] = token;
+        a.total[o + i] = total;
+        if (a.done_out) a.done_out[o + i] = beam >= 0 && (a.done[r0 + beam] || token == a.eos);
     }
 }
 
 template <bool F32>
-__global__ void __launch_bounds__(BM_THREADS) k_beam_select(BeamArgs a) {
+__global__ void __launch_bounds__(BM_THREADS, BM_CTAS) k_beam_select(BeamArgs a) {
     __shared__ BeamShared s;
     pdl_trigger();
-    pdl_wait();
     const uint32_t seg = blockIdx.x % a.segs;
     const uint64_t r = blockIdx.x / a.segs;
     const uint32_t entry = (uint32_t)(r / a.beams);
-    if (fabsf(a.scores[r]) < INFINITY && !(a.done && a.done[r])) {
-        const float2 p = scan_segment<F32>(a, s, r, seg);
-        float M = p.x;
-        double S = p.y;
-        if (a.segs > 1) {
-            const uint64_t at = r * a.segs + seg;
-            if (threadIdx.x == 0) a.seg_sum[at] = p;
-            for (uint32_t i = threadIdx.x; i < a.n; i += BM_THREADS) a.seg_keys[at * a.n + i] = i < s.count ? s.list[i] : 0ull;
-            if (!arrive(s, &a.row_count[r], a.segs)) return;
-            join_row(a, s, r, M, S);
-        }
-        if (threadIdx.x == 0) a.row_sum[r] = make_double2((double)M + log(S), (double)M);
-        for (uint32_t i = threadIdx.x; i < a.n; i += BM_THREADS) a.row_keys[r * a.n + i] = i < s.count ? s.list[i] : 0ull;
-    } else if (seg) {
-        return;
+    const BeamRow<F32> row(a.logits, a.stride, r, a.vocab);
+    pdl_wait();
+    // the score travels with the first logits
+    const bool read = fabsf(a.scores[r]) < INFINITY && !(a.done && a.done[r]);
+    uint4 x[BM_PIECES];
+    const uint32_t c0 = (seg * a.seg_blocks + (threadIdx.x >> 5) * (BM_PIECES * 32 / BM_BLOCK)) * BM_BLOCK + lane_id();
+    const uint32_t end = min((seg + 1) * a.seg_blocks * BM_BLOCK, row.pieces());
+#pragma unroll
+    for (uint32_t u = 0; u < BM_PIECES; u++) x[u] = row.load(c0 + u * 32, end);
+    if (read) {
+        const float2 p = scan_segment<F32>(a, s, row, r, seg, x);
+        if (threadIdx.x == 0) a.sums[r * a.segs + seg] = p;
     }
-    if (arrive(s, &a.entry_count[entry], a.beams)) join_entry<F32>(a, s, entry);
+    if (arrive(s, &a.count[entry], a.beams * a.segs)) join_entry<F32>(a, s, entry);
 }
 
-// Segments of a row: as many as fill the SMs with four CTAs each, of 4096
-// elements at least; their best n fit the list.
-static uint32_t beam_segments(uint64_t rows, uint32_t vocab, uint32_t n, uint32_t sms) {
-    const uint64_t want = (4ull * sms) / rows, most = (vocab + 4095) / 4096, fit = 2048 / n;
-    const uint64_t s = std::min(std::min(want, most), fit);
-    return (uint32_t)std::max<uint64_t>(s, 1);
+// Segments of a row: as many as fill the SMs with BM_CTAS each, of a turn at
+// least.
+constexpr uint32_t BM_TURN = BM_WARPS * BM_PIECES * 32 / BM_BLOCK;   // blocks that a CTA takes at a time
+static uint32_t beam_segments(uint64_t rows, uint32_t blocks, uint32_t sms) {
+    const uint64_t want = ((uint64_t)BM_CTAS * sms) / rows, most = blocks / BM_TURN;
+    return (uint32_t)std::max<uint64_t>(std::min<uint64_t>(std::min(want, most), 256), 1);
+}
+static uint32_t beam_blocks(uint32_t vocab, uint32_t V) {
+    const uint32_t pieces = (vocab + 2 * V - 2) / V;   // a row that begins inside a piece may touch one more
+    return (pieces + BM_BLOCK - 1) / BM_BLOCK;
 }
 static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Where the parts of a workspace begin; the last is its size.  The counters
-// have room for every call's, so that one workspace serves all sizes: an entry
-// each, and a row each where rows have segments, which are 2 BM_MAX_SMS rows
-// at most.
+// have room for every call's, so that one workspace serves all sizes.
 constexpr uint32_t BM_MAX_SMS = 160;
 constexpr uint32_t BM_MAX_BATCH = 65536;
 struct BeamSpace {
-    size_t row_count, row_sum, row_keys, seg_sum, seg_keys, bytes;
-    BeamSpace(uint32_t batch, uint32_t beams, uint32_t n, uint64_t segs) {
+    size_t sums, tops, bytes;
+    BeamSpace(uint32_t batch, uint32_t beams, uint32_t segs, uint32_t blocks) {
         const uint64_t rows = (uint64_t)batch * beams;
-        row_count = up256(4 * (size_t)BM_MAX_BATCH);
-        row_sum = row_count + up256(4 * 2 * BM_MAX_SMS);
-        row_keys = row_sum + up256(16 * rows);
-        seg_sum = row_keys + up256(8 * rows * n);
-        seg_keys = seg_sum + up256(8 * rows * segs);
-        bytes = seg_keys + 8 * rows * segs * n;
+        sums = up256(4 * (size_t)BM_MAX_BATCH);
+        tops = sums + up256(8 * rows * segs);
+        bytes = tops + 4 * rows * blocks;
     }
 };
 
@@ -529,9 +732,11 @@ struct BeamSpace {
 
 using namespace dgt;
 
+// For either type of logits: fp32 rows have more blocks, and so segments.
 extern "C" size_t dgt_beam_workspace_bytes(uint32_t batch, uint32_t beams, uint32_t vocab, uint32_t n) {
     if (!batch || !beams || !vocab || !n || n > BM_MAX_N) return 0;
-    return BeamSpace(batch, beams, n, beam_segments((uint64_t)batch * beams, vocab, n, BM_MAX_SMS)).bytes;
+    const uint32_t blocks = beam_blocks(vocab, 4);
+    return BeamSpace(batch, beams, beam_segments((uint64_t)batch * beams, blocks, BM_MAX_SMS), blocks).bytes;
 }
 
 extern "C" int dgt_beam_select(const void *d_logits, uint32_t f32, int64_t stride, const float *d_scores,
@@ -540,7 +745,7 @@ extern "C" int dgt_beam_select(const void *d_logits, uint32_t f32, int64_t strid
                                void *d_ws, size_t ws_bytes, void *stream) {
     if (f32 > 1) return DGT_ERR_ARG;
     if (beams == 0 || beams > BM_MAX_BEAMS || n == 0 || n > BM_MAX_N || beams * n > BM_MAX_JOIN || vocab == 0 ||
-        vocab > (1u << 24) || batch > 65536)
+        vocab > (1u << BM_BEAM_SHIFT) || batch > BM_MAX_BATCH)
         return DGT_ERR_SHAPE;
     if (batch == 0) return DGT_OK;
     if (!d_logits || !d_scores || !d_parent || !d_token || !d_total || ((uintptr_t)d_logits & (f32 ? 3 : 1)) ||
@@ -551,14 +756,13 @@ extern "C" int dgt_beam_select(const void *d_logits, uint32_t f32, int64_t strid
     DeviceInfo di;
     if (device_info(&di) != DGT_OK) return DGT_ERR_CUDA;
     const uint64_t rows = (uint64_t)batch * beams;
-    const uint32_t segs = beam_segments(rows, vocab, n, std::min((uint32_t)di.sms, BM_MAX_SMS)), V = f32 ? 4 : 8;
-    const BeamSpace at(batch, beams, n, segs);
+    const uint32_t blocks = beam_blocks(vocab, f32 ? 4 : 8);
+    const uint32_t segs = beam_segments(rows, blocks, std::min((uint32_t)di.sms, BM_MAX_SMS));
+    const BeamSpace at(batch, beams, segs, blocks);
     uint8_t *w = (uint8_t *)d_ws;
     const BeamArgs a{d_logits, stride, d_scores, d_done, eos, batch, beams, vocab, n, segs,
-                     ((vocab + 2 * V - 2) / V + segs - 1) / segs,   // a row that begins inside a piece may touch one more
-                     d_parent, d_token, d_total, d_done_out, (int32_t *)w, (int32_t *)(w + at.row_count),
-                     (float2 *)(w + at.seg_sum), (uint64_t *)(w + at.seg_keys), (double2 *)(w + at.row_sum),
-                     (uint64_t *)(w + at.row_keys)};
+                     ((blocks + segs - 1) / segs + BM_TURN - 1) / BM_TURN * BM_TURN, blocks, d_parent, d_token, d_total,
+                     d_done_out, (int32_t *)w, (float2 *)(w + at.sums), (float *)(w + at.tops)};
     const dim3 grid((unsigned)(rows * segs)), block(BM_THREADS);
     cudaStream_t st = (cudaStream_t)stream;
     const cudaError_t e = f32 ? launch_pdl(k_beam_select<true>, grid, block, 0, st, a)

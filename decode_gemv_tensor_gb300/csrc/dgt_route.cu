@@ -1,14 +1,20 @@
-// dgt_route.cu -- the router's choice of experts, a warp for each token.
+// dgt_route.cu -- the router's choice of experts.
 //
 //   s = softmax(l) or 1 / (1 + e^-l);  c = s + bias, or the order of l itself
 //   where there is no bias;  a group's value is the sum of its one or two best
 //   c;  the best groups stay, and of their experts the best topk are taken.
 //
-// Which expert is taken is decided as if in 64 bits: the order is found in
-// fp32 with a bound on its error, and a token whose neighbouring values, among
-// the chosen, the first one left out and the groups at their border, are not
-// further apart than that is decided again in fp64.  Logits alone are compared
-// as they are.
+// A token is GL neighbouring lanes' (32, or 8 or 16 where there are few experts
+// and choices), EPL neighbouring experts in each.  Few choices by a threshold
+// and ranks, others one by one: the maximum over the lanes' maxima, whose lane
+// looks for its next.
+//
+// Which expert is taken is decided as if in 64 bits.  The order is found in
+// fp32 with a bound on its error.  A token whose neighbouring values (of the
+// chosen, the first one left out, and the groups at their border) are not
+// further apart than that is decided again by a warp in two floats, to 2^-36,
+// and one where that is not enough in fp64.  Logits alone are compared as they
+// are.
 #include <cuda_runtime.h>
 
 #include "../../include/dgt.h"
@@ -19,6 +25,9 @@ namespace dgt {
 
 constexpr uint32_t RT_WARPS = 4;
 constexpr uint32_t RT_MAX_EXPERTS = 1024;
+constexpr uint32_t RT_FEW = 12;
+constexpr int RT_CTAS = 8;
+constexpr float RT_LOG2E = 1.4426950408889634f;
 
 struct RouteArgs {
     const void *logits;
@@ -27,7 +36,7 @@ struct RouteArgs {
     int32_t *ids;
     float *p;
     uint64_t tokens;
-    uint32_t experts, topk, groups, group_topk, group_best, f32, sigmoid, renorm;
+    uint32_t experts, topk, groups, group_topk, group_best, f32, sigmoid, renorm, vec, vec_bias;
     float scale;
 };
 
@@ -38,270 +47,561 @@ __device__ __forceinline__ uint32_t order32(float v) {
     const uint32_t b = __float_as_uint(v + 0.0f);
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ float value32(uint32_t k) {
-    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+__device__ __forceinline__ float value32(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
+
+template <uint32_t GL, typename T>
+__device__ __forceinline__ T lanes_max(T v) {
+#pragma unroll
+    for (uint32_t d = GL / 2; d >= 1; d >>= 1) {
+        const T o = __shfl_xor_sync(DGT_FULL, v, d);
+        v = o > v ? o : v;
+    }
+    return v;
 }
-__device__ __forceinline__ uint64_t order64(double v) {
-    if (v != v) return 1ull;
-    const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
-    return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+template <uint32_t GL, typename T>
+__device__ __forceinline__ T lanes_sum(T v) {
+#pragma unroll
+    for (uint32_t d = GL / 2; d >= 1; d >>= 1) v += __shfl_xor_sync(DGT_FULL, v, d);
+    return v;
+}
+template <uint32_t GL>
+__device__ __forceinline__ uint32_t lanes_top(uint32_t k) {
+    return GL == 32 ? __reduce_max_sync(DGT_FULL, k) : lanes_max<GL>(k);
+}
+template <uint32_t GL>
+__device__ __forceinline__ uint64_t lanes_top(uint64_t k) {
+    const uint32_t hi = lanes_top<GL>((uint32_t)(k >> 32));
+    return (uint64_t)hi << 32 | lanes_top<GL>((uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
 }
 
-__device__ __forceinline__ uint32_t warp_top(uint32_t k) { return __reduce_max_sync(DGT_FULL, k); }
-__device__ __forceinline__ uint64_t warp_top(uint64_t k) {
-    const uint32_t hi = __reduce_max_sync(DGT_FULL, (uint32_t)(k >> 32));
-    const uint32_t lo = __reduce_max_sync(DGT_FULL, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
-    return (uint64_t)hi << 32 | lo;
-}
-
-// The best `want` experts in order, lane j's the j-th, from every lane's EPL
-// keys of the experts EPL * lane ...; taken keys become 0.  next: the best key
-// left.
-template <int EPL, typename K>
-__device__ __forceinline__ uint32_t take(K (&key)[EPL], uint32_t want, K &mine, K &next) {
-    const uint32_t lane = lane_id();
+// The best `want` experts in order, lane j's of the token the j-th, from every
+// lane's keys of its experts; taken keys become 0.  next, next_id: the best
+// that is left.
+template <uint32_t GL, int EPL, typename K>
+__device__ __forceinline__ uint32_t take(K (&key)[EPL], uint32_t want, K &mine, K &next, uint32_t &next_id) {
+    const uint32_t lane = lane_id() % GL, first = lane_id() - lane;
     uint32_t id = 0;
     mine = 0;
     for (uint32_t j = 0;; j++) {
         K best = key[0];
-        uint32_t at = 0;
 #pragma unroll
-        for (int i = 1; i < EPL; i++)
-            if (key[i] > best) best = key[i], at = i;
-        const K top = warp_top(best);
+        for (int i = 1; i < EPL; i++) best = key[i] > best ? key[i] : best;
+        const K top = lanes_top<GL>(best);
+        const uint32_t owner = __ffs(__ballot_sync(DGT_FULL, best == top) >> first) - 1;   // the lowest lane has the lowest experts
+        uint32_t at = 0;
+        bool found = lane != owner;
+#pragma unroll
+        for (int i = 0; i < EPL; i++) {
+            const bool hit = !found && key[i] == top;
+            if (hit) at = i;
+            if (hit && j < want) key[i] = 0;
+            found |= hit;
+        }
+        const uint32_t e = owner * EPL + __shfl_sync(DGT_FULL, at, first + owner);
         if (j == want) {
-            next = top;
+            next = top, next_id = e;
             return id;
         }
-        const uint32_t owner = __ffs(__ballot_sync(DGT_FULL, best == top)) - 1;
-        const uint32_t e = __shfl_sync(DGT_FULL, at, owner);
-        if (lane == owner) {
-#pragma unroll
-            for (int i = 0; i < EPL; i++)
-                if (i == (int)at) key[i] = 0;
-        }
-        if (lane == j) id = owner * EPL + e, mine = top;
+        if (lane == j) id = e, mine = top;
     }
 }
 
+__device__ __forceinline__ float warp_top(float v) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// The same for a whole warp's token and few choices, without looking through
+// the lanes' experts for each: the (want + 1)-th largest of the lanes' maxima
+// is a threshold that want + 1 experts reach and not many more, and these find
+// their ranks among each other.  False where they are more than 32 or not all
+// are numbers above -inf.
 template <int EPL>
+__device__ __forceinline__ bool take_few(const float (&c)[EPL], uint32_t want, float2 (*list)[32], float &mine,
+                                         float &next, uint32_t &id, uint32_t &next_id) {
+    const uint32_t lane = lane_id();
+    float best = c[0];
+#pragma unroll
+    for (int i = 1; i < EPL; i++) best = fmaxf(best, c[i]);
+    float left = best, from = 0.0f;
+    for (uint32_t j = 0; j <= want; j++) {
+        from = warp_top(left);
+        if (lane == __ffs(__ballot_sync(DGT_FULL, left == from)) - 1) left = -INFINITY;
+    }
+    if (!(from > -INFINITY)) return false;
+    uint32_t count = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; i++) count += c[i] >= from;
+    uint32_t all, at = warp_excl_scan(count, &all);
+    if (all > 32) return false;
+    if (count) {
+#pragma unroll
+        for (int i = 0; i < EPL; i++)
+            if (c[i] >= from) list[0][at++] = make_float2(c[i], __uint_as_float(lane * EPL + i));
+    }
+    __syncwarp();
+    // in the order of the experts, so of two equal ones the earlier is the lower
+    const float2 own = list[0][min(lane, all - 1)];
+    uint32_t rank = 0;
+#pragma unroll 4
+    for (uint32_t j = 0; j < all; j++) {
+        const float o = list[0][j].x;
+        rank += o > own.x || (o == own.x && j < lane);
+    }
+    if (lane < all) list[1][rank] = own;
+    __syncwarp();
+    const float2 m = list[1][min(lane, want)], n = list[1][want];
+    mine = m.x, id = __float_as_uint(m.y);
+    next = n.x, next_id = __float_as_uint(n.y);
+    return true;
+}
+
 __device__ __forceinline__ float logit(const RouteArgs &a, const void *row, uint32_t e) {
     return a.f32 ? static_cast<const float *>(row)[e]
                  : __uint_as_float((uint32_t)static_cast<const uint16_t *>(row)[e] << 16);
 }
-
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor_sync(DGT_FULL, v, d));
-    return v;
+__device__ __forceinline__ const void *token_row(const RouteArgs &a, uint64_t token) {
+    return a.f32 ? (const void *)(static_cast<const float *>(a.logits) + token * a.stride)
+                 : (const void *)(static_cast<const uint16_t *>(a.logits) + token * a.stride);
 }
-template <typename T>
-__device__ __forceinline__ T warp_sum(T v) {
+// Experts e0 .. e0 + EPL - 1; -inf past the last.
+template <int EPL>
+__device__ __forceinline__ void load_logits(const RouteArgs &a, const void *row, uint32_t e0, float (&l)[EPL]) {
+    if (EPL % 4 == 0 && a.vec) {
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(DGT_FULL, v, d);
-    return v;
+        for (int i = 0; i < EPL; i += 4) {
+            if (e0 + i < a.experts) {
+                if (a.f32) {
+                    const float4 x = *reinterpret_cast<const float4 *>(static_cast<const float *>(row) + e0 + i);
+                    l[i] = x.x, l[i + 1] = x.y, l[i + 2] = x.z, l[i + 3] = x.w;
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(row) + e0 + i);
+                    l[i] = bf16lo(x.x), l[i + 1] = bf16hi(x.x), l[i + 2] = bf16lo(x.y), l[i + 3] = bf16hi(x.y);
+                }
+            } else {
+                l[i] = l[i + 1] = l[i + 2] = l[i + 3] = -INFINITY;
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; i++) l[i] = e0 + i < a.experts ? logit(a, row, e0 + i) : -INFINITY;
+}
+
+template <int EPL>
+__device__ __forceinline__ void load_bias(const RouteArgs &a, uint32_t e0, float (&b)[EPL]) {
+    if (EPL % 4 == 0 && a.vec_bias) {
+#pragma unroll
+        for (int i = 0; i < EPL; i += 4) {
+            const float4 x = e0 + i < a.experts ? *reinterpret_cast<const float4 *>(a.bias + e0 + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            b[i] = x.x, b[i + 1] = x.y, b[i + 2] = x.z, b[i + 3] = x.w;
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; i++) b[i] = e0 + i < a.experts ? a.bias[e0 + i] : 0.0f;
 }
 
 // e^(l - m) of a softmax: 1 where l is the largest, also when that is
 // infinite; 0 for -inf and NaN.
-template <typename T>
-__device__ __forceinline__ T soft_term(T l, T m) {
-    return l == m ? (l == (T)-INFINITY ? (T)0 : (T)1) : l == l ? exp(l - m) : (T)0;
-}
-template <>
-__device__ __forceinline__ float soft_term<float>(float l, float m) {
+__device__ __forceinline__ float soft_term(float l, float m) {
     return l == m ? (l == -INFINITY ? 0.0f : 1.0f) : l == l ? expf(l - m) : 0.0f;
 }
 __device__ __forceinline__ float sigmoid_of(float l) { return 1.0f / (1.0f + expf(-l)); }
-__device__ __forceinline__ double sigmoid_of(double l) { return 1.0 / (1.0 + exp(-l)); }
+// The same to 2^-22 of 1: for the order only.
+__device__ __forceinline__ float sigmoid_near(float l) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -RT_LOG2E));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
 
-// Two values in order that may be the other way round; infinite ones are what they are in any precision.
+// Two values in order that may be the other way round; infinite ones are what
+// they are in any precision.
 __device__ __forceinline__ bool near(float hi, float lo, float tol) {
     return fabsf(hi) < INFINITY && fabsf(lo) < INFINITY && hi - lo <= tol;
 }
 
-// Groups: lane g gets the value of group g, the sum of its `best` largest of
-// v[0 .. per), v in shared memory.
-template <typename T>
-__device__ __forceinline__ T group_value(const T *v, uint32_t per, uint32_t groups, uint32_t best) {
-    const uint32_t lane = lane_id();
-    if (lane >= groups) return (T)-INFINITY;
-    T one = (T)-INFINITY, two = (T)-INFINITY;
-    for (uint32_t i = 0; i < per; i++) {
-        const T x = v[lane * per + i];
-        if (x > one) two = one, one = x;
-        else if (x > two) two = x;
-    }
-    return best == 2 && per > 1 ? one + two : one;
+// ---- numbers for deciding again: fp64, and two floats h + l, |l| <= ulp(h) / 2
+struct Two {
+    float h, l;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+    const float s = a + b, t = s - a;
+    return {s, (a - (s - t)) + (b - t)};
 }
-// Which groups stay: bit g.
-template <typename K>
-__device__ __forceinline__ uint32_t keep_groups(K key, uint32_t groups, uint32_t keep) {
-    const uint32_t lane = lane_id();
-    uint32_t before = 0;
-    for (uint32_t g = 0; g < groups; g++) {
-        const K other = __shfl_sync(DGT_FULL, key, g);
-        before += other > key || (other == key && g < lane);
-    }
-    return __ballot_sync(DGT_FULL, lane < groups && before < keep);
+__device__ __forceinline__ Two quick(float a, float b) {   // |a| >= |b|
+    const float s = a + b;
+    return {s, b - (s - a)};
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+    const Two s = two_sum(a.h, b.h), t = two_sum(a.l, b.l), u = quick(s.h, s.l + t.h);
+    return quick(u.h, u.l + t.l);
+}
+__device__ __forceinline__ Two quotient(Two a, Two b) {
+    const float q = a.h / b.h, r = fmaf(-q, b.h, a.h) + (a.l - q * b.l);
+    return quick(q, r / b.h);
+}
+// 2^(j / 32)
+__device__ const float2 RT_POW[32] = {
+    {1.0f, 0.0f}, {1.0218971967697144f, -4.811559861650494e-08f}, {1.0442737340927124f, 4.8334701574503924e-08f}, {1.0671404600143433f, -5.9337519786595294e-08f},
+    {1.0905077457427979f, -1.3077539939843064e-08f}, {1.114386796951294f, -5.435540018083884e-08f}, {1.1387885808944702f, 5.386222312608879e-08f}, {1.1637248992919922f, -4.051441493402308e-08f},
+    {1.1892070770263672f, 3.797635272917432e-08f}, {1.215247392654419f, -3.267394887984665e-08f}, {1.2418577671051025f, 4.496838101886169e-08f}, {1.2690509557724f, 1.419333317542737e-09f},
+    {1.2968395948410034f, -4.018999533172973e-08f}, {1.3252366781234741f, -3.496373324196611e-08f}, {1.3542555570602417f, -1.0123349269974824e-08f}, {1.3839099407196045f, -5.875577357983275e-08f},
+    {1.4142135381698608f, 2.4203234971764687e-08f}, {1.4451807737350464f, 3.324199937537742e-08f}, {1.4768261909484863f, -4.500898853621038e-08f}, {1.5091644525527954f, -2.4959373234878512e-08f},
+    {1.5422108173370361f, 8.070904833346049e-09f}, {1.5759809017181396f, -5.661025426206834e-08f}, {1.610490322113037f, 9.836217174097328e-09f}, {1.6457555294036865f, -5.124972091152813e-08f},
+    {1.6817928552627563f, -2.4755326677450284e-08f}, {1.7186193466186523f, -4.8496175963919086e-08f}, {1.7562521696090698f, -9.235770370707996e-09f}, {1.7947090864181519f, -1.141504490931311e-08f},
+    {1.8340080976486206f, -1.1239277952768134e-08f}, {1.8741676807403564f, -4.663005626071026e-08f}, {1.9152065515518188f, 9.845328108326612e-09f}, {1.9571441411972046f, -1.7021804410433106e-08f},
+};
+// e^x to 2^-37 for -80 < x < 80: x = k ln 2 / 32 + r, 2^(k / 32) from the
+// table, e^r by its series (after P. T. P. Tang's table-driven exponential,
+// 1989).  ln 2 / 32 in three parts, the first of nine bits.  x in two floats.
+__device__ __forceinline__ Two two_exp(Two x) {
+    const float k = rintf(x.h * 46.16624130844683f);
+    const float q0 = fmaf(k, -0.02166748046875f, x.h), q1 = k * 6.631076251709805e-06f;
+    const float q1l = fmaf(k, 6.631076251709805e-06f, -q1) + k * -5.14560928046269e-14f;
+    const Two q = two_sum(q0, q1);
+    const float ql = q.l + q1l + x.l;
+    const int ki = (int)k;
+    const float2 t = RT_POW[ki & 31];
+    const float p = t.x * q.h, pl = fmaf(t.x, q.h, -p);
+    const float rest = fmaf(t.x, fmaf(q.h * q.h, fmaf(q.h, fmaf(q.h, 1.0f / 24.0f, 1.0f / 6.0f), 0.5f), ql), fmaf(t.y, q.h, t.y) + pl);
+    const Two s = quick(t.x, p), r = quick(s.h, s.l + rest);
+    const float unit = __uint_as_float((uint32_t)((ki >> 5) + 127) << 23);
+    return {r.h * unit, r.l * unit};
 }
 
-// A token in fp64 (rare): the same steps.
-template <int EPL>
-__device__ __noinline__ uint32_t decide64(const RouteArgs &a, const void *row, double *vals) {
-    const uint32_t lane = lane_id(), per = a.experts / a.groups;
-    double l[EPL], m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < EPL; i++) {
-        const uint32_t e = lane * EPL + i;
-        l[i] = e < a.experts ? (double)logit<EPL>(a, row, e) : -INFINITY;
-        if (l[i] > m) m = l[i];
+template <typename T>
+struct Exact;
+template <>
+struct Exact<double> {
+    static constexpr double off = 0.0;   // an order that stands
+    static __device__ double number(float x) { return x; }
+    static __device__ double soft(float l, float m) {
+        return l == m ? (l == -INFINITY ? 0.0 : 1.0) : l == l ? exp((double)l - (double)m) : 0.0;
     }
-    m = (double)warp_max((float)m);
-    double z = 0.0;
-    uint64_t key[EPL];
-    if (!a.sigmoid) {
+    static __device__ double divide(double a, double z) { return z == 0.0 ? 0.0 : a / z; }
+    static __device__ double sigmoid(float l) { return 1.0 / (1.0 + exp(-(double)l)); }
+    static __device__ uint64_t key(double v) {
+        if (v != v) return 1ull;
+        const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
+        return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+    }
+    static __device__ double sum(double a, double b) { return a + b; }
+};
+template <>
+struct Exact<Two> {
+    static constexpr float off = 0x1p-34f;
+    static __device__ Two number(float x) { return {x, 0.0f}; }
+    static __device__ Two soft(float l, float m) {
+        if (l == m) return {l == -INFINITY ? 0.0f : 1.0f, 0.0f};
+        if (!(l - m > -80.0f)) return {0.0f, 0.0f};   // below 2^-115
+        return two_exp(two_sum(l, -m));
+    }
+    static __device__ Two divide(Two a, Two z) { return z.h == 0.0f ? Two{0.0f, 0.0f} : quotient(a, z); }
+    static __device__ Two sigmoid(float l) {
+        if (l != l) return {l, 0.0f};
+        if (l < -80.0f) return {0.0f, 0.0f};
+        if (l > 80.0f) return {1.0f, 0.0f};
+        return quotient({1.0f, 0.0f}, Two{1.0f, 0.0f} + two_exp({-l, 0.0f}));
+    }
+    static __device__ uint64_t key(Two v) { return v.h != v.h ? 1ull : (uint64_t)order32(v.h) << 32 | order32(v.l); }
+    // not normalised where infinite: as the larger alone
+    static __device__ Two sum(Two a, Two b) {
+        const Two s = a + b;
+        return fabsf(s.h) < INFINITY ? s : Two{a.h + b.h, 0.0f};
+    }
+};
+// How far apart two keys' values are, as fp32.
+__device__ __forceinline__ float apart(Exact<double>, uint64_t, uint64_t) { return INFINITY; }
+__device__ __forceinline__ float apart(Exact<Two>, uint64_t hi, uint64_t lo) {
+    const float a = value32((uint32_t)(hi >> 32)), b = value32((uint32_t)(lo >> 32));
+    if (!(fabsf(a) < INFINITY && fabsf(b) < INFINITY)) return INFINITY;
+    return (a - b) + (value32((uint32_t)hi) - value32((uint32_t)lo));
+}
+
+// A token's choice by a whole warp; false where `off` cannot tell.  vals:
+// shared memory of a 64-bit key for each expert.
+template <int EPL, typename T>
+__device__ __noinline__ bool decide(const RouteArgs &a, const void *row, uint64_t *vals, uint32_t &id) {
+    using X = Exact<T>;
+    const uint32_t lane = lane_id(), per = a.experts / a.groups;
+    float l[EPL], m = -INFINITY;
+    load_logits<EPL>(a, row, lane * EPL, l);
+#pragma unroll
+    for (int i = 0; i < EPL; i++) m = fmaxf(m, l[i]);
+    m = lanes_max<32>(m);
+    T s[EPL], z = X::number(0.0f);
+    if (a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < EPL; i++) s[i] = X::sigmoid(l[i]);
+    } else {
 #pragma unroll
         for (int i = 0; i < EPL; i++) {
-            l[i] = soft_term<double>(l[i], m);
-            z += l[i];
+            s[i] = X::soft(l[i], m);
+            z = z + s[i];
         }
-        z = warp_sum(z);
-        if (z == 0.0) z = 1.0;
+#pragma unroll
+        for (uint32_t d = 16; d >= 1; d >>= 1) {
+            T o;
+            if constexpr (sizeof(T) == 8 && alignof(T) == 8) o = __shfl_xor_sync(DGT_FULL, z, d);
+            else o = {__shfl_xor_sync(DGT_FULL, z.h, d), __shfl_xor_sync(DGT_FULL, z.l, d)};
+            z = z + o;
+        }
+#pragma unroll
+        for (int i = 0; i < EPL; i++) s[i] = l[i] != l[i] ? X::number(l[i]) : X::divide(s[i], z);
     }
+    uint64_t key[EPL];
+    float big = 0.0f;   // the largest that is added
+    bool clear = true;
 #pragma unroll
     for (int i = 0; i < EPL; i++) {
         const uint32_t e = lane * EPL + i;
         key[i] = 0;
         if (e >= a.experts) continue;
-        const double x = (double)logit<EPL>(a, row, e);
-        const double s = x != x ? x : a.sigmoid ? sigmoid_of(x) : l[i] / z;
-        const double c = a.bias ? s + (double)a.bias[e] : s;
-        key[i] = order64(a.bias ? c : x);
-        if (a.groups > 1) vals[e] = c == c ? c : -INFINITY;
+        if (a.bias) {
+            s[i] = X::sum(s[i], X::number(a.bias[e]));
+            if (fabsf(a.bias[e]) < INFINITY) big = fmaxf(big, fabsf(a.bias[e]));
+        }
+        key[i] = a.bias ? X::key(s[i]) : (uint64_t)order32(l[i]) << 32;
+        if (a.groups > 1) vals[e] = X::key(s[i]);
     }
+    // error of a value: of a score below 2^-36, of the sum with a bias 2^-47 of that
+    const float off = X::off * (1.0f + lanes_max<32>(big) * 0x1p-11f);
     if (a.groups > 1) {
         __syncwarp();
-        const double v = group_value(vals, per, a.groups, a.group_best);
-        const uint32_t open = keep_groups(lane < a.groups ? order64(v) : 0ull, a.groups, a.group_topk);
+        uint64_t one = 1, two = 1;   // NaN counts as nothing
+        if (lane < a.groups)
+            for (uint32_t i = 0; i < per; i++) {
+                const uint64_t x = vals[lane * per + i];
+                if (x > one) two = one, one = x;
+                else if (x > two) two = x;
+            }
+        uint64_t value = one;
+        if (a.group_best == 2 && per > 1) {
+            // keys back to numbers: the sum of the best two
+            auto number = [](uint64_t k) -> T {
+                if (k <= 1) return X::number(-INFINITY);
+                if constexpr (sizeof(T) == 8 && alignof(T) == 8)
+                    return __longlong_as_double((int64_t)(k & 0x8000000000000000ull ? k ^ 0x8000000000000000ull : ~k));
+                else
+                    return T{value32((uint32_t)(k >> 32)), value32((uint32_t)k)};
+            };
+            value = X::key(X::sum(number(one), number(two)));
+        } else if (value <= 1) {
+            value = X::key(X::number(-INFINITY));
+        }
+        if (lane >= a.groups) value = 0;
+        uint32_t before = 0;
+        for (uint32_t g = 0; g < a.groups; g++) {
+            const uint64_t other = __shfl_sync(DGT_FULL, value, g);
+            before += other > value || (other == value && g < lane);
+        }
+        const uint32_t open = __ballot_sync(DGT_FULL, lane < a.groups && before < a.group_topk);
+        const uint32_t border = __ballot_sync(DGT_FULL, lane < a.groups && before == a.group_topk - 1);
+        const uint32_t behind = __ballot_sync(DGT_FULL, lane < a.groups && before == a.group_topk);
+        if (behind) {
+            const uint64_t hi = __shfl_sync(DGT_FULL, value, __ffs(border) - 1), lo = __shfl_sync(DGT_FULL, value, __ffs(behind) - 1);
+            clear = apart(X{}, hi, lo) > 4.0f * off;
+        }
 #pragma unroll
         for (int i = 0; i < EPL; i++)
             if (!(open >> ((lane * EPL + i) / per) & 1u)) key[i] = 0;
     }
     uint64_t mine, next;
-    return take<EPL>(key, a.topk, mine, next);
+    uint32_t next_id;
+    id = take<32, EPL>(key, a.topk, mine, next, next_id);
+    if (a.bias) {
+        const uint64_t after = __shfl_down_sync(DGT_FULL, mine, 1), below = lane + 1 < a.topk ? after : next;
+        const uint32_t other = __shfl_down_sync(DGT_FULL, id, 1), behind = lane + 1 < a.topk ? other : next_id;
+        // the same logit and bias are the same value
+        const bool unsure = lane < a.topk && below > 1 && !(apart(X{}, mine, below) > 2.0f * off) &&
+                            !(logit(a, row, id) == logit(a, row, behind) && a.bias[id] == a.bias[behind]);
+        clear &= !__any_sync(DGT_FULL, unsure);
+    }
+    return clear;
 }
 
-template <int EPL>
-__global__ void __launch_bounds__(RT_WARPS * 32) k_route(RouteArgs a) {
+// The greatest two of what a group's lanes hold, GLANES neighbouring ones.
+__device__ __forceinline__ void top_two(float &one, float &two, float x) {
+    two = fmaxf(two, fminf(one, x));
+    one = fmaxf(one, x);
+}
+
+template <uint32_t GL, int EPL>
+__global__ void __launch_bounds__(RT_WARPS * 32, EPL <= 8 ? RT_CTAS : 1) k_route(RouteArgs a) {
     extern __shared__ __align__(8) uint8_t smem[];
+    __shared__ float2 list[GL == 32 ? RT_WARPS : 1][2][32];
     pdl_trigger();
     pdl_wait();
-    const uint32_t lane = lane_id(), warp = threadIdx.x >> 5;
-    const uint64_t token = (uint64_t)blockIdx.x * RT_WARPS + warp;
-    if (token >= a.tokens) return;
-    const void *row = a.f32 ? (const void *)(static_cast<const float *>(a.logits) + token * a.stride)
-                            : (const void *)(static_cast<const uint16_t *>(a.logits) + token * a.stride);
-    double *vals = reinterpret_cast<double *>(smem) + warp * a.experts;   // of the groups' experts
+    const uint32_t lane = lane_id() % GL, warp = threadIdx.x >> 5;
+    const uint64_t mine_at = ((uint64_t)blockIdx.x * RT_WARPS + warp) * (32 / GL) + lane_id() / GL;
+    const bool live = mine_at < a.tokens;
+    if (__ballot_sync(DGT_FULL, live) == 0) return;
+    const uint64_t token = live ? mine_at : a.tokens - 1;
+    const void *row = token_row(a, token);
+    uint64_t *vals = reinterpret_cast<uint64_t *>(smem) + warp * a.experts;   // of the groups' experts
     float l[EPL], c[EPL];
     float m = -INFINITY;
+    load_logits<EPL>(a, row, lane * EPL, l);
 #pragma unroll
-    for (int i = 0; i < EPL; i++) {
-        const uint32_t e = lane * EPL + i;
-        l[i] = e < a.experts ? logit<EPL>(a, row, e) : -INFINITY;
-        m = fmaxf(m, l[i]);
-    }
-    m = warp_max(m);
+    for (int i = 0; i < EPL; i++) m = fmaxf(m, l[i]);
+    m = lanes_max<GL>(m);
     float inv = 1.0f;
     if (!a.sigmoid) {
         float z = 0.0f;
 #pragma unroll
         for (int i = 0; i < EPL; i++) {
-            c[i] = soft_term<float>(l[i], m);
+            c[i] = soft_term(l[i], m);
             z += c[i];
         }
-        z = warp_sum(z);
+        z = lanes_sum<GL>(z);
         inv = z == 0.0f ? 0.0f : 1.0f / z;
     }
-    uint32_t key[EPL];
-    const bool scored = a.bias || a.groups > 1;   // where scores, not logits, are compared
-#pragma unroll
-    for (int i = 0; i < EPL; i++) {
-        const uint32_t e = lane * EPL + i;
-        if (scored) {
-            c[i] = a.sigmoid ? sigmoid_of(l[i]) : l[i] != l[i] ? l[i] : c[i] * inv;
-            if (a.bias && e < a.experts) c[i] += a.bias[e];
-        }
-        key[i] = e < a.experts ? order32(a.bias ? c[i] : l[i]) : 0u;
-    }
-    // How far an fp32 score may be off.  A sigmoid, which is at most 1: expf within 2 units in the last place, a sum
-    // and a quotient, below 2^-21.  A softmax, which is at most inv: expf, a sum of EPL + 5 steps, a quotient and a
-    // product, below (EPL + 8) 2^-23.  Then half a unit of the sum with the bias.
-    const float off = a.sigmoid ? 0x1p-21f : (float)(EPL + 8) * 0x1p-23f * inv;
-    bool close = false;
-    if (a.groups > 1) {
-        const uint32_t per = a.experts / a.groups;
-        float *v = reinterpret_cast<float *>(vals);
+    // c: what is compared, the logits or scores; -inf past the last expert
+    if (a.bias || a.groups > 1) {
+        float b[EPL] = {};
+        if (a.bias) load_bias<EPL>(a, lane * EPL, b);
 #pragma unroll
         for (int i = 0; i < EPL; i++) {
-            const uint32_t e = lane * EPL + i;
-            if (e < a.experts) v[e] = c[i] == c[i] ? c[i] : -INFINITY;
+            const float s = l[i] != l[i] ? l[i] : a.sigmoid ? sigmoid_near(l[i]) : c[i] * inv;
+            c[i] = lane * EPL + i < a.experts ? s + b[i] : -INFINITY;
         }
-        __syncwarp();
-        const float gv = group_value(v, per, a.groups, a.group_best);
-        const uint32_t gk = lane < a.groups ? order32(gv) : 0u;
-        const uint32_t open = keep_groups(gk, a.groups, a.group_topk);
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL; i++) c[i] = l[i];
+    }
+    // How far an fp32 score may be off.  A sigmoid, which is at most 1: exponential and reciprocal within 2^-22, the
+    // product before it |l| 2^-24, of which s (1 - s) is left, a sum: below 2^-21.  A softmax, which is at most inv:
+    // expf, a sum of EPL + 5 steps, a quotient and a product, below (EPL + 8) 2^-23.  Then half a unit of the sum
+    // with the bias.
+    const float off = a.sigmoid ? 0x1p-21f : (float)(EPL + 8) * 0x1p-23f * inv;
+    bool close = false;
+    uint32_t shut = 0;
+    if (GL == 32 && a.groups > 1) {
+        const uint32_t per = a.experts / a.groups, held = per / EPL;   // lanes of a group
+        float one = -INFINITY, two = -INFINITY, big = 0.0f;
+        // a group in a power of two of whole lanes stays in registers
+        const bool whole = held * EPL == per && (held & (held - 1)) == 0;
+        uint32_t value;   // of group `group`, in its lanes
+        uint32_t group;
+        if (whole) {
+            group = lane / held;
+#pragma unroll
+            for (int i = 0; i < EPL; i++) {
+                big = fmaxf(big, c[i] > -INFINITY ? fabsf(c[i]) : 0.0f);
+                top_two(one, two, c[i]);
+            }
+            for (uint32_t d = 1; d < held; d <<= 1) {
+                const float o1 = __shfl_xor_sync(DGT_FULL, one, d), o2 = __shfl_xor_sync(DGT_FULL, two, d);
+                two = fmaxf(fmaxf(two, o2), fminf(one, o1));
+                one = fmaxf(one, o1);
+            }
+        } else {
+            group = lane;
+            float *v = reinterpret_cast<float *>(vals);
+#pragma unroll
+            for (int i = 0; i < EPL; i++) {
+                const uint32_t e = lane * EPL + i;
+                if (e >= a.experts) continue;
+                big = fmaxf(big, c[i] > -INFINITY ? fabsf(c[i]) : 0.0f);
+                v[e] = c[i];
+            }
+            __syncwarp();
+            if (lane < a.groups)
+                for (uint32_t i = 0; i < per; i++) top_two(one, two, v[lane * per + i]);
+            __syncwarp();
+        }
+        const float gv = a.group_best == 2 && per > 1 ? one + two : one;
+        value = group < a.groups ? order32(gv) : 0u;
+        uint32_t before = 0;
+        const uint32_t step = whole ? held : 1;
+        for (uint32_t g = 0; g < a.groups; g++) {
+            const uint32_t other = __shfl_sync(DGT_FULL, value, g * step);
+            before += other > value || (other == value && g < group);
+        }
+        const bool in = group < a.groups && before < a.group_topk;
         if (a.group_topk < a.groups) {
-            const bool in = open >> lane & 1u;
-            const float lo = value32(__reduce_min_sync(DGT_FULL, in ? gk : ~0u));
-            const float hi = value32(__reduce_max_sync(DGT_FULL, in ? 0u : gk));
-            float big = 0.0f;   // the sums of two may be smaller than what they add
-#pragma unroll
-            for (int i = 0; i < EPL; i++) big = fmaxf(big, fabsf(c[i]) < INFINITY ? fabsf(c[i]) : 0.0f);
-            close = near(lo, hi, 4.0f * off + 0x1p-21f * warp_max(big));
+            const float lo = value32(__reduce_min_sync(DGT_FULL, in ? value : ~0u));
+            const float hi = value32(__reduce_max_sync(DGT_FULL, in ? 0u : value));
+            // the sums of two may be smaller than what they add
+            close = near(lo, hi, 4.0f * off + 0x1p-21f * __uint_as_float(__reduce_max_sync(DGT_FULL, __float_as_uint(big))));
         }
+        // closed ones are below what can be taken: a bit of their own
+        if (whole) {
+            shut = in ? 0u : 0xFFFFFFFFu;
+        } else {
+            const uint32_t open = __ballot_sync(DGT_FULL, in);
 #pragma unroll
-        for (int i = 0; i < EPL; i++)
-            if (!(open >> ((lane * EPL + i) / per) & 1u)) key[i] = 0;
-        __syncwarp();
+            for (int i = 0; i < EPL; i++) shut |= (open >> ((lane * EPL + i) / per) & 1u ? 0u : 1u) << i;
+        }
     }
-    uint32_t mine, next;
-    uint32_t id = take<EPL>(key, a.topk, mine, next);
+    if (a.bias == nullptr && GL == 32 && a.groups > 1) {
+#pragma unroll
+        for (int i = 0; i < EPL; i++) c[i] = l[i];
+    }
+    if (GL == 32 && a.groups > 1) {
+#pragma unroll
+        for (int i = 0; i < EPL; i++) c[i] = shut >> i & 1u ? -INFINITY : c[i];
+    }
+    float hi, lo;   // lane j's choice, and what comes behind the last
+    uint32_t id, next_id;
+    if (GL < 32 || a.topk > RT_FEW || !take_few<EPL>(c, a.topk, list[warp], hi, lo, id, next_id)) {
+        uint32_t key[EPL], mine, next;
+#pragma unroll
+        for (int i = 0; i < EPL; i++) key[i] = lane * EPL + i < a.experts && !(shut >> i & 1u) ? order32(c[i]) : 0u;
+        id = take<GL, EPL>(key, a.topk, mine, next, next_id);
+        hi = value32(mine), lo = next > 1u ? value32(next) : -INFINITY;
+    }
     if (a.bias) {
-        const uint32_t after = __shfl_down_sync(DGT_FULL, mine, 1), below = lane + 1 < a.topk ? after : next;
-        const float hi = value32(mine), lo = value32(below);
-        close |= __any_sync(DGT_FULL, lane < a.topk && below > 1u &&
-                                          near(hi, lo, 2.0f * off + 0x1p-23f * (fabsf(lo) + fabsf(hi))));
+        const float after = __shfl_down_sync(DGT_FULL, hi, 1);
+        const uint32_t other = __shfl_down_sync(DGT_FULL, id, 1), behind = lane + 1 < a.topk ? other : next_id;
+        if (lane + 1 < a.topk) lo = after;
+        bool unsure = lane < a.topk && near(hi, lo, 2.0f * off + 0x1p-23f * (fabsf(lo) + fabsf(hi)));
+        // the same logit and bias are the same value
+        if (unsure) unsure = !(logit(a, row, id) == logit(a, row, behind) && a.bias[id] == a.bias[behind]);
+        close |= unsure;
     }
-    if (close) id = decide64<EPL>(a, row, vals);
+    uint32_t again = __ballot_sync(DGT_FULL, close && live);
+    while (again) {   // token by token, by the whole warp
+        const uint32_t sub = (__ffs(again) - 1) / GL;
+        again &= GL == 32 ? 0u : ~(((1u << (GL % 32)) - 1) << (sub * (GL % 32)));
+        constexpr int E32 = (GL * EPL + 31) / 32;
+        const void *r = token_row(a, __shfl_sync(DGT_FULL, token, sub * GL));
+        uint32_t best;
+        if (!decide<E32, Two>(a, r, vals, best)) decide<E32, double>(a, r, vals, best);
+        const uint32_t got = __shfl_sync(DGT_FULL, best, lane);   // lane j of the token gets the j-th
+        if (lane_id() / GL == sub) id = got;
+    }
 
     // weights
     const bool on = lane < a.topk;
-    const float x = on ? logit<EPL>(a, row, id) : -INFINITY;
+    const float x = on ? logit(a, row, id) : -INFINITY;
     float w;
     if (a.renorm) {
         // s / sum s as the quotient of what is left of both by the largest taken logit: nothing is lost to
         // scores below fp32's range
-        const float top = warp_max(x);
-        float q = soft_term<float>(x, top);
+        const float top = lanes_max<GL>(x == x ? x : -INFINITY);
+        float q = soft_term(x, top);
         // e^(l - top) (1 + e^top) / (1 + e^l) for a top below 0, else s itself
         if (a.sigmoid) q = top > 0.0f ? (x == x ? sigmoid_of(x) : 0.0f) : q * (1.0f + expf(top)) / (1.0f + expf(x));
-        const float sum = warp_sum(on ? q : 0.0f);
+        const float sum = lanes_sum<GL>(on ? q : 0.0f);
         w = sum > 0.0f ? q / sum : 0.0f;
     } else {
-        w = a.sigmoid ? (x == x ? sigmoid_of(x) : 0.0f) : soft_term<float>(x, m) * inv;
+        w = a.sigmoid ? (x == x ? sigmoid_of(x) : 0.0f) : soft_term(x, m) * inv;
     }
-    if (on) {
+    if (on && live) {
         a.ids[token * a.topk + lane] = (int32_t)id;
         a.p[token * a.topk + lane] = w * a.scale;
     }
 }
 
-template <int EPL>
+template <uint32_t GL, int EPL>
 static cudaError_t route_launch(const RouteArgs &a, cudaStream_t st) {
-    const uint64_t grid = (a.tokens + RT_WARPS - 1) / RT_WARPS;
+    const uint64_t per = RT_WARPS * (32 / GL), grid = (a.tokens + per - 1) / per;
     const size_t smem = a.groups > 1 ? (size_t)RT_WARPS * a.experts * 8 : 0;   // 32 KB at most
-    return launch_pdl(k_route<EPL>, dim3((unsigned)grid), dim3(RT_WARPS * 32), smem, st, a);
+    return launch_pdl(k_route<GL, EPL>, dim3((unsigned)grid), dim3(RT_WARPS * 32), smem, st, a);
 }
 
 }  // namespace dgt
@@ -320,15 +620,24 @@ extern "C" int dgt_route(const dgt_router *r, const void *d_logits, int64_t stri
     if (!d_logits || !d_ids || !d_p || ((uintptr_t)d_logits & (r->f32 ? 3 : 1)) ||
         (((uintptr_t)d_ids | (uintptr_t)d_p | (uintptr_t)r->d_bias) & 3))
         return DGT_ERR_ARG;
+    const bool vec = r->experts % 4 == 0 && (stride % 4 == 0 || tokens == 1) && ((uintptr_t)d_logits & (r->f32 ? 15 : 7)) == 0;
     const RouteArgs a{d_logits, stride, r->d_bias, d_ids, d_p, tokens, r->experts, r->topk, r->groups,
-                      r->group_topk, r->group_best, r->f32, r->sigmoid, r->renorm, r->scale};
+                      r->group_topk, r->group_best, r->f32, r->sigmoid, r->renorm, vec, r->experts % 4 == 0 && aligned16(r->d_bias), r->scale};
     cudaStream_t st = (cudaStream_t)stream;
-    const uint32_t epl = (r->experts + 31) / 32;
-    const cudaError_t e = epl <= 1   ? route_launch<1>(a, st)
-                          : epl <= 2 ? route_launch<2>(a, st)
-                          : epl <= 4 ? route_launch<4>(a, st)
-                          : epl <= 8 ? route_launch<8>(a, st)
-                          : epl <= 16 ? route_launch<16>(a, st)
-                                      : route_launch<32>(a, st);
+    const uint32_t E = r->experts, epl = (E + 31) / 32;
+    cudaError_t e;
+    if (r->groups == 1 && r->topk <= 8 && E <= 64)
+        e = E <= 8 ? route_launch<8, 1>(a, st) : E <= 16 ? route_launch<8, 2>(a, st) : E <= 32 ? route_launch<8, 4>(a, st) : route_launch<8, 8>(a, st);
+    else if (r->groups == 1 && r->topk <= 16 && E <= 128)
+        e = E <= 64 ? route_launch<16, 4>(a, st) : route_launch<16, 8>(a, st);
+    else
+        e = epl <= 1   ? route_launch<32, 1>(a, st)
+            : epl <= 2 ? route_launch<32, 2>(a, st)
+            : epl <= 4 ? route_launch<32, 4>(a, st)
+            : epl == 5 ? route_launch<32, 5>(a, st)
+            : epl <= 8 ? route_launch<32, 8>(a, st)
+            : epl <= 12 ? route_launch<32, 12>(a, st)
+            : epl <= 16 ? route_launch<32, 16>(a, st)
+                        : route_launch<32, 32>(a, st);
     return e == cudaSuccess ? DGT_OK : DGT_ERR_CUDA;
 }
