@@ -1075,7 +1075,7 @@ def kv_attention_shared_workspace(cache: KvCache, q_heads: int, groups: int, bat
 
 
 def kv_attention_shared(cache: KvCache, layer: int, q, seqs, prefix, shared, groups=None, cu=None, scale=None, out=None,
-                        lse=None, ws=None, status=None, stream=None, test_wait_polls=None):
+                        lse=None, ws=None, status=None, stream=None, always: bool = False, test_wait_polls=None):
     """dgt_kv_attention_shared: kv_attention (without a window) of sequences that
     share their first pages, which are read once for a group.  groups int32 [G +
     1]: where each group of neighbouring sequences begins in `seqs`, 0 first and
@@ -1083,8 +1083,9 @@ def kv_attention_shared(cache: KvCache, layer: int, q, seqs, prefix, shared, gro
     a group's shared tokens; shared int32 [G]: how many they are (whole pages of
     them are shared, what is behind comes from each sequence's own pages).  The
     sequences of a group list the same pages for them, as kv_fork and kv_reserve
-    leave them, and their new rows are behind them.  Returns out, bf16 [tokens,
-    q_heads, head_dim]."""
+    leave them, and their new rows are behind them.  always: also where sharing
+    saves little (DGT_KV_SHARE_ALWAYS).  Returns out, bf16 [tokens, q_heads,
+    head_dim]."""
     import torch
     tokens, heads, dim = q.shape
     batch, n = seqs.numel(), shared.numel()
@@ -1110,7 +1111,7 @@ def kv_attention_shared(cache: KvCache, layer: int, q, seqs, prefix, shared, gro
                                          None if groups is None else _i32(groups, "groups", n + 1), n,
                                          dim ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(ws),
                                          ws.numel() * ws.element_size(), _status(status),
-                                         test_wait_flags(test_wait_polls), _stream_on(cache.k, stream)),
+                                         test_wait_flags(test_wait_polls) | bool(always), _stream_on(cache.k, stream)),
            "dgt_kv_attention_shared")
     return out
 

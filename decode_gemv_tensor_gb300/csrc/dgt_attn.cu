@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, attn_ctas(D, NT)) k_kv_attentio
             const Slot s = slots[r.slot];
 
             if (s.np == 0) {
-                write_none<D, PART>(a, s, r.h, tid, AT_WARPS * 32);
+                write_none<D>(a, s, r.h, tid, AT_WARPS * 32);
                 at_hand = false;
                 continue;
             }
@@ -534,11 +534,6 @@ __global__ void __launch_bounds__(AT_WARPS * 32, attn_ctas(D, NT)) k_kv_attentio
                         float q = none ? 0.0f : ex2(finite_base(st[1]) - finite_base(st[0]) - W_LOG2) / st[2];
                         const uint32_t flat = s.row0 + row;
                         const uint64_t at = (uint64_t)(s.tok0 + flat / a.group) * a.q_heads + r.h * a.group + flat % a.group;
-                        if (PART == AT_FRONT) {
-                            *reinterpret_cast<float4 *>(a.front + at * D + d) = make_float4(v.x * q, v.y * q, v.z * q, v.w * q);
-                            if (d == 0) a.front_lse[at] = none ? -INFINITY : st[0] + __log2f(st[2]);
-                            continue;
-                        }
                         if (PART == AT_TAIL) {
                             const TailJoin tj = tail_join(a, s, at, none ? -INFINITY : st[0] + __log2f(st[2]));
                             float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -594,9 +589,7 @@ static int attn_launch_part(const AttnArgs &a, cudaStream_t st) {
 
 template <uint32_t D, uint32_t NT>
 static int attn_launch(const AttnArgs &a, AttnPart part, cudaStream_t st) {
-    return part == AT_ALL     ? attn_launch_part<D, NT, AT_ALL>(a, st)
-           : part == AT_FRONT ? attn_launch_part<D, NT, AT_FRONT>(a, st)
-                              : attn_launch_part<D, NT, AT_TAIL>(a, st);
+    return part == AT_ALL ? attn_launch_part<D, NT, AT_ALL>(a, st) : attn_launch_part<D, NT, AT_TAIL>(a, st);
 }
 
 // Rows of a tile, by an entry's rows (the mean of a batch): in n-tiles of
@@ -627,7 +620,7 @@ static uint64_t slot_count(uint32_t RT, uint32_t group, uint32_t batch, uint64_t
 // The row tile and how the work is cut, and the launch.
 static int attn_run(AttnArgs &a, AttnPart part, cudaStream_t st) {
     const uint32_t head_dim = a.c.head_dim;
-    const Plan plan = attn_plan(head_dim, a.group, a.batch, a.tokens);
+    const Plan plan = part == AT_FRONT ? Plan{0, prompt_rows(head_dim)} : attn_plan(head_dim, a.group, a.batch, a.tokens);
     const uint32_t nt = plan.nt, RT = plan.RT;
     a.slots = (uint32_t)slot_count(RT, a.group, a.batch, a.tokens, part == AT_FRONT || a.cu != nullptr);
     a.per_entry = (a.group + RT - 1) / RT;
@@ -661,11 +654,13 @@ using namespace dgt;
 
 // Arrival counters, then two partial results per CTA.
 constexpr size_t AT_COUNT_BYTES = (3 * AT_MAX_SMS * 4 + 255) / 256 * 256;   // a counter a CTA
+static size_t part_bytes(uint32_t head_dim, Plan p) {
+    return (size_t)AT_MAX_SMS * (p.nt ? attn_ctas(head_dim, p.nt) : 1) * 2 * p.RT * (head_dim + 4) * 4;
+}
 extern "C" size_t dgt_kv_attention_workspace_bytes(const dgt_kv_cache *cache, uint32_t q_heads, uint32_t batch,
                                                    uint64_t tokens) {
     if (!cache || cache->kv_heads == 0 || batch == 0 || q_heads < cache->kv_heads) return 0;
-    const Plan p = attn_plan(cache->head_dim, q_heads / cache->kv_heads, batch, tokens);
-    return AT_COUNT_BYTES + (size_t)AT_MAX_SMS * (p.nt ? attn_ctas(cache->head_dim, p.nt) : 1) * 2 * p.RT * (cache->head_dim + 4) * 4;
+    return AT_COUNT_BYTES + part_bytes(cache->head_dim, attn_plan(cache->head_dim, q_heads / cache->kv_heads, batch, tokens));
 }
 
 extern "C" int dgt_kv_attention_ex(const dgt_kv_cache *cache, uint32_t layer, const dgt_heads *q, uint64_t tokens,
@@ -707,18 +702,81 @@ extern "C" int dgt_kv_attention(const dgt_kv_cache *cache, uint32_t layer, const
                                ws_bytes, d_status, 0, stream);
 }
 
-// Shared pages.  Workspace: the counters of both launches, the front's
-// logarithms and quotients, then the partial results of each.
+// ---- shared pages
+struct GroupArgs {
+    dgt_kv_cache c;
+    const int32_t *group_at, *prefix, *shared, *cu;   // group_at NULL: one group
+    uint32_t groups, entries, group, rt;
+    uint64_t worth;                                   // reads of pages that sharing has to save
+    Groups g;
+    int32_t *status;
+};
+
+__global__ void __launch_bounds__(1024) k_kv_groups(GroupArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    for (uint32_t g = threadIdx.x; g <= a.groups; g += 1024) {
+        int32_t e = g ? (int32_t)a.entries : 0;
+        if (a.group_at) e = a.group_at[g];
+        if (e < 0 || (uint32_t)e > a.entries) {
+            set_status(a.status, DGT_ERR_ARG);
+            e = (int32_t)a.entries;
+        }
+        if (g < a.groups) {
+            const int32_t s = a.prefix[g], n = a.shared[g];
+            // its prefix holds them
+            const bool ok = s >= 0 && (uint32_t)s < a.c.max_seqs && n >= 0 && n <= a.c.lens[s] &&
+                            (uint64_t)n <= (uint64_t)a.c.max_pages * KV_P;
+            if (!ok) set_status(a.status, DGT_ERR_ARG);
+            a.g.front[g] = ok ? (uint32_t)n / KV_P : 0;
+        }
+        a.g.entry[g] = (uint32_t)e;
+        a.g.row[g] = a.cu ? (uint32_t)a.cu[e] : (uint32_t)e;
+    }
+    __syncthreads();
+    // Pages that are worth taking for all of a group's rows together: against every sequence on its own that saves
+    // (sequences - tiles) reads of each.
+    for (uint32_t g = threadIdx.x; g < a.groups; g += 1024) {
+        const uint64_t rows = (uint64_t)(a.g.row[g + 1] - a.g.row[g]) * a.group;
+        const uint32_t entries = a.g.entry[g + 1] - a.g.entry[g], tiles = (uint32_t)((rows + a.rt - 1) / a.rt);
+        const uint64_t saved = (uint64_t)a.g.front[g] * (entries > tiles ? entries - tiles : 0) * a.c.kv_heads * a.groups;
+        if (saved < a.worth) a.g.front[g] = 0;
+    }
+}
+
+// Reads of pages that sharing has to save: the launches before the tails cost
+// about 15 us, which is what few-row tiles take for reads of 256 MB out of L2.
+// Measured, 24 query and 8 kv heads of 128, one row a sequence: 16 sequences
+// of 4003 shared tokens (7400 reads) 34 us shared and 26 us each on its own, 48
+// (23000) 49 and 56 us, two groups of 16 of 20003 and 18600 (71000) 52 and 126
+// us.  On the tensor-core tiles a read costs four times that: 4 sequences of 30
+// rows, 5000 shared tokens (1200) 45 and 30 us.
+static uint64_t worth_reads(uint32_t head_dim, uint64_t rows) {
+    return (1u << 21) / head_dim / (attn_plan(head_dim, 1, 1, rows).nt ? 1 : 4);
+}
+// The most that the sequences of a call can share by their tables is worth it,
+// and one sequence's rows leave most of a tile empty: a full one gains nothing
+// from its neighbours (6 sequences of up to 512 tokens, 12040 shared: 309 us
+// shared, 278 us each on its own).
+static bool can_share(const dgt_kv_cache *c, uint32_t group, uint32_t groups, uint32_t batch, uint64_t tokens) {
+    const uint64_t rows = group * ((tokens + batch - 1) / batch), rt = prompt_rows(c->head_dim);
+    const uint64_t tiles = groups * ((group * ((tokens + groups - 1) / groups) + rt - 1) / rt);
+    return rows <= rt / 2 && batch > tiles &&
+           (batch - tiles) * c->max_pages * c->kv_heads >= worth_reads(c->head_dim, rows);
+}
+
+// Workspace: the counters of both launches, the groups, the fronts'
+// logarithms and quotients, then the partial results of each launch.
 struct SharedSpace {
-    size_t front_lse, front, front_part, tail_part, bytes;
-    SharedSpace(const dgt_kv_cache *c, uint32_t q_heads, uint32_t groups, uint32_t batch, uint64_t tokens) {
+    size_t groups, lse, out, part[2], bytes;
+    SharedSpace(const dgt_kv_cache *c, uint32_t q_heads, uint32_t ngroups, uint32_t batch, uint64_t tokens) {
         const uint64_t rows = tokens * q_heads;
-        const size_t tail = dgt_kv_attention_workspace_bytes(c, q_heads, batch, tokens);
-        front_lse = 2 * AT_COUNT_BYTES;
-        front = front_lse + (rows * 4 + 255) / 256 * 256;
-        front_part = front + rows * c->head_dim * 4;
-        tail_part = front_part + dgt_kv_attention_workspace_bytes(c, q_heads, groups, tokens) - AT_COUNT_BYTES;
-        bytes = tail_part + tail - AT_COUNT_BYTES;
+        groups = 2 * AT_COUNT_BYTES;
+        lse = groups + (12 * ((size_t)ngroups + 1) + 255) / 256 * 256;
+        out = lse + (rows * 4 + 255) / 256 * 256;
+        part[0] = out + rows * c->head_dim * 4;
+        part[1] = part[0] + part_bytes(c->head_dim, Plan{0, prompt_rows(c->head_dim)});
+        bytes = part[1] + dgt_kv_attention_workspace_bytes(c, q_heads, batch, tokens) - AT_COUNT_BYTES;
     }
 };
 
@@ -736,7 +794,7 @@ extern "C" int dgt_kv_attention_shared(const dgt_kv_cache *cache, uint32_t layer
     int rc = kv_check(cache);
     if (rc != DGT_OK) return rc;
     if (!q || layer >= cache->layers) return DGT_ERR_ARG;
-    if (flags & ~(DGT_TEST_SHORT_WAITS | DGT_TEST_WAIT_POLLS(0xFFFF))) return DGT_ERR_ARG;
+    if (flags & ~(DGT_KV_SHARE_ALWAYS | DGT_TEST_SHORT_WAITS | DGT_TEST_WAIT_POLLS(0xFFFF))) return DGT_ERR_ARG;
     if ((rc = batch_check(tokens, batch, d_cu)) != DGT_OK) return rc;
     if (groups > KV_MAX_BATCH) return DGT_ERR_SHAPE;
     if (tokens == 0 || batch == 0) return DGT_OK;
@@ -750,13 +808,24 @@ extern "C" int dgt_kv_attention_shared(const dgt_kv_cache *cache, uint32_t layer
     a.c = *cache;
     a.layer = layer, a.q_heads = q->heads, a.tokens = tokens, a.group = q->heads / cache->kv_heads;
     a.q = *q, a.cu = d_cu, a.scale_log2 = scale * LOG2E, a.out = d_out, a.lse = d_lse, a.status = d_status;
-    a.spin = wait_limit_from_flags(flags);
-    a.group_at = d_groups, a.prefix = d_prefix, a.shared = d_shared, a.groups = groups, a.entries = batch;
+    a.spin = wait_limit_from_flags(flags & ~DGT_KV_SHARE_ALWAYS);
+    a.groups = groups;
     uint8_t *w = (uint8_t *)d_ws;
-    a.front_lse = (float *)(w + at.front_lse), a.front = (float *)(w + at.front);
+    cudaStream_t st = (cudaStream_t)stream;
     AttnArgs f = a;
-    f.batch = groups, f.count = (int32_t *)w, f.part = (float *)(w + at.front_part);
-    if ((rc = attn_run(f, AT_FRONT, (cudaStream_t)stream)) != DGT_OK) return rc;
-    a.batch = batch, a.seqs = d_seqs, a.count = (int32_t *)(w + AT_COUNT_BYTES), a.part = (float *)(w + at.tail_part);
-    return attn_run(a, AT_TAIL, (cudaStream_t)stream);
+    a.seqs = d_seqs, a.batch = batch;
+    a.count = (int32_t *)(w + AT_COUNT_BYTES), a.part = (float *)(w + at.part[1]);
+    const bool always = flags & DGT_KV_SHARE_ALWAYS;
+    if (!always && !can_share(cache, a.group, groups, batch, tokens)) return attn_run(a, AT_ALL, st);
+
+    uint32_t *t = (uint32_t *)(w + at.groups);
+    f.g = a.g = Groups{t, t + groups + 1, t + 2 * ((size_t)groups + 1)};
+    const GroupArgs ga{*cache, d_groups, d_prefix, d_shared, d_cu, groups, batch, a.group, prompt_rows(cache->head_dim),
+                       always ? 0 : worth_reads(cache->head_dim, a.group * ((tokens + batch - 1) / batch)), a.g, d_status};
+    if (launch_pdl(k_kv_groups, dim3(1), dim3(1024), 0, st, ga) != cudaSuccess) return DGT_ERR_CUDA;
+    f.front_lse = a.front_lse = (float *)(w + at.lse), f.front = a.front = (float *)(w + at.out);
+    f.seqs = d_prefix, f.batch = groups;
+    f.count = (int32_t *)w, f.part = (float *)(w + at.part[0]);
+    if ((rc = attn_run(f, AT_FRONT, st)) != DGT_OK) return rc;
+    return attn_run(a, AT_TAIL, st);
 }

@@ -12,9 +12,9 @@
 // are read on the device: a captured graph follows them.
 //
 // Sequences that share their first pages: one launch takes these pages once
-// for all rows of a group (front) and leaves quotients and logarithms of the
-// sums in fp32, the next the pages behind them for each sequence (tail) and
-// joins the two.
+// for all rows of a group (front, on the tensor-core tiles) and leaves
+// quotients and logarithms of the sums in fp32, the next the pages behind them
+// for each sequence (tail) and joins the two.
 #pragma once
 #include <algorithm>
 
@@ -30,6 +30,13 @@ constexpr uint32_t AT_CHUNK = 64;      // row tiles described in shared memory a
 constexpr uint32_t AT_MAX_SMS = 160;   // a workspace has room for so many
 
 enum AttnPart { AT_ALL, AT_FRONT, AT_TAIL };
+
+// The groups of sequences that share pages: where each begins among the
+// entries and the token rows, and its shared pages.  A kernel before finds
+// them once, so that a CTA's slots have theirs without a chain of loads each.
+struct Groups {
+    uint32_t *entry, *row, *front;   // [groups + 1], [groups + 1], [groups]
+};
 
 struct AttnArgs {
     dgt_kv_cache c;
@@ -47,37 +54,11 @@ struct AttnArgs {
     uint32_t end;                // what a segment costs besides its pages, in pages
     float join;                  // what a part costs the join, in pages
     uint32_t spin;
-    // front and tail: the groups' first entries (NULL: one group), the sequences whose first tokens are shared, and
-    // how many are; a front's entries are the groups
-    const int32_t *group_at, *prefix, *shared;
-    uint32_t groups, entries;
+    // front and tail; a front's entries are the groups
+    Groups g;
+    uint32_t groups;
     float *front, *front_lse;    // [tokens, q_heads, head_dim], and log2 of the sums
 };
-
-// Where group g begins among the entries, and its shared pages.
-__device__ __forceinline__ uint32_t group_entry(const AttnArgs &a, uint32_t g) {
-    if (!a.group_at) return g ? a.entries : 0;
-    const int32_t e = a.group_at[g];
-    if (e >= 0 && (uint32_t)e <= a.entries) return (uint32_t)e;
-    set_status(a.status, DGT_ERR_ARG);
-    return a.entries;
-}
-__device__ __forceinline__ uint32_t front_pages(const AttnArgs &a, uint32_t g) {
-    const int32_t s = a.prefix[g], n = a.shared[g];
-    if (s >= 0 && (uint32_t)s < a.c.max_seqs && n >= 0 && n <= a.c.lens[s] && (uint64_t)n <= (uint64_t)a.c.max_pages * KV_P)
-        return (uint32_t)n / KV_P;
-    set_status(a.status, DGT_ERR_ARG);
-    return 0;
-}
-// The first token row of an entry.
-template <int PART>
-__device__ __forceinline__ uint32_t entry_row(const AttnArgs &a, uint32_t b) {
-    if (PART == AT_FRONT) {
-        const uint32_t e = group_entry(a, b);
-        return a.cu ? (uint32_t)a.cu[e] : e;
-    }
-    return (uint32_t)a.cu[b];
-}
 
 // A tile of query rows: rows [row0, row0 + rows) of its entry's flattened
 // (token, head of the group) rows, at positions pos0 + row / group.
@@ -128,7 +109,8 @@ __device__ __forceinline__ Slot slot_info(const AttnArgs &a, uint32_t slot, uint
     *units = 0;
     if (PART == AT_FRONT || a.cu) {
         // as item_entry and item_base
-        auto base = [&](uint32_t i) { return (uint32_t)((uint64_t)entry_row<PART>(a, i) * a.group / RT) + i; };
+        auto at = [&](uint32_t i) { return PART == AT_FRONT ? a.g.row[i] : (uint32_t)a.cu[i]; };
+        auto base = [&](uint32_t i) { return (uint32_t)((uint64_t)at(i) * a.group / RT) + i; };
         uint32_t lo = 0, hi = a.batch;
         while (hi - lo > 1) {
             const uint32_t mid = (lo + hi) >> 1;
@@ -137,8 +119,8 @@ __device__ __forceinline__ Slot slot_info(const AttnArgs &a, uint32_t slot, uint
         }
         b = lo;
         rt = slot - base(b);
-        s.tok0 = entry_row<PART>(a, b);
-        n = entry_row<PART>(a, b + 1) - s.tok0;
+        s.tok0 = at(b);
+        n = at(b + 1) - s.tok0;
         if ((uint64_t)s.tok0 + n > a.tokens) {
             set_status(a.status, DGT_ERR_ARG);
             return s;
@@ -154,8 +136,8 @@ __device__ __forceinline__ Slot slot_info(const AttnArgs &a, uint32_t slot, uint
     s.rows = (uint32_t)min((uint64_t)RT, all - first);
     *units = a.c.kv_heads * (1 + a.end);
     if (PART == AT_FRONT) {
-        s.seq = a.prefix[b];
-        s.np = front_pages(a, b);
+        s.seq = a.seqs[b];
+        s.np = a.g.front[b];
         s.pos0 = s.np * KV_P;   // behind every shared token
         *units = a.c.kv_heads * (s.per_head() + a.end);
         return s;
@@ -179,11 +161,11 @@ __device__ __forceinline__ Slot slot_info(const AttnArgs &a, uint32_t slot, uint
         uint32_t lo = 0, hi = a.groups;
         while (hi - lo > 1) {
             const uint32_t mid = (lo + hi) >> 1;
-            if (group_entry(a, mid) <= b) lo = mid;
+            if (a.g.entry[mid] <= b) lo = mid;
             else hi = mid;
         }
         uint32_t front = 0;
-        if (group_entry(a, lo) <= b && b < group_entry(a, lo + 1)) front = front_pages(a, lo);
+        if (a.g.entry[lo] <= b && b < a.g.entry[lo + 1]) front = a.g.front[lo];
         else set_status(a.status, DGT_ERR_ARG);
         if (front && s.pos0 < (int32_t)(front * KV_P)) {
             // new rows inside the shared pages
@@ -410,10 +392,9 @@ __device__ __forceinline__ Cuts cut_plan(const AttnArgs &a, Units all, const Slo
     return k;
 }
 
-// Rows that see nothing: out 0, lse -inf (a front's are not read).
-template <uint32_t D, int PART = AT_ALL>
+// Rows that see nothing: out 0, lse -inf.
+template <uint32_t D>
 __device__ __forceinline__ void write_none(const AttnArgs &a, const Slot &s, uint32_t h, uint32_t t, uint32_t threads) {
-    if (PART == AT_FRONT) return;
     for (uint32_t i = t; i < s.rows * (D / 8); i += threads) {
         const uint32_t flat = s.row0 + i / (D / 8);
         const uint64_t at = (uint64_t)(s.tok0 + flat / a.group) * a.q_heads + h * a.group + flat % a.group;
@@ -447,9 +428,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, const Slot &s, uin
         float quot = none ? 0.0f : ex2(finite_base(MU) - finite_base(M) - wlog2) / L;
         const uint32_t flat = s.row0 + row;
         const uint64_t at = (uint64_t)(s.tok0 + flat / a.group) * a.q_heads + h * a.group + flat % a.group;
-        if (AP == AT_FRONT) {
-            a.front_lse[at] = none ? -INFINITY : M + __log2f(L);
-        } else if (AP == AT_TAIL) {
+        if (AP == AT_TAIL) {
             const TailJoin j = tail_join(a, s, at, none ? -INFINITY : M + __log2f(L));
             quot *= j.tail;
             front[row] = j.front;
@@ -534,10 +513,6 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, const Slot &s, uin
             const uint32_t flat = s.row0 + i / Q;
             const uint64_t o = (uint64_t)(s.tok0 + flat / a.group) * a.q_heads + h * a.group + flat % a.group;
             const float f = ro[b].y;
-            if (AP == AT_FRONT) {
-                reinterpret_cast<float4 *>(a.front + o * D)[i % Q] = make_float4(v[b][0] * f, v[b][1] * f, v[b][2] * f, v[b][3] * f);
-                continue;
-            }
             float4 y = make_float4(v[b][0] * f, v[b][1] * f, v[b][2] * f, v[b][3] * f);
             if (AP == AT_TAIL && s.joins) {
                 const float4 x = reinterpret_cast<const float4 *>(a.front + o * D)[i % Q];

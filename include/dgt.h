@@ -792,13 +792,17 @@ int dgt_kv_attention_ex(const dgt_kv_cache *cache, uint32_t layer, const dgt_hea
  * length 0 has rows that see nothing.  A group whose prefix holds fewer than
  * d_shared[g] tokens is an error, and so are entries of no group, both reported
  * in d_status (their sequences then see only their pages behind none), and an
- * entry with rows inside the shared pages (these rows: out 0, lse -inf).
+ * entry with rows inside shared pages that are taken together (these rows: out
+ * 0, lse -inf).
  * The precision is dgt_kv_attention's; the two parts are joined in fp32.  d_ws:
  * dgt_kv_attention_shared_workspace_bytes(...) bytes, 256-byte aligned, zeroed
  * before its first use, of whatever sizes later; calls that may overlap need
- * one each.  groups <= 65536 (else DGT_ERR_SHAPE).  flags as in
- * dgt_kv_attention_ex.
+ * one each.  groups <= 65536 (else DGT_ERR_SHAPE).  Where sharing saves too few
+ * reads of pages to be worth its join, or the sequences have many rows each,
+ * every sequence is taken on its own; DGT_KV_SHARE_ALWAYS in the flags: not.
+ * Other flags as in dgt_kv_attention_ex.
  */
+#define DGT_KV_SHARE_ALWAYS 1u
 size_t dgt_kv_attention_shared_workspace_bytes(const dgt_kv_cache *cache, uint32_t q_heads, uint32_t groups,
                                                uint32_t batch, uint64_t tokens);
 int dgt_kv_attention_shared(const dgt_kv_cache *cache, uint32_t layer, const dgt_heads *q, uint64_t tokens,

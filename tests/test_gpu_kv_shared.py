@@ -76,12 +76,12 @@ class Forks:
     def q(self, rows, hq):
         return torch.randn(rows, hq, self.dim, generator=self.g, device="cuda").bfloat16()
 
-    def call(self, q, counts, shared=None, **kw):
+    def call(self, q, counts, shared=None, always=True, **kw):
         one = all(n == 1 for n in counts)
         many = len(self.prompts) > 1
         return dgt.kv_attention_shared(self.c, self.layer, q, i32(*self.slots), i32(*range(len(self.prompts))),
                                        i32(*(shared or self.prompts)), groups=i32(*self.groups) if many else None,
-                                       cu=None if one else i32(*cu_of(counts)), **kw)
+                                       cu=None if one else i32(*cu_of(counts)), always=always, **kw)
 
     def check(self, q, counts, shared=None, scale=None, **kw):
         st = i32(0)
@@ -236,7 +236,8 @@ def test_what_the_device_reports():
 
     def call(seqs=f.slots, prefix=(0, 1), shared=(300, 200), groups=(0, 2, 4)):
         st = i32(0)
-        y = dgt.kv_attention_shared(f.c, 0, q, i32(*seqs), i32(*prefix), i32(*shared), groups=i32(*groups), status=st)
+        y = dgt.kv_attention_shared(f.c, 0, q, i32(*seqs), i32(*prefix), i32(*shared), groups=i32(*groups), status=st,
+                                    always=True)
         return y, dgt.read_status(st)
 
     y, st = call()
@@ -289,7 +290,7 @@ def test_a_stream_and_a_graph_that_follows_the_lengths():
     with torch.cuda.graph(g):
         dgt.kv_reserve(f.c, seqs, ones, start=start)
         dgt.kv_append(f.c, 0, k, v, seqs, start)
-        dgt.kv_attention_shared(f.c, 0, q, seqs, prefix, shared, out=out, ws=ws)
+        dgt.kv_attention_shared(f.c, 0, q, seqs, prefix, shared, out=out, ws=ws, always=True)
     for _ in range(70):
         g.replay()
     f.lens = [471] * 3

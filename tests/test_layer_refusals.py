@@ -139,4 +139,4 @@ def test_shared_attention_refuses(lib):
     assert call(g=65537) == SHAPE and call(t=5) == ARG and call(t=(1 << 24) + 1, cu=P) == SHAPE
     assert call(q=heads(6)) == SHAPE and call(q=heads(4 * 65)) == SHAPE and call(q=heads(8, ts=1025)) == ARG
     assert call(ws=None) == ARG and call(ws=P + 64) == ARG and call(n=need - 1) == ARG
-    assert call(flags=1) == ARG and call(t=0, b=0) == 0
+    assert call(flags=1 << 3) == ARG and call(t=0, b=0) == 0
