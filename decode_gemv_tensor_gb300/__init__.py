@@ -10,11 +10,12 @@ Names follow the C ABI: pack, unpack, write, read, upload, load_r4,
 load_r4_into, r4_to_bf16, gemv, gemv_bf16, gemv_slices, moe_gemv,
 moe_gemv_bf16, gemm, gemm_bf16, gemm_rebuild, gemm_plan, moe_gemm, moe_gemm_bf16,
 add_rmsnorm, silu_mul, silu_mul_rows, repeat, weighted_sum, exponent_stats,
-rotate, kv_append, kv_read, kv_attention, kv_reserve, kv_fork, kv_free,
-kv_copy_pages, kv_compact, read_status; Rotary and KvCache hold a rotation's
-frequencies and a paged 8-bit cache; DecodeStep and MoeDecodeStep compose a
-batch-1 decode step from them, with a StepAttention over a cache or without,
-and capture it in a CUDA graph.
+block_norm, route, beam_select, rotate, kv_append, kv_read, kv_attention,
+kv_attention_shared, kv_reserve, kv_reorder, kv_fork, kv_free, kv_copy_pages,
+kv_compact, read_status; Rotary and KvCache hold a rotation's frequencies and a
+paged 8-bit cache; DecodeStep and MoeDecodeStep compose a batch-1 decode step
+from them, with a StepAttention over a cache, StepNorms behind the blocks and a
+Router, or without, and capture it in a CUDA graph.
 """
 from __future__ import annotations
 
@@ -1263,6 +1264,54 @@ class StepAttention:
                      out=out.view(q.shape), ws=self.ws[q.shape[1]], status=self.status, stream=stream)
 
 
+class StepNorms:
+    """Norms behind the blocks of a decode step (models that norm a block's
+    output as well as its input), with gates and a scaled residual: block j of
+    the step (2l: layer l's attention, 2l + 1: its feed-forward part) adds
+    x = residual x + scale norm(y, post[j]) gate[j] instead of x + y.  post:
+    bf16 vectors, or None for blocks without; gate: bf16 vectors or None;
+    offset: added to the weights of all norms of the step (1 where they are
+    stored less 1).  Block j uses post[j % len(post)] and gate[j % len(gate)].
+    For DecodeStep and MoeDecodeStep."""
+
+    def __init__(self, post=None, gate=None, scale: float = 1.0, residual: float = 1.0, offset: float = 0.0):
+        self.post, self.gate, self.scale, self.residual, self.offset = post, gate, scale, residual, offset
+
+    def __call__(self, block, x, y, gamma, eps, h, stream=None):
+        """The norm before block `block`, behind the output y of the one before (None before the first)."""
+        if y is None:
+            block_norm(x, pre=gamma, offset=self.offset, eps=eps, x_out=x, h=h, stream=stream)
+            return
+        pick = lambda w: None if w is None else w[(block - 1) % len(w)]
+        block_norm(x, y, pre=gamma, post=pick(self.post), gate=pick(self.gate), scale=self.scale,
+                   residual=self.residual, offset=self.offset, eps=eps, x_out=x, h=h, stream=stream)
+
+
+class Router:
+    """The routing of a MoeDecodeStep from the token itself: logits = weights[l]
+    h (gemv_bf16), then route.  weights: bf16 tensors [experts, hidden], bias:
+    float32 vectors [experts] or None, of layer l at l % len; the others as in
+    route.  Steps that may run at a time need one each."""
+
+    def __init__(self, weights, topk: int, score: str = "softmax", bias=None, groups: int = 1, group_topk: int = 1,
+                 group_best: int = 2, renorm: bool = True, scale: float = 1.0):
+        import torch
+        self.weights, self.bias, self.topk = weights, bias, topk
+        self.kw = dict(score=score, groups=groups, group_topk=group_topk, group_best=group_best, renorm=renorm, scale=scale)
+        experts, dev = weights[0].shape[0], weights[0].device
+        self.y = torch.empty(experts, dtype=torch.bfloat16, device=dev), torch.empty(experts, device=dev)
+        self.ids = torch.empty((1, topk), dtype=torch.int32, device=dev)
+        self.p = torch.empty((1, topk), device=dev)
+        torch.cuda.synchronize(dev)     # the products stream the weights before their dependency wait
+
+    def __call__(self, layer: int, h, stream=None):
+        """(ids int32 [topk], p float32 [topk]) of the vector h, bf16 [hidden]; the same buffers each time."""
+        gemv_bf16(self.weights[layer % len(self.weights)], h, *self.y, stream=stream, static_weights=True)
+        bias = None if self.bias is None else self.bias[layer % len(self.bias)]
+        route(self.y[1].view(1, -1), self.topk, bias=bias, ids=self.ids, p=self.p, stream=stream, **self.kw)
+        return self.ids.view(-1), self.p.view(-1)
+
+
 class DecodeStep:
     """One batch-1 decode step through a stack of dense decoder layers, every
     op a kernel of this library.  Per layer, with the fp32 residual stream x:
@@ -1274,7 +1323,8 @@ class DecodeStep:
     and a final h = rmsnorm(x, g_final).  Without `attention` the output
     projection reads the value vector repeated over the query heads, as above;
     with a StepAttention a is the attention of the new token over its cache,
-    and every step appends one token.  layers: list of dicts proj -> R4 (or bf16 tensors [rows, cols] for
+    and every step appends one token.  norms: a StepNorms, for norms behind the
+    blocks too.  layers: list of dicts proj -> R4 (or bf16 tensors [rows, cols] for
     the twin), either q, k, v, o, gate, up, down, or the stacked form qkv
     (rows of q, then k, then v; k and v of equal size), o, gate_up (rows of
     gate, then up) and down, which computes the same step with one product
@@ -1284,9 +1334,9 @@ class DecodeStep:
     The R4 step and the BF16 step over the same weights give bit-identical
     outputs."""
 
-    def __init__(self, layers, gammas, depth=None, eps=1e-5, device=None, attention=None):
+    def __init__(self, layers, gammas, depth=None, eps=1e-5, device=None, attention=None, norms=None):
         import torch
-        self.attention = attention
+        self.attention, self.norms = attention, norms
         self.layers, self.gammas, self.eps = layers, gammas, eps
         self.depth = depth or len(layers)
         w0 = layers[0]
@@ -1323,6 +1373,12 @@ class DecodeStep:
         # (DGT_GEMV_STATIC_WEIGHTS): everything that wrote them must be done
         torch.cuda.synchronize(dev)
 
+    def _norm(self, block, gamma, h, y, stream):
+        if self.norms is None:
+            add_rmsnorm(self.x, gamma, self.eps, h, y, stream)
+        else:
+            self.norms(block, self.x, y, gamma, self.eps, h, stream)
+
     def _gemv(self, W, x, p, stream):
         # the step's weights are only read: they stream while the previous kernel ends
         y, y32 = self.y[p]
@@ -1340,8 +1396,8 @@ class DecodeStep:
             self.attention.begin(stream)
         for l in range(self.depth):
             W = self.layers[l % len(self.layers)]
-            add_rmsnorm(self.x, self.gammas[gi % (len(self.gammas) - 1)], self.eps, self.h,
-                        None if l == 0 else self.y["down"][1], stream)
+            self._norm(gi, self.gammas[gi % (len(self.gammas) - 1)], self.h, None if l == 0 else self.y["down"][1],
+                       stream)
             gi += 1
             for p in (("qkv",) if self.fused else ("q", "k", "v")):
                 self._gemv(W[p], self.h, p, stream)
@@ -1350,13 +1406,13 @@ class DecodeStep:
             else:
                 repeat(self.v16, self.a.numel(), self.a, stream)
             self._gemv(W["o"], self.a, "o", stream)
-            add_rmsnorm(self.x, self.gammas[gi % (len(self.gammas) - 1)], self.eps, self.h, self.y["o"][1], stream)
+            self._norm(gi, self.gammas[gi % (len(self.gammas) - 1)], self.h, self.y["o"][1], stream)
             gi += 1
             for p in (("gate_up",) if self.fused else ("gate", "up")):
                 self._gemv(W[p], self.h, p, stream)
             silu_mul(self.g32, self.u32, self.m, stream)
             self._gemv(W["down"], self.m, "down", stream)
-        add_rmsnorm(self.x, self.gammas[-1], self.eps, self.out, self.y["down"][1], stream)
+        self._norm(gi, self.gammas[-1], self.out, self.y["down"][1], stream)
 
     def __call__(self, x0, stream=None):
         """Eager step from the fp32 input x0: returns (x, out)."""
@@ -1415,19 +1471,19 @@ class MoeDecodeStep:
     and a final rmsnorm.  Wgate, Wup ([E * ffn, hidden]) and Wdown
     ([E * hidden, ffn]) stack the experts; the gate and up gathers take the
     token's h once for all its slots, the down gather takes slot j's m_j as
-    its own input.  Routing is an input (the router is not part of the
-    format).  layers: dicts with q, k, v, o, gate, up, down (R4, or bf16
+    its own input.  layers: dicts with q, k, v, o, gate, up, down (R4, or bf16
     tensors for the twin), or the stacked form qkv, o, gate_up, down, where
     gate_up stacks expert e's gate rows and then its up rows as expert e's
     block ([E * 2 ffn, hidden]): one product for q, k, v and one gather for
     gate and up.  routes: per layer (ids int32 [topk], p float32 [topk]) on
-    the device; layer l uses layers[l % len] and routes[l % len].  attention: a
-    StepAttention, as in DecodeStep.  The R4 step and the BF16 step give
+    the device; layer l uses layers[l % len] and routes[l % len].  Or a Router,
+    which finds them from h.  attention: a StepAttention, norms: a StepNorms, as
+    in DecodeStep.  The R4 step and the BF16 step give
     bit-identical outputs."""
 
-    def __init__(self, layers, gammas, routes, n_experts, depth=None, eps=1e-5, attention=None):
+    def __init__(self, layers, gammas, routes, n_experts, depth=None, eps=1e-5, attention=None, norms=None):
         import torch
-        self.attention = attention
+        self.attention, self.norms = attention, norms
         self.layers, self.gammas, self.routes, self.E, self.eps = layers, gammas, routes, n_experts, eps
         self.depth = depth or len(layers)
         w0 = layers[0]
@@ -1436,7 +1492,7 @@ class MoeDecodeStep:
         shape = (lambda w: (w.rows, w.cols)) if self.r4 else (lambda w: tuple(w.shape))
         hidden = shape(w0["o"])[0]
         ffn = shape(w0["down"])[1]
-        topk = routes[0][0].numel()
+        topk = routes.topk if isinstance(routes, Router) else routes[0][0].numel()
         dev = w0["o"].sm.device if self.r4 else w0["o"].device
         self.hidden, self.ffn, self.topk = hidden, ffn, topk
         f32 = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)
@@ -1467,6 +1523,8 @@ class MoeDecodeStep:
             attention.prepare(nq, self.depth)
         torch.cuda.synchronize(dev)     # the products stream weights before their dependency wait
 
+    _norm = DecodeStep._norm
+
     def _gemv(self, W, x, p, stream):
         y, y32 = self.y[p]
         if self.r4:
@@ -1484,8 +1542,7 @@ class MoeDecodeStep:
             self.attention.begin(stream)
         for l in range(self.depth):
             W = self.layers[l % len(self.layers)]
-            ids, p = self.routes[l % len(self.routes)]
-            add_rmsnorm(self.x, self.gammas[(2 * l) % ng], self.eps, self.h, None if l == 0 else self.comb, stream)
+            self._norm(2 * l, self.gammas[(2 * l) % ng], self.h, None if l == 0 else self.comb, stream)
             for pr in (("qkv",) if self.fused else ("q", "k", "v")):
                 self._gemv(W[pr], self.h, pr, stream)
             if self.attention is not None:
@@ -1493,7 +1550,11 @@ class MoeDecodeStep:
             else:
                 repeat(self.v16, self.a.numel(), self.a, stream)
             self._gemv(W["o"], self.a, "o", stream)
-            add_rmsnorm(self.x, self.gammas[(2 * l + 1) % ng], self.eps, self.h, self.y["o"][1], stream)
+            self._norm(2 * l + 1, self.gammas[(2 * l + 1) % ng], self.h, self.y["o"][1], stream)
+            if isinstance(self.routes, Router):
+                ids, p = self.routes(l, self.h, stream)
+            else:
+                ids, p = self.routes[l % len(self.routes)]
             ids1 = ids.view(1, self.topk)
             if self.fused:
                 self._moe(W["gate_up"], ids1, self.h.view(1, -1), self.ws_g, self.ygu, stream)
@@ -1504,7 +1565,7 @@ class MoeDecodeStep:
                 silu_mul(self.yg, self.yu, self.m.view(-1), stream)
             self._moe(W["down"], ids.view(self.topk, 1), self.m, self.ws_d, self.yd, stream)
             weighted_sum(self.yd, p, self.comb, stream)
-        add_rmsnorm(self.x, self.gammas[-1], self.eps, self.out, self.comb, stream)
+        self._norm(2 * self.depth, self.gammas[-1], self.out, self.comb, stream)
 
     def __call__(self, x0, stream=None):
         import torch

@@ -131,7 +131,7 @@ struct BeamShared {
     uint16_t order[BM_MAX_JOIN];
     double lse[BM_MAX_BEAMS];
     float2 sum[BM_MAX_BEAMS];
-    float shift[BM_MAX_BEAMS];
+    float shift[BM_MAX_BEAMS], score[BM_MAX_BEAMS];
     uint64_t best[BM_MAX_N];
     uint64_t top[BM_THREADS];
     float2 part[BM_WARPS];
@@ -151,8 +151,10 @@ __device__ __forceinline__ float2 join_sums(float2 p, uint32_t count) {
     for (int d = 16; d >= 1; d >>= 1) S += __shfl_xor_sync(DGT_FULL, S, d);
     return make_float2(B, S);
 }
+// Its logarithm, to 2^-19: a unit in the last place of logf, whose argument is
+// below 2^25 (in fp64 the function takes a microsecond).
 __device__ __forceinline__ double log_sum(float2 p) {
-    return p.y > 0.0f && p.y < INFINITY && fabsf(p.x) < INFINITY ? (double)p.x + log((double)p.y) : (double)INFINITY;
+    return p.y > 0.0f && p.y < INFINITY && fabsf(p.x) < INFINITY ? (double)p.x + (double)logf(p.y) : (double)INFINITY;
 }
 
 // The list's best n (fewer, when it has fewer) to its beginning, in order;
@@ -473,9 +475,18 @@ __device__ __forceinline__ double sum_again(const BeamArgs &a, uint64_t r, float
 // they are too many.  A block's largest total is in fp32, off by less than the
 // slack; a threshold that n blocks reach at least is the least of the warps'
 // k-th largest of their threads' largest, k warps >= n.
+constexpr uint32_t BM_KEEP = 16;
+// The first blocks of the thread: neighbouring blocks go to different warps.
+__device__ __forceinline__ uint32_t first_block() { return lane_id() * BM_WARPS + (threadIdx.x >> 5); }
+__device__ __forceinline__ void load_tops(const BeamArgs &a, uint64_t r0, float (&t)[BM_KEEP]) {
+    const uint32_t all = a.beams * a.row_blocks;
+#pragma unroll
+    for (uint32_t j = 0; j < BM_KEEP; j++)
+        t[j] = first_block() + j * BM_THREADS < all ? __ldcg(&a.tops[r0 * a.row_blocks + first_block() + j * BM_THREADS]) : -INFINITY;
+}
 template <bool F32>
-__device__ __forceinline__ bool read_again(const BeamArgs &a, BeamShared &s, uint64_t r0) {
-    constexpr uint32_t V = BeamRow<F32>::V, PIECES = BM_BLOCK / 32, KEEP = 16, TOGETHER = 4;
+__device__ __forceinline__ bool read_again(const BeamArgs &a, BeamShared &s, uint64_t r0, float (&t)[BM_KEEP]) {
+    constexpr uint32_t V = BeamRow<F32>::V, PIECES = BM_BLOCK / 32, KEEP = BM_KEEP, TOGETHER = 4;
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t all = a.beams * a.row_blocks;
     const float inv = 1.0f / (float)a.row_blocks;
@@ -489,11 +500,8 @@ __device__ __forceinline__ bool read_again(const BeamArgs &a, BeamShared &s, uin
         const float shift = s.shift[beam_of(i)];
         return shift > -INFINITY ? top + shift : -INFINITY;
     };
-    // neighbouring blocks go to different warps, a thread's first KEEP stay in registers
-    const uint32_t mine0 = lane * BM_WARPS + warp;
-    float t[KEEP], top = -INFINITY;
-#pragma unroll
-    for (uint32_t j = 0; j < KEEP; j++) t[j] = mine0 + j * BM_THREADS < all ? __ldcg(&tops[mine0 + j * BM_THREADS]) : -INFINITY;
+    const uint32_t mine0 = first_block();
+    float top = -INFINITY;
 #pragma unroll
     for (uint32_t j = 0; j < KEEP; j++) {
         if (mine0 + j * BM_THREADS < all) t[j] = total_of(mine0 + j * BM_THREADS, t[j]);
@@ -570,6 +578,8 @@ template <bool F32>
 __device__ __forceinline__ void join_entry(const BeamArgs &a, BeamShared &s, uint32_t entry) {
     const uint32_t tid = threadIdx.x, lane = tid & 31, n = a.n;
     const uint64_t r0 = (uint64_t)entry * a.beams;
+    float tops[BM_KEEP];   // on their way while the sums are joined
+    load_tops(a, r0, tops);
     if (tid == 0) s.blocks = 0, s.found = 0, s.refine = 0;
     // a beam without a score, without a finite sum, or at its end offers nothing of its row
     for (uint32_t b = tid / 32; b < a.beams; b += BM_WARPS) {
@@ -578,14 +588,14 @@ __device__ __forceinline__ void join_entry(const BeamArgs &a, BeamShared &s, uin
         if (lane == 0) s.sum[b] = p;
     }
     __syncthreads();
-    // fp64 is slow here: a lane for each beam, not a warp
     if (tid < a.beams) {
         const double lse = log_sum(s.sum[tid]);
-        s.lse[tid] = lse;
-        s.shift[tid] = lse < (double)INFINITY ? (float)((double)a.scores[r0 + tid] - lse) : -INFINITY;
+        const float score = a.scores[r0 + tid];
+        s.lse[tid] = lse, s.score[tid] = score;
+        s.shift[tid] = lse < (double)INFINITY ? (float)((double)score - lse) : -INFINITY;
     }
     __syncthreads();
-    if (!read_again<F32>(a, s, r0)) {
+    if (!read_again<F32>(a, s, r0, tops)) {
         // too many: the best n of each row
         __syncthreads();
         if (tid == 0) s.found = 0;
@@ -610,7 +620,7 @@ __device__ __forceinline__ void join_entry(const BeamArgs &a, BeamShared &s, uin
     const uint32_t count = s.found;
     auto total_of = [&](uint32_t i) {
         const uint32_t b = s.place[i] >> BM_BEAM_SHIFT;
-        const double score = (double)a.scores[r0 + b], lse = s.lse[b];
+        const double score = (double)s.score[b], lse = s.lse[b];
         return lse < (double)INFINITY ? score + ((double)s.logit[i] - lse) : score;
     };
     auto sort = [&]() {
