@@ -608,7 +608,7 @@ struct Plan {
 static Plan attn_plan(uint32_t head_dim, uint32_t group, uint32_t batch, uint64_t tokens) {
     const uint64_t rows = group * ((tokens + batch - 1) / batch);
     const uint64_t most = head_dim == 64 ? 24 : head_dim == 128 ? 16 : 8;
-    if (rows > most) return {0, prompt_rows(head_dim)};
+    if (rows > most) return {0, prompt_rows(head_dim, AT_ALL)};
     const uint32_t nt = (uint32_t)((rows + 7) / 8);
     return {nt, 8 * nt};
 }
@@ -620,7 +620,7 @@ static uint64_t slot_count(uint32_t RT, uint32_t group, uint32_t batch, uint64_t
 // The row tile and how the work is cut, and the launch.
 static int attn_run(AttnArgs &a, AttnPart part, cudaStream_t st) {
     const uint32_t head_dim = a.c.head_dim;
-    const Plan plan = part == AT_FRONT ? Plan{0, prompt_rows(head_dim)} : attn_plan(head_dim, a.group, a.batch, a.tokens);
+    const Plan plan = part == AT_FRONT ? Plan{0, prompt_rows(head_dim, part)} : attn_plan(head_dim, a.group, a.batch, a.tokens);
     const uint32_t nt = plan.nt, RT = plan.RT;
     a.slots = (uint32_t)slot_count(RT, a.group, a.batch, a.tokens, part == AT_FRONT || a.cu != nullptr);
     a.per_entry = (a.group + RT - 1) / RT;
@@ -748,7 +748,7 @@ __global__ void __launch_bounds__(1024) k_kv_groups(GroupArgs a) {
 // about 15 us, which is what few-row tiles take for reads of 256 MB out of L2.
 // Measured, 24 query and 8 kv heads of 128, one row a sequence: 16 sequences
 // of 4003 shared tokens (7400 reads) 34 us shared and 26 us each on its own, 48
-// (23000) 49 and 56 us, two groups of 16 of 20003 and 18600 (71000) 52 and 126
+// (23000) 43 and 55 us, two groups of 16 of 20003 and 18600 (71000) 50 and 125
 // us.  On the tensor-core tiles a read costs four times that: 4 sequences of 30
 // rows, 5000 shared tokens (1200) 45 and 30 us.
 static uint64_t worth_reads(uint32_t head_dim, uint64_t rows) {
@@ -759,9 +759,9 @@ static uint64_t worth_reads(uint32_t head_dim, uint64_t rows) {
 // from its neighbours (6 sequences of up to 512 tokens, 12040 shared: 309 us
 // shared, 278 us each on its own).
 static bool can_share(const dgt_kv_cache *c, uint32_t group, uint32_t groups, uint32_t batch, uint64_t tokens) {
-    const uint64_t rows = group * ((tokens + batch - 1) / batch), rt = prompt_rows(c->head_dim);
+    const uint64_t rows = group * ((tokens + batch - 1) / batch), rt = prompt_rows(c->head_dim, AT_FRONT);
     const uint64_t tiles = groups * ((group * ((tokens + groups - 1) / groups) + rt - 1) / rt);
-    return rows <= rt / 2 && batch > tiles &&
+    return rows <= prompt_rows(c->head_dim, AT_ALL) / 2 && batch > tiles &&
            (batch - tiles) * c->max_pages * c->kv_heads >= worth_reads(c->head_dim, rows);
 }
 
@@ -775,7 +775,7 @@ struct SharedSpace {
         lse = groups + (12 * ((size_t)ngroups + 1) + 255) / 256 * 256;
         out = lse + (rows * 4 + 255) / 256 * 256;
         part[0] = out + rows * c->head_dim * 4;
-        part[1] = part[0] + part_bytes(c->head_dim, Plan{0, prompt_rows(c->head_dim)});
+        part[1] = part[0] + part_bytes(c->head_dim, Plan{0, prompt_rows(c->head_dim, AT_FRONT)});
         bytes = part[1] + dgt_kv_attention_workspace_bytes(c, q_heads, batch, tokens) - AT_COUNT_BYTES;
     }
 };
@@ -820,7 +820,7 @@ extern "C" int dgt_kv_attention_shared(const dgt_kv_cache *cache, uint32_t layer
 
     uint32_t *t = (uint32_t *)(w + at.groups);
     f.g = a.g = Groups{t, t + groups + 1, t + 2 * ((size_t)groups + 1)};
-    const GroupArgs ga{*cache, d_groups, d_prefix, d_shared, d_cu, groups, batch, a.group, prompt_rows(cache->head_dim),
+    const GroupArgs ga{*cache, d_groups, d_prefix, d_shared, d_cu, groups, batch, a.group, prompt_rows(cache->head_dim, AT_FRONT),
                        always ? 0 : worth_reads(cache->head_dim, a.group * ((tokens + batch - 1) / batch)), a.g, d_status};
     if (launch_pdl(k_kv_groups, dim3(1), dim3(1024), 0, st, ga) != cudaSuccess) return DGT_ERR_CUDA;
     f.front_lse = a.front_lse = (float *)(w + at.lse), f.front = a.front = (float *)(w + at.out);

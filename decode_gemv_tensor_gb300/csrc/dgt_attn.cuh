@@ -202,7 +202,7 @@ __device__ __forceinline__ TailJoin tail_join(const AttnArgs &a, const Slot &s, 
 }
 
 // Many rows (dgt_prompt.cu): the rows of its tile, and its launch.
-uint32_t prompt_rows(uint32_t head_dim);
+uint32_t prompt_rows(uint32_t head_dim, AttnPart part);
 int prompt_launch(const AttnArgs &a, AttnPart part, cudaStream_t st);
 
 // Units and row tiles that hold rows, counted together.

@@ -35,9 +35,11 @@ constexpr uint32_t PR_WARPS = 15;    // 0-7 rows, 8-11 values to fp16, 12-13 mat
 constexpr uint32_t PR_CONV = 128;    // threads that convert values
 constexpr uint32_t PR_META = 16;
 
-template <uint32_t D>
+template <uint32_t D, int AP>
 struct PromptCfg {
-    static constexpr uint32_t NSTR = D <= 128 ? 2 : 1, RT = 128 * NSTR;   // row tiles of 128
+    // Row tiles of 128: a front's rows rarely fill two, and more CTAs have a share of them (48 sequences of 4003 shared
+    // tokens, 24 / 8 heads of 128, 144 rows: 43 us; in tiles of two 49 us).
+    static constexpr uint32_t NSTR = D <= 128 && AP != AT_FRONT ? 2 : 1, RT = 128 * NSTR;
     static constexpr uint32_t RB = D < 128 ? 64 : 128, PAN = D / RB;       // operand row bytes, panels
     static constexpr uint32_t PB = KV_P * D;                               // bytes of a page's block
     static constexpr uint32_t KS = D <= 128 ? 6 : 3, VS = D <= 128 ? 4 : 2, WS = VS;   // stages: keys, values, fp16 values
@@ -149,7 +151,7 @@ __device__ __forceinline__ void add_front(const AttnArgs &a, uint64_t at, float 
 
 template <uint32_t D, int PART = AT_ALL>
 __global__ void __launch_bounds__(PR_WARPS * 32, 1) k_kv_prompt(AttnArgs a) {
-    using Cfg = PromptCfg<D>;
+    using Cfg = PromptCfg<D, PART>;
     constexpr uint32_t NSTR = Cfg::NSTR, RT = Cfg::RT, RB = Cfg::RB, PAN = Cfg::PAN, PB = Cfg::PB, QP = Cfg::QP,
                        KS = Cfg::KS, VS = Cfg::VS, WS = Cfg::WS;
     extern __shared__ uint8_t smem_raw[];
@@ -776,12 +778,12 @@ static int prompt_launch_part(const AttnArgs &a, cudaStream_t st) {
     const uint64_t bit = di.device < 64 ? 1ull << di.device : 0;
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
         if (cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)PromptCfg<D>::bytes) != cudaSuccess)
+                                 (int)PromptCfg<D, PART>::bytes) != cudaSuccess)
             return DGT_ERR_CUDA;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
     const unsigned grid = std::min((unsigned)di.sms, AT_MAX_SMS);
-    return launch_pdl(fn, dim3(grid), dim3(PR_WARPS * 32), PromptCfg<D>::bytes, st, a) == cudaSuccess ? DGT_OK
+    return launch_pdl(fn, dim3(grid), dim3(PR_WARPS * 32), PromptCfg<D, PART>::bytes, st, a) == cudaSuccess ? DGT_OK
                                                                                                       : DGT_ERR_CUDA;
 }
 
@@ -792,7 +794,7 @@ static int prompt_launch_d(const AttnArgs &a, AttnPart part, cudaStream_t st) {
                               : prompt_launch_part<D, AT_TAIL>(a, st);
 }
 
-uint32_t prompt_rows(uint32_t head_dim) { return head_dim <= 128 ? 256 : 128; }
+uint32_t prompt_rows(uint32_t head_dim, AttnPart part) { return head_dim <= 128 && part != AT_FRONT ? 256 : 128; }
 
 int prompt_launch(const AttnArgs &a, AttnPart part, cudaStream_t st) {
     switch (a.c.head_dim) {
