@@ -701,7 +701,8 @@ def block_norm(x, y=None, pre=None, post=None, gate=None, scale: float = 1.0, re
     rows = shape[0] if len(shape) == 2 else 1
     sx = _row_stride(x, "x", shape, dev)
     if x_out is None:
-        x_out, so = _empty(x, shape, dtype, stream), n
+        x_out, so = torch.empty_like(x, memory_format=torch.contiguous_format) if stream is None else \
+            _new(shape, dtype, x.device, stream), n
     else:
         so = _row_stride(x_out, "x_out", shape, dev)
         if x_out.dtype is not dtype or (rows > 1 and abs(so) < n):

@@ -14,6 +14,13 @@
 // sums are made again, from terms of about 2^-35 (a table of 2^(j/32), a short
 // polynomial, three floats) added as whole numbers: rows of the same logits in
 // any order then have the same sum, and beams that tie are seen to.
+//
+// What bounds it: many rows HBM (24 x 8 of 262144 bf16 logits, one beam in
+// eight at its end: 34 us, of which the stream of 88 MB takes 16 to 19 and the
+// join of the last entry 9), few the steps of the join (four beams of 128256,
+// one alive: 11.6 us; 6 x 5 of 50257 fp32: 13.5).  A stream that collects the
+// candidates itself, with a threshold and a list in shared memory, took 45 us
+// for the first.
 #include <cuda_runtime.h>
 
 #include <algorithm>

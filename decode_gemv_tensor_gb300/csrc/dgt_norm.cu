@@ -5,6 +5,13 @@
 //   r(v) = 1 / sqrt(mean v^2 + eps).
 // Everything is fp32 in between; x' and h are each rounded once, h from x'
 // before its rounding.
+//
+// What bounds it: HBM for many rows (8191 of 3840, x and y fp32: 67.6 us, 6.5
+// TB/s, 96 % of the measured copy rate), for one row the launch and two
+// reductions (2.7 us).  Every row is read once and held in registers: a CTA a
+// row, of as many threads as it has 16-byte pieces of 8 elements, so that no
+// more than one barrier stands between a row's two reductions; rows of up to
+// 32 pieces in part of a warp, several a CTA.
 #include <cuda_runtime.h>
 
 #include "../../include/dgt.h"
@@ -51,14 +58,33 @@ __device__ __forceinline__ void store_row(void *p, bool f32, uint64_t at, const 
         } else {
             uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; i++)
-                w[i] = f32_to_bf16_rne(v[2 * i]) | (uint32_t)f32_to_bf16_rne(v[2 * i + 1]) << 16;
+            for (int i = 0; i < 4; i++) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     } else if (f32) {
         static_cast<float *>(p)[at] = v[0];
     } else {
         static_cast<uint16_t *>(p)[at] = f32_to_bf16_rne(v[0]);
+    }
+}
+
+// The same for elements [at, at + W) of a row of n of which some may be outside
+// it: those read as 0 and are not stored.
+template <int W>
+__device__ __forceinline__ void load_edge(const void *p, bool f32, uint64_t row, int at, uint32_t n, float (&v)[W]) {
+#pragma unroll
+    for (int i = 0; i < W; i++) {
+        float x[1] = {0.0f};
+        if (at + i >= 0 && at + i < (int)n) load_row<1>(p, f32, row + at + i, x);
+        v[i] = x[0];
+    }
+}
+template <int W>
+__device__ __forceinline__ void store_edge(void *p, bool f32, uint64_t row, int at, uint32_t n, const float (&v)[W]) {
+#pragma unroll
+    for (int i = 0; i < W; i++) {
+        const float x[1] = {v[i]};
+        if (at + i >= 0 && at + i < (int)n) store_row<1>(p, f32, row + at + i, x);
     }
 }
 
@@ -80,9 +106,12 @@ __device__ __forceinline__ float row_sum(float v, uint32_t group, float *part) {
 }
 
 // J vectors of W elements a thread; a row is `group` threads' (CTA: all of
-// them).
-template <int W, int J, bool CTA>
-__global__ void __launch_bounds__(1024) k_block_norm(NormArgs a, uint32_t group) {
+// them).  SHIFT: rows that begin anywhere, all tensors' at the same place of a
+// 16-byte piece; their pieces are as aligned as ever, the first and last of a
+// row cut, and the weights, which begin at their own, are read one by one (1000
+// rows of 12345 bf16: 48 us; everything one by one 81 us).
+template <int W, int J, bool CTA, bool SHIFT>
+__global__ void __launch_bounds__(1024, 1) k_block_norm(NormArgs a, uint32_t group) {
     __shared__ float part[2][32];
     pdl_trigger();
     pdl_wait();
@@ -92,21 +121,36 @@ __global__ void __launch_bounds__(1024) k_block_norm(NormArgs a, uint32_t group)
     const bool live = row < a.rows;
     const uint64_t r = live ? row : a.rows - 1;   // rows behind the last are computed and not stored
     const bool xf = io.x_f32, yf = io.y_f32;
-    auto col = [&](int j) { return (t + j * group) * W; };
-    auto in = [&](int j) { return col(j) < a.n; };
+    const int ph = SHIFT ? (int)(((int64_t)r * io.x_stride) & 7) : 0;
+    auto col = [&](int j) { return (int)((t + j * group) * W) - ph; };
+    auto in = [&](int j) { return col(j) < (int)a.n; };
+    auto whole = [&](int j) { return !SHIFT || (col(j) >= 0 && col(j) + W <= (int)a.n); };
+    auto load = [&](const void *p, bool f32, int64_t stride, int j, float (&v)[W]) {
+        if (whole(j) && (!SHIFT || stride || ph == 0)) load_row<W>(p, f32, r * stride + col(j), v);
+        else load_edge<W>(p, f32, r * stride, col(j), a.n, v);
+    };
+    auto store = [&](void *p, bool f32, int64_t stride, int j, const float (&v)[W]) {
+        if (whole(j)) store_row<W>(p, f32, r * stride + col(j), v);
+        else store_edge<W>(p, f32, r * stride, col(j), a.n, v);
+    };
     float x[J][W], u[J][W];
     const float inv_n = 1.0f / (float)a.n;
 #pragma unroll
     for (int j = 0; j < J; j++) {
 #pragma unroll
         for (int i = 0; i < W; i++) u[j][i] = 0.0f;
-        if (io.y && in(j)) load_row<W>(io.y, yf, r * io.y_stride + col(j), u[j]);
+        if (io.y && in(j)) load(io.y, yf, io.y_stride, j, u[j]);
     }
-#pragma unroll
-    for (int j = 0; j < J; j++) {
+    // x travels with y, where both fit the registers
+    constexpr bool EARLY = J * W <= 16;
+    auto load_x = [&](int j) {
 #pragma unroll
         for (int i = 0; i < W; i++) x[j][i] = 0.0f;
-        if (in(j)) load_row<W>(io.x, xf, r * io.x_stride + col(j), x[j]);
+        if (in(j)) load(io.x, xf, io.x_stride, j, x[j]);
+    };
+    if (EARLY) {
+#pragma unroll
+        for (int j = 0; j < J; j++) load_x(j);
     }
     if (io.post) {
         float ss = 0.0f;
@@ -119,7 +163,7 @@ __global__ void __launch_bounds__(1024) k_block_norm(NormArgs a, uint32_t group)
         for (int j = 0; j < J; j++) {
             if (!in(j)) continue;
             float w[W];
-            load_row<W>(io.post, false, col(j), w);
+            load(io.post, false, 0, j, w);
 #pragma unroll
             for (int i = 0; i < W; i++) u[j][i] = u[j][i] * f * (a.offset + w[i]);
         }
@@ -127,10 +171,11 @@ __global__ void __launch_bounds__(1024) k_block_norm(NormArgs a, uint32_t group)
     float ss = 0.0f;
 #pragma unroll
     for (int j = 0; j < J; j++) {
+        if (!EARLY) load_x(j);
         if (!in(j)) continue;
         if (io.gate) {
             float g[W];
-            load_row<W>(io.gate, false, r * io.gate_stride + col(j), g);
+            load(io.gate, false, io.gate_stride, j, g);
 #pragma unroll
             for (int i = 0; i < W; i++) u[j][i] *= g[i];
         }
@@ -140,7 +185,7 @@ __global__ void __launch_bounds__(1024) k_block_norm(NormArgs a, uint32_t group)
             if (io.y) x[j][i] = fmaf(a.scale, u[j][i], x[j][i]);
             ss = fmaf(x[j][i], x[j][i], ss);
         }
-        if (io.x_out && live) store_row<W>(io.x_out, xf, r * io.xo_stride + col(j), x[j]);
+        if (io.x_out && live) store(io.x_out, xf, io.xo_stride, j, x[j]);
     }
     if (io.h) {
         const float f = 1.0f / sqrtf(row_sum<CTA>(ss, group, part[1]) * inv_n + a.eps);
@@ -148,26 +193,26 @@ __global__ void __launch_bounds__(1024) k_block_norm(NormArgs a, uint32_t group)
         for (int j = 0; j < J; j++) {
             if (!in(j)) continue;
             float w[W];
-            load_row<W>(io.pre, false, col(j), w);
+            load(io.pre, false, 0, j, w);
 #pragma unroll
             for (int i = 0; i < W; i++) w[i] = x[j][i] * f * (a.offset + w[i]);
-            if (live) store_row<W>(io.h, false, r * io.h_stride + col(j), w);
+            if (live) store(io.h, false, io.h_stride, j, w);
         }
     }
 }
 
-template <int W, int J>
+template <int W, int J, bool SHIFT = false>
 static cudaError_t norm_launch(NormArgs &a, cudaStream_t st) {
-    const uint32_t need = (a.n + W * J - 1) / (W * J);   // threads of a row
+    const uint32_t need = (a.n + (SHIFT ? 7 : 0) + W * J - 1) / (W * J);   // threads of a row
     if (need <= 32) {
         uint32_t group = 1;
         while (group < need) group *= 2;
         a.rows_cta = 256 / group;
         const uint64_t grid = (a.rows + a.rows_cta - 1) / a.rows_cta;
-        return launch_pdl(k_block_norm<W, J, false>, dim3((unsigned)grid), dim3(256), 0, st, a, group);
+        return launch_pdl(k_block_norm<W, J, false, SHIFT>, dim3((unsigned)grid), dim3(256), 0, st, a, group);
     }
     const uint32_t threads = (need + 31) / 32 * 32;
-    return launch_pdl(k_block_norm<W, J, true>, dim3((unsigned)a.rows), dim3(threads), 0, st, a, threads);
+    return launch_pdl(k_block_norm<W, J, true, SHIFT>, dim3((unsigned)a.rows), dim3(threads), 0, st, a, threads);
 }
 
 }  // namespace dgt
@@ -189,18 +234,23 @@ extern "C" int dgt_block_norm(const dgt_norm *io, uint64_t rows, uint32_t n, flo
     NormArgs a{*io, rows, n, 0, scale, residual, offset, eps};
     const uintptr_t all = (uintptr_t)io->x | (uintptr_t)io->x_out | (uintptr_t)io->y | (uintptr_t)io->h |
                           (uintptr_t)io->pre | (uintptr_t)io->post | (uintptr_t)io->gate;
-    int64_t strides = rows > 1 ? io->x_stride : 0;
+    // the strides' places in a piece, and where they differ
+    const int64_t s0 = rows > 1 ? io->x_stride : 0;
+    int64_t odd = 0;
     if (rows > 1) {
-        if (io->x_out) strides |= io->xo_stride;
-        if (io->y) strides |= io->y_stride;
-        if (io->h) strides |= io->h_stride;
-        if (io->gate) strides |= io->gate_stride;
+        if (io->x_out) odd |= io->xo_stride ^ s0;
+        if (io->y) odd |= io->y_stride ^ s0;
+        if (io->h) odd |= io->h_stride ^ s0;
+        if (io->gate && io->gate_stride) odd |= io->gate_stride ^ s0;
     }
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
-    // 16-byte pieces where everything allows them
-    if (n % 8 == 0 && (all & 15) == 0 && (strides & 7) == 0)
+    // 16-byte pieces where everything allows them; cut ones at the rows' ends cost more than they save in short rows
+    // (60000 of 125: 57 us, one by one 40; 3000 of 1025: 11.4, of 1023 one by one 14.4)
+    if ((all & 15) == 0 && (odd & 7) == 0 && n % 8 == 0 && (s0 & 7) == 0)
         e = n <= 8192 ? norm_launch<8, 1>(a, st) : n <= 16384 ? norm_launch<8, 2>(a, st) : norm_launch<8, 4>(a, st);
+    else if ((all & 15) == 0 && (odd & 7) == 0 && n > 512)
+        e = n <= 8184 ? norm_launch<8, 1, true>(a, st) : n <= 16376 ? norm_launch<8, 2, true>(a, st) : n <= 32760 ? norm_launch<8, 4, true>(a, st) : norm_launch<1, 32>(a, st);
     else
         e = n <= 4096 ? norm_launch<1, 4>(a, st) : n <= 16384 ? norm_launch<1, 16>(a, st) : norm_launch<1, 32>(a, st);
     return e == cudaSuccess ? DGT_OK : DGT_ERR_CUDA;

@@ -15,6 +15,12 @@
 // further apart than that is decided again by a warp in two floats, to 2^-36,
 // and one where that is not enough in fp64.  Logits alone are compared as they
 // are.
+//
+// What bounds it: instructions and the steps of a token that wait for one
+// another (8201 tokens, 256 experts in 8 groups, sigmoid and bias: 19 us, of
+// which 3 decide a token or two again and 5 are the groups; the logits' bytes
+// take 1.3).  One token of 128 experts 3.7 us.  fp64 alone for the close ones
+// took 16 us of 36; a score of its own for each lane's logit is what stays.
 #include <cuda_runtime.h>
 
 #include "../../include/dgt.h"
@@ -25,8 +31,8 @@ namespace dgt {
 
 constexpr uint32_t RT_WARPS = 4;
 constexpr uint32_t RT_MAX_EXPERTS = 1024;
-constexpr uint32_t RT_FEW = 12;
-constexpr int RT_CTAS = 8;
+constexpr uint32_t RT_FEW = 12;   // choices by threshold: 8 of 256 experts 8.8 us for 8201 tokens, one by one 12.0
+constexpr int RT_CTAS = 8;   // CTAs an SM: 8201 tokens 19.0 us, 20.3 with 10, 23.1 with what 80 registers allow
 constexpr float RT_LOG2E = 1.4426950408889634f;
 
 struct RouteArgs {
@@ -626,6 +632,8 @@ extern "C" int dgt_route(const dgt_router *r, const void *d_logits, int64_t stri
     cudaStream_t st = (cudaStream_t)stream;
     const uint32_t E = r->experts, epl = (E + 31) / 32;
     cudaError_t e;
+    // Few experts leave most of a warp empty: 90000 tokens of 16 experts 14 us, with a warp each 41; 16000 of 128 12.9
+    // and 13.3.
     if (r->groups == 1 && r->topk <= 8 && E <= 64)
         e = E <= 8 ? route_launch<8, 1>(a, st) : E <= 16 ? route_launch<8, 2>(a, st) : E <= 32 ? route_launch<8, 4>(a, st) : route_launch<8, 8>(a, st);
     else if (r->groups == 1 && r->topk <= 16 && E <= 128)
