@@ -769,6 +769,8 @@ extern "C" int dgt_beam_select(const void *d_logits, uint32_t f32, int64_t strid
         (((uintptr_t)d_scores | (uintptr_t)d_parent | (uintptr_t)d_token | (uintptr_t)d_total) & 3))
         return DGT_ERR_ARG;
     if ((d_done && (eos < 0 || (uint32_t)eos >= vocab)) || (d_done_out && !d_done)) return DGT_ERR_ARG;
+    // scores and ends are read until the last output is written
+    if (d_total == d_scores || (d_done_out && d_done_out == d_done)) return DGT_ERR_ARG;
     if (!d_ws || ((uintptr_t)d_ws & 255) || ws_bytes < dgt_beam_workspace_bytes(batch, beams, vocab, n)) return DGT_ERR_ARG;
     DeviceInfo di;
     if (device_info(&di) != DGT_OK) return DGT_ERR_CUDA;

@@ -210,9 +210,33 @@ def test_refusals():
     with pytest.raises(ValueError):
         dgt.beam_select(x.half(), s, 4)
     for kw in (dict(n=65), dict(n=4, done=torch.zeros(2, 2, dtype=torch.uint8, device="cuda")),
-               dict(n=4, ws=torch.zeros(256, dtype=torch.uint8, device="cuda"))):
+               dict(n=4, ws=torch.zeros(256, dtype=torch.uint8, device="cuda")), dict(n=2, total=s)):
         with pytest.raises(dgt.DgtError):
             dgt.beam_select(x, s, **kw)
+
+
+def test_two_calls_at_a_time():
+    """On two streams, a workspace each."""
+    runs = []
+    for seed in (1, 2):
+        x, s = inputs(8, 4, 60000, BF16, seed)
+        runs.append((x, s, dgt.beam_select(x, s, 8), dgt.beam_workspace(8, 4, 60000, 8), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for x, s, _, ws, stream in runs:
+            got.append(dgt.beam_select(x, s, 8, ws=ws, stream=stream))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, runs[i % 2][2]))
+
+
+def test_few_blocks_and_many_choices():
+    """Rows of a few blocks of 1 KB: fewer than the choices, and as many as the warps."""
+    for vocab, beams, n in ((100, 2, 64), (513, 1, 16), (1500, 1, 64), (3001, 2, 33), (4100, 4, 16), (2000, 32, 64)):
+        for dt in (F32, BF16):
+            x, s = inputs(2, beams, vocab, dt, vocab)
+            check(x, s, n)
 
 
 # ---- kv_reorder
@@ -262,6 +286,19 @@ def test_reorder(groups, beams, width, other):
     c = cache_of(rows, lens, slots * width)
     st = i32(0)
     dgt.kv_reorder(c, i32(*seqs), i32(*parent), dst=i32(*dst) if other else None, status=st)
+    new, nl = reorder_reference(rows, lens, seqs, parent, dst)
+    assert c.table.tolist() == new and c.lens.tolist() == nl
+    assert torch.equal(c.refs, refs_of(c)) and dgt.read_status(st) == 0
+
+
+def test_reorder_over_groups_that_read_one_another():
+    """All at once: targets that other groups read still give what they were."""
+    rows = [[i * 2, i * 2 + 1] for i in range(6)]
+    lens = [10 + i for i in range(6)]
+    seqs, dst, parent = ((0, 1, 2), (3, 4, 5)), ((3, 4, 5), (0, 1, 2)), ((1, 1, 0), (2, -1, 0))
+    c = cache_of(rows, lens)
+    st = i32(0)
+    dgt.kv_reorder(c, i32(*seqs), i32(*parent), dst=i32(*dst), status=st)
     new, nl = reorder_reference(rows, lens, seqs, parent, dst)
     assert c.table.tolist() == new and c.lens.tolist() == nl
     assert torch.equal(c.refs, refs_of(c)) and dgt.read_status(st) == 0

@@ -157,6 +157,17 @@ def test_many_small_groups():
     f.check(f.q(300, 4), [1] * 300)
 
 
+@pytest.mark.parametrize("hq,hk,dim", [(24, 8, 128), (16, 8, 256), (32, 8, 64)])
+def test_shared_by_itself_where_it_pays(hq, hk, dim):
+    """Without `always`: groups that are worth it beside one that is not, and in a cache whose tables could hold more
+    than any of them has."""
+    own = [[1 + i % 70 for i in range(70)], [2, 1], [1] * 60]
+    f = Forks([9000, 300, 8100], own, hk, dim, seed=dim + 1, max_pages=400)
+    f.check(f.q(132, hq), [1] * 132, always=False)
+    few = Forks([500], [[1, 20, 3]], hk, dim, seed=dim + 2, max_pages=4000)
+    few.check(few.q(3, hq), [1] * 3, always=False)
+
+
 def test_fewer_shared_tokens_than_there_are():
     f = Forks([1000], [[1, 80, 20]], 4, 128, seed=1)
     for shared in (0, 1, 63, 64, 500, 999, 1000):

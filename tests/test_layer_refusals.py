@@ -64,7 +64,7 @@ def test_route_pointers_and_sizes(lib):
     assert lib.dgt_route(None, P, 64, 1, P, P, None) == ARG
 
 
-def beam(lib, l=P, f32=0, s=P, done=None, eos=-1, batch=2, beams=4, vocab=1000, n=8, parent=P, token=P, total=P,
+def beam(lib, l=P, f32=0, s=P, done=None, eos=-1, batch=2, beams=4, vocab=1000, n=8, parent=P, token=P, total=4 * P,
          done_out=None, ws=P, short=0):
     need = int(lib.dgt_beam_workspace_bytes(batch, beams, vocab, n))
     return lib.dgt_beam_select(l, f32, vocab, s, done, eos, batch, beams, vocab, n, parent, token, total, done_out, ws,
@@ -77,7 +77,8 @@ def beam(lib, l=P, f32=0, s=P, done=None, eos=-1, batch=2, beams=4, vocab=1000, 
     (dict(batch=65537), SHAPE), (dict(l=None), ARG), (dict(s=None), ARG), (dict(parent=None), ARG),
     (dict(token=None), ARG), (dict(total=None), ARG), (dict(f32=2), ARG), (dict(l=P + 1), ARG),
     (dict(l=P + 2, f32=1), ARG), (dict(s=P + 2), ARG), (dict(done=P), ARG), (dict(done=P, eos=1000), ARG),
-    (dict(done_out=P), ARG), (dict(ws=None), ARG), (dict(ws=P + 64), ARG), (dict(short=1), ARG)])
+    (dict(done_out=P), ARG), (dict(s=2 * P, total=2 * P), ARG), (dict(done=2 * P, eos=1, done_out=2 * P, total=3 * P), ARG),
+    (dict(ws=None), ARG), (dict(ws=P + 64), ARG), (dict(short=1), ARG)])
 def test_beam_select_refuses(lib, change, code):
     assert beam(lib, **change) == code
 
