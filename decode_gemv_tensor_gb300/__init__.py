@@ -660,8 +660,12 @@ def _here(x, name):
 
 
 def _empty(like, shape, dtype, stream):
-    """_new beside a tensor, without its cost where the current stream is meant."""
-    return like.new_empty(shape, dtype=dtype) if stream is None else _new(shape, dtype, like.device, stream)
+    """_new beside a tensor, without its cost where the current stream is meant
+    (torch.empty: Tensor.new_empty between launches takes a microsecond more)."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    return _new(shape, dtype, like.device, stream)
 
 
 def _row_stride(x, name, shape, dev):
@@ -834,8 +838,13 @@ def beam_select(logits, scores, n: int, eos: int = -1, done=None, parent=None, t
         _vector(x, name, batch * n, dt, dev)
         return x
 
-    parent, token = given(parent, "parent", torch.int32), given(token, "token", torch.int32)
-    total = given(total, "total", torch.float32)
+    if stream is None and parent is None and token is None and total is None:
+        where, i32 = logits.device, torch.int32
+        parent, token = torch.empty(out, dtype=i32, device=where), torch.empty(out, dtype=i32, device=where)
+        total = torch.empty(out, dtype=torch.float32, device=where)
+    else:
+        parent, token = given(parent, "parent", torch.int32), given(token, "token", torch.int32)
+        total = given(total, "total", torch.float32)
     if done is not None:
         done_out = given(done_out, "done_out", torch.uint8)
     if ws is None:
