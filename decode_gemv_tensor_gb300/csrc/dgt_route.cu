@@ -413,7 +413,7 @@ __device__ __noinline__ bool decide(const RouteArgs &a, const void *row, uint64_
         }
 #pragma unroll
         for (int i = 0; i < EPL; i++)
-            if (!(open >> ((lane * EPL + i) / per) & 1u)) key[i] = 0;
+            if (lane * EPL + i < a.experts && !(open >> (lane * EPL + i) / per & 1u)) key[i] = 0;
     }
     uint64_t mine, next;
     uint32_t next_id;
@@ -429,9 +429,10 @@ __device__ __noinline__ bool decide(const RouteArgs &a, const void *row, uint64_
     return clear;
 }
 
-// The greatest two of what a group's lanes hold, GLANES neighbouring ones.
+// The greatest two of what a group's lanes hold.  fmaxf leaves a NaN out, and has to see x first: the least of `one` and
+// a NaN is `one`, which would count twice.
 __device__ __forceinline__ void top_two(float &one, float &two, float x) {
-    two = fmaxf(two, fminf(one, x));
+    two = fminf(one, fmaxf(two, x));
     one = fmaxf(one, x);
 }
 
@@ -540,7 +541,10 @@ __global__ void __launch_bounds__(RT_WARPS * 32, EPL <= 8 ? RT_CTAS : 1) k_route
         } else {
             const uint32_t open = __ballot_sync(DGT_FULL, in);
 #pragma unroll
-            for (int i = 0; i < EPL; i++) shut |= (open >> ((lane * EPL + i) / per) & 1u ? 0u : 1u) << i;
+            for (int i = 0; i < EPL; i++) {
+                const uint32_t e = lane * EPL + i;
+                shut |= (e < a.experts && open >> e / per & 1u ? 0u : 1u) << i;
+            }
         }
     }
     if (a.bias == nullptr && GL == 32 && a.groups > 1) {

@@ -95,6 +95,22 @@ def test_values_that_differ_by_less_than_fp32_can_tell(score):
         check(x[r:r + 1], 8, score=score, bias=b, groups=8, group_topk=3)
 
 
+@pytest.mark.parametrize("experts,groups,keep", [(160, 32, 9), (60, 20, 5), (96, 3, 2), (84, 12, 4), (341, 31, 11),
+                                                 (992, 31, 30), (264, 2, 1)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("best", [1, 2])
+def test_close_groups(experts, groups, keep, score, best):
+    """Groups whose values add up to nearly the same, in numbers of groups that leave lanes over."""
+    x = logits(100, experts, seed=experts)
+    x[3, ::7] = float("nan")
+    x[5, experts // groups:] = -INF
+    s = torch.softmax(x.double(), -1) if score == "softmax" else torch.sigmoid(x.double())
+    for r in range(6, 100, 13):
+        check(x[r:r + 1], min(8, keep), score=score, bias=(0.5 - s[r]).float(), groups=groups, group_topk=keep,
+              group_best=best)
+    check(x, min(8, keep), score=score, groups=groups, group_topk=keep, group_best=best)
+
+
 def test_ties_take_the_lower_expert():
     x = torch.zeros(3, 128, device="cuda")
     x[1, 100:] = 1.0
