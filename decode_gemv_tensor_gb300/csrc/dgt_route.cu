@@ -377,13 +377,22 @@ __device__ __noinline__ bool decide(const RouteArgs &a, const void *row, uint64_
     const float off = X::off * (1.0f + lanes_max<32>(big) * 0x1p-11f);
     if (a.groups > 1) {
         __syncwarp();
+        // lane g the best two of group g, found by as many lanes as there are for each
+        uint32_t share = 32;
+        while (share * a.groups > 32) share >>= 1;
         uint64_t one = 1, two = 1;   // NaN counts as nothing
-        if (lane < a.groups)
-            for (uint32_t i = 0; i < per; i++) {
-                const uint64_t x = vals[lane * per + i];
-                if (x > one) two = one, one = x;
-                else if (x > two) two = x;
-            }
+        auto put = [&](uint64_t x) {
+            two = x > one ? one : x > two ? x : two;
+            one = x > one ? x : one;
+        };
+        const uint32_t g = lane / share;
+        if (g < a.groups)
+            for (uint32_t i = lane % share; i < per; i += share) put(vals[g * per + i]);
+        for (uint32_t d = 1; d < share; d <<= 1) {
+            const uint64_t o1 = __shfl_xor_sync(DGT_FULL, one, d), o2 = __shfl_xor_sync(DGT_FULL, two, d);
+            put(o1), put(o2);
+        }
+        one = __shfl_sync(DGT_FULL, one, lane * share % 32), two = __shfl_sync(DGT_FULL, two, lane * share % 32);
         uint64_t value = one;
         if (a.group_best == 2 && per > 1) {
             // keys back to numbers: the sum of the best two
@@ -479,11 +488,12 @@ __global__ void __launch_bounds__(RT_WARPS * 32, EPL <= 8 ? RT_CTAS : 1) k_route
 #pragma unroll
         for (int i = 0; i < EPL; i++) c[i] = l[i];
     }
-    // How far an fp32 score may be off.  A sigmoid, which is at most 1: exponential and reciprocal within 2^-22, the
-    // product before it |l| 2^-24, of which s (1 - s) is left, a sum: below 2^-21.  A softmax, which is at most inv:
-    // expf, a sum of EPL + 5 steps, a quotient and a product, below (EPL + 8) 2^-23.  Then half a unit of the sum
-    // with the bias.
-    const float off = a.sigmoid ? 0x1p-21f : (float)(EPL + 8) * 0x1p-23f * inv;
+    // How far an fp32 score may be off.  A sigmoid, which is at most 1: of the exponential's 2^-22 and the product's
+    // |l| 2^-24 before it s (1 - s) is left, at most 2^-24 and 0.28 2^-24 with the factor's own rounding; of the
+    // reciprocal's 2^-23 and the sum's 2^-24 all: below 4.3 2^-24 (2^-21 sent more tokens to `decide`: 8201 of 256
+    // experts with a bias 14.4 us, 11.5 with this).  A softmax, which is at most inv: expf, a sum of EPL + 5 steps, a
+    // quotient and a product, below (EPL + 8) 2^-23.  Then half a unit of the sum with the bias.
+    const float off = a.sigmoid ? 4.3f * 0x1p-24f : (float)(EPL + 8) * 0x1p-23f * inv;
     bool close = false;
     uint32_t shut = 0;
     if (GL == 32 && a.groups > 1) {
