@@ -605,7 +605,10 @@ __global__ void __launch_bounds__(RT_WARPS * 32, EPL <= 8 ? RT_CTAS : 1) k_route
         const float top = lanes_max<GL>(x == x ? x : -INFINITY);
         float q = soft_term(x, top);
         // e^(l - top) (1 + e^top) / (1 + e^l) for a top below 0, else s itself
-        if (a.sigmoid) q = top > 0.0f ? (x == x ? sigmoid_of(x) : 0.0f) : q * (1.0f + expf(top)) / (1.0f + expf(x));
+        if (a.sigmoid) {
+            q = top > 0.0f ? sigmoid_of(x) : q * (1.0f + expf(top)) / (1.0f + expf(x));
+            if (x != x) q = 0.0f;
+        }
         const float sum = lanes_sum<GL>(on ? q : 0.0f);
         w = sum > 0.0f ? q / sum : 0.0f;
     } else {

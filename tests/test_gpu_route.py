@@ -139,6 +139,17 @@ def test_masked_infinite_and_not_a_number():
     check(logits(50, 64), 8, bias=b)
 
 
+def test_not_a_number_beside_negative_logits():
+    """A choice without a score takes nothing from the others' weights."""
+    x = -logits(40, 64, seed=10).abs() - 0.1
+    for r in range(40):
+        x[r, torch.randperm(64, generator=torch.Generator().manual_seed(r))[:25 + r].cuda()] = float("nan")
+    for renorm in (False, True):
+        for kw in (dict(), dict(bias=bias_of(64)), dict(groups=8, group_topk=6)):
+            ids, p = check(x, 32, score="sigmoid", renorm=renorm, **kw)
+            assert bool((p[:39].sum(1) > 0).all()) and not bool(p[39].any())   # the last holds nothing else
+
+
 def test_scores_below_the_range_of_fp32_keep_their_quotients():
     x = logits(20, 32, seed=3) - 300.0
     ids, p = check(x, 4, score="sigmoid")
