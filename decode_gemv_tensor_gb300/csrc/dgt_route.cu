@@ -434,6 +434,19 @@ __device__ __noinline__ bool decide(const RouteArgs &a, const void *row, uint64_
         const bool unsure = lane < a.topk && below > 1 && !(apart(X{}, mine, below) > 2.0f * off) &&
                             !(logit(a, row, id) == logit(a, row, behind) && a.bias[id] == a.bias[behind]);
         clear &= !__any_sync(DGT_FULL, unsure);
+        // what is left, against the last choice: one that is not the same but as close may be before it
+        const uint64_t last = __shfl_sync(DGT_FULL, mine, a.topk - 1);
+        const uint32_t e_last = __shfl_sync(DGT_FULL, id, a.topk - 1);
+        if (clear && next > 1 && !(apart(X{}, last, next) > 2.0f * off)) {
+            bool hidden = false;
+#pragma unroll
+            for (int i = 0; i < EPL; i++) {
+                const uint32_t e = lane * EPL + i;
+                if (key[i] > 1 && !(apart(X{}, last, key[i]) > 2.0f * off))
+                    hidden |= !(logit(a, row, e) == logit(a, row, e_last) && a.bias[e] == a.bias[e_last]);
+            }
+            clear = !__any_sync(DGT_FULL, hidden);
+        }
     }
     return clear;
 }
@@ -579,8 +592,9 @@ __global__ void __launch_bounds__(RT_WARPS * 32, EPL <= 8 ? RT_CTAS : 1) k_route
         const uint32_t other = __shfl_down_sync(DGT_FULL, id, 1), behind = lane + 1 < a.topk ? other : next_id;
         if (lane + 1 < a.topk) lo = after;
         bool unsure = lane < a.topk && near(hi, lo, 2.0f * off + 0x1p-23f * (fabsf(lo) + fabsf(hi)));
-        // the same logit and bias are the same value
-        if (unsure) unsure = !(logit(a, row, id) == logit(a, row, behind) && a.bias[id] == a.bias[behind]);
+        // The same logit and bias are the same value; behind the last choice such a one may hide a third that is as
+        // close.
+        if (unsure && lane + 1 < a.topk) unsure = !(logit(a, row, id) == logit(a, row, behind) && a.bias[id] == a.bias[behind]);
         close |= unsure;
     }
     uint32_t again = __ballot_sync(DGT_FULL, close && live);

@@ -150,6 +150,25 @@ def test_not_a_number_beside_negative_logits():
             assert bool((p[:39].sum(1) > 0).all()) and not bool(p[39].any())   # the last holds nothing else
 
 
+@pytest.mark.parametrize("experts,topk", [(16, 1), (16, 5), (128, 4), (256, 8), (256, 20)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_copies_at_the_cut_hide_no_other(experts, topk, score):
+    """The last choice and the next are copies, and a third value is closer to theirs than fp32 can tell."""
+    for seed in range(20):
+        x = logits(1, experts, seed=seed)
+        at = torch.randperm(experts, generator=torch.Generator().manual_seed(seed))[:topk + 2].tolist()
+        a, b, c = at[:3]
+        x[0, b] = x[0, a]
+        s = (torch.softmax(x.double(), -1) if score == "softmax" else torch.sigmoid(x.double()))[0]
+        bias = torch.full((experts,), -4.0, device="cuda")
+        bias[at[3:]] = 4.0                     # topk - 1 that are chosen in any case
+        bias[[a, b]] = 0.25
+        bias[c] = (0.25 + s[a] - s[c]).float()
+        check(x, topk, score=score, bias=bias)
+        if experts == 256 and topk < 9:
+            check(x, topk, score=score, bias=bias, groups=4, group_topk=4)
+
+
 def test_scores_below_the_range_of_fp32_keep_their_quotients():
     x = logits(20, 32, seed=3) - 300.0
     ids, p = check(x, 4, score="sigmoid")
