@@ -37,7 +37,7 @@ constexpr uint32_t BM_PIECES = 4;                                 // 16-byte pie
 constexpr uint32_t BM_BLOCK = 64;                                 // pieces of a block
 constexpr uint32_t BM_CAP = BM_MAX_N * BM_PIECES * 8 + BM_MAX_N;  // of the list
 constexpr float BM_LOG2E = 1.4426950408889634f;
-constexpr float BM_HUGE = 1e38f;
+constexpr float BM_HUGE = 0x1p30f;                                // above it v - base is taken before the product with L
 constexpr float BM_OFF = 0x1p-17f;                                // totals of two beams may be off against each other
 constexpr float BM_GROW = 10.0f;                                  // logits above a thread's reference that its sum stands
 
@@ -326,7 +326,8 @@ __device__ __forceinline__ float sum_of(const uint4 (&x)[BM_PIECES], float bl) {
     return a + b;
 }
 
-// The same where v L may be out of range: sum e^(v - base).
+// The same for |base| above BM_HUGE, where what bl was rounded by no longer is a sane exponent: sum e^(v - base).  At
+// BM_HUGE it is below 2^6, so that 2^24 terms of a thread stay within 2^103.
 template <bool F32>
 __device__ __forceinline__ float sum_of_huge(const uint4 (&x)[BM_PIECES], float base) {
     float sum = 0.0f;
@@ -368,8 +369,9 @@ __device__ __forceinline__ float2 scan_segment(const BeamArgs &a, BeamShared &s,
         if (top > base + BM_GROW || (base == -INFINITY && top > base)) {
             const bool big = fabsf(top) > BM_HUGE;
             const float to = big ? 0.0f : top * BM_LOG2E;
-            // nothing is left of a sum that is so far below
-            const float f = big || huge || base == -INFINITY ? 0.0f : beam_ex2(bl - to);
+            // sum e^v is what is held times 2^(base L + was), from here on times 2^(top L + off)
+            const float was = huge ? 0.0f : fmaf(-base, BM_LOG2E, bl), off = big ? 0.0f : fmaf(-top, BM_LOG2E, to);
+            const float f = base == -INFINITY ? 0.0f : beam_ex2(fmaf(base - top, BM_LOG2E, was - off));
             sum *= f, low *= f;
             base = top, bl = to, huge = big;
         }

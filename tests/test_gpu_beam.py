@@ -162,6 +162,28 @@ def test_masked_and_infinite_logits():
     check(x, s, 4)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("mask", [-1e4, -1e9, -1.1e9, -3e12, -1e20, -1e30, -3e38])
+def test_masks_of_any_size(dtype, mask):
+    """Rows whose beginning, end or most is masked by a finite number, and one that is masked throughout."""
+    x, s = inputs(3, 4, 20011, dtype, 31)
+    x[0, :9000] = x[1, 5:] = x[2, ::2] = x[4, 10001:] = x[5] = mask
+    x[6, torch.arange(20011, device="cuda") % 1024 < 1000] = mask
+    x[7, :-1] = mask
+    check(x, s, 9)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("size", [1e3, 1e5, 1e8, 1e9, 1e10, 1e16, 1e30])
+def test_logits_of_any_size(dtype, size):
+    x, s = inputs(2, 3, 9001, dtype, 32)
+    x[::2] = (x[::2].double() * size).to(dtype)
+    check(x, s, 9)
+    y = torch.arange(9001, device="cuda", dtype=torch.float64) - 4500.0
+    check((y * size / 100).to(dtype)[None].repeat(2, 1), s[:1, :2].contiguous(), 5)
+    check((size - y.abs() * 5).to(dtype)[None], s[:1, :1].contiguous(), 5)    # near one another
+
+
 def test_strides_and_offsets():
     wide = torch.randn(6, 10007, device="cuda").bfloat16()
     s = -torch.rand(2, 3, device="cuda")
