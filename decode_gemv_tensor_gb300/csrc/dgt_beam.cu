@@ -144,7 +144,7 @@ struct BeamShared {
     float2 part[BM_WARPS];
     uint64_t thr;
     float warp_top[BM_WARPS];
-    uint32_t count, blocks, found, last, refine;
+    uint32_t count, blocks, found, last, refine, ties;
 };
 
 // The sum of (B, S) of lanes 0 .. count - 1; the same in every lane.
@@ -589,7 +589,7 @@ __device__ __forceinline__ void join_entry(const BeamArgs &a, BeamShared &s, uin
     const uint64_t r0 = (uint64_t)entry * a.beams;
     float tops[BM_KEEP];   // on their way while the sums are joined
     load_tops(a, r0, tops);
-    if (tid == 0) s.blocks = 0, s.found = 0, s.refine = 0;
+    if (tid == 0) s.blocks = 0, s.found = 0, s.refine = 0, s.ties = 0;
     // a beam without a score, without a finite sum, or at its end offers nothing of its row
     for (uint32_t b = tid / 32; b < a.beams; b += BM_WARPS) {
         float2 p = make_float2(-INFINITY, 0.0f);
@@ -632,7 +632,8 @@ __device__ __forceinline__ void join_entry(const BeamArgs &a, BeamShared &s, uin
         const double score = (double)s.score[b], lse = s.lse[b];
         return lse < (double)INFINITY ? score + ((double)s.logit[i] - lse) : score;
     };
-    auto sort = [&]() {
+    // By total, then beam, then (where told to look) logit, then place.
+    auto sort = [&](bool logits) {
         for (uint32_t i = tid; i < count; i += BM_THREADS) {
             const uint64_t bits = (uint64_t)__double_as_longlong(total_of(i) + 0.0);
             s.total[i] = bits ^ ((uint64_t)((int64_t)bits >> 63) | 0x8000000000000000ull);
@@ -647,17 +648,25 @@ __device__ __forceinline__ void join_entry(const BeamArgs &a, BeamShared &s, uin
                 const uint64_t o = s.total[j];
                 rank += o > t || (o == t && s.place[j] < at);
             }
+            if (logits) {   // of one beam and total those with a greater logit instead of those at a lower place
+                for (uint32_t j = 0; j < count; j++)
+                    if (s.total[j] == t && s.place[j] >> BM_BEAM_SHIFT == at >> BM_BEAM_SHIFT && s.logit[j] != s.logit[i])
+                        rank += (s.logit[j] > s.logit[i]) - (s.place[j] < at);
+            }
             s.order[rank] = (uint16_t)i;
         }
         __syncthreads();
     };
-    sort();
-    // Totals of two beams that may be the other way round: then two neighbours in this order are, and one of them is
-    // not further behind the n-th.
+    sort(false);
+    // A beam's logits out of order are of totals that are equal in 64 bits.  Totals of two beams may be the other way
+    // round: then two neighbours in this order are, and one of them is not further behind the n-th.
     const double last = count > n ? total_of(s.order[n - 1]) - (double)BM_OFF : -INFINITY;
     for (uint32_t i = tid; i + 1 < count; i += BM_THREADS) {
         const uint32_t p = s.order[i], q = s.order[i + 1];
-        if (s.place[p] >> BM_BEAM_SHIFT == s.place[q] >> BM_BEAM_SHIFT) continue;
+        if (s.place[p] >> BM_BEAM_SHIFT == s.place[q] >> BM_BEAM_SHIFT) {
+            if (s.logit[p] < s.logit[q]) s.ties = 1;
+            continue;
+        }
         const double t = total_of(q);
         if (t >= last && total_of(p) - t <= (double)BM_OFF) s.refine = 1;
     }
@@ -681,8 +690,8 @@ __device__ __forceinline__ void join_entry(const BeamArgs &a, BeamShared &s, uin
             if (tid == 0) s.lse[beam] = lse;
         }
         __syncthreads();
-        sort();
     }
+    if (s.refine || s.ties) sort(true);
     const uint64_t o = (uint64_t)entry * n;
     for (uint32_t i = tid; i < n; i += BM_THREADS) {
         uint32_t at = 0xFFFFFFFFu;

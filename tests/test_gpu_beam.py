@@ -184,6 +184,16 @@ def test_logits_of_any_size(dtype, size):
     check((size - y.abs() * 5).to(dtype)[None], s[:1, :1].contiguous(), 5)    # near one another
 
 
+@pytest.mark.parametrize("vocab", [40, 3000])
+def test_totals_that_are_equal_in_64_bits(vocab):
+    """Within a beam the greater logit is first all the same, whichever way the candidates are found."""
+    x = inputs(4, 1, vocab, F32, 33)[0] * 1e-30
+    got = dgt.beam_select(x, torch.full((2, 2), -3.0, device="cuda"), 30)
+    for e in range(2):
+        order = torch.sort(x[2 * e], descending=True, stable=True)[1][:30]
+        assert torch.equal(got[1][e].long(), order) and not bool(got[0][e].any())
+
+
 def test_strides_and_offsets():
     wide = torch.randn(6, 10007, device="cuda").bfloat16()
     s = -torch.rand(2, 3, device="cuda")
