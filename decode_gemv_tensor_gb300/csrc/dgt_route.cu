@@ -327,6 +327,22 @@ __device__ __forceinline__ float apart(Exact<Two>, uint64_t hi, uint64_t lo) {
     return (a - b) + (value32((uint32_t)hi) - value32((uint32_t)lo));
 }
 
+// Whether the groups of a mask have the same best logits, and so, without a bias, the same value: their order stands
+// then.  (fp64 instead takes 15 us for a token: 8201 tokens of 256 bf16 logits in 8 groups 29 us, 19 with this.)
+__device__ __noinline__ bool same_best(const RouteArgs &a, const void *row, uint32_t groups) {
+    const uint32_t lane = lane_id(), per = a.experts / a.groups;
+    uint32_t one = 0, two = 0;
+    if (groups >> lane & 1u)
+        for (uint32_t i = 0; i < per; i++) {
+            const uint32_t x = order32(logit(a, row, lane * per + i));
+            two = max(two, min(one, x));
+            one = max(one, x);
+        }
+    if (a.group_best == 1) two = 0;
+    const uint32_t at = __ffs(groups) - 1, o = __shfl_sync(DGT_FULL, one, at), t = __shfl_sync(DGT_FULL, two, at);
+    return !__any_sync(DGT_FULL, (groups >> lane & 1u) && (one != o || two != t));
+}
+
 // A token's choice by a whole warp; false where `off` cannot tell.  vals:
 // shared memory of a 64-bit key for each expert.
 template <int EPL, typename T>
@@ -419,6 +435,10 @@ __device__ __noinline__ bool decide(const RouteArgs &a, const void *row, uint64_
         if (behind) {
             const uint64_t hi = __shfl_sync(DGT_FULL, value, __ffs(border) - 1), lo = __shfl_sync(DGT_FULL, value, __ffs(behind) - 1);
             clear = apart(X{}, hi, lo) > 4.0f * off;
+            if (!clear && !a.bias) {
+                const bool close = lane < a.groups && !(apart(X{}, max(hi, value), min(hi, value)) > 4.0f * off);
+                clear = same_best(a, row, __ballot_sync(DGT_FULL, close));
+            }
         }
 #pragma unroll
         for (int i = 0; i < EPL; i++)
