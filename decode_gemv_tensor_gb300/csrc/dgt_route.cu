@@ -17,7 +17,7 @@
 // are.
 //
 // What bounds it: instructions and the steps of a token that wait for one
-// another (8201 tokens, 256 experts in 8 groups, sigmoid and bias: 19 us, of
+// another (8201 tokens, 256 experts in 8 groups, sigmoid and bias: 19.5 us, of
 // which 3 decide a token or two again and 5 are the groups; the logits' bytes
 // take 1.3).  One token of 128 experts 3.7 us.  fp64 alone for the close ones
 // took 16 us of 36; a score of its own for each lane's logit is what stays.
@@ -328,7 +328,7 @@ __device__ __forceinline__ float apart(Exact<Two>, uint64_t hi, uint64_t lo) {
 }
 
 // Whether the groups of a mask have the same best logits, and so, without a bias, the same value: their order stands
-// then.  (fp64 instead takes 15 us for a token: 8201 tokens of 256 bf16 logits in 8 groups 29 us, 19 with this.)
+// then.  (fp64 takes some 15 us for a token: 8201 tokens of 256 bf16 logits in 8 groups 29 us, 19 with this.)
 __device__ __noinline__ bool same_best(const RouteArgs &a, const void *row, uint32_t groups) {
     const uint32_t lane = lane_id(), per = a.experts / a.groups;
     uint32_t one = 0, two = 0;
